@@ -17,7 +17,11 @@ from ._binding import (  # noqa: F401
     attn_fwd_ex,
     attn_fwd_noalloc,
     attn_fwd_packed,
+    attn_fwd_paged,
     attn_fwd_visited,
+    attn_paged_append,
+    attn_paged_tables,
+    attn_paged_workspace,
     attn_release_workspace,
     attn_strerror,
     attn_tile_shape,

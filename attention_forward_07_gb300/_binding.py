@@ -26,6 +26,10 @@ EXPORTS = (
     "attn_fwd_visited",
     "attn_fwd_noalloc",
     "attn_fwd_ex",
+    "attn_paged_tables",
+    "attn_paged_append",
+    "attn_fwd_paged",
+    "attn_paged_workspace",
     "attn_check",
     "attn_release_workspace",
     "attn_debug_counters",
@@ -47,6 +51,38 @@ class FwdParams(ctypes.Structure):
                 ("stream", ctypes.c_void_p), ("visited", ctypes.c_void_p), ("seqlens_q", ctypes.c_void_p),
                 ("seqlens_k", ctypes.c_void_p), ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
                 ("max_seqlen_q", ctypes.c_int), ("max_seqlen_k", ctypes.c_int)]
+
+
+def _fields(text):
+    """A struct's fields from 'type: names' lines; p = pointer, i = int, l = long long, u = unsigned long long, f = float."""
+    kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int, "l": ctypes.c_longlong, "u": ctypes.c_ulonglong, "f": ctypes.c_float}
+    return [(name, kinds[kind]) for kind, names in (line.split(":") for line in text.strip().splitlines()) for name in names.split()]
+
+
+class PagedTablesParams(ctypes.Structure):
+    """attn_paged_tables_params_t of include/attn.h."""
+    _fields_ = _fields("""p: ctx_lens new_lens block_table free_pages free_count free_count_out cu_seqlens_q seqlens_k slots positions
+i: B table_width table_stride max_free max_rows page_size num_pages
+p: stream""")
+
+
+class PagedAppendParams(ctypes.Structure):
+    """attn_paged_append_params_t of include/attn.h."""
+    _fields_ = _fields("""p: k_new v_new k_cache v_cache slots
+l: k_row_stride k_head_stride v_row_stride v_head_stride cache_page_stride cache_head_stride cache_row_stride
+i: rows Hkv d num_pages page_size dtype
+p: stream""")
+
+
+class FwdPagedParams(ctypes.Structure):
+    """attn_fwd_paged_params_t of include/attn.h."""
+    _fields_ = _fields("""p: q k_cache v_cache o lse block_table cu_seqlens_q seqlens_k workspace
+u: workspace_bytes
+l: q_row_stride q_head_stride o_row_stride o_head_stride cache_page_stride cache_head_stride cache_row_stride
+i: B Hq Hkv d total_q max_seqlen_q num_pages page_size table_width table_stride causal window_left window_right
+f: scale
+i: dtype
+p: stream""")
 
 
 class AttnError(RuntimeError):
@@ -81,6 +117,14 @@ def library():
         lib.attn_fwd_noalloc.restype = i
         lib.attn_fwd_ex.argtypes = [ctypes.POINTER(FwdParams)]
         lib.attn_fwd_ex.restype = i
+        lib.attn_paged_tables.argtypes = [ctypes.POINTER(PagedTablesParams)]
+        lib.attn_paged_tables.restype = i
+        lib.attn_paged_append.argtypes = [ctypes.POINTER(PagedAppendParams)]
+        lib.attn_paged_append.restype = i
+        lib.attn_fwd_paged.argtypes = [ctypes.POINTER(FwdPagedParams)]
+        lib.attn_fwd_paged.restype = i
+        lib.attn_paged_workspace.argtypes = [ctypes.POINTER(FwdPagedParams), ctypes.POINTER(ctypes.c_ulonglong)]
+        lib.attn_paged_workspace.restype = i
         lib.attn_check.argtypes = [p]
         lib.attn_check.restype = i
         lib.attn_release_workspace.argtypes = [p]
@@ -215,6 +259,170 @@ def attn_fwd_packed(q, k, v, o, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_se
     rc = library().attn_fwd_ex(ctypes.byref(prm))
     if rc != 0:
         raise AttnError(rc, "attn_fwd_ex")
+
+
+def _paged_launch(call, device, stream):
+    """Runs call(stream handle) with `device` current, on `stream` or torch's current stream there."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("the paged operators take CUDA tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the tensors are on {device}, the stream on {stream.device}")
+    if torch.cuda.current_device() == device.index:
+        return call(stream)
+    with torch.cuda.device(device):
+        return call(stream)
+
+
+def _index_ptr(t, name, n, device):
+    """Address of a contiguous int32 vector of n entries on `device`."""
+    import torch
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on {device}")
+    return t.data_ptr()
+
+
+def _table_strides(t, B, device):
+    import torch
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 2 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"block_table must be int32 [{B}, pages] on {device}, each row contiguous")
+    return t.shape[1], t.stride(0) if B > 1 else t.shape[1]
+
+
+def _rows_strides(t, name, shape, dtype, device):
+    """(row, head) strides of a packed [H, rows, d] tensor."""
+    if t.dtype != dtype or t.device != device or t.shape != shape or t.stride(2) != 1:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, its last dimension contiguous")
+    return t.stride(1), t.stride(0)
+
+
+def _cache_strides(k_cache, v_cache, dtype, device):
+    """(page, head, row) strides of [num_pages, Hkv, page_size, d] caches."""
+    s = k_cache.stride()
+    if (k_cache.dim() != 4 or k_cache.dtype != dtype or v_cache.dtype != dtype or k_cache.device != device or
+            v_cache.device != device or v_cache.shape != k_cache.shape or v_cache.stride() != s or s[3] != 1):
+        raise ValueError(f"k_cache and v_cache must be {dtype} [num_pages, Hkv, page_size, d] on {device}, of the same strides, "
+                         "their last dimension contiguous")
+    return s[0], s[1], s[2]
+
+
+def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages, cu_seqlens_q, seqlens_k,
+                      slots, positions=None, free_count_out=None, stream=None):
+    """Block tables, slot map, positions and row offsets of a serving step from its requests' lengths.
+
+    int32 device tensors: ctx_lens, new_lens [B] (tokens cached, tokens to come), block_table [B, W] (in / out: the
+    pages added are filled in), free_pages [F] with free_count [1] (taken from the end) -> cu_seqlens_q [B+1],
+    seqlens_k [B], slots and positions [max rows] (-1 behind the last new row), free_count_out [1] (default: free_count
+    itself).  See include/attn.h."""
+    dev = ctx_lens.device
+    B = ctx_lens.shape[0]
+    width, stride = _table_strides(block_table, B, dev)
+    rows, nfree = slots.shape[0], free_pages.shape[0]
+    if free_count_out is None:
+        free_count_out = free_count
+    prm = PagedTablesParams(_index_ptr(ctx_lens, "ctx_lens", B, dev), _index_ptr(new_lens, "new_lens", B, dev),
+                            block_table.data_ptr(), _index_ptr(free_pages, "free_pages", nfree, dev),
+                            _index_ptr(free_count, "free_count", 1, dev), _index_ptr(free_count_out, "free_count_out", 1, dev),
+                            _index_ptr(cu_seqlens_q, "cu_seqlens_q", B + 1, dev), _index_ptr(seqlens_k, "seqlens_k", B, dev),
+                            _index_ptr(slots, "slots", rows, dev),
+                            None if positions is None else _index_ptr(positions, "positions", rows, dev),
+                            B, width, stride, nfree, rows, page_size, num_pages)
+
+    def call(st):
+        prm.stream = st.cuda_stream
+        return library().attn_paged_tables(ctypes.byref(prm))
+    rc = _paged_launch(call, dev, stream)
+    if rc != 0:
+        raise AttnError(rc, "attn_paged_tables")
+
+
+def attn_paged_append(k_new, v_new, k_cache, v_cache, slots, stream=None):
+    """Write new rows k_new, v_new [Hkv, rows, d] to their slots (int32 [rows]; negative: left out) of the caches
+    [num_pages, Hkv, page_size, d].  Any strides whose last dimension is contiguous; see include/attn.h."""
+    dev, dtype = k_new.device, k_new.dtype
+    code = _dtype_code(k_new)
+    cs = _cache_strides(k_cache, v_cache, dtype, dev)
+    num_pages, Hkv, page_size, d = k_cache.shape
+    rows = slots.shape[0]
+    if rows == 0:
+        return
+    shape = (Hkv, rows, d)
+    prm = PagedAppendParams(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                            _index_ptr(slots, "slots", rows, dev), *_rows_strides(k_new, "k_new", shape, dtype, dev),
+                            *_rows_strides(v_new, "v_new", shape, dtype, dev), *cs, rows, Hkv, d, num_pages, page_size, code)
+
+    def call(st):
+        prm.stream = st.cuda_stream
+        return library().attn_paged_append(ctypes.byref(prm))
+    rc = _paged_launch(call, dev, stream)
+    if rc != 0:
+        raise AttnError(rc, "attn_paged_append")
+
+
+_workspace_sizes = {}
+
+
+def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, lse=None, causal=False,
+                   window_left=-1, window_right=-1, scale=None, workspace=None, stream=None):
+    """Attention of packed query rows over a paged cache: q/o [Hq, total_q, d], caches [num_pages, Hkv, page_size, d] (any
+    strides whose last dimension is contiguous), lse fp32 [Hq, total_q] or None; block_table int32 [B, W], cu_seqlens_q
+    int32 [B+1], seqlens_k int32 [B] (keys per request, the new rows' own included).  One token per request, a few or whole
+    chunks, mixed freely.  workspace: a uint8 tensor of attn_paged_workspace() bytes for calls that do not run at the same
+    time; None takes one from torch's allocator.  See include/attn.h."""
+    import torch
+    dev, dtype = q.device, q.dtype
+    code = _dtype_code(q)
+    Hq, total_q, d = shape = q.shape
+    cs = _cache_strides(k_cache, v_cache, dtype, dev)
+    num_pages, Hkv, page_size, dk = k_cache.shape
+    if dk != d:
+        raise ValueError("q and the caches disagree on d")
+    B = seqlens_k.shape[0]
+    width, tstride = _table_strides(block_table, B, dev)
+    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != shape[:2] or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous fp32 {(Hq, total_q)} on {dev}")
+    if total_q == 0:
+        return
+    prm = FwdPagedParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+                         block_table.data_ptr(), _index_ptr(cu_seqlens_q, "cu_seqlens_q", B + 1, dev),
+                         _index_ptr(seqlens_k, "seqlens_k", B, dev), None, 0, *_rows_strides(q, "q", shape, dtype, dev),
+                         *_rows_strides(o, "o", shape, dtype, dev), *cs, B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size,
+                         width, tstride, int(bool(causal)), window_left, window_right, d ** -0.5 if scale is None else scale, code)
+
+    def call(st):
+        ws = workspace
+        if ws is None:
+            key = (dev.index, Hq, Hkv, d, max_seqlen_q)
+            n = _workspace_sizes.get(key)
+            if n is None:
+                n = _workspace_sizes[key] = _paged_workspace(prm)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            if st != torch.cuda.current_stream(dev):
+                ws.record_stream(st)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        prm.workspace = ws.data_ptr()
+        prm.workspace_bytes = ws.numel() * ws.element_size()
+        prm.stream = st.cuda_stream
+        return library().attn_fwd_paged(ctypes.byref(prm))
+    rc = _paged_launch(call, dev, stream)
+    if rc != 0:
+        raise AttnError(rc, "attn_fwd_paged")
+
+
+def _paged_workspace(prm) -> int:
+    n = ctypes.c_ulonglong(0)
+    rc = library().attn_paged_workspace(ctypes.byref(prm), ctypes.byref(n))
+    if rc != 0:
+        raise AttnError(rc, "attn_paged_workspace")
+    return n.value
+
+
+def attn_paged_workspace(Hq, Hkv, d, max_seqlen_q) -> int:
+    """Bytes of workspace attn_fwd_paged wants on the current device."""
+    return _paged_workspace(FwdPagedParams(B=1, Hq=Hq, Hkv=Hkv, d=d, max_seqlen_q=max_seqlen_q))
 
 
 def attn_check(stream=None) -> int:

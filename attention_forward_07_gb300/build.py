@@ -12,8 +12,8 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "attn_fwd.cu")]
-HEADERS = [os.path.join(HERE, "csrc", "ptx.cuh"), os.path.join(ROOT, "include", "attn.h")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("attn_fwd.cu", "paged_attn.cu", "paged_cache.cu")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("ptx.cuh", "host.h")] + [os.path.join(ROOT, "include", "attn.h")]
 OUT = os.path.join(HERE, "libattn.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
@@ -36,17 +36,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return OUT
     tmp = OUT + f".tmp{os.getpid()}"
-    cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", os.path.join(ROOT, "include"), "-o", tmp, *SOURCES]
+    cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
     if verbose:
         cmd.insert(2, "-Xptxas=-v")
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libattn.so")
-    if verbose:
-        sys.stderr.write(r.stderr)
-    os.replace(tmp, OUT)
+    objects = [tmp + f".{i}.o" for i in range(len(SOURCES))]
+    try:
+        # the sources side by side, then the link
+        jobs = [subprocess.Popen(cmd + ["-c", s, "-o", o], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+                for s, o in zip(SOURCES, objects)]
+        outs = [j.communicate()[0] for j in jobs]
+        failed = any(j.returncode != 0 for j in jobs)
+        if not failed:
+            r = subprocess.run(cmd + ["-shared", "-o", tmp, *objects], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+            outs.append(r.stdout)
+            failed = r.returncode != 0
+        if failed or verbose:
+            sys.stderr.write("".join(outs))
+        if failed:
+            raise RuntimeError("nvcc failed building libattn.so")
+        os.replace(tmp, OUT)
+    finally:
+        for f in objects:
+            if os.path.exists(f):
+                os.remove(f)
     return OUT
 
 

@@ -58,6 +58,7 @@
 #include <unordered_map>
 
 #include "attn.h"
+#include "host.h"
 #include "ptx.cuh"
 
 namespace attn {
@@ -203,7 +204,8 @@ struct Params {
 }  // namespace attn
 
 // Device status words, one per stream slot (the host gives every (device, stream) pair a
-// slot; streams beyond the table share slot 0): bit 0 = a barrier wait ran out of time.
+// slot; streams beyond the table share slot 0): bit 0 = a barrier wait ran out of time,
+// bit 1 = a paged operator met a page id, slot or page count out of range.
 constexpr int STATUS_SLOTS = 1024;
 __device__ unsigned int g_attn_status[STATUS_SLOTS];
 // Work queue per stream slot: [2 s] = next unit to hand out, [2 s + 1] = CTAs that have
@@ -1917,6 +1919,20 @@ attn_fwd_params_t square_params(const void* q, const void* k, const void* v, voi
 }  // namespace
 }  // namespace attn
 
+// What the paged operators' sources need of the state above (host.h).
+namespace attn {
+
+int host_device(int& sms, int& dev) { return device_info(sms, dev); }
+
+int host_status_word(int dev, void* stream, unsigned int** word) {
+  void* base = nullptr;
+  if (cudaGetSymbolAddress(&base, g_attn_status) != cudaSuccess || !base) return ATTN_ERR_CUDA;
+  *word = static_cast<unsigned int*>(base) + stream_state(dev, stream, true)->slot;
+  return ATTN_OK;
+}
+
+}  // namespace attn
+
 // ====================================================================== C-ABI
 extern "C" {
 
@@ -1966,7 +1982,7 @@ int attn_check(void* stream) {
             cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
       return ATTN_ERR_CUDA;
-    return ATTN_ERR_TIMEOUT;
+    return (status & attn::STATUS_TIMEOUT) ? ATTN_ERR_TIMEOUT : ATTN_ERR_PAGE;
   }
   return ATTN_OK;
 }
@@ -2000,6 +2016,7 @@ const char* attn_strerror(int status) {
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_TIMEOUT: return "kernel barrier wait timed out";
     case ATTN_ERR_DEVICE: return "no usable sm_103 device";
+    case ATTN_ERR_PAGE: return "page id, slot or page count out of range";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,660 @@
+// paged_attn.cu -- attention of packed query rows over a paged key/value cache (attn_fwd_paged).
+//
+//     O[t, hq] = sum_j softmax_j( scale <Q[t, hq], K_j> ) V_j,   LSE[t, hq] = ln sum_j exp(...)
+//
+// over the keys j of row t's request that its position and window keep, K_j and V_j found
+// through the request's block table.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "attn.h"
+#include "host.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr float LN2 = 0.69314718055994530942f;
+
+struct PagedParams {
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  float* lse;
+  const int *table, *cu_q, *lens_k;
+  long long q_row, q_head, o_row, o_head;  // strides in elements
+  long long c_page, c_head, c_row;
+  int B, Hq, Hkv, g, total_q, max_q, num_pages, page_size, width, table_stride;
+  int wl, er;  // band: keys pos - wl .. pos + er (-1: unbounded)
+  float scale_log2;
+  unsigned int* status;
+  float* part_o;     // [2 * grid][16][D] partial sums of V, not normalised
+  float2* part_ml;   // [2 * grid][16] their exponent base (exp2 domain) and sum of weights
+  struct Split* split;  // [grid]
+};
+
+// An item whose tiles CTA c begins and others finish: the partial results to join.
+struct Split {
+  int b, h, blk;  // b < 0: none
+  int parts;      // slots 2c + 1, 2(c + 1), 2(c + 2), ...
+};
+
+// Query rows, keys and first query row of request b, whatever the arrays hold.
+__device__ __forceinline__ void request_span(const PagedParams& p, int b, int& row0, int& sq, int& sk) {
+  row0 = min(max(__ldg(p.cu_q + b), 0), p.total_q);
+  sq = min(min(max(__ldg(p.cu_q + b + 1), row0), p.total_q) - row0, p.max_q);
+  sk = (int)min((long long)max(__ldg(p.lens_k + b), 0), (long long)p.width * p.page_size);
+}
+
+// Keys that query row i (of sq, against sk keys) keeps: [lo, hi).
+__device__ __forceinline__ int row_lo(const PagedParams& p, int i, int off) {
+  return p.wl < 0 ? 0 : (int)max(0ll, (long long)i + off - p.wl);
+}
+__device__ __forceinline__ int row_hi(const PagedParams& p, int i, int off, int sk) {
+  return p.er < 0 ? sk : (int)min((long long)sk, (long long)i + off + p.er + 1);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  } else {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+}
+
+// ------------------------------------------------------------------ few rows: the memory-bound path
+// An item is (request, K/V head, block of 16 packed rows), row r of a request's K/V head being query
+// token r / g, query head r % g of the group: one pass over the keys serves the whole group.  Each
+// key costs 4 d bytes and 16 * 4 d flops, far below the machine's ratio, so the keys' stream from memory is
+// the floor and everything else has to hide behind it:
+//  * the items' key tiles, laid end to end, are cut into equal runs, one per CTA, whatever the
+//    lengths: no CTA has more to read than another.  Items cut across CTAs leave partial results
+//    (at most two to a CTA) that rows_join_kernel puts together;
+//  * the four warps of a CTA take a quarter of each tile's keys each, with a ring of asynchronous copies,
+//    a running maximum, sum and accumulator of their own: nothing synchronises them before the item's end;
+//  * a lane holds the places of the next 32 page rows, so the table is read once per 32 copies;
+//  * mma.sync with the keys as the N side: 16 rows are its smallest M, and its operands come by
+//    ldmatrix straight from the copied rows (128-byte tcgen05 tiles would be an eighth full).
+template <int D>
+struct Rows {
+  static constexpr int WARPS = 4, NTHREADS = 32 * WARPS;
+  static constexpr int KPW = D == 128 ? 16 : 32;  // keys of a warp's stage: 8 KiB of K and V
+  static constexpr int NG = KPW / 16;             // groups of 16 keys: each lies in one page
+  static constexpr int TK = WARPS * KPW;          // keys of a tile
+  static constexpr int NST = 3;
+  static constexpr int STAGE = 2 * KPW * D * 2;
+  static constexpr int SMEM = WARPS * NST * STAGE;
+  static constexpr int CTAS_PER_SM = 2;
+  static constexpr int MIN_TILES = 2;             // tiles a CTA takes at least
+  static_assert(NST * STAGE >= 16 * D * 4, "a warp's ring holds its accumulator at the end");
+};
+
+// What the runs' arithmetic needs to know of a request.
+struct RowsItem {
+  int row0, sq, sk, off, R, nblk;
+};
+template <int D>
+__device__ __forceinline__ RowsItem rows_request(const PagedParams& p, int b) {
+  RowsItem it;
+  request_span(p, b, it.row0, it.sq, it.sk);
+  it.off = it.sk - it.sq;
+  it.R = it.sq * p.g;
+  it.nblk = (it.R + 15) / 16;
+  return it;
+}
+// Keys [lo, hi) that any row of block blk keeps and the tiles [t0, t1) that hold them (one tile of
+// nothing where no key is kept: the item still writes its rows).
+template <int D>
+__device__ __forceinline__ void rows_range(const PagedParams& p, const RowsItem& it, int blk, int& lo, int& hi, int& t0, int& t1) {
+  const int i0 = blk * 16 / p.g, i1 = (min(blk * 16 + 16, it.R) - 1) / p.g;
+  lo = row_lo(p, i0, it.off);
+  hi = row_hi(p, i1, it.off, it.sk);
+  if (hi <= lo) lo = hi = 0;
+  t0 = lo / Rows<D>::TK;
+  t1 = hi > lo ? (hi - 1) / Rows<D>::TK + 1 : t0 + 1;
+}
+template <int D>
+__device__ __forceinline__ long long rows_weight(const PagedParams& p, const RowsItem& it) {
+  long long w = 0;
+  for (int blk = 0; blk < it.nblk; ++blk) {
+    int lo, hi, t0, t1;
+    rows_range<D>(p, it, blk, lo, hi, t0, t1);
+    w += t1 - t0;
+  }
+  return w * p.Hkv;
+}
+// First tile of CTA c's run out of n tiles over `ctas` runs, and the CTA whose run holds tile x.
+__device__ __forceinline__ long long run_begin(long long n, int ctas, int c) { return n * c / ctas; }
+__device__ __forceinline__ int run_of(long long n, int ctas, long long x) { return (int)(((x + 1) * ctas - 1) / n); }
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes into shared memory, zeros where `bytes` is 0 (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_kernel(const __grid_constant__ PagedParams p) {
+  using C = Rows<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ long long warp_sum[C::WARPS];
+  __shared__ int4 start_s;            // b, h, blk, tile of the run's first tile
+  __shared__ float2 ml_s[C::WARPS][16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- this CTA's run: sum the weights, find where it begins
+  const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS;
+  const int rb0 = min(tid * per, p.B), rb1 = min(rb0 + per, p.B);
+  long long own = 0;
+  for (int b = rb0; b < rb1; ++b) own += rows_weight<D>(p, rows_request<D>(p, b));
+  long long incl = own;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, s);
+    if (lane >= s) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long n = 0, before = incl - own;
+#pragma unroll
+  for (int w = 0; w < C::WARPS; ++w) {
+    if (w < warp) before += warp_sum[w];
+    n += warp_sum[w];
+  }
+  const int ctas = (int)min((long long)gridDim.x, (n + C::MIN_TILES - 1) / C::MIN_TILES);
+  const int cta = blockIdx.x;
+  if (tid == 0) p.split[cta].b = -1;
+  if (cta >= ctas) return;
+  const long long run0 = run_begin(n, ctas, cta), run1 = run_begin(n, ctas, cta + 1);
+  if (run0 >= before && run0 < before + own) {
+    long long at = before;
+    int b = rb0;
+    RowsItem it;
+    for (;; ++b) {
+      it = rows_request<D>(p, b);
+      const long long w = rows_weight<D>(p, it);
+      if (run0 < at + w) {
+        const long long per_head = w / p.Hkv;
+        int h = (int)((run0 - at) / per_head), blk = 0;
+        long long rest = (run0 - at) - h * per_head;
+        for (;; ++blk) {
+          int lo, hi, t0, t1;
+          rows_range<D>(p, it, blk, lo, hi, t0, t1);
+          if (rest < t1 - t0) {
+            start_s = make_int4(b, h, blk, t0 + (int)rest);
+            break;
+          }
+          rest -= t1 - t0;
+        }
+        break;
+      }
+      at += w;
+    }
+  }
+  __syncthreads();
+  int b = start_s.x, h = start_s.y, blk = start_s.z, tile = start_s.w;
+  RowsItem it = rows_request<D>(p, b);
+
+  const uint32_t ring = smem_u32(smem) + warp * (C::NST * C::STAGE);
+  float* ringf = reinterpret_cast<float*>(smem + warp * (C::NST * C::STAGE));
+  constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks of a row, rows of one copy of the warp
+  const int crow = lane / CPR, cchunk = lane % CPR;
+  const int fr = lane >> 2, fc = (lane & 3) * 2;  // fragment row and column pair
+
+  for (long long pos = run0; pos < run1;) {
+    int lo, hi, t0, t1;
+    rows_range<D>(p, it, blk, lo, hi, t0, t1);
+    const int ntiles = (int)min((long long)(t1 - tile), run1 - pos);
+    const bool begins = tile == t0, ends = tile + ntiles == t1;
+
+    // Q fragments: rows fr and fr + 8 of the block (rows past the last one are copies of it)
+    uint32_t qf[D / 16][4];
+    int klo[2], khi[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = min(blk * 16 + fr + 8 * x, it.R - 1);
+      const int i = r / p.g;
+      klo[x] = row_lo(p, i, it.off);
+      khi[x] = row_hi(p, i, it.off, it.sk);
+      const uint16_t* src = p.q + (long long)(it.row0 + i) * p.q_row + (long long)(h * p.g + r - i * p.g) * p.q_head + fc;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        qf[s][x] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16));
+        qf[s][x + 2] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16 + 8));
+      }
+    }
+    // tiles whose every key is kept by every row need no mask
+    const int lo_all = row_lo(p, (min(blk * 16 + 16, it.R) - 1) / p.g, it.off), hi_all = row_hi(p, blk * 16 / p.g, it.off, it.sk);
+
+    const uint16_t* kh = p.k + h * p.c_head;
+    const uint16_t* vh = p.v + h * p.c_head;
+    const int* row = p.table + (long long)b * p.table_stride;
+    long long place = -1;  // lane's entry of the next 32 groups: element offset of its first row, -1 = none
+    const auto issue = [&](int s) {
+      if (s < ntiles) {
+        if ((s * C::NG) % 32 == 0) {
+          const int e = s + lane / C::NG;  // the lane's tile
+          const int key = (tile + e) * C::TK + warp * C::KPW + (lane % C::NG) * 16;
+          place = -1;
+          if (e < ntiles && key < hi && key + 16 > lo) {
+            const int idx = key / p.page_size;
+            const int pg = __ldg(row + idx);
+            if ((unsigned)pg < (unsigned)p.num_pages)
+              place = (long long)pg * p.c_page + (long long)(key - idx * p.page_size) * p.c_row;
+            else
+              atomicOr(p.status, STATUS_PAGE);
+          }
+        }
+        const uint32_t st = ring + (s % C::NST) * C::STAGE;
+        const int key0 = (tile + s) * C::TK + warp * C::KPW;
+#pragma unroll
+        for (int gq = 0; gq < C::NG; ++gq) {
+          const long long at = __shfl_sync(0xffffffffu, place, (s * C::NG + gq) % 32);
+#pragma unroll
+          for (int x = 0; x < 16 / RPI; ++x) {
+            const int r = gq * 16 + x * RPI + crow;
+            const int key = key0 + r;
+            const bool ok = at >= 0 && key >= lo && key < hi;
+            const long long src = ok ? at + (long long)(x * RPI + crow) * p.c_row + cchunk * 8 : 0;
+            const uint32_t dst = st + r * (D * 2) + ((cchunk ^ (r & 7)) * 16);
+            copy16(dst, kh + src, ok ? 16u : 0u);
+            copy16(dst + C::KPW * D * 2, vh + src, ok ? 16u : 0u);
+          }
+        }
+      }
+      copy_commit();
+    };
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s) issue(s);
+    for (int s = 0; s < ntiles; ++s) {
+      copy_wait<C::NST - 2>();
+      __syncwarp();
+      issue(s + C::NST - 1);
+      const uint32_t st = ring + (s % C::NST) * C::STAGE;
+      const int key0 = (tile + s) * C::TK + warp * C::KPW;
+      if (key0 >= hi || key0 + C::KPW <= lo) continue;  // no key of this warp's quarter
+
+      // S = Q K^T: 16 rows x KPW keys
+      float sc[2 * C::NG][4];
+#pragma unroll
+      for (int x = 0; x < 2 * C::NG; ++x) sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+        for (int gq = 0; gq < C::NG; ++gq) {
+          uint32_t kf[4];
+          const int r = gq * 16 + (lane >> 4) * 8 + (lane & 7), c = 2 * ks + ((lane >> 3) & 1);
+          ldsm_x4(st + r * (D * 2) + ((c ^ (r & 7)) * 16), kf);
+          mma_16816<BF16>(sc[2 * gq], qf[ks], kf[0], kf[1]);
+          mma_16816<BF16>(sc[2 * gq + 1], qf[ks], kf[2], kf[3]);
+        }
+      }
+      if (key0 < lo_all || key0 + C::KPW > hi_all) {
+#pragma unroll
+        for (int x = 0; x < 2 * C::NG; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + x * 8 + fc + (e & 1);
+            if (key < klo[e >> 1] || key >= khi[e >> 1]) sc[x][e] = -INFINITY;
+          }
+      }
+      // running maximum (exp2 domain): it moves only when it grows by more than 8, so the
+      // accumulator is rarely rescaled and weights stay below 2^8
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int x = 0; x < 2 * C::NG; ++x) {
+        mx[0] = fmaxf(mx[0], fmaxf(sc[x][0], sc[x][1]));
+        mx[1] = fmaxf(mx[1], fmaxf(sc[x][2], sc[x][3]));
+      }
+      bool grow = false;
+      float mn[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2)) * p.scale_log2;
+        mn[x] = mx[x] > m[x] + 8.f ? mx[x] : m[x];
+        grow |= mn[x] != m[x];
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float alpha = mn[x] == m[x] ? 1.f : ex2_approx(m[x] - mn[x]);
+          l[x] *= alpha;
+          m[x] = mn[x];
+#pragma unroll
+          for (int y = 0; y < D / 8; ++y) {
+            o[y][2 * x] *= alpha;
+            o[y][2 * x + 1] *= alpha;
+          }
+        }
+      }
+      const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+      for (int x = 0; x < 2 * C::NG; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[x][e] = ex2_approx(fmaf(sc[x][e], p.scale_log2, -mu[e >> 1]));
+          l[e >> 1] += sc[x][e];
+        }
+      // O += P V, the weights rounded to the values' type (as a matrix instruction takes them; the
+      // sum l keeps them in 32 bits)
+#pragma unroll
+      for (int gq = 0; gq < C::NG; ++gq) {
+        const uint32_t pf[4] = {pack2<BF16>(sc[2 * gq][0], sc[2 * gq][1]), pack2<BF16>(sc[2 * gq][2], sc[2 * gq][3]),
+                                pack2<BF16>(sc[2 * gq + 1][0], sc[2 * gq + 1][1]), pack2<BF16>(sc[2 * gq + 1][2], sc[2 * gq + 1][3])};
+        const int r = gq * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t vf[4];
+          const int c = 2 * x + (lane >> 4);
+          ldsm_x4_trans(st + C::KPW * D * 2 + r * (D * 2) + ((c ^ (r & 7)) * 16), vf);
+          mma_16816<BF16>(o[2 * x], pf, vf[0], vf[1]);
+          mma_16816<BF16>(o[2 * x + 1], pf, vf[2], vf[3]);
+        }
+      }
+    }
+    copy_wait<0>();
+    __syncwarp();
+
+    // ---- join the four warps through their rings: row r's 8-column chunk c at chunk c ^ (r & 7)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      const int r = fr + 8 * x;
+      if ((lane & 3) == 0) ml_s[warp][r] = make_float2(m[x], l[x]);
+#pragma unroll
+      for (int y = 0; y < D / 8; ++y)
+        *reinterpret_cast<float2*>(ringf + r * D + ((y ^ (r & 7)) * 8) + fc) = make_float2(o[y][2 * x], o[y][2 * x + 1]);
+    }
+    __syncthreads();
+    {
+      const int r = tid / 8;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml_s[w][r].x);
+      float f[C::WARPS], ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) {
+        f[w] = ml_s[w][r].x == -INFINITY ? 0.f : ex2_approx(ml_s[w][r].x - mm);
+        ll += f[w] * ml_s[w][r].y;
+      }
+      const bool whole = begins && ends;
+      const int slot = 2 * cta + (begins ? 1 : 0);
+      const int rr = blk * 16 + r;
+      const int i = rr / p.g, hq = h * p.g + rr - i * p.g;
+      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const int phys = (tid & 7) + 8 * j, col = (phys ^ (r & 7)) * 8;
+        float acc[8] = {};
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float4* src = reinterpret_cast<const float4*>(smem + w * (C::NST * C::STAGE)) + (r * D + phys * 8) / 4;
+          const float4 a = src[0], c = src[1];
+          acc[0] = fmaf(f[w], a.x, acc[0]);
+          acc[1] = fmaf(f[w], a.y, acc[1]);
+          acc[2] = fmaf(f[w], a.z, acc[2]);
+          acc[3] = fmaf(f[w], a.w, acc[3]);
+          acc[4] = fmaf(f[w], c.x, acc[4]);
+          acc[5] = fmaf(f[w], c.y, acc[5]);
+          acc[6] = fmaf(f[w], c.z, acc[6]);
+          acc[7] = fmaf(f[w], c.w, acc[7]);
+        }
+        if (whole) {
+          if (rr < it.R)
+            *reinterpret_cast<uint4*>(p.o + (long long)(it.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
+                make_uint4(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv),
+                           pack2<BF16>(acc[4] * inv, acc[5] * inv), pack2<BF16>(acc[6] * inv, acc[7] * inv));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)slot * 16 + r) * D + col);
+          dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        }
+      }
+      if ((tid & 7) == 0) {
+        if (!whole) p.part_ml[slot * 16 + r] = make_float2(mm, ll);
+        else if (rr < it.R && p.lse)
+          p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
+      }
+      if (begins && !ends && tid == 0) {
+        // the CTAs that hold the item's other tiles: up to the one whose run reaches its end
+        p.split[cta] = Split{b, h, blk, run_of(n, ctas, pos + (t1 - tile) - 1) - cta + 1};
+      }
+    }
+    __syncthreads();  // the rings are free again
+
+    pos += ntiles;
+    if (pos >= run1) break;
+    // next item: the head's next block, the next head, the next request with rows
+    if (++blk == it.nblk) {
+      blk = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do it = rows_request<D>(p, ++b);
+        while (it.nblk == 0);
+      }
+    }
+    rows_range<D>(p, it, blk, lo, hi, t0, t1);
+    tile = t0;
+  }
+}
+
+// Joins the partial results of split items: one CTA per (run that begins one, row), its four warps share
+// out the parts and each lane takes D / 32 columns.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int E = D / 32;
+  const Split sp = p.split[blockIdx.x];
+  if (sp.b < 0) return;
+  const RowsItem it = rows_request<D>(p, sp.b);
+  const int r = blockIdx.y, rr = sp.blk * 16 + r;
+  if (rr >= it.R) return;
+  __shared__ float acc_s[4][D];
+  __shared__ float2 ml_s[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = -INFINITY, l = 0.f, acc[E] = {};
+  for (int x = warp; x < sp.parts; x += 4) {
+    const int slot = x == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + x);
+    const float2 ml = p.part_ml[slot * 16 + r];
+    const float* src = p.part_o + ((long long)slot * 16 + r) * D + lane * E;
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = src[e];
+    const float mn = fmaxf(m, ml.x);
+    const float fa = m == -INFINITY ? 0.f : ex2_approx(m - mn), fb = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+    l = l * fa + ml.y * fb;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * fa + v[e] * fb;
+    m = mn;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
+  if (lane == 0) ml_s[warp] = make_float2(m, l);
+  __syncthreads();
+  if (warp != 0) return;
+  float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml_s[w].x);
+  float out[E] = {};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = ml_s[w].x == -INFINITY ? 0.f : ex2_approx(ml_s[w].x - mm);
+    ll += f * ml_s[w].y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = fmaf(f, acc_s[w][lane * E + e], out[e]);
+  }
+  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  const int i = rr / p.g, hq = sp.h * p.g + rr - i * p.g;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (long long)(it.row0 + i) * p.o_row + (long long)hq * p.o_head + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = pack2<BF16>(out[2 * e] * inv, out[2 * e + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host side
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Workspace: rows path partials.
+struct Plan {
+  int rows_grid;
+  size_t off_ml, off_split, bytes;
+  Plan(const attn_fwd_paged_params_t& a, int sms) {
+    rows_grid = 2 * sms;
+    const size_t slots = 2 * (size_t)rows_grid * 16;
+    off_ml = round256(slots * a.d * sizeof(float));
+    off_split = off_ml + round256(slots * sizeof(float2));
+    bytes = off_split + round256((size_t)rows_grid * sizeof(Split));
+  }
+};
+
+bool misaligned(const void* ptr, unsigned int to) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
+
+int check_shape(const attn_fwd_paged_params_t& a) {
+  if (a.B < 1 || a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv != 0 || a.max_seqlen_q < 1) return ATTN_ERR_INVALID;
+  if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (a.Hq / a.Hkv > 128) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int check(const attn_fwd_paged_params_t& a) {
+  if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.block_table || !a.cu_seqlens_q || !a.seqlens_k || !a.workspace)
+    return ATTN_ERR_INVALID;
+  int rc = check_shape(a);
+  if (rc != ATTN_OK) return rc;
+  if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (a.total_q < 1 || a.num_pages < 1 || a.table_width < 1 || a.table_stride < a.table_width || a.page_size < 16 ||
+      a.page_size % 16 != 0 || (long long)a.table_width * a.page_size > INT_MAX - 4096 ||
+      (long long)a.total_q * (a.Hq / a.Hkv) > INT_MAX - 4096 || a.window_left < -1 || a.window_right < -1)
+    return ATTN_ERR_INVALID;
+  if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return ATTN_ERR_INVALID;
+  for (const void* ptr : {a.q, a.k_cache, a.v_cache, (const void*)a.o})
+    if (misaligned(ptr, 16)) return ATTN_ERR_INVALID;
+  for (const void* ptr : {(const void*)a.lse, (const void*)a.block_table, (const void*)a.cu_seqlens_q, (const void*)a.seqlens_k})
+    if (misaligned(ptr, 4)) return ATTN_ERR_INVALID;
+  if (misaligned(a.workspace, 256)) return ATTN_ERR_INVALID;
+  for (long long s : {a.q_row_stride, a.q_head_stride, a.o_row_stride, a.o_head_stride, a.cache_page_stride, a.cache_head_stride,
+                      a.cache_row_stride})
+    if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID;
+  return ATTN_OK;
+}
+
+template <int D, bool BF16>
+int launch_rows(const PagedParams& p, const Plan& plan, cudaStream_t st, int dev) {
+  using C = Rows<D>;
+  static std::atomic<unsigned long long> attr_set{0};  // bit per device
+  const unsigned long long bit = 1ull << dev;
+  if (!(attr_set.load() & bit)) {
+    if (cudaFuncSetAttribute(rows_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    attr_set.fetch_or(bit);
+  }
+  rows_kernel<D, BF16><<<plan.rows_grid, C::NTHREADS, C::SMEM, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  rows_join_kernel<D, BF16><<<dim3(plan.rows_grid, 16), 128, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+int attn_paged_workspace(const attn_fwd_paged_params_t* params, unsigned long long* bytes) {
+  using namespace attn;
+  if (!params || !bytes) return ATTN_ERR_INVALID;
+  int rc = check_shape(*params);
+  if (rc != ATTN_OK) return rc;
+  int sms = 0, dev = 0;
+  if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
+  *bytes = Plan(*params, sms).bytes;
+  return ATTN_OK;
+}
+
+int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
+  using namespace attn;
+  if (!params) return ATTN_ERR_INVALID;
+  const attn_fwd_paged_params_t& a = *params;
+  int rc = check(a);
+  if (rc != ATTN_OK) return rc;
+  int sms = 0, dev = 0;
+  if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
+  const Plan plan(a, sms);
+  if (a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
+  PagedParams p = {};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.k = static_cast<const uint16_t*>(a.k_cache);
+  p.v = static_cast<const uint16_t*>(a.v_cache);
+  p.o = static_cast<uint16_t*>(a.o);
+  p.lse = a.lse;
+  p.table = a.block_table;
+  p.cu_q = a.cu_seqlens_q;
+  p.lens_k = a.seqlens_k;
+  p.q_row = a.q_row_stride;
+  p.q_head = a.q_head_stride;
+  p.o_row = a.o_row_stride;
+  p.o_head = a.o_head_stride;
+  p.c_page = a.cache_page_stride;
+  p.c_head = a.cache_head_stride;
+  p.c_row = a.cache_row_stride;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.g = a.Hq / a.Hkv;
+  p.total_q = a.total_q;
+  p.max_q = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.width = a.table_width;
+  p.table_stride = a.table_stride;
+  p.wl = a.window_left;
+  p.er = a.causal ? 0 : a.window_right;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+  p.split = reinterpret_cast<Split*>(ws + plan.off_split);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+  const bool bf16 = a.dtype == ATTN_BF16;
+  if (a.d == 64) return bf16 ? launch_rows<64, true>(p, plan, st, dev) : launch_rows<64, false>(p, plan, st, dev);
+  return bf16 ? launch_rows<128, true>(p, plan, st, dev) : launch_rows<128, false>(p, plan, st, dev);
+}
+
+}  // extern "C"

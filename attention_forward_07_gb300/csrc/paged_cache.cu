@@ -1,0 +1,270 @@
+// paged_cache.cu -- the bookkeeping of a paged key/value cache: block tables and slot maps
+// from request lengths, and the write of new key / value rows into their slots.
+
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "attn.h"
+#include "host.h"
+
+namespace attn {
+namespace {
+
+// ------------------------------------------------------------------ tables
+// With held_b = ceil(ctx_b / P), want_b = ceil((ctx_b + new_b) / P), need_b = want_b - held_b and
+// N_b, C_b the sums of need and new over the requests before b, the n-th page handed out is
+// free[count - 1 - n], request b's page held_b + i is the (N_b + i)-th, and new row t of request
+// b is at position ctx_b + t - C_b.
+//
+// One launch and no state between calls: every CTA sums all lengths by itself (a block-wide scan
+// of two counters, kept in shared memory), then the threads of all CTAs share out the pages and
+// the rows and find their request by bisection.  A slot on a page added in this call comes
+// straight from the free list, so no CTA waits for another's table entries.  The CTAs are one
+// cluster, and its barrier orders the reads of free_count before its one write, which may be in
+// place.  What bounds it is latency: the chain lengths -> scan -> bisection -> free list -> slot.
+constexpr int TABLES_THREADS = 1024;
+constexpr int TABLES_MAX_B = 16384;
+
+struct TablesParams {
+  attn_paged_tables_params_t a;
+  unsigned int* status;
+};
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Last request b with pre[b] <= x (pre[0] = 0, non-decreasing, x < pre[B]): the one that holds x.
+__device__ __forceinline__ int holder(const int* pre, int B, int x) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __grid_constant__ TablesParams p) {
+  const attn_paged_tables_params_t& a = p.a;
+  extern __shared__ int pre[];       // rows_pre[B + 1], need_pre[B + 1]
+  __shared__ int2 warp_sum[32];
+  const int B = a.B, P = a.page_size;
+  int* rows_pre = pre;
+  int* need_pre = pre + B + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int count = min(max(*a.free_count, 0), a.max_free);
+  const int count_in = *a.free_count;
+  __syncthreads();
+  cluster_arrive();  // free_count is read (the wait stands before its write)
+
+  // block-wide exclusive scan of (new, need), `per` neighbouring requests to a thread
+  const int per = (B + TABLES_THREADS - 1) / TABLES_THREADS;
+  const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  int2 sum = make_int2(0, 0);
+  for (int b = b0; b < b1; ++b) {
+    const int ctx = max(__ldg(a.ctx_lens + b), 0), add = max(__ldg(a.new_lens + b), 0);
+    rows_pre[b] = sum.x;
+    need_pre[b] = sum.y;
+    sum.x += add;
+    sum.y += (ctx + add + P - 1) / P - (ctx + P - 1) / P;
+    if (blockIdx.x == 0) a.seqlens_k[b] = ctx + add;
+  }
+  int2 incl = sum;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, s), y = __shfl_up_sync(0xffffffffu, incl.y, s);
+    if (lane >= s) incl.x += x, incl.y += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int2 w = warp_sum[lane];
+    const int2 own = w;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, w.x, s), y = __shfl_up_sync(0xffffffffu, w.y, s);
+      if (lane >= s) w.x += x, w.y += y;
+    }
+    warp_sum[lane] = make_int2(w.x - own.x, w.y - own.y);
+    if (lane == 31) rows_pre[B] = w.x, need_pre[B] = w.y;
+  }
+  __syncthreads();
+  const int2 before = make_int2(warp_sum[warp].x + incl.x - sum.x, warp_sum[warp].y + incl.y - sum.y);
+  for (int b = b0; b < b1; ++b) rows_pre[b] += before.x, need_pre[b] += before.y;
+  __syncthreads();
+  const int total = rows_pre[B], need = need_pre[B];
+
+  bool bad = count_in != count || need > count || total > a.max_rows;
+  const auto free_page = [&](int n) {
+    const int id = (unsigned)n < (unsigned)count ? __ldg(a.free_pages + (count - 1 - n)) : -1;
+    return id >= 0 && id < a.num_pages ? id : -1;
+  };
+  const int nthr = gridDim.x * TABLES_THREADS, gid = blockIdx.x * TABLES_THREADS + tid;
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= B; b += TABLES_THREADS) a.cu_seqlens_q[b] = rows_pre[b];
+  for (int n = gid; n < need; n += nthr) {
+    const int b = holder(need_pre, B, n);
+    const int i = (max(__ldg(a.ctx_lens + b), 0) + P - 1) / P + (n - need_pre[b]);
+    const int id = free_page(n);
+    const bool fits = (unsigned)i < (unsigned)a.table_width;
+    if (fits) a.block_table[(long long)b * a.table_stride + i] = id;
+    bad |= id < 0 || !fits;
+  }
+  for (int t = gid; t < a.max_rows; t += nthr) {
+    int slot = -1, pos = -1;
+    if (t < total) {
+      const int b = holder(rows_pre, B, t);
+      const int ctx = max(__ldg(a.ctx_lens + b), 0), held = (ctx + P - 1) / P;
+      pos = ctx + (t - rows_pre[b]);
+      const int i = pos / P;
+      int id = -1;
+      if ((unsigned)i < (unsigned)a.table_width) {
+        id = i < held ? a.block_table[(long long)b * a.table_stride + i] : free_page(need_pre[b] + i - held);
+        if (id >= a.num_pages) id = -1;
+      }
+      if (id >= 0) slot = id * P + (pos - i * P);
+      else bad = true;
+    }
+    a.slots[t] = slot;
+    if (a.positions) a.positions[t] = pos;
+  }
+  if (bad) atomicOr(p.status, STATUS_PAGE);
+  cluster_wait();
+  if (gid == 0) *a.free_count_out = max(count - need, 0);
+}
+
+// ------------------------------------------------------------------ append
+// cache[slot / P][h][slot % P][:] = new[h][t][:].  One warp takes a row t, reads its slot once
+// (the division by P is the row's, not each chunk's) and moves the row's 2 * Hkv * d / 8 chunks of 16
+// bytes of K and V, up to eight in flight to a lane.  Memory-bound: every byte is read and written once.
+constexpr int APPEND_WARPS = 4;
+
+struct AppendParams {
+  attn_paged_append_params_t a;
+  unsigned int* status;
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * APPEND_WARPS) paged_append_kernel(const __grid_constant__ AppendParams p) {
+  const attn_paged_append_params_t& a = p.a;
+  constexpr int CPR = D / 8, UNROLL = 8;  // 16-byte chunks of a row
+  const int lane = threadIdx.x & 31;
+  const int nwarps = gridDim.x * APPEND_WARPS;
+  const int per_side = a.Hkv * CPR;
+  for (int t = blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5); t < a.rows; t += nwarps) {
+    const int slot = __ldg(a.slots + t);
+    const int page = slot / a.page_size;
+    if (slot < 0) continue;
+    if (page >= a.num_pages) {
+      if (lane == 0) atomicOr(p.status, STATUS_PAGE);
+      continue;
+    }
+    const long long dst0 = (long long)page * a.cache_page_stride + (long long)(slot - page * a.page_size) * a.cache_row_stride;
+    for (int c0 = lane; c0 < 2 * per_side; c0 += 32 * UNROLL) {
+      uint4 x[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int c = c0 + 32 * u;
+        if (c < 2 * per_side) {
+          const bool v = c >= per_side;
+          const int e = v ? c - per_side : c;
+          const uint16_t* src = static_cast<const uint16_t*>(v ? a.v_new : a.k_new);
+          x[u] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(e / CPR) * (v ? a.v_head_stride : a.k_head_stride) +
+                                                      (long long)t * (v ? a.v_row_stride : a.k_row_stride) + (e % CPR) * 8));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int c = c0 + 32 * u;
+        if (c < 2 * per_side) {
+          const bool v = c >= per_side;
+          const int e = v ? c - per_side : c;
+          uint16_t* dst = static_cast<uint16_t*>(v ? a.v_cache : a.k_cache);
+          *reinterpret_cast<uint4*>(dst + dst0 + (long long)(e / CPR) * a.cache_head_stride + (e % CPR) * 8) = x[u];
+        }
+      }
+    }
+  }
+}
+
+bool misaligned(const void* ptr, unsigned int to) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+int attn_paged_tables(const attn_paged_tables_params_t* params) {
+  using namespace attn;
+  if (!params) return ATTN_ERR_INVALID;
+  const attn_paged_tables_params_t& a = *params;
+  if (!a.ctx_lens || !a.new_lens || !a.block_table || !a.free_pages || !a.free_count || !a.free_count_out || !a.cu_seqlens_q ||
+      !a.seqlens_k || !a.slots)
+    return ATTN_ERR_INVALID;
+  for (const void* ptr : {(const void*)a.ctx_lens, (const void*)a.new_lens, (const void*)a.block_table, (const void*)a.free_pages,
+                          (const void*)a.free_count, (const void*)a.free_count_out, (const void*)a.cu_seqlens_q,
+                          (const void*)a.seqlens_k, (const void*)a.slots, (const void*)a.positions})
+    if (misaligned(ptr, 4)) return ATTN_ERR_INVALID;
+  if (a.B < 1 || a.B > TABLES_MAX_B || a.table_width < 1 || a.table_stride < a.table_width || a.max_free < 0 || a.max_rows < 1 ||
+      a.page_size < 16 || a.page_size % 16 != 0 || a.num_pages < 1 || (long long)a.num_pages * a.page_size > INT_MAX)
+    return ATTN_ERR_INVALID;
+  int sms = 0, dev = 0;
+  int rc = host_device(sms, dev);
+  if (rc != ATTN_OK) return rc;
+  TablesParams p{a, nullptr};
+  if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
+  const size_t smem = 2 * ((size_t)a.B + 1) * sizeof(int);
+  if (smem > 47 * 1024 &&
+      cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  // a CTA for every four rows of its threads, up to the portable cluster of eight
+  int ctas = 1;
+  while (ctas < 8 && (long long)ctas * 4 * TABLES_THREADS < a.max_rows) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(TABLES_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(a.stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_tables_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_paged_append(const attn_paged_append_params_t* params) {
+  using namespace attn;
+  if (!params) return ATTN_ERR_INVALID;
+  const attn_paged_append_params_t& a = *params;
+  if (!a.k_new || !a.v_new || !a.k_cache || !a.v_cache || !a.slots) return ATTN_ERR_INVALID;
+  for (const void* ptr : {a.k_new, a.v_new, (const void*)a.k_cache, (const void*)a.v_cache})
+    if (misaligned(ptr, 16)) return ATTN_ERR_INVALID;
+  if (misaligned(a.slots, 4)) return ATTN_ERR_INVALID;
+  if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (a.rows < 1 || a.Hkv < 1 || a.Hkv > (1 << 16) || a.num_pages < 1 || a.page_size < 16 || a.page_size % 16 != 0 ||
+      (long long)a.num_pages * a.page_size > INT_MAX)
+    return ATTN_ERR_INVALID;
+  for (long long s : {a.k_row_stride, a.k_head_stride, a.v_row_stride, a.v_head_stride, a.cache_page_stride, a.cache_head_stride,
+                      a.cache_row_stride})
+    if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID;
+  int sms = 0, dev = 0;
+  int rc = host_device(sms, dev);
+  if (rc != ATTN_OK) return rc;
+  AppendParams p{a, nullptr};
+  if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
+  const long long want = ((long long)a.rows + APPEND_WARPS - 1) / APPEND_WARPS;
+  const int grid = (int)(want < 16ll * sms ? want : 16ll * sms);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+  if (a.d == 64) paged_append_kernel<64><<<grid, 32 * APPEND_WARPS, 0, st>>>(p);
+  else paged_append_kernel<128><<<grid, 32 * APPEND_WARPS, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

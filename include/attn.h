@@ -90,7 +90,8 @@ typedef enum {
     ATTN_ERR_UNSUPPORTED = -2, /* a head dim or dtype the library has no kernel for */
     ATTN_ERR_CUDA = -3,        /* a CUDA runtime/driver call failed (launch, tensor map) */
     ATTN_ERR_TIMEOUT = -4,     /* a kernel barrier wait ran out of time; outputs undefined */
-    ATTN_ERR_DEVICE = -5       /* no usable sm_103 device */
+    ATTN_ERR_DEVICE = -5,      /* no usable sm_103 device */
+    ATTN_ERR_PAGE = -6         /* a kernel met a page id, slot or page count out of range */
 } attn_status_t;
 
 /*
@@ -200,10 +201,139 @@ int attn_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float
                      float scale, int dtype, void *stream);
 
 /*
+ * ---------------------------------------------------------------- paged key/value cache
+ *
+ * A serving step over a cache whose keys and values live in pages: attn_paged_tables turns
+ * the requests' lengths into block tables and a slot map, attn_paged_append writes the
+ * step's new key / value rows to their slots, and attn_fwd_paged attends from the step's
+ * query rows (one token per request, a few, or whole chunks, mixed freely) over the cache.
+ *
+ * Layout.  k_cache, v_cache: num_pages pages of page_size rows for Hkv heads of d elements.
+ * Element (page, h, row, x) is at page*cache_page_stride + h*cache_head_stride +
+ * row*cache_row_stride + x (in elements, the same strides for k and v), so pages may hold
+ * their heads one after the other ([num_pages][Hkv][page_size][d]) or their rows one after
+ * the other ([num_pages][page_size][Hkv][d]), inside larger buffers or not.  New rows, q and
+ * o are packed, request after request, with a row and a head stride of their own.  Strides
+ * are multiples of 8, pointers to rows 16-byte aligned; page_size is a multiple of 16.
+ * Slot s is row s % page_size of page s / page_size.
+ * block_table: int32, row b at block_table + b*table_stride, table_width entries: request
+ * b's token at position p is in page block_table[b][p / page_size], row p % page_size.
+ *
+ * All lengths, tables and slots are read on the device, in stream order, so a captured
+ * sequence of these calls can be replayed after the arrays' contents changed.  The calls
+ * keep no state between them.  Index arrays are int32, 4-byte aligned, device memory.
+ * Bad values in them fault nothing: a page id outside [0, num_pages), a slot at or past
+ * num_pages*page_size, a free list that runs out or a table that is too narrow is left out
+ * as described with each call, and recorded as ATTN_ERR_PAGE in the stream's status word,
+ * which attn_check(stream) reports.
+ */
+
+/*
+ * attn_paged_tables -- block tables, slot map, positions and row offsets of a step.
+ * Request b has ctx_lens[b] tokens in the cache and brings new_lens[b] more (0: idle;
+ * negative lengths count as 0).  Pages that it lacks for ctx + new tokens come from the end
+ * of the free list: free_pages[0 .. *free_count - 1] are free, the first page that is handed
+ * out is the last of them, requests are served in ascending order, each request's pages
+ * likewise, and *free_count_out (which may be free_count itself) is what is left.
+ * Writes
+ *   block_table[b][i], only for the pages added, i = ceil(ctx/page_size) ..
+ *                      ceil((ctx+new)/page_size) - 1 (the others are kept);
+ *   cu_seqlens_q[0..B]: offsets of the requests' new rows; seqlens_k[b] = ctx + new;
+ *   slots[t], positions[t] (or NULL) for t < max_rows: the slot and the position of new row
+ *                      t, -1 behind the last one.
+ * When pages run out, when a table row is too narrow, or when a page id (of the free list or
+ * of the page that request b's new tokens start in) is out of range, the slots concerned
+ * are -1 and so are the table entries that exist; rows past max_rows get no slot.  Each of these
+ * sets ATTN_ERR_PAGE.  cu_seqlens_q and seqlens_k are as if all had been well; *free_count_out
+ * is never below 0.  No output overlaps an input but free_count_out.  1 <= B <= 16384; num_pages*page_size, and the sums of the lengths, fit 31 bits.
+ */
+typedef struct {
+    const int *ctx_lens, *new_lens; /* [B] */
+    int *block_table;               /* in / out */
+    const int *free_pages;          /* [max_free] */
+    const int *free_count;          /* [1], at most max_free (more is cut) */
+    int *free_count_out;            /* [1] */
+    int *cu_seqlens_q;              /* [B+1] */
+    int *seqlens_k;                 /* [B] */
+    int *slots, *positions;         /* [max_rows]; positions may be NULL */
+    int B, table_width, table_stride, max_free, max_rows, page_size, num_pages;
+    void *stream;
+} attn_paged_tables_params_t;
+
+int attn_paged_tables(const attn_paged_tables_params_t *params);
+
+/*
+ * attn_paged_append -- write new key and value rows into the cache: row t of head h goes to
+ * slot slots[t].  A negative slot leaves row t out (rows behind the last request, as
+ * attn_paged_tables marks them); one at or past num_pages*page_size too, with ATTN_ERR_PAGE.
+ * Slots are distinct (the rows of a slot that is named twice would overwrite each other in
+ * no particular order).  k_new, v_new: element (h, t, x) at h*head + t*row + x of their own
+ * strides; they do not overlap the cache.  num_pages*page_size fits 31 bits.
+ */
+typedef struct {
+    const void *k_new, *v_new;
+    void *k_cache, *v_cache;
+    const int *slots; /* [rows] */
+    long long k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+    long long cache_page_stride, cache_head_stride, cache_row_stride;
+    int rows, Hkv, d, num_pages, page_size, dtype;
+    void *stream;
+} attn_paged_append_params_t;
+
+int attn_paged_append(const attn_paged_append_params_t *params);
+
+/*
+ * attn_fwd_paged -- attention of packed query rows over the paged cache.  Request b's query
+ * rows are cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 of q, o and lse (offsets non-decreasing,
+ * cu_seqlens_q[0] >= 0; rows past total_q are not touched); its keys are its first
+ * seqlens_k[b] cache rows (cut to [0, table_width*page_size]), the query rows' own among them
+ * where they have been appended.  Query i of a request with sq rows and sk keys sits at key
+ * position i + sk - sq; causal, window_left and window_right as for attn_fwd_ex, with sk < sq
+ * allowed (rows without a key give O = 0, LSE = -inf).  Requests longer than max_seqlen_q
+ * (>= 1) are cut to their first max_seqlen_q rows.  Rows of q, o and lse outside every
+ * request are neither read into a result nor written.
+ * Element (hq, t, x) of q is at t*q_row_stride + hq*q_head_stride + x, of o likewise with its own
+ * strides; lse is [Hq][total_q] or NULL.  Hq / Hkv <= 128.
+ * Cache rows that no query row of the request may see, behind its last key, ahead of its
+ * window, or on pages listed for none of its keys, may hold anything; those that one of its query
+ * rows sees hold finite values.  A page id out of range sets ATTN_ERR_PAGE; its keys then count as
+ * zeros.
+ * workspace: device memory, 256-byte aligned, of at least the size that
+ * attn_paged_workspace gives for the same parameters; its contents are of no account before and
+ * after the call, and calls that may run at the same time (two captured graphs among
+ * them) each take their own.
+ */
+typedef struct {
+    const void *q, *k_cache, *v_cache;
+    void *o;
+    float *lse;
+    const int *block_table, *cu_seqlens_q, *seqlens_k;
+    void *workspace;
+    unsigned long long workspace_bytes;
+    long long q_row_stride, q_head_stride, o_row_stride, o_head_stride;
+    long long cache_page_stride, cache_head_stride, cache_row_stride;
+    int B, Hq, Hkv, d, total_q, max_seqlen_q;
+    int num_pages, page_size, table_width, table_stride;
+    int causal, window_left, window_right;
+    float scale;
+    int dtype;
+    void *stream;
+} attn_fwd_paged_params_t;
+
+int attn_fwd_paged(const attn_fwd_paged_params_t *params);
+
+/*
+ * attn_paged_workspace -- bytes of workspace that attn_fwd_paged wants for these parameters
+ * on the current device.  It goes by Hq, Hkv, d and max_seqlen_q alone and reads no pointer.
+ */
+int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long long *bytes);
+
+/*
  * attn_check -- read (and clear) the status word of `stream` on the current
  * device, in stream order after the work enqueued on it so far, and synchronise
  * the stream: ATTN_OK, ATTN_ERR_TIMEOUT if a launch on this stream gave up on a
- * barrier wait, or ATTN_ERR_CUDA if the stream itself reports an error.  Launches
+ * barrier wait, ATTN_ERR_PAGE if one met a page id, slot or page count out of range
+ * (and none timed out), or ATTN_ERR_CUDA if the stream itself reports an error.  Launches
  * on other streams do not affect it (streams share a word only past the first
  * 1023 distinct streams of a device, and for attn_fwd_noalloc calls on streams
  * attn_fwd has not used).
