@@ -60,100 +60,9 @@
 #include "attn.h"
 #include "host.h"
 #include "ptx.cuh"
+#include "roles.cuh"
 
 namespace attn {
-
-constexpr int BM = 128;        // query rows per Q tile = TMEM lanes
-constexpr int QT = 2;          // Q tiles per work unit
-constexpr int UNIT_ROWS = BM * QT;
-constexpr int BN = 128;        // keys per K/V tile
-constexpr int NTHREADS = 384;  // 12 warps
-constexpr int REGS_LAUNCH = 168;
-constexpr int NINFO = 4;       // depth of the tile-descriptor ring
-constexpr int TMEM_COLS = 512;
-constexpr int FLAG_END = 4;    // info entry marking the end of a work unit
-constexpr int FLAG_EXIT = 8;   // info entry telling the consumers that no unit is left
-constexpr float LN2 = 0.69314718055994530942f;
-
-// NONE: every key; CAUSAL: keys up to the aligned position; BAND: keys in
-// [key_lo(i), key_hi(i)) per query row (sliding windows); CUSTOM: kept-bit words from the
-// mask pre-pass (which folds any band in).  The first two keep their bounds cheap.
-enum MaskMode { MASK_NONE = 0, MASK_CAUSAL = 1, MASK_CUSTOM = 2, MASK_BAND = 3 };
-
-template <int D, int MODE>
-struct Layout {
-  static_assert(D == 64 || D == 128, "head dim");
-  static constexpr int HALVES = D / 64;                  // 128-byte swizzle spans per row
-  static constexpr int Q_TILE_BYTES = BM * D * 2;
-  static constexpr int KV_TILE_BYTES = BN * D * 2;
-  // d = 64 (short sequences, many units per CTA) double-buffers the Q tiles so the next
-  // unit's Q load overlaps the current unit; d = 128 spends that room on K/V slots.
-  static constexpr int QBUF = (D == 64) ? 2 : 1;
-  // With two Q buffers a unit's buffer is not refilled before the unit after next, so its
-  // epilogue can stage O there and write it out coalesced (8 softmax warps x 32 rows x d
-  // fp16/bf16 = exactly one buffer); the buffer is released when those warps are done.
-  static constexpr bool STAGE_O = (QBUF == 2);
-  static constexpr int QEMPTY_COUNT = 1 + (STAGE_O ? QT * 4 : 0);  // MMA commit + softmax warps
-  // TMEM.  d = 128: S_t (fp32, 128 columns) at t * 128, P_t (fp16/bf16 pairs) over its first 64
-  // columns, O_t at 256 + t * 128.  d = 64: a ring of three S slots at 0, 128, 256 shared by the
-  // two Q tiles (the n-th Q.K^T of the CTA goes to slot n % 3, its P over the slot's first 64
-  // columns), O_t at 384 + t * 64: a Q tile's next Q.K^T runs while its softmax works on the
-  // current one.
-  static constexpr bool RING = (D == 64);
-  static constexpr int S_SLOTS = RING ? 3 : QT;
-  static constexpr int O_COL = RING ? 384 : 256;
-  static constexpr int O_STRIDE = RING ? 64 : 128;
-  static_assert(S_SLOTS * 128 + QT * O_STRIDE <= TMEM_COLS, "TMEM columns");
-  // Registers per thread after setmaxnreg: the load / MMA warpgroup and the two softmax
-  // warpgroups share the launch's 384 x 168 (the ring bookkeeping of d = 64 costs the MMA
-  // warp a few; its softmax, with a 64-column O, needs fewer).
-  static constexpr int REGS_LOADMMA = (D == 64) ? 96 : 88;
-  static constexpr int REGS_SOFTMAX = (D == 64) ? 200 : 208;
-  static_assert(128 * REGS_LOADMMA + 256 * REGS_SOFTMAX <= NTHREADS * REGS_LAUNCH, "register split");
-  // With one Q buffer (d = 128) the epilogue stages O through a 32 KiB area of its own,
-  // 4 KiB per softmax warp, one 64-column half at a time (custom masks need that room for
-  // their mask words and write O directly).
-  static constexpr bool STAGE_SEP = (D == 128 && MODE != MASK_CUSTOM);
-  static constexpr int STAGE_BYTES = STAGE_SEP ? QT * 4 * 32 * 128 : 0;
-  // Separate K and V rings: K(j) is read by the two QK^T of tile j, V(j) by the two P.V
-  // one tile later, so each ring is released right after its own last reader.
-  static constexpr int KSLOT = (D == 128) ? 2 : 4;
-  static constexpr int VSLOT = (D == 128) ? 2 : 4;
-  static constexpr int OFF_Q = 0;
-  static constexpr int Q_BUF_BYTES = QT * Q_TILE_BYTES;
-  static constexpr int OFF_K = OFF_Q + QBUF * Q_BUF_BYTES;
-  static constexpr int OFF_V = OFF_K + KSLOT * KV_TILE_BYTES;
-  static constexpr int OFF_STAGE = OFF_V + VSLOT * KV_TILE_BYTES;
-  static constexpr int OFF_WORDS = OFF_STAGE + STAGE_BYTES;
-  static constexpr int WORDS_PER_ENTRY = UNIT_ROWS * (BN / 32);
-  static constexpr int OFF_HDR = OFF_WORDS + (MODE == MASK_CUSTOM ? NINFO * WORDS_PER_ENTRY * 4 : 0);
-  static constexpr int OFF_BAR = OFF_HDR + NINFO * 32;
-  // barrier indices
-  static constexpr int B_QFULL = 0, B_QEMPTY = QBUF, B_KFULL = 2 * QBUF,
-                       B_KEMPTY = B_KFULL + KSLOT, B_VFULL = B_KEMPTY + KSLOT,
-                       B_VEMPTY = B_VFULL + VSLOT, B_IFULL = B_VEMPTY + VSLOT,
-                       B_IEMPTY = B_IFULL + NINFO,
-                       B_STILE = B_IEMPTY + NINFO, B_PREADY = B_STILE + S_SLOTS,
-                       B_ODONE = B_PREADY + QT, B_OPV = B_ODONE + QT, B_DRAIN = B_OPV + QT,
-                       NBAR = B_DRAIN + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int BYTES = OFF_MISC + 16;
-  static constexpr int SMEM_ALLOC = BYTES + 1024;  // slack for 1024-byte alignment
-  static_assert(SMEM_ALLOC <= 232448, "shared memory");
-  // Over half of the SM's shared memory: one CTA per SM, so TMEM (512 columns) never
-  // has to be shared between resident CTAs.
-  static_assert(SMEM_ALLOC > 116 * 1024, "one CTA per SM");
-};
-
-struct InfoHdr {
-  int j;      // key tile index
-  int flags;  // bit t: Q tile t computes this key tile; FLAG_END: end of unit
-  int sq, sk;  // the unit's query and key lengths (per batch entry with seqlens arrays)
-  int qoff;    // packed layouts: the entry's first row in q / o / lse
-  int bh, qb;  // the work unit this entry belongs to: b * Hq + hq, 256-row block
-  int pad;
-};
-static_assert(sizeof(InfoHdr) == 32, "descriptor slot size");
 
 struct Params {
   CUtensorMap tm_q, tm_k, tm_v;  // 3-D maps {d, S, B*H}, box {64, 128, 1}, 128B swizzle
@@ -214,45 +123,6 @@ __device__ unsigned int g_attn_status[STATUS_SLOTS];
 __device__ unsigned int g_sched[2 * STATUS_SLOTS];
 
 namespace attn {
-
-// Slow path of a bounded barrier wait (inlined: a shared non-inlined callee cannot serve
-// warps running under different setmaxnreg budgets).  Gives up when another thread has aborted, when
-// the wait has lasted timeout_us, or after an iteration cap, and then aborts the CTA and marks the
-// launch's status slot (abort_flag[1], set from the launch parameters at kernel start).
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                       uint32_t timeout_us) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 0; it < (1u << 28); ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if ((it & 15u) == 15u && globaltimer_ns() - t0 > 1000ull * timeout_us) break;
-  }
-  *abort_flag = 1;
-  atomicOr(&g_attn_status[abort_flag[1] & (STATUS_SLOTS - 1)], 1u);
-  return false;
-}
-
-__device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                      uint32_t timeout_us) {
-  if (mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, abort_flag, timeout_us);
-}
-
-// Warp-uniform variant: every lane waits, and the warp only proceeds if all lanes did.
-__device__ __forceinline__ bool bwait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           uint32_t timeout_us) {
-  bool ok = bwait(bar, parity, abort_flag, timeout_us);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// Wait used only while draining after an abort: ignores the abort flag, short limit.
-__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 0; it < (1u << 24); ++it) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((it & 15u) == 15u && globaltimer_ns() - t0 > 200000000ull) return;
-  }
-}
 
 // k-th unit of this CTA in the snake order, or -1 when it has none left.
 __device__ __forceinline__ int unit_at(int k, int num_units) {
@@ -339,17 +209,6 @@ __device__ __forceinline__ int key_hi(const Params& p, int i, int off, int sk) {
 }  // namespace attn
 
 namespace attn {
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (BF16) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&h);
-  } else {
-    __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&h);
-  }
-}
 
 // ------------------------------------------------------------------ load warp (warp 0)
 template <int D, bool BF16, int MODE>
@@ -604,178 +463,24 @@ drain:
 
 namespace attn {
 
-// ------------------------------------------------------------------ MMA issuer (warp 1)
-// The whole warp runs this code converged (descriptors in uniform registers); elect.sync
-// picks the lane that issues each tcgen05 instruction.  Per tile descriptor e (key tile j)
-// and Q tile t:
-//   d = 128:  O_t (+)= P_t(prev) . V(prev)   once softmax t has written P for the previous tile,
-//             S_t     = Q_t . K(j)^T         then signal softmax t;
-//             S_t / P_t share TMEM columns, so S_t is rewritten only after the P.V that reads it.
-//   d = 64:   S(n)    = Q_t . K(j)^T         into ring slot n % 3 (the CTA's n-th Q.K^T),
-//             O_t (+)= P_t(prev) . V(prev)   from the slot of the previous tile's S,
-//             so the next S of a Q tile is computed while its softmax still works on the
-//             current one.  At most two slots hold an S or P whose P.V is not yet issued when
-//             a Q.K^T is issued, so the third is free; each P.V is followed by a commit on
-//             OPV(t), which the softmax waits for before it rescales O_t.
-// Each ring slot of K / V is released by a commit right after its last reader.
-template <int D, bool BF16, int MODE>
-__device__ __forceinline__ void mma_role(const Params& p, uint32_t base, uint8_t* gbase,
-                                         volatile int* abort_flag, uint32_t tmem, int lane) {
-  using L = Layout<D, MODE>;
-  const uint32_t to = p.timeout_us;
-  const uint32_t bars = base + L::OFF_BAR;
-  volatile InfoHdr* hdr = reinterpret_cast<volatile InfoHdr*>(gbase + L::OFF_HDR);
-  constexpr uint32_t ID_QK = idesc_f16acc32(BF16, false, false, BM, BN);
-  constexpr uint32_t ID_PV = idesc_f16acc32(BF16, false, true, BM, D);
-  const bool pair = MODE != MASK_CUSTOM && p.pair;
-
-  uint32_t q_par = 0, ie_par = 0, kpar = 0, vpar = 0, p_par0 = 0, p_par1 = 0;  // q_par: bit per Q buffer
-  int kslot = 0, vslot = 0, ie = 0;
-  int nqk = 0;                 // d = 64: ring slot of the next Q.K^T
-  int pslot0 = 0, pslot1 = 0;  // d = 64: ring slot holding P_t of the previous key tile
-
-  for (int k = 0;; ++k) {
-    // the unit's first descriptor names it (the loop below waits on it again, at once)
-    if (!bwait_warp(bars + 8u * (L::B_IFULL + ie), ie_par, abort_flag, to)) goto drain;
-    if (hdr[ie].flags & FLAG_EXIT) {
-      mbar_arrive_elect(bars + 8u * (L::B_IEMPTY + ie));
-      break;
-    }
-    const int bh = hdr[ie].bh, qb = hdr[ie].qb;
-    const int b = bh / p.Hq, hq = bh - b * p.Hq;
-    const int qbuf = k % L::QBUF;
-    if (!bwait_warp(bars + 8u * (L::B_QFULL + qbuf), (q_par >> qbuf) & 1u, abort_flag, to)) goto drain;
-    q_par ^= 1u << qbuf;
-    tc_fence_after();
-
-    bool have_prev = false, pv0 = false, pv1 = false;
-    int prev_flags = 0, prev_vslot = 0;
-    uint32_t prev_vpar = 0;
-    while (true) {
-      if (!bwait_warp(bars + 8u * (L::B_IFULL + ie), ie_par, abort_flag, to)) goto drain;
-      const int j = hdr[ie].j;
-      const int flags = hdr[ie].flags;
-      const bool end = (flags & FLAG_END) != 0;
-      const int cur_kslot = kslot, cur_vslot = vslot;
-      const uint32_t cur_kpar = kpar, cur_vpar = vpar;
-      if (!end) {
-        if (++kslot == L::KSLOT) { kslot = 0; kpar ^= 1u; }
-        if (++vslot == L::VSLOT) { vslot = 0; vpar ^= 1u; }
-      }
-      // End of unit: every Q_t K^T of the unit is in the pipe, so the Q buffer is released
-      // (to the next unit's load) before the last P.V, which does not read it.
-      if (end) tc_commit_elect(bars + 8u * (L::B_QEMPTY + qbuf));
-      if (have_prev) {
-        if (!bwait_warp(bars + 8u * (L::B_VFULL + prev_vslot), prev_vpar, abort_flag, to)) goto drain;
-        tc_fence_after();
-      }
-      bool k_ready = false;
-
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        int& pslot = t ? pslot1 : pslot0;
-        int new_slot = t;
-#pragma unroll
-        for (int step = 0; step < 2; ++step) {
-          // d = 64 issues this tile's Q.K^T first, d = 128 its P.V first
-          if ((step == 0) == L::RING) {
-            if (!end && ((flags >> t) & 1)) {
-              if (!k_ready) {
-                if (!bwait_warp(bars + 8u * (L::B_KFULL + cur_kslot), cur_kpar, abort_flag, to)) goto drain;
-                tc_fence_after();
-                k_ready = true;
-              }
-              if constexpr (L::RING) {
-                new_slot = nqk;
-                nqk = nqk == L::S_SLOTS - 1 ? 0 : nqk + 1;
-              }
-              const uint32_t s_col = tmem + new_slot * 128;
-              const uint32_t qbase = base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES;
-              const uint32_t kbase = base + L::OFF_K + cur_kslot * L::KV_TILE_BYTES;
-              // Q and K as K-major operands: 16 elements (32 bytes) per step inside a
-              // 128-byte swizzle row, the next 64 elements one half-tile further.
-              if constexpr (D == 64) {
-                // d = 64 issues twice the instructions per flop: the descriptors are built
-                // once and stepped through their start-address field (address >> 4 in the
-                // low 14 bits; every offset here keeps it below 2^14)
-                const uint64_t qd = sdesc_sw128(qbase, 16, 1024), kd = sdesc_sw128(kbase, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-                  mma_ss_elect(s_col, qd + off, kd + off, ID_QK, kk > 0 ? 1u : 0u);
-                }
-              } else {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
-                  mma_ss_elect(s_col, sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + off, 16, 1024),
-                               ID_QK, kk > 0 ? 1u : 0u);
-                }
-              }
-              tc_commit_elect(bars + 8u * (L::B_STILE + new_slot));
-              if (p.visited && lane == 0)
-                p.visited[((size_t)(b * p.Hq + hq + (pair ? t : 0)) * p.nqt + (qb * QT + (pair ? 0 : t))) * p.nkt + j] = 1;
-              __syncwarp();
-            }
-          } else {
-            if (have_prev && ((prev_flags >> t) & 1)) {
-              uint32_t& pp = t ? p_par1 : p_par0;
-              if (!bwait_warp(bars + 8u * (L::B_PREADY + t), pp, abort_flag, to)) goto drain;
-              pp ^= 1u;
-              tc_fence_after();
-              bool& started = t ? pv1 : pv0;
-              const uint32_t p_col = tmem + (L::RING ? pslot : t) * 128;
-              const uint32_t vbase = base + L::OFF_V + prev_vslot * L::KV_TILE_BYTES;
-              // V tile as the MN-major B operand: 16 keys per step (2048 bytes), the two
-              // 64-column halves of d are KV_TILE_BYTES/2 apart, 8-key groups 1024 apart.
-              if constexpr (D == 64) {
-                const uint64_t vd = sdesc_sw128(vbase, BN * 128, 1024);
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                  mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4),
-                               ID_PV, (started || kk > 0) ? 1u : 0u);
-              } else {
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                  mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8,
-                               sdesc_sw128(vbase + kk * 16 * 128, BN * 128, 1024), ID_PV,
-                               (started || kk > 0) ? 1u : 0u);
-              }
-              started = true;
-              if constexpr (L::RING) tc_commit_elect(bars + 8u * (L::B_OPV + t));
-            }
-            // end of unit: O_t is complete once its last P.V is -- signal it now, so softmax t
-            // starts its epilogue without waiting for the other Q tile's P.V
-            if (end && (t ? pv1 : pv0)) tc_commit_elect(bars + 8u * (L::B_ODONE + t));
-            if (t == QT - 1 && have_prev) tc_commit_elect(bars + 8u * (L::B_VEMPTY + prev_vslot));
-          }
-        }
-        if constexpr (L::RING) {
-          if (!end && ((flags >> t) & 1)) pslot = new_slot;
-        }
-      }
-      if (!end) tc_commit_elect(bars + 8u * (L::B_KEMPTY + cur_kslot));
-      mbar_arrive_elect(bars + 8u * (L::B_IEMPTY + ie));
-      if (++ie == NINFO) { ie = 0; ie_par ^= 1u; }
-      if (end) break;
-      have_prev = true;
-      prev_flags = flags;
-      prev_vslot = cur_vslot;
-      prev_vpar = cur_vpar;
-    }
+// What the MMA warp does for this kernel beside its multiplications: it records the computed blocks.
+template <int MODE>
+struct FwdEnv {
+  static constexpr bool SCRUB = false;
+  const Params& p;
+  int b, hq, qb;
+  __device__ __forceinline__ void unit(volatile InfoHdr& h) {
+    const int bh = h.bh;
+    qb = h.qb;
+    b = bh / p.Hq;
+    hq = bh - b * p.Hq;
   }
-  return;
-
-drain:
-  // Aborted: wait until every MMA this warp issued has finished before TMEM is freed.
-  tc_commit_elect(bars + 8u * L::B_DRAIN);
-  wait_drain(bars + 8u * L::B_DRAIN, 0);
-  __syncwarp();
-}
-
-}  // namespace attn
-
-namespace attn {
+  __device__ __forceinline__ void computed(int t, int j, int lane) {
+    const bool pair = MODE != MASK_CUSTOM && p.pair;
+    if (p.visited && lane == 0)
+      p.visited[((size_t)(b * p.Hq + hq + (pair ? t : 0)) * p.nqt + (qb * QT + (pair ? 0 : t))) * p.nkt + j] = 1;
+  }
+};
 
 // ------------------------------------------------------------------ softmax warpgroup t
 // Thread r of the warpgroup owns query row qb*256 + t*128 + r, i.e. TMEM lane r.
@@ -870,115 +575,29 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t base, uin
       if (!bwait_warp(bars + 8u * (L::B_STILE + slot), spar, abort_flag, to)) return;
       if constexpr (!L::RING) s_par ^= 1u;
       tc_fence_after();
-      // Scores: the first 64 columns are loaded and reduced while the last 64 are in flight.
-      uint32_t sr[128];
-      uint32_t(&sa)[64] = *reinterpret_cast<uint32_t(*)[64]>(&sr[0]);
-      uint32_t(&sb)[64] = *reinterpret_cast<uint32_t(*)[64]>(&sr[64]);
-      tmem_ld32x32b_x64_wait(s_addr, sa);
-      tmem_ld32x32b_x64(s_addr + 64, sb);
-
-      // Mask: excluded scores become -inf (weight exactly 0).
-      // band / key bound: kept columns of this tile are [lo, hi) relative to its first key
-      const int off = sk - sq;
-      const int hi = (MODE == MASK_NONE ? sk
-                      : MODE == MASK_CAUSAL ? min(sk, i + off + 1)
-                                            : key_hi(p, i, off, sk)) - j * BN;
-      const int lo = (MODE == MASK_BAND) ? key_lo(p, i, off) - j * BN : 0;
-      const bool edge = (MODE != MASK_CUSTOM) && __any_sync(0xffffffffu, hi < BN || lo > 0);
-      const uint32_t wa[4] = {wv.x, wv.y, wv.z, wv.w};
-      auto mask_half = [&](uint32_t(&h)[64], int c0) {
-        if constexpr (MODE == MASK_CUSTOM) {
+      const auto make_mask = [&] {
+        // band / key bound: kept columns of this tile are [lo, hi) relative to its first key
+        const int off = sk - sq;
+        const int hi = (MODE == MASK_NONE ? sk
+                        : MODE == MASK_CAUSAL ? min(sk, i + off + 1)
+                                              : key_hi(p, i, off, sk)) - j * BN;
+        const int lo = (MODE == MASK_BAND) ? key_lo(p, i, off) - j * BN : 0;
+        const bool edge = (MODE != MASK_CUSTOM) && __any_sync(0xffffffffu, hi < BN || lo > 0);
+        const uint32_t wa[4] = {wv.x, wv.y, wv.z, wv.w};
+        return [=](uint32_t(&h)[64], int c0) {
+          if constexpr (MODE == MASK_CUSTOM) {
 #pragma unroll
-          for (int cc = 0; cc < 64; ++cc)
-            if (!((wa[(c0 + cc) >> 5] >> ((c0 + cc) & 31)) & 1u)) h[cc] = __float_as_uint(-INFINITY);
-        } else if (edge) {
+            for (int cc = 0; cc < 64; ++cc)
+              if (!((wa[(c0 + cc) >> 5] >> ((c0 + cc) & 31)) & 1u)) h[cc] = __float_as_uint(-INFINITY);
+          } else if (edge) {
 #pragma unroll
-          for (int cc = 0; cc < 64; ++cc)
-            if (c0 + cc >= hi || c0 + cc < lo) h[cc] = __float_as_uint(-INFINITY);
-        }
-      };
-      // Row max of one half: four independent 3-input max chains, chain x over h[16x, 16x+16).
-      auto max_half = [&](const uint32_t(&h)[64]) {
-        float a4[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          a4[x] = fmaxf(__uint_as_float(h[16 * x]), __uint_as_float(h[16 * x + 1]));
-#pragma unroll
-          for (int e = 2; e < 16; e += 2)
-            a4[x] = fmax3(a4[x], __uint_as_float(h[16 * x + e]), __uint_as_float(h[16 * x + e + 1]));
-        }
-        return fmax3(a4[0], a4[1], fmaxf(a4[2], a4[3]));
-      };
-      mask_half(sa, 0);
-      const float mx_a = max_half(sa);
-      tmem_wait_ld();
-      tmem_fence_regs_x64(sb);
-      mask_half(sb, 64);
-      const float mx = fmaxf(mx_a, max_half(sb));
-
-      // Lazy rescaling: the exponent base m only moves when the row max exceeds it by more
-      // than 8 (weights stay <= 2^8); O and l are always scaled with the same base, so the
-      // final O / l and LSE = ln2 * (m + log2 l) are exact.
-      const float mx_s = mx * c;
-      const bool grow = mx_s > m + 8.f;  // also true on the first kept key (m = -inf)
-      const float m_new = grow ? mx_s : m;
-      const float alpha = grow ? ex2_approx(m - m_new) : 1.f;
-      const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-
-      // Correction: rescale this row of O (only warps where some row moved its base).
-      if (nact > 0 && __any_sync(0xffffffffu, grow)) {
-        if constexpr (L::RING) {
-          // d = 64: this tile's S was computed before the previous P.V was issued; wait
-          // until that P.V (OPV phase np - 1, the latest that can have completed) is done
-          if (!bwait_warp(bars + 8u * (L::B_OPV + t), (uint32_t)(np - 1) & 1u, abort_flag, to)) return;
-          tc_fence_after();
-        }
-        const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll
-        for (int ch = 0; ch < D / 16; ++ch) {
-          uint32_t ob[16];
-          tmem_ld32x32b_x16_wait(o_addr + ch * 16, ob);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            float lo, hi;
-            f2_unpack(fmul2(f2_pack(__uint_as_float(ob[2 * x]), __uint_as_float(ob[2 * x + 1])), a2), lo, hi);
-            ob[2 * x] = __float_as_uint(lo);
-            ob[2 * x + 1] = __float_as_uint(hi);
+            for (int cc = 0; cc < 64; ++cc)
+              if (c0 + cc >= hi || c0 + cc < lo) h[cc] = __float_as_uint(-INFINITY);
           }
-          tmem_st32x32b_x16(o_addr + ch * 16, ob);
-        }
-      }
-
-      // P = 2^(s*c - m): packed FMA for the arguments, MUFU ex2, four packed partial sums.
-      const uint64_t c2 = f2_pack(c, c);
-      const uint64_t nm2 = f2_pack(-m_use, -m_use);
-      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-      // P_t goes over the first 64 columns of S_t, in four stores so each overlaps the
-      // exponentials of the next quarter (and few packed words are live at a time).
-#pragma unroll
-      for (int hh = 0; hh < 4; ++hh) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int cc = 0; cc < 16; ++cc) {
-          const int e = hh * 16 + cc;
-          float e0, e1;
-          f2_unpack(ffma2(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), c2, nm2), e0, e1);
-          const float p0 = ex2_approx(e0);
-          const float p1 = ex2_approx(e1);
-          acc[cc & 3] = fadd2(acc[cc & 3], f2_pack(p0, p1));
-          pk[cc] = pack2<BF16>(p0, p1);
-        }
-        tmem_st32x32b_x16(s_addr + hh * 16, pk);
-      }
-      tmem_wait_st();
-      float s0, s1, s2, s3, s4, s5, s6, s7;
-      f2_unpack(acc[0], s0, s1);
-      f2_unpack(acc[1], s2, s3);
-      f2_unpack(acc[2], s4, s5);
-      f2_unpack(acc[3], s6, s7);
-      const float sum = ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
-      l = l * alpha + sum;
-      m = m_new;
+        };
+      };
+      if (!softmax_tile<D, BF16, L>(s_addr, o_addr, c, make_mask, bars + 8u * (L::B_OPV + t), np, nact, abort_flag, to, m, l))
+        return;
       tc_fence_before();
       // d = 64: the next S may already be there, so a fast warp could start the next tile
       // and arrive again before the slowest warp has arrived for this one; the warpgroup
@@ -1149,31 +768,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_fwd_kernel(const __grid_cons
   const uint32_t bars = base + L::OFF_BAR;
 
   if (threadIdx.x == 0) {
-    for (int qb2 = 0; qb2 < L::QBUF; ++qb2) {
-      mbar_init(bars + 8u * (L::B_QFULL + qb2), 1);
-      mbar_init(bars + 8u * (L::B_QEMPTY + qb2), L::QEMPTY_COUNT);
-    }
-    for (int s = 0; s < L::KSLOT; ++s) {
-      mbar_init(bars + 8u * (L::B_KFULL + s), 1);
-      mbar_init(bars + 8u * (L::B_KEMPTY + s), 1);
-    }
-    for (int s = 0; s < L::VSLOT; ++s) {
-      mbar_init(bars + 8u * (L::B_VFULL + s), 1);
-      mbar_init(bars + 8u * (L::B_VEMPTY + s), 1);
-    }
-    for (int e = 0; e < NINFO; ++e) {
-      mbar_init(bars + 8u * (L::B_IFULL + e), 1);                 // load-warp lane 0
-      mbar_init(bars + 8u * (L::B_IEMPTY + e), 1 + QT * BM);      // MMA thread + softmax threads
-    }
-    for (int sl = 0; sl < L::S_SLOTS; ++sl) mbar_init(bars + 8u * (L::B_STILE + sl), 1);
-    for (int t = 0; t < QT; ++t) {
-      mbar_init(bars + 8u * (L::B_PREADY + t), BM);
-      mbar_init(bars + 8u * (L::B_ODONE + t), 1);
-      mbar_init(bars + 8u * (L::B_OPV + t), 1);
-    }
-    mbar_init(bars + 8u * L::B_DRAIN, 1);
+    init_barriers<L>(bars);
     abort_flag[0] = 0;
-    abort_flag[1] = p.status_slot;
+    *reinterpret_cast<unsigned int* volatile*>(abort_flag + 1) = &g_attn_status[p.status_slot & (STATUS_SLOTS - 1)];
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -1202,7 +799,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_fwd_kernel(const __grid_cons
     if (warp == 0) {
       load_role<D, BF16, MODE>(p, base, gbase, abort_flag, lane);
     } else if (warp == 1) {
-      mma_role<D, BF16, MODE>(p, base, gbase, abort_flag, tmem, lane);
+      FwdEnv<MODE> env{p, 0, 0, 0};
+      mma_role<D, BF16, L>(env, p.timeout_us, base, gbase, abort_flag, tmem, lane);
     }
   } else {
     setmaxnreg_inc<L::REGS_SOFTMAX>();
