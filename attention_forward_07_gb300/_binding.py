@@ -394,7 +394,7 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     def call(st):
         ws = workspace
         if ws is None:
-            key = (dev.index, Hq, Hkv, d, max_seqlen_q)
+            key = (dev.index, B, Hq, Hkv, d, total_q, max_seqlen_q)
             n = _workspace_sizes.get(key)
             if n is None:
                 n = _workspace_sizes[key] = _paged_workspace(prm)
@@ -420,9 +420,9 @@ def _paged_workspace(prm) -> int:
     return n.value
 
 
-def attn_paged_workspace(Hq, Hkv, d, max_seqlen_q) -> int:
+def attn_paged_workspace(B, Hq, Hkv, d, total_q, max_seqlen_q) -> int:
     """Bytes of workspace attn_fwd_paged wants on the current device."""
-    return _paged_workspace(FwdPagedParams(B=1, Hq=Hq, Hkv=Hkv, d=d, max_seqlen_q=max_seqlen_q))
+    return _paged_workspace(FwdPagedParams(B=B, Hq=Hq, Hkv=Hkv, d=d, total_q=total_q, max_seqlen_q=max_seqlen_q))
 
 
 def attn_check(stream=None) -> int:

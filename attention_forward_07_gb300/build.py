@@ -12,8 +12,8 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("attn_fwd.cu", "paged_attn.cu", "paged_cache.cu")]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("ptx.cuh", "host.h", "roles.cuh")] + [os.path.join(ROOT, "include", "attn.h")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("attn_fwd.cu", "paged_attn.cu", "paged_tile.cu", "paged_cache.cu")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("ptx.cuh", "host.h", "roles.cuh", "paged.cuh")] + [os.path.join(ROOT, "include", "attn.h")]
 OUT = os.path.join(HERE, "libattn.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

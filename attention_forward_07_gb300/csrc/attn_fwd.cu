@@ -1076,14 +1076,16 @@ std::atomic<unsigned long long> g_ws_allocs{0}, g_map_encodes{0}, g_map_hits{0};
 // Tensor maps cached by (kind, address, dims, box rows): a map holds nothing but these, so a
 // cached map is valid for any later call that names the same buffer with the same shape.
 // Least-recently-used replacement over a small table.
-enum MapKind { MAP_F16 = 0, MAP_BF16 = 1, MAP_WORDS = 2 };
+enum MapKind { MAP_F16 = 0, MAP_BF16 = 1, MAP_WORDS = 2, MAP4_F16 = 3, MAP4_BF16 = 4 };
 struct MapKey {
   int kind;
   const void* ptr;
   long long d0, d1, d2;
   int box_rows;
+  Map4 four;  // 4-D maps: everything but kind and ptr
   bool operator==(const MapKey& o) const {
-    return kind == o.kind && ptr == o.ptr && d0 == o.d0 && d1 == o.d1 && d2 == o.d2 && box_rows == o.box_rows;
+    return kind == o.kind && ptr == o.ptr && d0 == o.d0 && d1 == o.d1 && d2 == o.d2 && box_rows == o.box_rows &&
+           std::memcmp(&four, &o.four, sizeof four) == 0;
   }
 };
 constexpr int MAP_CACHE = 64;
@@ -1138,7 +1140,7 @@ int encode_map(CUtensorMap* m, const void* ptr, bool bf16, int d, int S, long lo
 }
 
 int make_map(CUtensorMap* m, const void* ptr, bool bf16, int d, int S, long long BH, int box_rows = 128) {
-  return cached_map(m, MapKey{bf16 ? MAP_BF16 : MAP_F16, ptr, d, S, BH, box_rows},
+  return cached_map(m, MapKey{bf16 ? MAP_BF16 : MAP_F16, ptr, d, S, BH, box_rows, {}},
                     [&](CUtensorMap* out) { return encode_map(out, ptr, bf16, d, S, BH, box_rows); });
 }
 
@@ -1159,7 +1161,7 @@ int encode_mask_map(CUtensorMap* m, const uint32_t* words4, int W4, int Sq, int 
 }
 
 int make_mask_map(CUtensorMap* m, const uint32_t* words4, int W4, int Sq, int nmb, int box_rows) {
-  return cached_map(m, MapKey{MAP_WORDS, words4, W4, Sq, nmb, box_rows},
+  return cached_map(m, MapKey{MAP_WORDS, words4, W4, Sq, nmb, box_rows, {}},
                     [&](CUtensorMap* out) { return encode_mask_map(out, words4, W4, Sq, nmb, box_rows); });
 }
 
@@ -1425,10 +1427,7 @@ int fwd_impl(const attn_fwd_params_t& a, bool noalloc = false) {
   p.lens_k = a.seqlens_k;
   p.causal = (p.er >= 0 && p.wl < 0) ? 1 : 0;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  {
-    const unsigned long long us = (g_timeout_ns.load() + 999ull) / 1000ull;
-    p.timeout_us = us > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)us;
-  }
+  p.timeout_us = host_timeout_us();
   p.inject = g_inject.exchange(0);
   const int grid = p.num_units < sms ? p.num_units : sms;
   const int mode = a.mask_bits                        ? MASK_CUSTOM
@@ -1521,6 +1520,32 @@ attn_fwd_params_t square_params(const void* q, const void* k, const void* v, voi
 namespace attn {
 
 int host_device(int& sms, int& dev) { return device_info(sms, dev); }
+
+int host_take_inject() { return g_inject.exchange(0); }
+
+uint32_t host_timeout_us() {
+  const unsigned long long us = (g_timeout_ns.load() + 999ull) / 1000ull;
+  return us > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)us;
+}
+
+int host_map4(CUtensorMap* m, const void* ptr, bool bf16, const Map4& t) {
+  return cached_map(m, MapKey{bf16 ? MAP4_BF16 : MAP4_F16, ptr, 0, 0, 0, 0, t}, [&](CUtensorMap* out) -> int {
+    auto enc = tensor_map_encoder();
+    if (!enc) return ATTN_ERR_CUDA;
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+      dims[i] = (cuuint64_t)t.dims[i];
+      box[i] = (cuuint32_t)t.box[i];
+      if (i) strides[i - 1] = (cuuint64_t)t.strides[i - 1];
+    }
+    return enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? ATTN_OK
+               : ATTN_ERR_CUDA;
+  });
+}
 
 int host_status_word(int dev, void* stream, unsigned int** word) {
   void* base = nullptr;

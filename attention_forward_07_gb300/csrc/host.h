@@ -1,5 +1,8 @@
 // host.h -- host-side state of the library that its sources share (defined in attn_fwd.cu).
 #pragma once
+#include <cuda.h>
+
+#include <cstdint>
 
 namespace attn {
 
@@ -8,6 +11,20 @@ constexpr unsigned int STATUS_TIMEOUT = 1u, STATUS_PAGE = 2u;
 
 // The current device and its SM count; ATTN_ERR_DEVICE unless it is an sm_103 GPU.
 int host_device(int& sms, int& dev);
+
+// The longest a kernel may wait on one barrier, in microseconds.
+uint32_t host_timeout_us();
+
+// The armed state of attn_debug_inject, which one launch takes.
+int host_take_inject();
+
+// 4-D tensor map of fp16 / bf16 with 128-byte swizzle, from the library's cache: extents and box in
+// elements, strides of dimensions 1-3 in bytes.  What lies outside reads as zeros.
+struct Map4 {
+  long long dims[4], strides[3];
+  int box[4];
+};
+int host_map4(CUtensorMap* m, const void* ptr, bool bf16, const Map4& t);
 
 // Device address of the status word of `stream` (what attn_check reads and clears).
 int host_status_word(int dev, void* stream, unsigned int** word);

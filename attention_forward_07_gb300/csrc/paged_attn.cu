@@ -16,28 +16,12 @@
 
 #include "attn.h"
 #include "host.h"
+#include "paged.cuh"
 #include "ptx.cuh"
+#include "roles.cuh"
 
 namespace attn {
 namespace {
-
-constexpr float LN2 = 0.69314718055994530942f;
-
-struct PagedParams {
-  const uint16_t *q, *k, *v;
-  uint16_t* o;
-  float* lse;
-  const int *table, *cu_q, *lens_k;
-  long long q_row, q_head, o_row, o_head;  // strides in elements
-  long long c_page, c_head, c_row;
-  int B, Hq, Hkv, g, total_q, max_q, num_pages, page_size, width, table_stride;
-  int wl, er;  // band: keys pos - wl .. pos + er (-1: unbounded)
-  float scale_log2;
-  unsigned int* status;
-  float* part_o;     // [2 * grid][16][D] partial sums of V, not normalised
-  float2* part_ml;   // [2 * grid][16] their exponent base (exp2 domain) and sum of weights
-  struct Split* split;  // [grid]
-};
 
 // An item whose tiles CTA c begins and others finish: the partial results to join.
 struct Split {
@@ -45,31 +29,11 @@ struct Split {
   int parts;      // slots 2c + 1, 2(c + 1), 2(c + 2), ...
 };
 
-// Query rows, keys and first query row of request b, whatever the arrays hold.
-__device__ __forceinline__ void request_span(const PagedParams& p, int b, int& row0, int& sq, int& sk) {
-  row0 = min(max(__ldg(p.cu_q + b), 0), p.total_q);
-  sq = min(min(max(__ldg(p.cu_q + b + 1), row0), p.total_q) - row0, p.max_q);
-  sk = (int)min((long long)max(__ldg(p.lens_k + b), 0), (long long)p.width * p.page_size);
-}
-
-// Keys that query row i (of sq, against sk keys) keeps: [lo, hi).
-__device__ __forceinline__ int row_lo(const PagedParams& p, int i, int off) {
-  return p.wl < 0 ? 0 : (int)max(0ll, (long long)i + off - p.wl);
-}
-__device__ __forceinline__ int row_hi(const PagedParams& p, int i, int off, int sk) {
-  return p.er < 0 ? sk : (int)min((long long)sk, (long long)i + off + p.er + 1);
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (BF16) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&h);
-  } else {
-    __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&h);
-  }
-}
+struct RowsParams : PagedParams {
+  float* part_o;    // [2 * grid][16][D] partial sums of V, not normalised
+  float2* part_ml;  // [2 * grid][16] their exponent base (exp2 domain) and sum of weights
+  Split* split;     // [grid]
+};
 
 // ------------------------------------------------------------------ few rows: the memory-bound path
 // An item is (request, K/V head, block of 16 packed rows), row r of a request's K/V head being query
@@ -103,18 +67,18 @@ struct RowsItem {
   int row0, sq, sk, off, R, nblk;
 };
 template <int D>
-__device__ __forceinline__ RowsItem rows_request(const PagedParams& p, int b) {
+__device__ __forceinline__ RowsItem rows_request(const RowsParams& p, int b) {
   RowsItem it;
   request_span(p, b, it.row0, it.sq, it.sk);
   it.off = it.sk - it.sq;
   it.R = it.sq * p.g;
-  it.nblk = (it.R + 15) / 16;
+  it.nblk = it.R <= ROWS_MAX ? (it.R + 15) / 16 : 0;
   return it;
 }
 // Keys [lo, hi) that any row of block blk keeps and the tiles [t0, t1) that hold them (one tile of
 // nothing where no key is kept: the item still writes its rows).
 template <int D>
-__device__ __forceinline__ void rows_range(const PagedParams& p, const RowsItem& it, int blk, int& lo, int& hi, int& t0, int& t1) {
+__device__ __forceinline__ void rows_range(const RowsParams& p, const RowsItem& it, int blk, int& lo, int& hi, int& t0, int& t1) {
   const int i0 = blk * 16 / p.g, i1 = (min(blk * 16 + 16, it.R) - 1) / p.g;
   lo = row_lo(p, i0, it.off);
   hi = row_hi(p, i1, it.off, it.sk);
@@ -123,7 +87,7 @@ __device__ __forceinline__ void rows_range(const PagedParams& p, const RowsItem&
   t1 = hi > lo ? (hi - 1) / Rows<D>::TK + 1 : t0 + 1;
 }
 template <int D>
-__device__ __forceinline__ long long rows_weight(const PagedParams& p, const RowsItem& it) {
+__device__ __forceinline__ long long rows_weight(const RowsParams& p, const RowsItem& it) {
   long long w = 0;
   for (int blk = 0; blk < it.nblk; ++blk) {
     int lo, hi, t0, t1;
@@ -164,7 +128,7 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_kernel(const __grid_constant__ RowsParams p) {
   using C = Rows<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long warp_sum[C::WARPS];
@@ -479,7 +443,7 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
 // Joins the partial results of split items: one CTA per (run that begins one, row), its four warps share
 // out the parts and each lane takes D / 32 columns.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ RowsParams p) {
   constexpr int E = D / 32;
   const Split sp = p.split[blockIdx.x];
   if (sp.b < 0) return;
@@ -529,25 +493,30 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ host side
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-// Workspace: rows path partials.
+// Workspace: the partial results of this path, then the tcgen05 path's scratch.  A path that the shapes
+// rule out takes none.
 struct Plan {
+  bool rows, tiles;
   int rows_grid;
-  size_t off_ml, off_split, bytes;
+  size_t off_ml, off_split, off_tile, bytes;
   Plan(const attn_fwd_paged_params_t& a, int sms) {
     rows_grid = 2 * sms;
     const size_t slots = 2 * (size_t)rows_grid * 16;
     off_ml = round256(slots * a.d * sizeof(float));
     off_split = off_ml + round256(slots * sizeof(float2));
-    bytes = off_split + round256((size_t)rows_grid * sizeof(Split));
+    off_tile = off_split + round256((size_t)rows_grid * sizeof(Split));
+    const int g = a.Hq / a.Hkv;
+    rows = g <= ROWS_MAX;
+    tiles = (long long)a.max_seqlen_q * g > ROWS_MAX;
+    if (!rows) off_tile = 0;
+    bytes = off_tile + (tiles ? tile_workspace(a, sms) : 0);
   }
 };
 
 bool misaligned(const void* ptr, unsigned int to) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
 
 int check_shape(const attn_fwd_paged_params_t& a) {
-  if (a.B < 1 || a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv != 0 || a.max_seqlen_q < 1) return ATTN_ERR_INVALID;
+  if (a.B < 1 || a.B > 16384 || a.total_q < 1 || a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv != 0 || a.max_seqlen_q < 1) return ATTN_ERR_INVALID;
   if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (a.Hq / a.Hkv > 128) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
@@ -559,9 +528,9 @@ int check(const attn_fwd_paged_params_t& a) {
   int rc = check_shape(a);
   if (rc != ATTN_OK) return rc;
   if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
-  if (a.total_q < 1 || a.num_pages < 1 || a.table_width < 1 || a.table_stride < a.table_width || a.page_size < 16 ||
+  if (a.num_pages < 1 || a.table_width < 1 || a.table_stride < a.table_width || a.page_size < 16 ||
       a.page_size % 16 != 0 || (long long)a.table_width * a.page_size > INT_MAX - 4096 ||
-      (long long)a.total_q * (a.Hq / a.Hkv) > INT_MAX - 4096 || a.window_left < -1 || a.window_right < -1)
+      (long long)a.total_q * a.Hq > INT_MAX - (1 << 27) || a.window_left < -1 || a.window_right < -1)
     return ATTN_ERR_INVALID;
   if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return ATTN_ERR_INVALID;
   for (const void* ptr : {a.q, a.k_cache, a.v_cache, (const void*)a.o})
@@ -572,11 +541,15 @@ int check(const attn_fwd_paged_params_t& a) {
   for (long long s : {a.q_row_stride, a.q_head_stride, a.o_row_stride, a.o_head_stride, a.cache_page_stride, a.cache_head_stride,
                       a.cache_row_stride})
     if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID;
+  // the strides of dimensions with more than one entry
+  if (a.cache_row_stride == 0 || (a.num_pages > 1 && a.cache_page_stride == 0) || (a.Hkv > 1 && a.cache_head_stride == 0) ||
+      (a.Hq > 1 && (a.q_head_stride == 0 || a.o_head_stride == 0)) || (a.total_q > 1 && (a.q_row_stride == 0 || a.o_row_stride == 0)))
+    return ATTN_ERR_INVALID;
   return ATTN_OK;
 }
 
 template <int D, bool BF16>
-int launch_rows(const PagedParams& p, const Plan& plan, cudaStream_t st, int dev) {
+int launch_rows(const RowsParams& p, const Plan& plan, cudaStream_t st, int dev) {
   using C = Rows<D>;
   static std::atomic<unsigned long long> attr_set{0};  // bit per device
   const unsigned long long bit = 1ull << dev;
@@ -617,7 +590,7 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
   if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
   const Plan plan(a, sms);
   if (a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
-  PagedParams p = {};
+  RowsParams p = {};
   p.q = static_cast<const uint16_t*>(a.q);
   p.k = static_cast<const uint16_t*>(a.k_cache);
   p.v = static_cast<const uint16_t*>(a.v_cache);
@@ -653,8 +626,13 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
   p.split = reinterpret_cast<Split*>(ws + plan.off_split);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
   const bool bf16 = a.dtype == ATTN_BF16;
-  if (a.d == 64) return bf16 ? launch_rows<64, true>(p, plan, st, dev) : launch_rows<64, false>(p, plan, st, dev);
-  return bf16 ? launch_rows<128, true>(p, plan, st, dev) : launch_rows<128, false>(p, plan, st, dev);
+  p.timeout_us = host_timeout_us();
+  if (plan.rows) {
+    if (a.d == 64) rc = bf16 ? launch_rows<64, true>(p, plan, st, dev) : launch_rows<64, false>(p, plan, st, dev);
+    else rc = bf16 ? launch_rows<128, true>(p, plan, st, dev) : launch_rows<128, false>(p, plan, st, dev);
+    if (rc != ATTN_OK) return rc;
+  }
+  return plan.tiles ? tile_launch(p, a, ws + plan.off_tile, sms, dev, st) : ATTN_OK;
 }
 
 }  // extern "C"

@@ -293,7 +293,8 @@ int attn_paged_append(const attn_paged_append_params_t *params);
  * (>= 1) are cut to their first max_seqlen_q rows.  Rows of q, o and lse outside every
  * request are neither read into a result nor written.
  * Element (hq, t, x) of q is at t*q_row_stride + hq*q_head_stride + x, of o likewise with its own
- * strides; lse is [Hq][total_q] or NULL.  Hq / Hkv <= 128.
+ * strides; lse is [Hq][total_q] or NULL.  Hq / Hkv <= 128, B <= 16384.  Strides of dimensions of more
+ * than one entry are positive.
  * Cache rows that no query row of the request may see, behind its last key, ahead of its
  * window, or on pages listed for none of its keys, may hold anything; those that one of its query
  * rows sees hold finite values.  A page id out of range sets ATTN_ERR_PAGE; its keys then count as
@@ -324,7 +325,7 @@ int attn_fwd_paged(const attn_fwd_paged_params_t *params);
 
 /*
  * attn_paged_workspace -- bytes of workspace that attn_fwd_paged wants for these parameters
- * on the current device.  It goes by Hq, Hkv, d and max_seqlen_q alone and reads no pointer.
+ * on the current device.  It goes by B, Hq, Hkv, d, total_q and max_seqlen_q alone and reads no pointer.
  */
 int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long long *bytes);
 

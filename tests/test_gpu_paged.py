@@ -326,7 +326,7 @@ def test_repeated_calls_are_bit_identical(lq):
 
 def test_other_streams_and_own_workspace():
     bt = Batch([1, 70, 1], [500, 300, 90], 8, 2, 128, "f16", 16, seed=15)
-    ws = torch.full((af.attn_paged_workspace(8, 2, 128, bt.max_q) + 64,), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((af.attn_paged_workspace(3, 8, 2, 128, 71 + 1, bt.max_q) + 64,), 255, dtype=torch.uint8, device="cuda")
     outs = []
     streams = [torch.cuda.Stream() for _ in range(3)]
     dev = bt.device()
@@ -449,3 +449,22 @@ def test_a_captured_step_replayed():
         a.verify(na)
         b.verify(nb)
     af.attn_check()
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """The chunk path's waits are bounded, as attn_fwd's are: a Q tile that never comes ends the launch with a status."""
+    lib = af.library()
+    bt = Batch([70, 1], [90, 50], 4, 2, 128, "bf16", 16, seed=16)
+    assert lib.attn_set_wait_timeout_ns(50_000_000) == 0
+    try:
+        assert lib.attn_debug_inject(1) == 0
+        _attend(bt, True, -1, -1, 0.1)
+        with pytest.raises(af.AttnError) as e:
+            af.attn_check()
+        assert e.value.status == -4
+    finally:
+        lib.attn_debug_inject(0)
+        lib.attn_set_wait_timeout_ns(0)
+    o, lse = _attend(bt, True, -1, -1, 0.1)
+    af.attn_check()
+    bt.check(o.cpu(), lse.cpu(), True, -1, -1, 0.1)

@@ -45,7 +45,8 @@ REFUSALS = (
     [("attend", {k: P + 2}, -1) for k in ("lse", "block_table", "cu_seqlens_q", "seqlens_k")] +
     [("attend", {k: v}, -1) for k in ATTEND if k.endswith("_stride") and k != "table_stride" for v in (60, -64)] +
     [("attend", kw, st) for kw, st in (
-        (dict(B=0), -1), (dict(Hq=3), -1), (dict(Hkv=0), -1), (dict(d=80), -2), (dict(dtype=7), -2), (dict(total_q=0), -1),
+        (dict(B=0), -1), (dict(B=16385), -1), (dict(cache_row_stride=0), -1), (dict(cache_page_stride=0), -1), (dict(cache_head_stride=0), -1),
+        (dict(q_head_stride=0), -1), (dict(q_row_stride=0), -1), (dict(o_head_stride=0), -1), (dict(o_row_stride=0), -1), (dict(Hq=3), -1), (dict(Hkv=0), -1), (dict(d=80), -2), (dict(dtype=7), -2), (dict(total_q=0), -1),
         (dict(max_seqlen_q=0), -1), (dict(num_pages=0), -1), (dict(page_size=0), -1), (dict(page_size=8), -1), (dict(page_size=40), -1),
         (dict(table_width=0), -1), (dict(table_stride=3), -1), (dict(window_left=-2), -1), (dict(window_right=-2), -1),
         (dict(scale=0.0), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(Hq=258, Hkv=2), -2),
@@ -77,7 +78,7 @@ def test_valid_calls_without_a_device(lib):
     for op in ("tables", "append", "attend"):
         assert _call(lib, op, {}) == -5
     with pytest.raises(af.AttnError):
-        af.attn_paged_workspace(8, 2, 128, 1)
+        af.attn_paged_workspace(1, 8, 2, 128, 1, 1)
 
 
 def test_status_has_a_text(lib):
