@@ -6,9 +6,10 @@
 // assembled from TMA boxes of up to page_size rows, which land in the 128-byte-swizzled tile that the
 // MMA warp of roles.cuh expects.  Roles, TMEM and barriers are those of attn_fwd.cu.
 //
-// Work: a plan kernel weighs every unit by its key tiles, cuts units along the keys where they are too few
-// or too unequal to fill the machine, and lists the parts longest first; the attention kernel takes them from
-// a queue; the results of cut units are joined by a third kernel.
+// Work: a plan kernel weighs every unit by its key tiles and lists them longest first.  The attention
+// kernel takes from a queue first whole units, as many as give every SM the same number, then runs: the rest of the
+// units laid end to end and cut into equal lengths, so no SM waits for another's last unit, and few units
+// still fill the machine.  The results of cut units (at most two pieces to a run) are joined by a third kernel.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -26,21 +27,22 @@ namespace {
 
 constexpr int FLAG_SCRUB = 16;  // the key tile holds rows that no query row of the unit sees
 
+// Written by the plan.  Line coordinates count key tiles over all (unit, head) pairs in order, heads inside.
 struct TileQueue {
-  int nparts;          // entries of the list; each stands for Hkv parts
-  unsigned int next;   // next (entry, head) to hand out
-  int njoins;          // cut units to join, times heads
-  int nslots;
+  unsigned int next;    // next queue entry
+  int whole, runs;      // entries: whole (unit, head) pairs, then runs
+  int njoins;           // cut (unit, head) pairs
+  int units;
+  long long line0, line;  // where the runs' line begins, its length
 };
-struct TilePart {
+struct TileUnit {
   int b, blk;
-  int j0, j1;   // key tiles
-  int slot;     // -1: the whole unit; else partial result slot + h
-  int pad[3];
+  int j0, w;      // key tiles j0 .. j0 + w - 1 (one where no key is seen: the unit still writes its rows)
+  long long cum;  // weights of the units before
 };
 struct TileJoin {
-  int b, blk;
-  int slot, parts;  // part k of head h in slot + k * Hkv + h
+  int unit, h;
+  int run, parts;  // slots 2 run + 1, 2 (run + 1), 2 (run + 2), ...
 };
 
 struct TileParams : PagedParams {
@@ -48,12 +50,11 @@ struct TileParams : PagedParams {
   int T;          // tokens of a Q tile
   int box_rows;   // rows of one K/V box
   TileQueue* queue;
-  TilePart* parts;
-  TileJoin* joins;
-  int* weights;    // [units per head]
-  float* part_o;   // [slots][256][D]
-  float2* part_ml; // [slots][256]
-  int max_units, max_slots;
+  TileUnit* units;   // [max_units + 1], longest first
+  TileJoin* joins;   // [max runs]: every cut pair holds a run's beginning
+  float* part_o;     // [2 max runs][256][D]
+  float2* part_ml;   // [2 max runs][256]
+  int max_units;
   int inject;
 };
 
@@ -79,171 +80,172 @@ __device__ __forceinline__ bool tile_keys(const TileParams& p, int sq, int sk, i
   return true;
 }
 
-// ------------------------------------------------------------------ plan
-// One CTA.  Units are numbered request by request (requests of the other path have none); a unit's
-// weight is its key tiles.  Cutting every unit into parts of at most c tiles costs about
-//     ceil(parts / SMs) * (weight of a part + 2)   key-tile steps, a part's start and end counting as two
-// (measured), two more where it is a piece whose result has to be joined; c is chosen among
-// ceil(largest / k) for 32 values of k, one to a warp.
-constexpr int PLAN_THREADS = 1024, PLAN_BINS = 1024;
-constexpr int MIN_PART = 4;  // tiles of a piece
+// First tile of run i out of n over a line, and the run that holds tile x of it.
+__device__ __forceinline__ long long run_begin(long long line, int n, int i) { return line * i / n; }
+__device__ __forceinline__ int run_of(long long line, int n, long long x) { return (int)(((x + 1) * n - 1) / line); }
 
-__device__ __forceinline__ int plan_cut(int warp) {  // 1 .. 16, then wider steps to 152
-  return warp < 16 ? warp + 1 : warp < 24 ? 18 + 2 * (warp - 16) : warp < 28 ? 36 + 8 * (warp - 24) : 76 + 25 * (warp - 28);
+// ------------------------------------------------------------------ plan
+// One CTA.  Units (of one head) are numbered request by request, requests of the other path having none,
+// and sorted by weight into 32 classes, stably, so that equal inputs give equal cuts.  Bound by latency: two
+// passes over the lengths, one over the units for each of weigh, sort, sum.
+constexpr int PLAN_THREADS = 1024;
+constexpr int MIN_RUN = 4;   // tiles of a run at least
+constexpr int MAX_SPLIT = 3; // runs per SM at most
+
+// Exclusive sum over the block's threads of x, and the total.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = x;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, incl, s);
+    if (lane >= s) incl += y;
+  }
+  __syncthreads();  // warp_sum may still be read from the scan before
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const T w = warp_sum[lane];
+    T y = w;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const T z = __shfl_up_sync(0xffffffffu, y, s);
+      if (lane >= s) y += z;
+    }
+    warp_sum[lane] = y - w;
+    if (lane == 31) warp_sum[32] = y;
+  }
+  __syncthreads();
+  total = warp_sum[32];
+  return warp_sum[warp] + incl - x;
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) tile_plan_kernel(const __grid_constant__ TileParams p, int sms) {
   grid_launch_dependents();
   extern __shared__ int pre[];  // units before each request, [B + 1]
-  __shared__ int warp_sum[32], bins[PLAN_BINS];
-  __shared__ float est_s[32];
-  __shared__ int best_s, wmax_s, slots_s, joins_s;
+  __shared__ int sum_s[33], rank_s[32][33];
+  __shared__ long long sum64_s[33];
+  __shared__ int wmax_s, wmin_s, joins_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit_tokens = QT * p.T;
-  const auto units_of = [&](int b) {
-    int row0, sq, sk;
-    request_span(p, b, row0, sq, sk);
-    return sq * p.g > ROWS_MAX ? (sq + unit_tokens - 1) / unit_tokens : 0;
-  };
   const int per = (p.B + PLAN_THREADS - 1) / PLAN_THREADS;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int own = 0;
-  for (int b = b0; b < b1; ++b) pre[b] = own, own += units_of(b);
-  int incl = own;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, s);
-    if (lane >= s) incl += x;
+  int own = 0, total;
+  for (int b = b0; b < b1; ++b) {
+    int row0, sq, sk;
+    request_span(p, b, row0, sq, sk);
+    pre[b] = own;
+    own += sq * p.g > ROWS_MAX ? (sq + unit_tokens - 1) / unit_tokens : 0;
   }
-  if (lane == 31) warp_sum[warp] = incl;
-  if (tid == 0) wmax_s = slots_s = joins_s = 0;
-  bins[tid] = 0;
-  __syncthreads();
-  if (warp == 0) {
-    const int w = warp_sum[lane];
-    int x = w;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, s);
-      if (lane >= s) x += y;
-    }
-    warp_sum[lane] = x - w;
-    if (lane == 31) pre[p.B] = x;
-  }
-  __syncthreads();
-  const int before = warp_sum[warp] + incl - own;
+  if (tid == 0) wmax_s = joins_s = 0, wmin_s = INT_MAX;
+  rank_s[warp][lane] = 0;
+  if (lane == 0) rank_s[warp][32] = 0;
+  const int before = block_scan(own, sum_s, total);
   for (int b = b0; b < b1; ++b) pre[b] += before;
+  if (tid == 0) pre[p.B] = total;
   __syncthreads();
-  const int units = min(pre[p.B], p.max_units);  // (more only where the row offsets overlap)
-  const auto find = [&](int u) {
+  const int units = min(total, p.max_units);  // (more only where the row offsets overlap)
+  const auto unit_at = [&](int u) {
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[mid] <= u) lo = mid;
       else hi = mid;
     }
-    return lo;
+    TileUnit x;
+    x.b = lo;
+    x.blk = u - pre[lo];
+    int row0, sq, sk, k0, k1;
+    request_span(p, x.b, row0, sq, sk);
+    tile_keys(p, sq, sk, x.blk, 0, QT, k0, k1);
+    x.j0 = k0 / BN;
+    x.w = max((k1 + BN - 1) / BN - x.j0, 1);
+    x.cum = 0;
+    return x;
   };
-  const auto key_tiles = [&](int b, int blk, int& j0, int& j1) {
-    int row0, sq, sk, lo, hi;
-    request_span(p, b, row0, sq, sk);
-    tile_keys(p, sq, sk, blk, 0, QT, lo, hi);
-    j0 = lo / BN;
-    j1 = (hi + BN - 1) / BN;
-  };
-  int wmax = 0;
-  for (int u = tid; u < units; u += PLAN_THREADS) {
-    const int b = find(u);
-    int j0, j1;
-    key_tiles(b, u - pre[b], j0, j1);
-    p.weights[u] = j1 - j0;
-    wmax = max(wmax, j1 - j0);
+  // every warp takes a stretch of neighbouring units
+  const int stretch = (units + PLAN_THREADS - 1) / PLAN_THREADS * 32;
+  const int u0 = min(warp * stretch, units), u1 = min(u0 + stretch, units);
+  int wmax = 0, wmin = INT_MAX;
+  for (int u = u0 + lane; u < u1; u += 32) {
+    const int w = unit_at(u).w;
+    wmax = max(wmax, w);
+    wmin = min(wmin, w);
   }
   wmax = __reduce_max_sync(0xffffffffu, wmax);
-  if (lane == 0) atomicMax(&wmax_s, wmax);
+  wmin = __reduce_min_sync(0xffffffffu, wmin);
+  if (lane == 0) {
+    atomicMax(&wmax_s, wmax);
+    atomicMin(&wmin_s, wmin);
+  }
   __syncthreads();
   wmax = max(wmax_s, 1);
-  const auto cap_of = [&](int k) { return max((wmax + k - 1) / k, min(wmax, MIN_PART)); };
-  {
-    const int c = cap_of(plan_cut(warp));
-    long long w = 0;
-    int n = 0, cut = 0;
-    for (int u = lane; u < units; u += 32) {
-      const int x = p.weights[u], m = max((x + c - 1) / c, 1);
-      w += x;
-      n += m;
-      if (m > 1) cut += m;
-    }
-#pragma unroll
-    for (int s = 16; s; s >>= 1) {
-      w += __shfl_xor_sync(0xffffffffu, w, s);
-      n += __shfl_xor_sync(0xffffffffu, n, s);
-      cut += __shfl_xor_sync(0xffffffffu, cut, s);
-    }
-    if (lane == 0) {
-      const float parts = (float)n * p.Hkv, cost = ((float)w * p.Hkv + 2.f * parts + 2.f * (float)cut * p.Hkv) / fmaxf(parts, 1.f);
-      const float waves = ceilf(parts / sms);
-      const float est = fmaxf(waves * cost, (float)c + 2.f);
-      est_s[warp] = (long long)cut * p.Hkv <= p.max_slots ? est : INFINITY;  // (k = 1 cuts nothing)
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    float e = est_s[lane];
-    int k = lane;
-#pragma unroll
-    for (int s = 16; s; s >>= 1) {
-      const float e2 = __shfl_xor_sync(0xffffffffu, e, s);
-      const int k2 = __shfl_xor_sync(0xffffffffu, k, s);
-      if (e2 < e || (e2 == e && k2 < k)) e = e2, k = k2;
-    }
-    if (lane == 0) best_s = cap_of(plan_cut(k));
-  }
-  __syncthreads();
-  const int c = best_s;
-  // counting sort of the parts, longest first
-  const auto bin_of = [&](int x, int m) { return PLAN_BINS - 1 - (int)((long long)((x + m - 1) / m) * (PLAN_BINS - 1) / c); };
-  for (int u = tid; u < units; u += PLAN_THREADS) {
-    const int x = p.weights[u], m = max((x + c - 1) / c, 1);
-    atomicAdd(&bins[bin_of(x, m)], m);
+  const auto class_of = [&](int w) { return 31 - (int)((long long)(w - 1) * 32 / wmax); };
+  for (int at = u0; at < u1; at += 32) {
+    const int c = at + lane < u1 ? class_of(unit_at(at + lane).w) : 32;  // (class 32: no unit)
+    const unsigned int same = __match_any_sync(0xffffffffu, c);
+    if (lane == __ffs(same) - 1) rank_s[warp][c] += __popc(same);
+    __syncwarp();
   }
   __syncthreads();
   {
-    const int x = bins[tid];
-    int in = x;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, in, s);
-      if (lane >= s) in += y;
-    }
-    if (lane == 31) warp_sum[warp] = in;
-    __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
-    bins[tid] = base + in - x;
+    // where each warp's units of each class go: classes outside, warps inside
+    const int c = tid >> 5, w = tid & 31;
+    const int x = rank_s[w][c];
+    const int at = block_scan(x, sum_s, total);
+    rank_s[w][c] = at;
   }
   __syncthreads();
-  for (int u = tid; u < units; u += PLAN_THREADS) {
-    const int b = find(u), blk = u - pre[b];
-    int j0, j1;
-    key_tiles(b, blk, j0, j1);
-    const int x = j1 - j0, m = max((x + c - 1) / c, 1);
-    const int at = atomicAdd(&bins[bin_of(x, m)], m);
-    int slot = -1;
-    if (m > 1) {
-      slot = atomicAdd(&slots_s, m * p.Hkv);
-      p.joins[atomicAdd(&joins_s, 1)] = TileJoin{b, blk, slot, m};
+  for (int at = u0; at < u1; at += 32) {
+    TileUnit x = {};
+    int c = 32;
+    if (at + lane < u1) {
+      x = unit_at(at + lane);
+      c = class_of(x.w);
     }
-    for (int k = 0; k < m; ++k)
-      p.parts[at + k] = TilePart{b, blk, j0 + (int)((long long)x * k / m), j0 + (int)((long long)x * (k + 1) / m),
-                                 m > 1 ? slot + k * p.Hkv : -1, {0, 0, 0}};
+    const unsigned int same = __match_any_sync(0xffffffffu, c);
+    const int to = rank_s[warp][c] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (lane == __ffs(same) - 1) rank_s[warp][c] += __popc(same);
+    __syncwarp();
+    if (c < 32) p.units[to] = x;
   }
   __syncthreads();
-  if (tid == 0) {
-    int n = 0;
-    for (int w = 0; w < 32; ++w) n += warp_sum[w];
-    *p.queue = TileQueue{n, 0u, joins_s * p.Hkv, slots_s};
+  // weights before each unit, in the sorted order
+  const int chunk = (units + PLAN_THREADS - 1) / PLAN_THREADS;
+  const int s0 = min(tid * chunk, units), s1 = min(s0 + chunk, units);
+  long long weight = 0, all;
+  for (int s = s0; s < s1; ++s) weight += p.units[s].w;
+  long long cum = block_scan(weight, sum64_s, all);
+  for (int s = s0; s < s1; ++s) {
+    p.units[s].cum = cum;
+    cum += p.units[s].w;
   }
+  if (tid == 0) p.units[units].cum = all;
+  __syncthreads();
+
+  // Whole pairs: full waves of the longest, where none is longer than an SM's share.
+  const long long pairs = (long long)units * p.Hkv, share = all * p.Hkv / sms;
+  const int whole = wmax <= share ? (int)(pairs / sms * sms) : 0;
+  const auto line_of = [&](long long x) {
+    const int s = (int)(x / p.Hkv);
+    return p.units[s].cum * p.Hkv + (s < units ? (x - (long long)s * p.Hkv) * p.units[s].w : 0);
+  };
+  const long long line0 = line_of(whole), line = all * p.Hkv - line0;
+  // Runs: one per SM; more where the whole pairs before them differ, so that the SMs that are done
+  // earlier take more.
+  const long long len = line / sms + 1;
+  const int split = whole ? (int)min((long long)MAX_SPLIT, 1 + 2ll * (wmax - wmin_s) / len) : 1;
+  const int runs = line ? (int)max(1ll, min((long long)split * sms, line / MIN_RUN)) : 0;
+  for (long long x = whole + tid; x < pairs; x += PLAN_THREADS) {
+    const int s = (int)(x / p.Hkv), h = (int)(x - (long long)s * p.Hkv);
+    const long long at = line_of(x) - line0;
+    const int first = run_of(line, runs, at), last = run_of(line, runs, at + p.units[s].w - 1);
+    if (first != last) p.joins[atomicAdd(&joins_s, 1)] = TileJoin{s, h, first, last - first + 1};
+  }
+  __syncthreads();
+  if (tid == 0) *p.queue = TileQueue{0u, whole, runs, joins_s, units, line0, line};
 }
 
 // ------------------------------------------------------------------ load warp
@@ -258,28 +260,70 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
   uint32_t kpar = 1, vpar = 1, ie_par = 1;
   uint32_t kpend = 0, kpend_par = 0, vpend = 0, vpend_par = 0;
   bool inject = p.inject != 0;
-  const unsigned int total = (unsigned int)p.queue->nparts * p.Hkv;
+  const int whole = p.queue->whole, runs = p.queue->runs;
   // the lane's box of a key tile: chunk of box_rows keys, 64-column half
   const int nbox = BN / p.box_rows * L::HALVES;
   const int chunk = lane / L::HALVES, half = lane % L::HALVES;
 
   unsigned int q_next = 0;
   if (lane == 0) q_next = atomicAdd(&p.queue->next, 1u);
+  int s = 0, h = 0, run = 0;  // unit (in the plan's order), head; run being worked off
+  long long left = 0;         // tiles of the run that are left
   for (int k = 0;; ++k) {
-    const unsigned int x = __shfl_sync(0xffffffffu, q_next, 0);
-    if (x >= total) {
-      if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
-      if (lane == 0) {
-        hdr[ie].j = -1;
-        hdr[ie].flags = FLAG_EXIT;
-        mbar_arrive(bars + 8u * (L::B_IFULL + ie));
+    TileUnit pt;
+    int slot = -1, from = 0, tiles;  // this piece: tiles from .. from + tiles of the unit
+    if (left > 0) {
+      // the run's next unit
+      if (++h == p.Hkv) {
+        h = 0;
+        ++s;
       }
-      __syncwarp();
-      break;
+      pt = p.units[s];
+      tiles = (int)min((long long)pt.w, left);
+      left -= tiles;
+      if (tiles < pt.w) slot = 2 * run + 1;
+    } else {
+      const unsigned int x = __shfl_sync(0xffffffffu, q_next, 0);
+      if (x >= (unsigned int)(whole + runs)) {
+        if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
+        if (lane == 0) {
+          hdr[ie].j = -1;
+          hdr[ie].flags = FLAG_EXIT;
+          mbar_arrive(bars + 8u * (L::B_IFULL + ie));
+        }
+        __syncwarp();
+        break;
+      }
+      if (lane == 0) q_next = atomicAdd(&p.queue->next, 1u);
+      if (x < (unsigned int)whole) {
+        s = (int)(x / p.Hkv);
+        h = (int)(x % p.Hkv);
+        pt = p.units[s];
+        tiles = pt.w;
+      } else {
+        run = (int)x - whole;
+        const long long line = p.queue->line, at = run_begin(line, runs, run);
+        left = run_begin(line, runs, run + 1) - at;
+        const long long pos = p.queue->line0 + at;
+        // the last unit whose pairs begin at or before pos, 32 probes at a time
+        int lo = whole / p.Hkv, hi = p.queue->units;
+        while (hi - lo > 1) {
+          const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
+          const unsigned int yes = __ballot_sync(0xffffffffu, probe < hi && p.units[probe].cum * p.Hkv <= pos);
+          lo += (31 - __clz(yes)) * step;  // (lane 0 always says yes)
+          hi = min(hi, lo + step);
+        }
+        s = lo;
+        pt = p.units[s];
+        const long long in = pos - pt.cum * p.Hkv;
+        h = (int)(in / pt.w);
+        from = (int)(in - (long long)h * pt.w);
+        tiles = (int)min((long long)(pt.w - from), left);
+        left -= tiles;
+        if (tiles < pt.w) slot = from == 0 ? 2 * run + 1 : 2 * run;
+      }
     }
-    if (lane == 0) q_next = atomicAdd(&p.queue->next, 1u);
-    const TilePart pt = p.parts[x / p.Hkv];
-    const int h = (int)(x % p.Hkv);
+    const int j0 = pt.j0 + from, j1 = j0 + tiles;
     int row0, sq, sk, lo, hi;
     request_span(p, pt.b, row0, sq, sk);
     tile_keys(p, sq, sk, pt.blk, 0, QT, lo, hi);
@@ -294,7 +338,6 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
       jhi[t] = (e + BN - 1) / BN;
     }
     const int tok0 = pt.blk * QT * p.T;
-    const int slot = pt.slot < 0 ? -1 : pt.slot + h;
     const int* table = p.table + (long long)pt.b * p.table_stride;
 
     const int qbuf = k % L::QBUF;
@@ -346,11 +389,11 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
       }
     };
     int page, row, page_next = 0, row_next = 0;
-    if (pt.j0 < pt.j1) place(pt.j0, page_next, row_next);
-    for (int j = pt.j0; j < pt.j1; ++j) {
+    place(j0, page_next, row_next);
+    for (int j = j0; j < j1; ++j) {
       page = page_next;
       row = row_next;
-      if (j + 1 < pt.j1) place(j + 1, page_next, row_next);  // the table's latency passes behind this tile's loads
+      if (j + 1 < j1) place(j + 1, page_next, row_next);  // the table's latency passes behind this tile's loads
       const bool a0 = j >= jlo[0] && j < jhi[0], a1 = j >= jlo[1] && j < jhi[1];
       if (!a0 && !a1) continue;
       if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
@@ -651,15 +694,16 @@ __global__ void __launch_bounds__(256) tile_join_kernel(const __grid_constant__ 
   const int rows = p.queue->njoins * UNIT_ROWS, nwarps = gridDim.x * 8;
   for (int x = blockIdx.x * 8 + (threadIdx.x >> 5); x < rows; x += nwarps) {
     const int row = x % UNIT_ROWS, rest = x / UNIT_ROWS;
-    const TileJoin jn = p.joins[rest / p.Hkv];
-    const int h = rest % p.Hkv, t = row / BM, r = row % BM;
+    const TileJoin jn = p.joins[rest];
+    const TileUnit un = p.units[jn.unit];
+    const int h = jn.h, t = row / BM, r = row % BM;
     int row0, sq, sk;
-    request_span(p, jn.b, row0, sq, sk);
-    const int tok0 = (jn.blk * QT + t) * p.T;
+    request_span(p, un.b, row0, sq, sk);
+    const int tok0 = (un.blk * QT + t) * p.T;
     if (r >= min(p.T, sq - tok0) * p.g) continue;
     float m = -INFINITY, l = 0.f, acc[E] = {};
     for (int k = 0; k < jn.parts; ++k) {
-      const long long at = (long long)(jn.slot + k * p.Hkv + h) * UNIT_ROWS + row;
+      const long long at = (long long)(k == 0 ? 2 * jn.run + 1 : 2 * (jn.run + k)) * UNIT_ROWS + row;
       const float2 ml = p.part_ml[at];
       const float* src = p.part_o + at * D + lane * E;
       float v[E];
@@ -683,8 +727,8 @@ __global__ void __launch_bounds__(256) tile_join_kernel(const __grid_constant__ 
 
 // ------------------------------------------------------------------ host side
 struct TilePlan {
-  int T, max_units, max_slots, max_parts;
-  size_t off_parts, off_joins, off_weights, off_ml, off_o, bytes;
+  int T, max_units, max_runs;
+  size_t off_units, off_joins, off_ml, off_o, bytes;
   TilePlan(const attn_fwd_paged_params_t& a, int sms) {
     const int g = a.Hq / a.Hkv;
     T = BM / g;
@@ -693,14 +737,13 @@ struct TilePlan {
     const long long by_rows = (long long)a.total_q / (QT * T) + a.B;
     const long long by_len = (long long)a.B * ((longest + QT * T - 1) / (QT * T));
     max_units = (int)(by_rows < by_len ? by_rows : by_len);  // by_rows <= total_q / 2 + B
-    max_slots = 4 * sms;  // room for as many pieces
-    max_parts = max_units + max_slots;
-    off_parts = 256;
-    off_joins = off_parts + round256((size_t)max_parts * sizeof(TilePart));
-    off_weights = off_joins + round256((size_t)max_slots * sizeof(TileJoin));
-    off_ml = off_weights + round256((size_t)max_units * sizeof(int));
-    off_o = off_ml + round256((size_t)max_slots * UNIT_ROWS * sizeof(float2));
-    bytes = off_o + round256((size_t)max_slots * UNIT_ROWS * a.d * sizeof(float));
+    max_runs = MAX_SPLIT * sms;
+    const size_t slots = 2 * (size_t)max_runs;
+    off_units = 256;
+    off_joins = off_units + round256((size_t)(max_units + 1) * sizeof(TileUnit));
+    off_ml = off_joins + round256((size_t)max_runs * sizeof(TileJoin));
+    off_o = off_ml + round256(slots * UNIT_ROWS * sizeof(float2));
+    bytes = off_o + round256(slots * UNIT_ROWS * a.d * sizeof(float));
   }
 };
 
@@ -719,8 +762,7 @@ int launch_tiles(const TileParams& p, int sms, int dev, cudaStream_t st) {
   tile_plan_kernel<<<1, PLAN_THREADS, ((size_t)p.B + 1) * sizeof(int), st>>>(p, sms);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  const long long most = ((long long)p.max_units + p.max_slots) * p.Hkv;
-  cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+  cfg.gridDim = dim3(sms);
   cfg.blockDim = dim3(NTHREADS);
   cfg.dynamicSmemBytes = L::SMEM_ALLOC;
   cfg.stream = st;
@@ -762,13 +804,11 @@ int tile_launch(const PagedParams& base, const attn_fwd_paged_params_t& a, void*
     return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.queue = reinterpret_cast<TileQueue*>(ws);
-  p.parts = reinterpret_cast<TilePart*>(ws + plan.off_parts);
+  p.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);
   p.joins = reinterpret_cast<TileJoin*>(ws + plan.off_joins);
-  p.weights = reinterpret_cast<int*>(ws + plan.off_weights);
   p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
   p.max_units = plan.max_units;
-  p.max_slots = plan.max_slots;
   p.inject = host_take_inject();
   if (a.d == 64) return bf16 ? launch_tiles<64, true>(p, sms, dev, st) : launch_tiles<64, false>(p, sms, dev, st);
   return bf16 ? launch_tiles<128, true>(p, sms, dev, st) : launch_tiles<128, false>(p, sms, dev, st);
