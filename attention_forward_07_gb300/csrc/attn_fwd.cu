@@ -466,7 +466,7 @@ namespace attn {
 // What the MMA warp does for this kernel beside its multiplications: it records the computed blocks.
 template <int MODE>
 struct FwdEnv {
-  static constexpr bool SCRUB = false;
+  static constexpr bool SCRUB = false, ALTERNATE = false;
   const Params& p;
   int b, hq, qb;
   __device__ __forceinline__ void unit(volatile InfoHdr& h) {
@@ -1076,16 +1076,16 @@ std::atomic<unsigned long long> g_ws_allocs{0}, g_map_encodes{0}, g_map_hits{0};
 // Tensor maps cached by (kind, address, dims, box rows): a map holds nothing but these, so a
 // cached map is valid for any later call that names the same buffer with the same shape.
 // Least-recently-used replacement over a small table.
-enum MapKind { MAP_F16 = 0, MAP_BF16 = 1, MAP_WORDS = 2, MAP4_F16 = 3, MAP4_BF16 = 4 };
+enum MapKind { MAP_F16 = 0, MAP_BF16 = 1, MAP_WORDS = 2, MAP5_F16 = 3, MAP5_BF16 = 4 };
 struct MapKey {
   int kind;
   const void* ptr;
   long long d0, d1, d2;
   int box_rows;
-  Map4 four;  // 4-D maps: everything but kind and ptr
+  Map5 five;  // 5-D maps: everything but kind and ptr
   bool operator==(const MapKey& o) const {
     return kind == o.kind && ptr == o.ptr && d0 == o.d0 && d1 == o.d1 && d2 == o.d2 && box_rows == o.box_rows &&
-           std::memcmp(&four, &o.four, sizeof four) == 0;
+           std::memcmp(&five, &o.five, sizeof five) == 0;
   }
 };
 constexpr int MAP_CACHE = 64;
@@ -1528,18 +1528,18 @@ uint32_t host_timeout_us() {
   return us > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)us;
 }
 
-int host_map4(CUtensorMap* m, const void* ptr, bool bf16, const Map4& t) {
-  return cached_map(m, MapKey{bf16 ? MAP4_BF16 : MAP4_F16, ptr, 0, 0, 0, 0, t}, [&](CUtensorMap* out) -> int {
+int host_map5(CUtensorMap* m, const void* ptr, bool bf16, const Map5& t) {
+  return cached_map(m, MapKey{bf16 ? MAP5_BF16 : MAP5_F16, ptr, 0, 0, 0, 0, t}, [&](CUtensorMap* out) -> int {
     auto enc = tensor_map_encoder();
     if (!enc) return ATTN_ERR_CUDA;
-    cuuint64_t dims[4], strides[3];
-    cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 4; ++i) {
+    cuuint64_t dims[5], strides[4];
+    cuuint32_t box[5], estr[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < 5; ++i) {
       dims[i] = (cuuint64_t)t.dims[i];
       box[i] = (cuuint32_t)t.box[i];
       if (i) strides[i - 1] = (cuuint64_t)t.strides[i - 1];
     }
-    return enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims,
+    return enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(ptr), dims,
                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? ATTN_OK

@@ -18,13 +18,13 @@ uint32_t host_timeout_us();
 // The armed state of attn_debug_inject, which one launch takes.
 int host_take_inject();
 
-// 4-D tensor map of fp16 / bf16 with 128-byte swizzle, from the library's cache: extents and box in
-// elements, strides of dimensions 1-3 in bytes.  What lies outside reads as zeros.
-struct Map4 {
-  long long dims[4], strides[3];
-  int box[4];
+// 5-D tensor map of fp16 / bf16 with 128-byte swizzle, from the library's cache: extents and box in
+// elements, strides of dimensions 1-4 in bytes.  What lies outside reads as zeros.
+struct Map5 {
+  long long dims[5], strides[4];
+  int box[5], pad;  // (pad: so that maps compare byte by byte)
 };
-int host_map4(CUtensorMap* m, const void* ptr, bool bf16, const Map4& t);
+int host_map5(CUtensorMap* m, const void* ptr, bool bf16, const Map5& t);
 
 // Device address of the status word of `stream` (what attn_check reads and clears).
 int host_status_word(int dev, void* stream, unsigned int** word);

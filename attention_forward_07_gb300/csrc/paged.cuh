@@ -14,6 +14,38 @@
 namespace attn {
 
 constexpr int ROWS_MAX = 16;
+constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile
+
+// Written by the plan.  Line coordinates count key tiles over all (unit, head) pairs in order, heads inside.
+struct TileQueue {
+  unsigned int next;    // next queue entry (a CTA starts with that of its own number)
+  int whole, runs;      // entries: whole (unit, head) pairs, then runs
+  int njoins;           // cut (unit, head) pairs
+  int units;
+  long long line0, line;  // where the runs' line begins, its length
+};
+struct TileUnit {
+  int b, blk;
+  int j0, w;      // key tiles j0 .. j0 + w - 1 (one where no key is seen: the unit still writes its rows)
+  long long cum;  // weights of the units before
+  int row0, sq, sk, pad;
+};
+struct TileJoin {
+  int unit, h;
+  int run, parts;  // slots 2 run + 1, 2 (run + 1), 2 (run + 2), ...
+};
+
+// Scratch of the tcgen05 path.
+struct TileWork {
+  TileQueue* queue;
+  TileUnit* units;   // [max_units + 1], longest first
+  TileJoin* joins;   // [max runs]: every cut pair holds a run's beginning
+  float* part_o;     // [2 max runs][256][D]: unscaled O of a piece
+  float2* part_ml;   // [2 max runs][256]: its exponent base (exp2 domain) and sum of weights
+  int T;             // tokens of a Q tile
+  int max_units;     // 0: no request takes this path
+  int sms;
+};
 
 struct PagedParams {
   const uint16_t *q, *k, *v;
@@ -27,6 +59,7 @@ struct PagedParams {
   float scale_log2;
   unsigned int* status;
   uint32_t timeout_us;  // longest barrier wait (microseconds)
+  TileWork tile;
 };
 
 // Query rows, keys and first query row of request b, whatever the arrays hold.
@@ -44,9 +77,39 @@ __device__ __forceinline__ int row_hi(const PagedParams& p, int i, int off, int 
   return p.er < 0 ? sk : (int)min((long long)sk, (long long)i + off + p.er + 1);
 }
 
-// Scratch of the tcgen05 path behind the other path's, and its launches (plan, attention, join).
-size_t tile_workspace(const attn_fwd_paged_params_t& a, int sms);
-int tile_launch(const PagedParams& p, const attn_fwd_paged_params_t& a, void* workspace, int sms, int dev, cudaStream_t st);
+// Tokens and keys of Q tiles [t0, t1) of block blk: false where it has no token.
+__device__ __forceinline__ bool tile_keys(const PagedParams& p, int sq, int sk, int blk, int t0, int t1, int& lo, int& hi) {
+  const int i0 = (blk * TILE_QT + t0) * p.tile.T, i1 = min((blk * TILE_QT + t1) * p.tile.T, sq) - 1;
+  lo = hi = 0;
+  if (i0 > i1) return false;
+  const int a = row_lo(p, i0, sk - sq), e = row_hi(p, i1, sk - sq, sk);
+  if (e > a) lo = a, hi = e;
+  return true;
+}
+
+// First tile of run i out of n over a line of tiles, and the run that holds tile x of it.
+__host__ __device__ __forceinline__ long long run_begin(long long line, int n, int i) { return line * i / n; }
+__device__ __forceinline__ int run_of(long long line, int n, long long x) { return (int)(((x + 1) * n - 1) / line); }
+
+// Launches the tcgen05 path's attention kernel.
+int tile_launch(const PagedParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st);
+
+// Launches a kernel that may start before the one ahead of it on the stream has finished; it waits for
+// that one (griddepcontrol.wait) before it touches memory.
+template <class P>
+int launch_dependent(void (*kern)(P), dim3 grid, unsigned int threads, size_t smem, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
 
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 

@@ -30,9 +30,10 @@ struct Split {
 };
 
 struct RowsParams : PagedParams {
-  float* part_o;    // [2 * grid][16][D] partial sums of V, not normalised
-  float2* part_ml;  // [2 * grid][16] their exponent base (exp2 domain) and sum of weights
-  Split* split;     // [grid]
+  float* part_o;    // [2 * rows_grid][16][D] partial sums of V, not normalised
+  float2* part_ml;  // [2 * rows_grid][16] their exponent base (exp2 domain) and sum of weights
+  Split* split;     // [rows_grid]
+  int rows_grid;    // CTAs of this path
 };
 
 // ------------------------------------------------------------------ few rows: the memory-bound path
@@ -72,7 +73,7 @@ __device__ __forceinline__ RowsItem rows_request(const RowsParams& p, int b) {
   request_span(p, b, it.row0, it.sq, it.sk);
   it.off = it.sk - it.sq;
   it.R = it.sq * p.g;
-  it.nblk = it.R <= ROWS_MAX ? (it.R + 15) / 16 : 0;
+  it.nblk = it.R <= ROWS_MAX && it.R > 0 ? 1 : 0;
   return it;
 }
 // Keys [lo, hi) that any row of block blk keeps and the tiles [t0, t1) that hold them (one tile of
@@ -96,9 +97,167 @@ __device__ __forceinline__ long long rows_weight(const RowsParams& p, const Rows
   }
   return w * p.Hkv;
 }
-// First tile of CTA c's run out of n tiles over `ctas` runs, and the CTA whose run holds tile x.
-__device__ __forceinline__ long long run_begin(long long n, int ctas, int c) { return n * c / ctas; }
-__device__ __forceinline__ int run_of(long long n, int ctas, long long x) { return (int)(((x + 1) * ctas - 1) / n); }
+// ------------------------------------------------------------------ plan
+// What the tcgen05 path works off, by one CTA of 128 threads while the others run the few-row path.  Units
+// (of one head) are numbered request by request, requests of the other path having none, and sorted by
+// weight into 32 classes, stably, so that equal inputs give equal cuts.  Bound by latency: one pass over the
+// requests, then one over the units for each of weigh, sort, sum.
+constexpr int PLAN_THREADS = 128, PLAN_WARPS = PLAN_THREADS / 32;
+constexpr int MIN_RUN = 4;   // tiles of a run at least
+constexpr int MAX_SPLIT = 3; // runs per SM at most
+
+// Exclusive sum over the block's threads of x, and the total.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = x;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, incl, s);
+    if (lane >= s) incl += y;
+  }
+  __syncthreads();  // warp_sum may still be read from the scan before
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < PLAN_WARPS; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  return before + incl - x;
+}
+
+// `pre` holds B + 1 ints of shared memory (units before each request).
+__device__ __forceinline__ void tile_plan(const PagedParams& p, int* pre) {
+  __shared__ int sum_s[PLAN_WARPS], rank_s[PLAN_WARPS][33];
+  __shared__ long long sum64_s[PLAN_WARPS];
+  __shared__ int wmax_s, wmin_s, joins_s;
+  const TileWork& tw = p.tile;
+  const int sms = tw.sms;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit_tokens = TILE_QT * tw.T;
+  const int per = (p.B + PLAN_THREADS - 1) / PLAN_THREADS;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int own = 0, total;
+  for (int b = b0; b < b1; ++b) {
+    int row0, sq, sk;
+    request_span(p, b, row0, sq, sk);
+    pre[b] = own;
+    own += sq * p.g > ROWS_MAX ? (sq + unit_tokens - 1) / unit_tokens : 0;
+  }
+  if (tid == 0) wmax_s = joins_s = 0, wmin_s = INT_MAX;
+  for (int x = lane; x < 33; x += 32) rank_s[warp][x] = 0;
+  const int before = block_scan(own, sum_s, total);
+  for (int b = b0; b < b1; ++b) pre[b] += before;
+  if (tid == 0) pre[p.B] = total;
+  __syncthreads();
+  const int units = min(total, tw.max_units);  // (more only where the row offsets overlap)
+  const auto unit_at = [&](int u) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    TileUnit x;
+    x.b = lo;
+    x.blk = u - pre[lo];
+    int row0, sq, sk, k0, k1;
+    request_span(p, x.b, row0, sq, sk);
+    tile_keys(p, sq, sk, x.blk, 0, TILE_QT, k0, k1);
+    x.j0 = k0 / TILE_KEYS;
+    x.w = max((k1 + TILE_KEYS - 1) / TILE_KEYS - x.j0, 1);
+    x.cum = x.pad = 0;
+    x.row0 = row0;
+    x.sq = sq;
+    x.sk = sk;
+    return x;
+  };
+  // every warp takes a stretch of neighbouring units
+  const int stretch = (units + PLAN_THREADS - 1) / PLAN_THREADS * 32;
+  const int u0 = min(warp * stretch, units), u1 = min(u0 + stretch, units);
+  int wmax = 0, wmin = INT_MAX;
+  for (int u = u0 + lane; u < u1; u += 32) {
+    const int w = unit_at(u).w;
+    wmax = max(wmax, w);
+    wmin = min(wmin, w);
+  }
+  wmax = __reduce_max_sync(0xffffffffu, wmax);
+  wmin = __reduce_min_sync(0xffffffffu, wmin);
+  if (lane == 0) {
+    atomicMax(&wmax_s, wmax);
+    atomicMin(&wmin_s, wmin);
+  }
+  __syncthreads();
+  wmax = max(wmax_s, 1);
+  const auto class_of = [&](int w) { return 31 - (int)((long long)(w - 1) * 32 / wmax); };
+  for (int at = u0; at < u1; at += 32) {
+    const int c = at + lane < u1 ? class_of(unit_at(at + lane).w) : 32;  // (class 32: no unit)
+    const unsigned int same = __match_any_sync(0xffffffffu, c);
+    if (lane == __ffs(same) - 1) rank_s[warp][c] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  {
+    // where each warp's units of each class go: classes outside, warps inside
+    const int c = tid / PLAN_WARPS, w = tid % PLAN_WARPS;
+    const int x = rank_s[w][c];
+    const int at = block_scan(x, sum_s, total);
+    rank_s[w][c] = at;
+  }
+  __syncthreads();
+  for (int at = u0; at < u1; at += 32) {
+    TileUnit x = {};
+    int c = 32;
+    if (at + lane < u1) {
+      x = unit_at(at + lane);
+      c = class_of(x.w);
+    }
+    const unsigned int same = __match_any_sync(0xffffffffu, c);
+    const int to = rank_s[warp][c] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (lane == __ffs(same) - 1) rank_s[warp][c] += __popc(same);
+    __syncwarp();
+    if (c < 32) tw.units[to] = x;
+  }
+  __syncthreads();
+  // weights before each unit, in the sorted order
+  const int chunk = (units + PLAN_THREADS - 1) / PLAN_THREADS;
+  const int s0 = min(tid * chunk, units), s1 = min(s0 + chunk, units);
+  long long weight = 0, all;
+  for (int s = s0; s < s1; ++s) weight += tw.units[s].w;
+  long long cum = block_scan(weight, sum64_s, all);
+  for (int s = s0; s < s1; ++s) {
+    tw.units[s].cum = cum;
+    cum += tw.units[s].w;
+  }
+  if (tid == 0) tw.units[units].cum = all;
+  __syncthreads();
+
+  // Whole pairs: full waves of the longest, where none is longer than an SM's share.
+  const long long pairs = (long long)units * p.Hkv, share = all * p.Hkv / sms;
+  const int whole = wmax <= share ? (int)(pairs / sms * sms) : 0;
+  const auto line_of = [&](long long x) {
+    const int s = (int)(x / p.Hkv);
+    return tw.units[s].cum * p.Hkv + (s < units ? (x - (long long)s * p.Hkv) * tw.units[s].w : 0);
+  };
+  const long long line0 = line_of(whole), line = all * p.Hkv - line0;
+  // Runs: one per SM; more where the whole pairs before them differ, so that the SMs that are done
+  // earlier take more.
+  const long long len = line / sms + 1;
+  const int split = whole ? (int)min((long long)MAX_SPLIT, 1 + 2ll * (wmax - wmin_s) / len) : 1;
+  const int runs = line ? (int)max(1ll, min((long long)split * sms, line / MIN_RUN)) : 0;
+  for (long long x = whole + tid; x < pairs; x += PLAN_THREADS) {
+    const int s = (int)(x / p.Hkv), h = (int)(x - (long long)s * p.Hkv);
+    const long long at = line_of(x) - line0;
+    const int first = run_of(line, runs, at), last = run_of(line, runs, at + tw.units[s].w - 1);
+    if (first != last) tw.joins[atomicAdd(&joins_s, 1)] = TileJoin{s, h, first, last - first + 1};
+  }
+  __syncthreads();
+  if (tid == 0) *tw.queue = TileQueue{(unsigned int)sms, whole, runs, joins_s, units, line0, line};
+}
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -131,6 +290,12 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_kernel(const __grid_constant__ RowsParams p) {
   using C = Rows<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (p.tile.max_units > 0 && blockIdx.x == 0) {
+    tile_plan(p, reinterpret_cast<int*>(smem));
+    return;
+  }
   __shared__ long long warp_sum[C::WARPS];
   __shared__ int4 start_s;            // b, h, blk, tile of the run's first tile
   __shared__ float2 ml_s[C::WARPS][16];
@@ -155,8 +320,8 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
     if (w < warp) before += warp_sum[w];
     n += warp_sum[w];
   }
-  const int ctas = (int)min((long long)gridDim.x, (n + C::MIN_TILES - 1) / C::MIN_TILES);
-  const int cta = blockIdx.x;
+  const int ctas = (int)min((long long)p.rows_grid, (n + C::MIN_TILES - 1) / C::MIN_TILES);
+  const int cta = (int)blockIdx.x - ((int)gridDim.x - p.rows_grid);
   if (tid == 0) p.split[cta].b = -1;
   if (cta >= ctas) return;
   const long long run0 = run_begin(n, ctas, cta), run1 = run_begin(n, ctas, cta + 1);
@@ -440,76 +605,160 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
   }
 }
 
-// Joins the partial results of split items: one CTA per (run that begins one, row), its four warps share
-// out the parts and each lane takes D / 32 columns.
+// ------------------------------------------------------------------ join
+// Puts the partial results of cut items and units together: for a row of theirs
+//     m = max m_k, O = sum 2^(m_k - m) O_k / sum 2^(m_k - m) l_k, LSE = ln2 (m + log2 sum).
+// A CTA takes a cut item of the few-row path (at most 16 rows) or 16 rows of a cut unit of the tcgen05 path;
+// its warps share out the rows, and where there are fewer rows than warps, a row's parts.  The parts were
+// just written and are mostly in L2; four are in flight at a time.
+constexpr int JOIN_WARPS = 16;
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int E = D / 32;
-  const Split sp = p.split[blockIdx.x];
-  if (sp.b < 0) return;
-  const RowsItem it = rows_request<D>(p, sp.b);
-  const int r = blockIdx.y, rr = sp.blk * 16 + r;
-  if (rr >= it.R) return;
-  __shared__ float acc_s[4][D];
-  __shared__ float2 ml_s[4];
+__global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int E = D / 32;  // columns of a lane
+  __shared__ float acc_s[JOIN_WARPS][D];
+  __shared__ float2 ml_s[JOIN_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float m = -INFINITY, l = 0.f, acc[E] = {};
-  for (int x = warp; x < sp.parts; x += 4) {
-    const int slot = x == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + x);
-    const float2 ml = p.part_ml[slot * 16 + r];
-    const float* src = p.part_o + ((long long)slot * 16 + r) * D + lane * E;
-    float v[E];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int items = p.rows_grid;
+  const int total = items + (p.tile.max_units > 0 ? p.tile.queue->njoins * (TILE_QT * TILE_ROWS / JOIN_WARPS) : 0);
+  for (int x = blockIdx.x; x < total; x += gridDim.x) {
+    int rows, row0, h, parts, first, stride, slot0;  // part k of row r: record (k ? slot0 + k * stride : first) + r
+    int tok0;
+    const float* part_o;
+    const float2* part_ml;
+    if (x < items) {
+      const Split sp = p.split[x];
+      if (sp.b < 0) continue;
+      int sq, sk;
+      request_span(p, sp.b, row0, sq, sk);
+      rows = sq * p.g;
+      tok0 = 0;
+      h = sp.h;
+      parts = sp.parts;
+      first = (2 * x + 1) * 16;
+      slot0 = 2 * x * 16;
+      stride = 2 * 16;
+      part_o = p.part_o;
+      part_ml = p.part_ml;
+    } else {
+      constexpr int CHUNKS = TILE_QT * TILE_ROWS / JOIN_WARPS;
+      const int y = x - items, chunk = y % CHUNKS;
+      const TileJoin jn = p.tile.joins[y / CHUNKS];
+      const TileUnit un = p.tile.units[jn.unit];
+      const int t = chunk / (CHUNKS / TILE_QT), r0 = chunk % (CHUNKS / TILE_QT) * JOIN_WARPS;  // Q tile, first row in it
+      row0 = un.row0;
+      tok0 = (un.blk * TILE_QT + t) * p.tile.T;
+      rows = min(min(p.tile.T, un.sq - tok0) * p.g - r0, JOIN_WARPS);
+      if (rows <= 0) continue;
+      tok0 = tok0 * p.g + r0;  // (as packed row)
+      h = jn.h;
+      parts = jn.parts;
+      const int in = t * TILE_ROWS + r0;
+      first = (2 * jn.run + 1) * (TILE_QT * TILE_ROWS) + in;
+      slot0 = 2 * jn.run * (TILE_QT * TILE_ROWS) + in;
+      stride = 2 * TILE_QT * TILE_ROWS;
+      part_o = p.tile.part_o;
+      part_ml = p.tile.part_ml;
+    }
+    int share = 1;  // warps to a row
+    while (share * 2 * rows <= JOIN_WARPS) share *= 2;
+    const int r = warp / share, sub = warp % share;
+    float m = -INFINITY, l = 0.f, acc[E] = {};
+    if (r < rows) {
+      constexpr int AHEAD = 4;
+      for (int k0 = sub; k0 < parts; k0 += share * AHEAD) {
+        float2 ml[AHEAD];
+        float v[AHEAD][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = src[e];
-    const float mn = fmaxf(m, ml.x);
-    const float fa = m == -INFINITY ? 0.f : ex2_approx(m - mn), fb = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
-    l = l * fa + ml.y * fb;
+        for (int a = 0; a < AHEAD; ++a) {
+          const int k = k0 + a * share;
+          const long long at = (k ? slot0 + (long long)k * stride : first) + r;
+          ml[a] = k < parts ? part_ml[at] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * fa + v[e] * fb;
-    m = mn;
+          for (int e = 0; e < E; ++e) v[a][e] = k < parts ? part_o[at * D + lane * E + e] : 0.f;
+        }
+        float mn = m;
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) mn = fmaxf(mn, ml[a].x);
+        const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+          const float fa = ml[a].x == -INFINITY ? 0.f : ex2_approx(ml[a].x - mn);
+          l = fmaf(ml[a].y, fa, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(v[a][e], fa, acc[e]);
+        }
+        m = mn;
+      }
+    }
+    if (share > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
+      if (lane == 0) ml_s[warp] = make_float2(m, l);
+      __syncthreads();
+      if (sub == 0 && r < rows) {
+        float mm = m;
+        for (int w = 1; w < share; ++w) mm = fmaxf(mm, ml_s[warp + w].x);
+        const float f = m == -INFINITY ? 0.f : ex2_approx(m - mm);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+        for (int w = 1; w < share; ++w) {
+          const float2 ml = ml_s[warp + w];
+          const float fw = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+          l = fmaf(ml.y, fw, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(acc_s[warp + w][lane * E + e], fw, acc[e]);
+        }
+        m = mm;
+      }
+    }
+    if (sub != 0 || r >= rows) continue;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int rr = tok0 + r, i = rr / p.g, hq = h * p.g + rr - i * p.g;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (long long)(row0 + i) * p.o_row + (long long)hq * p.o_head + lane * E);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[(long long)hq * p.total_q + row0 + i] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
-  if (lane == 0) ml_s[warp] = make_float2(m, l);
-  __syncthreads();
-  if (warp != 0) return;
-  float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml_s[w].x);
-  float out[E] = {};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ml_s[w].x == -INFINITY ? 0.f : ex2_approx(ml_s[w].x - mm);
-    ll += f * ml_s[w].y;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = fmaf(f, acc_s[w][lane * E + e], out[e]);
-  }
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
-  const int i = rr / p.g, hq = sp.h * p.g + rr - i * p.g;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (long long)(it.row0 + i) * p.o_row + (long long)hq * p.o_head + lane * E);
-#pragma unroll
-  for (int e = 0; e < E / 2; ++e) dst[e] = pack2<BF16>(out[2 * e] * inv, out[2 * e + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host side
-// Workspace: the partial results of this path, then the tcgen05 path's scratch.  A path that the shapes
-// rule out takes none.
+// Workspace: the few-row path's partial results, then, where a request may take the tcgen05 path, that
+// path's scratch.
 struct Plan {
-  bool rows, tiles;
-  int rows_grid;
-  size_t off_ml, off_split, off_tile, bytes;
+  int rows_grid, T, max_units;
+  size_t off_ml, off_split, off_queue, off_units, off_joins, off_tile_ml, off_tile_o, bytes;
   Plan(const attn_fwd_paged_params_t& a, int sms) {
+    const int g = a.Hq / a.Hkv;
     rows_grid = 2 * sms;
     const size_t slots = 2 * (size_t)rows_grid * 16;
     off_ml = round256(slots * a.d * sizeof(float));
     off_split = off_ml + round256(slots * sizeof(float2));
-    off_tile = off_split + round256((size_t)rows_grid * sizeof(Split));
-    const int g = a.Hq / a.Hkv;
-    rows = g <= ROWS_MAX;
-    tiles = (long long)a.max_seqlen_q * g > ROWS_MAX;
-    if (!rows) off_tile = 0;
-    bytes = off_tile + (tiles ? tile_workspace(a, sms) : 0);
+    off_queue = off_split + round256((size_t)rows_grid * sizeof(Split));
+    T = TILE_ROWS / g;
+    const int longest = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+    if ((long long)longest * g <= ROWS_MAX) {
+      max_units = 0;
+      bytes = off_queue;
+      return;
+    }
+    // units of a head: every request's tokens over 2 T, rounded up
+    const long long by_rows = (long long)a.total_q / (TILE_QT * T) + a.B;  // <= total_q / 2 + B
+    const long long by_len = (long long)a.B * ((longest + TILE_QT * T - 1) / (TILE_QT * T));
+    max_units = (int)(by_rows < by_len ? by_rows : by_len);
+    const size_t max_runs = (size_t)MAX_SPLIT * sms, pieces = 2 * max_runs * TILE_QT * TILE_ROWS;
+    off_units = off_queue + 256;
+    off_joins = off_units + round256((size_t)(max_units + 1) * sizeof(TileUnit));
+    off_tile_ml = off_joins + round256(max_runs * sizeof(TileJoin));
+    off_tile_o = off_tile_ml + round256(pieces * sizeof(float2));
+    bytes = off_tile_o + round256(pieces * a.d * sizeof(float));
   }
 };
 
@@ -545,11 +794,17 @@ int check(const attn_fwd_paged_params_t& a) {
   if (a.cache_row_stride == 0 || (a.num_pages > 1 && a.cache_page_stride == 0) || (a.Hkv > 1 && a.cache_head_stride == 0) ||
       (a.Hq > 1 && (a.q_head_stride == 0 || a.o_head_stride == 0)) || (a.total_q > 1 && (a.q_row_stride == 0 || a.o_row_stride == 0)))
     return ATTN_ERR_INVALID;
+  // the tensor maps of the caches take page and head as one coordinate
+  if (a.num_pages > 1 && a.Hkv > 1) {
+    const long long big = a.cache_page_stride > a.cache_head_stride ? a.cache_page_stride : a.cache_head_stride;
+    const long long unit = a.cache_page_stride + a.cache_head_stride - big;
+    if (big % unit != 0 || (big == a.cache_page_stride ? a.num_pages : a.Hkv) > (INT_MAX - (1 << 20)) / (big / unit)) return ATTN_ERR_UNSUPPORTED;
+  }
   return ATTN_OK;
 }
 
 template <int D, bool BF16>
-int launch_rows(const RowsParams& p, const Plan& plan, cudaStream_t st, int dev) {
+int launch(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& plan, int sms, int dev, cudaStream_t st) {
   using C = Rows<D>;
   static std::atomic<unsigned long long> attr_set{0};  // bit per device
   const unsigned long long bit = 1ull << dev;
@@ -558,10 +813,11 @@ int launch_rows(const RowsParams& p, const Plan& plan, cudaStream_t st, int dev)
       return ATTN_ERR_CUDA;
     attr_set.fetch_or(bit);
   }
-  rows_kernel<D, BF16><<<plan.rows_grid, C::NTHREADS, C::SMEM, st>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  rows_join_kernel<D, BF16><<<dim3(plan.rows_grid, 16), 128, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const bool tiles = p.tile.max_units > 0;
+  int rc = launch_dependent(rows_kernel<D, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
+  if (rc == ATTN_OK && tiles) rc = tile_launch(p, a, sms, dev, st);
+  if (rc != ATTN_OK) return rc;
+  return launch_dependent(join_kernel<D, BF16>, dim3(plan.rows_grid), 32 * JOIN_WARPS, 0, st, p);
 }
 
 }  // namespace
@@ -625,14 +881,21 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
   p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   p.split = reinterpret_cast<Split*>(ws + plan.off_split);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
-  const bool bf16 = a.dtype == ATTN_BF16;
   p.timeout_us = host_timeout_us();
-  if (plan.rows) {
-    if (a.d == 64) rc = bf16 ? launch_rows<64, true>(p, plan, st, dev) : launch_rows<64, false>(p, plan, st, dev);
-    else rc = bf16 ? launch_rows<128, true>(p, plan, st, dev) : launch_rows<128, false>(p, plan, st, dev);
-    if (rc != ATTN_OK) return rc;
+  p.rows_grid = plan.rows_grid;
+  p.tile.T = plan.T;
+  p.tile.max_units = plan.max_units;
+  p.tile.sms = sms;
+  if (plan.max_units > 0) {
+    p.tile.queue = reinterpret_cast<TileQueue*>(ws + plan.off_queue);
+    p.tile.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);
+    p.tile.joins = reinterpret_cast<TileJoin*>(ws + plan.off_joins);
+    p.tile.part_ml = reinterpret_cast<float2*>(ws + plan.off_tile_ml);
+    p.tile.part_o = reinterpret_cast<float*>(ws + plan.off_tile_o);
   }
-  return plan.tiles ? tile_launch(p, a, ws + plan.off_tile, sms, dev, st) : ATTN_OK;
+  const bool bf16 = a.dtype == ATTN_BF16;
+  if (a.d == 64) return bf16 ? launch<64, true>(p, a, plan, sms, dev, st) : launch<64, false>(p, a, plan, sms, dev, st);
+  return bf16 ? launch<128, true>(p, a, plan, sms, dev, st) : launch<128, false>(p, a, plan, sms, dev, st);
 }
 
 }  // extern "C"

@@ -25,36 +25,15 @@
 namespace attn {
 namespace {
 
-constexpr int FLAG_SCRUB = 16;  // the key tile holds rows that no query row of the unit sees
-
-// Written by the plan.  Line coordinates count key tiles over all (unit, head) pairs in order, heads inside.
-struct TileQueue {
-  unsigned int next;    // next queue entry
-  int whole, runs;      // entries: whole (unit, head) pairs, then runs
-  int njoins;           // cut (unit, head) pairs
-  int units;
-  long long line0, line;  // where the runs' line begins, its length
-};
-struct TileUnit {
-  int b, blk;
-  int j0, w;      // key tiles j0 .. j0 + w - 1 (one where no key is seen: the unit still writes its rows)
-  long long cum;  // weights of the units before
-};
-struct TileJoin {
-  int unit, h;
-  int run, parts;  // slots 2 run + 1, 2 (run + 1), 2 (run + 2), ...
-};
+constexpr int FLAG_SCRUB = 16;  // the key tile holds rows that no query row of the request sees: those outside
+                                // [flags >> 8 & 255, flags >> 16 & 255)
+constexpr int FLAG_ALT = 32;    // both Q tiles hold the unit's one tile of rows and take its key tiles by turns
 
 struct TileParams : PagedParams {
   CUtensorMap tm_q, tm_k, tm_v;
-  int T;          // tokens of a Q tile
   int box_rows;   // rows of one K/V box
-  TileQueue* queue;
-  TileUnit* units;   // [max_units + 1], longest first
-  TileJoin* joins;   // [max runs]: every cut pair holds a run's beginning
-  float* part_o;     // [2 max runs][256][D]
-  float2* part_ml;   // [2 max runs][256]
-  int max_units;
+  int z_page, z_head, z_extent;  // the maps' page-and-head coordinate: page * z_page + h * z_head, below z_extent
+  unsigned int g_inverse;  // 65536 / g + 1: row / g = row * g_inverse >> 16 for rows below 128
   int inject;
 };
 
@@ -62,191 +41,44 @@ struct TileHdr {
   int j, flags;
   int row0, sq, sk;
   int h, blk, slot;
-  int lo, hi;  // keys that any row of the unit sees
-  int pad[2];
 };
-static_assert(sizeof(TileHdr) == 48, "descriptor slot size");
+static_assert(sizeof(TileHdr) == 32, "descriptor slot size");
 
 template <int D>
-using TileLayout = Layout<D, MASK_BAND, TileHdr>;
+using TileLayout = Layout<D, MASK_BAND, TileHdr, true>;
 
-// Tokens and keys of Q tiles [t0, t1) of block blk: false where it has no token.
-__device__ __forceinline__ bool tile_keys(const TileParams& p, int sq, int sk, int blk, int t0, int t1, int& lo, int& hi) {
-  const int i0 = (blk * QT + t0) * p.T, i1 = min((blk * QT + t1) * p.T, sq) - 1;
-  lo = hi = 0;
-  if (i0 > i1) return false;
-  const int a = row_lo(p, i0, sk - sq), e = row_hi(p, i1, sk - sq, sk);
-  if (e > a) lo = a, hi = e;
-  return true;
+// Keys that any query row of a request sees.
+__device__ __forceinline__ void request_keys(const TileParams& p, int sq, int sk, int& lo, int& hi) {
+  lo = row_lo(p, 0, sk - sq);
+  hi = row_hi(p, sq - 1, sk - sq, sk);
 }
 
-// First tile of run i out of n over a line, and the run that holds tile x of it.
-__device__ __forceinline__ long long run_begin(long long line, int n, int i) { return line * i / n; }
-__device__ __forceinline__ int run_of(long long line, int n, long long x) { return (int)(((x + 1) * n - 1) / line); }
-
-// ------------------------------------------------------------------ plan
-// One CTA.  Units (of one head) are numbered request by request, requests of the other path having none,
-// and sorted by weight into 32 classes, stably, so that equal inputs give equal cuts.  Bound by latency: two
-// passes over the lengths, one over the units for each of weigh, sort, sum.
-constexpr int PLAN_THREADS = 1024;
-constexpr int MIN_RUN = 4;   // tiles of a run at least
-constexpr int MAX_SPLIT = 3; // runs per SM at most
-
-// Exclusive sum over the block's threads of x, and the total.
-template <class T>
-__device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T incl = x;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, incl, s);
-    if (lane >= s) incl += y;
-  }
-  __syncthreads();  // warp_sum may still be read from the scan before
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    const T w = warp_sum[lane];
-    T y = w;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const T z = __shfl_up_sync(0xffffffffu, y, s);
-      if (lane >= s) y += z;
+// The lane's box of key tile j of request b: chunk of box_rows keys, its place in the cache (z: page and
+// head as one coordinate, row group in the page).  Boxes with no key of [lo, hi) lie past the last page and
+// read as zeros, as do those whose page is out of range.
+struct TileBox {
+  int chunk, z, group;
+  __device__ __forceinline__ TileBox(const TileParams& p, int b, int h, int j, int lo, int hi, int lane) {
+    chunk = lane * p.box_rows;
+    z = p.z_extent;
+    group = 0;
+    const int key = j * BN + chunk;
+    if (chunk < BN && key < hi && key + p.box_rows > lo) {
+      const int idx = key / p.page_size;
+      const int page = __ldg(p.table + (long long)b * p.table_stride + idx);
+      group = (key - idx * p.page_size) >> 3;
+      if ((unsigned)page < (unsigned)p.num_pages) z = page * p.z_page + h * p.z_head;
+      else atomicOr(p.status, STATUS_PAGE);
     }
-    warp_sum[lane] = y - w;
-    if (lane == 31) warp_sum[32] = y;
   }
-  __syncthreads();
-  total = warp_sum[32];
-  return warp_sum[warp] + incl - x;
-}
-
-__global__ void __launch_bounds__(PLAN_THREADS) tile_plan_kernel(const __grid_constant__ TileParams p, int sms) {
-  grid_launch_dependents();
-  extern __shared__ int pre[];  // units before each request, [B + 1]
-  __shared__ int sum_s[33], rank_s[32][33];
-  __shared__ long long sum64_s[33];
-  __shared__ int wmax_s, wmin_s, joins_s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit_tokens = QT * p.T;
-  const int per = (p.B + PLAN_THREADS - 1) / PLAN_THREADS;
-  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int own = 0, total;
-  for (int b = b0; b < b1; ++b) {
-    int row0, sq, sk;
-    request_span(p, b, row0, sq, sk);
-    pre[b] = own;
-    own += sq * p.g > ROWS_MAX ? (sq + unit_tokens - 1) / unit_tokens : 0;
-  }
-  if (tid == 0) wmax_s = joins_s = 0, wmin_s = INT_MAX;
-  rank_s[warp][lane] = 0;
-  if (lane == 0) rank_s[warp][32] = 0;
-  const int before = block_scan(own, sum_s, total);
-  for (int b = b0; b < b1; ++b) pre[b] += before;
-  if (tid == 0) pre[p.B] = total;
-  __syncthreads();
-  const int units = min(total, p.max_units);  // (more only where the row offsets overlap)
-  const auto unit_at = [&](int u) {
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    TileUnit x;
-    x.b = lo;
-    x.blk = u - pre[lo];
-    int row0, sq, sk, k0, k1;
-    request_span(p, x.b, row0, sq, sk);
-    tile_keys(p, sq, sk, x.blk, 0, QT, k0, k1);
-    x.j0 = k0 / BN;
-    x.w = max((k1 + BN - 1) / BN - x.j0, 1);
-    x.cum = 0;
-    return x;
-  };
-  // every warp takes a stretch of neighbouring units
-  const int stretch = (units + PLAN_THREADS - 1) / PLAN_THREADS * 32;
-  const int u0 = min(warp * stretch, units), u1 = min(u0 + stretch, units);
-  int wmax = 0, wmin = INT_MAX;
-  for (int u = u0 + lane; u < u1; u += 32) {
-    const int w = unit_at(u).w;
-    wmax = max(wmax, w);
-    wmin = min(wmin, w);
-  }
-  wmax = __reduce_max_sync(0xffffffffu, wmax);
-  wmin = __reduce_min_sync(0xffffffffu, wmin);
-  if (lane == 0) {
-    atomicMax(&wmax_s, wmax);
-    atomicMin(&wmin_s, wmin);
-  }
-  __syncthreads();
-  wmax = max(wmax_s, 1);
-  const auto class_of = [&](int w) { return 31 - (int)((long long)(w - 1) * 32 / wmax); };
-  for (int at = u0; at < u1; at += 32) {
-    const int c = at + lane < u1 ? class_of(unit_at(at + lane).w) : 32;  // (class 32: no unit)
-    const unsigned int same = __match_any_sync(0xffffffffu, c);
-    if (lane == __ffs(same) - 1) rank_s[warp][c] += __popc(same);
+  template <int D>
+  __device__ __forceinline__ void load(const TileParams& p, const CUtensorMap* map, uint32_t dst, uint32_t full, int lane) const {
+    if (lane == 0) mbar_expect_tx(full, BN * D * 2);
+    __syncwarp();
+    if (chunk < BN) tma_load_5d(dst + chunk * D * 2, map, full, 0, 0, 0, group, z);
     __syncwarp();
   }
-  __syncthreads();
-  {
-    // where each warp's units of each class go: classes outside, warps inside
-    const int c = tid >> 5, w = tid & 31;
-    const int x = rank_s[w][c];
-    const int at = block_scan(x, sum_s, total);
-    rank_s[w][c] = at;
-  }
-  __syncthreads();
-  for (int at = u0; at < u1; at += 32) {
-    TileUnit x = {};
-    int c = 32;
-    if (at + lane < u1) {
-      x = unit_at(at + lane);
-      c = class_of(x.w);
-    }
-    const unsigned int same = __match_any_sync(0xffffffffu, c);
-    const int to = rank_s[warp][c] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (lane == __ffs(same) - 1) rank_s[warp][c] += __popc(same);
-    __syncwarp();
-    if (c < 32) p.units[to] = x;
-  }
-  __syncthreads();
-  // weights before each unit, in the sorted order
-  const int chunk = (units + PLAN_THREADS - 1) / PLAN_THREADS;
-  const int s0 = min(tid * chunk, units), s1 = min(s0 + chunk, units);
-  long long weight = 0, all;
-  for (int s = s0; s < s1; ++s) weight += p.units[s].w;
-  long long cum = block_scan(weight, sum64_s, all);
-  for (int s = s0; s < s1; ++s) {
-    p.units[s].cum = cum;
-    cum += p.units[s].w;
-  }
-  if (tid == 0) p.units[units].cum = all;
-  __syncthreads();
-
-  // Whole pairs: full waves of the longest, where none is longer than an SM's share.
-  const long long pairs = (long long)units * p.Hkv, share = all * p.Hkv / sms;
-  const int whole = wmax <= share ? (int)(pairs / sms * sms) : 0;
-  const auto line_of = [&](long long x) {
-    const int s = (int)(x / p.Hkv);
-    return p.units[s].cum * p.Hkv + (s < units ? (x - (long long)s * p.Hkv) * p.units[s].w : 0);
-  };
-  const long long line0 = line_of(whole), line = all * p.Hkv - line0;
-  // Runs: one per SM; more where the whole pairs before them differ, so that the SMs that are done
-  // earlier take more.
-  const long long len = line / sms + 1;
-  const int split = whole ? (int)min((long long)MAX_SPLIT, 1 + 2ll * (wmax - wmin_s) / len) : 1;
-  const int runs = line ? (int)max(1ll, min((long long)split * sms, line / MIN_RUN)) : 0;
-  for (long long x = whole + tid; x < pairs; x += PLAN_THREADS) {
-    const int s = (int)(x / p.Hkv), h = (int)(x - (long long)s * p.Hkv);
-    const long long at = line_of(x) - line0;
-    const int first = run_of(line, runs, at), last = run_of(line, runs, at + p.units[s].w - 1);
-    if (first != last) p.joins[atomicAdd(&joins_s, 1)] = TileJoin{s, h, first, last - first + 1};
-  }
-  __syncthreads();
-  if (tid == 0) *p.queue = TileQueue{0u, whole, runs, joins_s, units, line0, line};
-}
+};
 
 // ------------------------------------------------------------------ load warp
 template <int D>
@@ -260,13 +92,21 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
   uint32_t kpar = 1, vpar = 1, ie_par = 1;
   uint32_t kpend = 0, kpend_par = 0, vpend = 0, vpend_par = 0;
   bool inject = p.inject != 0;
-  const int whole = p.queue->whole, runs = p.queue->runs;
-  // the lane's box of a key tile: chunk of box_rows keys, 64-column half
-  const int nbox = BN / p.box_rows * L::HALVES;
-  const int chunk = lane / L::HALVES, half = lane % L::HALVES;
+  const unsigned int whole = p.tile.queue->whole, entries = whole + p.tile.queue->runs;
 
-  unsigned int q_next = 0;
-  if (lane == 0) q_next = atomicAdd(&p.queue->next, 1u);
+  // The first entry is the CTA's own number, later ones come from the queue, one ahead and no more (an SM
+  // that held two would leave another without).  While a unit's first tiles load, the next entry and,
+  // where it is a whole pair, its unit arrive.
+  unsigned int x_next = blockIdx.x, raw = 0;
+  TileUnit u_next = {};
+  if (x_next < whole) u_next = p.tile.units[x_next / p.Hkv];
+  bool asked = false;  // raw is on its way
+  const auto fetch = [&] {
+    if (!asked) return;
+    x_next = __shfl_sync(0xffffffffu, raw, 0);
+    if (x_next < whole) u_next = p.tile.units[x_next / p.Hkv];
+    asked = false;
+  };
   int s = 0, h = 0, run = 0;  // unit (in the plan's order), head; run being worked off
   long long left = 0;         // tiles of the run that are left
   for (int k = 0;; ++k) {
@@ -278,13 +118,13 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
         h = 0;
         ++s;
       }
-      pt = p.units[s];
+      pt = p.tile.units[s];
       tiles = (int)min((long long)pt.w, left);
       left -= tiles;
       if (tiles < pt.w) slot = 2 * run + 1;
     } else {
-      const unsigned int x = __shfl_sync(0xffffffffu, q_next, 0);
-      if (x >= (unsigned int)(whole + runs)) {
+      const unsigned int x = x_next;
+      if (x >= entries) {
         if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
         if (lane == 0) {
           hdr[ie].j = -1;
@@ -294,27 +134,28 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
         __syncwarp();
         break;
       }
-      if (lane == 0) q_next = atomicAdd(&p.queue->next, 1u);
-      if (x < (unsigned int)whole) {
-        s = (int)(x / p.Hkv);
+      pt = u_next;
+      if (lane == 0) raw = atomicAdd(&p.tile.queue->next, 1u);
+      asked = true;
+      if (x < whole) {
         h = (int)(x % p.Hkv);
-        pt = p.units[s];
         tiles = pt.w;
       } else {
-        run = (int)x - whole;
-        const long long line = p.queue->line, at = run_begin(line, runs, run);
+        run = (int)(x - whole);
+        const int runs = (int)(entries - whole);
+        const long long line = p.tile.queue->line, at = run_begin(line, runs, run);
         left = run_begin(line, runs, run + 1) - at;
-        const long long pos = p.queue->line0 + at;
+        const long long pos = p.tile.queue->line0 + at;
         // the last unit whose pairs begin at or before pos, 32 probes at a time
-        int lo = whole / p.Hkv, hi = p.queue->units;
+        int lo = (int)whole / p.Hkv, hi = p.tile.queue->units;
         while (hi - lo > 1) {
           const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
-          const unsigned int yes = __ballot_sync(0xffffffffu, probe < hi && p.units[probe].cum * p.Hkv <= pos);
+          const unsigned int yes = __ballot_sync(0xffffffffu, probe < hi && p.tile.units[probe].cum * p.Hkv <= pos);
           lo += (31 - __clz(yes)) * step;  // (lane 0 always says yes)
           hi = min(hi, lo + step);
         }
         s = lo;
-        pt = p.units[s];
+        pt = p.tile.units[s];
         const long long in = pos - pt.cum * p.Hkv;
         h = (int)(in / pt.w);
         from = (int)(in - (long long)h * pt.w);
@@ -324,8 +165,8 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
       }
     }
     const int j0 = pt.j0 + from, j1 = j0 + tiles;
-    int row0, sq, sk, lo, hi;
-    request_span(p, pt.b, row0, sq, sk);
+    const int row0 = pt.row0, sq = pt.sq, sk = pt.sk;
+    int lo, hi;
     tile_keys(p, sq, sk, pt.blk, 0, QT, lo, hi);
     int jlo[QT], jhi[QT];  // key tiles of each Q tile, [jlo, jhi)
     bool rows1 = false;
@@ -337,8 +178,12 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
       jlo[t] = a / BN;
       jhi[t] = (e + BN - 1) / BN;
     }
-    const int tok0 = pt.blk * QT * p.T;
-    const int* table = p.table + (long long)pt.b * p.table_stride;
+    // One tile of rows only: both Q tiles take it and its key tiles by turns, so that one's products
+    // run while the other's softmax does.
+    const bool alt = !rows1 && tiles > 1;
+    int scrub_lo, scrub_hi;
+    request_keys(p, sq, sk, scrub_lo, scrub_hi);
+    const int tok0 = pt.blk * QT * p.tile.T;
 
     const int qbuf = k % L::QBUF;
     if (!bwait_warp(bars + 8u * (L::B_QEMPTY + qbuf), (q_empty_par >> qbuf) & 1u, abort_flag, to)) goto drain;
@@ -346,14 +191,14 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
     if (!inject) {
       if (lane == 0) {
         const uint32_t fb = bars + 8u * (L::B_QFULL + qbuf);
-        mbar_expect_tx(fb, (uint32_t)((rows1 ? 2 : 1) * p.T * p.g * D * 2));
+        mbar_expect_tx(fb, (uint32_t)((rows1 || alt ? 2 : 1) * p.tile.T * p.g * D * 2));
 #pragma unroll
         for (int t = 0; t < QT; ++t)
 #pragma unroll
           for (int hh = 0; hh < L::HALVES; ++hh)
-            if (t == 0 || rows1)
-              tma_load_4d(base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES + hh * BM * 128, &p.tm_q, fb, hh * 64, 0,
-                          row0 + tok0 + t * p.T, h);
+            if (t == 0 || rows1 || alt)
+              tma_load_5d(base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES + hh * BM * 128, &p.tm_q, fb, hh * 64, 0,
+                          row0 + tok0 + (alt ? 0 : t * p.tile.T), h, 0);
       }
       q_pend |= 1u << qbuf;
       q_pend_par = (q_pend_par & ~(1u << qbuf)) | ((((q_empty_par >> qbuf) & 1u)) << qbuf);
@@ -369,65 +214,41 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
       hdr[ie].h = h;
       hdr[ie].blk = pt.blk;
       hdr[ie].slot = slot;
-      hdr[ie].lo = lo;
-      hdr[ie].hi = hi;
       mbar_arrive(bars + 8u * (L::B_IFULL + ie));
     };
-    // page and row of the lane's box of key tile j; the page past the last one where no row sees its keys
-    const auto place = [&](int j, int& page, int& row) {
-      const int key = j * BN + chunk * p.box_rows;
-      page = p.num_pages;
-      row = 0;
-      if (lane < nbox && key < hi && key + p.box_rows > lo) {
-        const int idx = key / p.page_size;
-        row = key - idx * p.page_size;
-        page = __ldg(table + idx);
-        if ((unsigned)page >= (unsigned)p.num_pages) {
-          atomicOr(p.status, STATUS_PAGE);
-          page = p.num_pages;
-        }
-      }
-    };
-    int page, row, page_next = 0, row_next = 0;
-    place(j0, page_next, row_next);
     for (int j = j0; j < j1; ++j) {
-      page = page_next;
-      row = row_next;
-      if (j + 1 < j1) place(j + 1, page_next, row_next);  // the table's latency passes behind this tile's loads
-      const bool a0 = j >= jlo[0] && j < jhi[0], a1 = j >= jlo[1] && j < jhi[1];
+      bool a0 = j >= jlo[0] && j < jhi[0], a1 = j >= jlo[1] && j < jhi[1];
       if (!a0 && !a1) continue;
+      if (alt) {
+        a1 = (j - j0) & 1;
+        a0 = !a1;
+      }
+      const TileBox box(p, pt.b, h, j, lo, hi, lane);  // looked up while the slots are still taken
       if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
-      if (lane == 0) describe(j, (a0 ? 1 : 0) | (a1 ? 2 : 0) | (lo > j * BN || hi < (j + 1) * BN ? FLAG_SCRUB : 0));
+      if (lane == 0) {
+        int flags = (a0 ? 1 : 0) | (a1 ? 2 : 0) | (alt ? FLAG_ALT : 0);
+        const int r0 = max(scrub_lo - j * BN, 0), r1 = min(scrub_hi - j * BN, BN);
+        if (r0 > 0 || r1 < BN) flags |= FLAG_SCRUB | r0 << 8 | r1 << 16;
+        describe(j, flags);
+      }
       __syncwarp();
       if (++ie == NINFO) { ie = 0; ie_par ^= 1u; }
 
       if (!bwait_warp(bars + 8u * (L::B_KEMPTY + kslot), kpar, abort_flag, to)) goto drain;
-      {
-        const uint32_t fb = bars + 8u * (L::B_KFULL + kslot);
-        if (lane == 0) mbar_expect_tx(fb, L::KV_TILE_BYTES);
-        __syncwarp();
-        if (lane < nbox)
-          tma_load_4d(base + L::OFF_K + kslot * L::KV_TILE_BYTES + half * BN * 128 + chunk * p.box_rows * 128, &p.tm_k, fb, half * 64, row, h,
-                      page);
-      }
+      box.load<D>(p, &p.tm_k, base + L::OFF_K + kslot * L::KV_TILE_BYTES, bars + 8u * (L::B_KFULL + kslot), lane);
       kpend |= 1u << kslot;
       kpend_par = (kpend_par & ~(1u << kslot)) | ((kpar ^ 1u) << kslot);
       if (++kslot == L::KSLOT) { kslot = 0; kpar ^= 1u; }
       if (!bwait_warp(bars + 8u * (L::B_VEMPTY + vslot), vpar, abort_flag, to)) goto drain;
-      {
-        const uint32_t fb = bars + 8u * (L::B_VFULL + vslot);
-        if (lane == 0) mbar_expect_tx(fb, L::KV_TILE_BYTES);
-        __syncwarp();
-        if (lane < nbox)
-          tma_load_4d(base + L::OFF_V + vslot * L::KV_TILE_BYTES + half * BN * 128 + chunk * p.box_rows * 128, &p.tm_v, fb, half * 64, row, h,
-                      page);
-      }
+      box.load<D>(p, &p.tm_v, base + L::OFF_V + vslot * L::KV_TILE_BYTES, bars + 8u * (L::B_VFULL + vslot), lane);
       vpend |= 1u << vslot;
       vpend_par = (vpend_par & ~(1u << vslot)) | ((vpar ^ 1u) << vslot);
       if (++vslot == L::VSLOT) { vslot = 0; vpar ^= 1u; }
+      if (j > j0) fetch();
     }
+    fetch();
     if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
-    if (lane == 0) describe(-1, FLAG_END);
+    if (lane == 0) describe(-1, FLAG_END | (alt ? FLAG_ALT : 0));
     __syncwarp();
     if (++ie == NINFO) { ie = 0; ie_par ^= 1u; }
   }
@@ -447,25 +268,22 @@ drain:
 }
 
 // What the MMA warp does beside its multiplications: it zeroes the rows of a V tile that no query row
-// of the unit sees (past the last key, ahead of the window), which may hold anything; their weights are 0,
-// and 0 * NaN would not be.
+// of the request sees (past the last key, ahead of the window), which may hold anything; their weights are
+// 0, and 0 * NaN would not be.
 template <int D>
 struct TileEnv {
-  static constexpr bool SCRUB = true;
-  int lo = 0, hi = 0;
-  __device__ __forceinline__ void unit(volatile TileHdr& h) {
-    lo = h.lo;
-    hi = h.hi;
-  }
+  static constexpr bool SCRUB = true, ALTERNATE = true;
+  static __device__ __forceinline__ bool alternate(int flags) { return flags & FLAG_ALT; }
+  __device__ __forceinline__ void unit(volatile TileHdr&) {}
   __device__ __forceinline__ void computed(int, int, int) {}
-  __device__ __forceinline__ void scrub(int flags, int j, uint8_t* v, int lane) {
+  __device__ __forceinline__ void scrub(int flags, uint8_t* v, int lane) {
     if (!(flags & FLAG_SCRUB)) return;
-    const int r0 = lo - j * BN, r1 = hi - j * BN;
+    const int r0 = flags >> 8 & 255, r1 = flags >> 16 & 255;
     for (int r = lane >> 3; r < BN; r += 4) {
       if (r >= r0 && r < r1) continue;
 #pragma unroll
       for (int hh = 0; hh < D / 64; ++hh)
-        *reinterpret_cast<uint4*>(v + hh * BN * 128 + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(v + (r >> 3) * TileLayout<D>::KV_SBO + hh * 1024 + (r & 7) * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -485,10 +303,18 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
   const uint32_t o_addr = tmem + lane_off + L::O_COL + t * L::O_STRIDE;
   const float c = p.scale_log2;
   // packed row -> token of the tile, head of the group; rows past T g stand in for the last one
-  const int rr = min(r, p.T * p.g - 1), my_tok = rr / p.g;
+  const auto token_of = [&](int row) { return (int)(row * p.g_inverse >> 16); };
 
   uint32_t s_par = 0, o_par = 0, ie_par = 0;
   int ie = 0, nq = 0, np = 0;
+  // both softmax warpgroups: what either wrote before is seen by the other after
+  const auto meet = [&](bool second) -> bool {
+    tc_fence_before();
+    mbar_arrive(bars + 8u * L::B_XCHG);
+    if (!bwait_warp(bars + 8u * L::B_XCHG, (uint32_t)second, abort_flag, to)) return false;
+    tc_fence_after();
+    return true;
+  };
 
   for (int k = 0;; ++k) {
     if (!bwait_warp(bars + 8u * (L::B_IFULL + ie), ie_par, abort_flag, to)) return;
@@ -496,11 +322,15 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       mbar_arrive(bars + 8u * (L::B_IEMPTY + ie));
       break;
     }
-    const int row0 = hdr[ie].row0, sq = hdr[ie].sq, h = hdr[ie].h, slot_out = hdr[ie].slot;
-    const int tok0 = (hdr[ie].blk * QT + t) * p.T;  // the tile's first token
-    const int sk = hdr[ie].sk;
-    const int i = min(tok0 + my_tok, sq - 1);
-    const int klo = row_lo(p, i, sk - sq), khi = row_hi(p, i, sk - sq, sk);
+    const auto first_token = [&](int e) { return (hdr[e].blk * QT + (hdr[e].flags & FLAG_ALT ? 0 : t)) * p.tile.T; };
+    int klo, khi;
+    {
+      const int sq = hdr[ie].sq, sk = hdr[ie].sk, i = min(first_token(ie) + token_of(min(r, p.tile.T * p.g - 1)), sq - 1);
+      klo = row_lo(p, i, sk - sq);
+      khi = row_hi(p, i, sk - sq, sk);
+    }
+    int row0 = 0, sq = 0, h = 0, slot_out = 0, tok0 = 0;  // the unit's place, read at its end
+    bool alt = false;
     float m = -INFINITY, l = 0.f;
     int nact = 0;
 
@@ -510,6 +340,14 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       const int flags = hdr[ie].flags;
       const bool end = (flags & FLAG_END) != 0;
       const bool act = !end && ((flags >> t) & 1);
+      if (end) {
+        row0 = hdr[ie].row0;
+        sq = hdr[ie].sq;
+        h = hdr[ie].h;
+        slot_out = hdr[ie].slot;
+        tok0 = first_token(ie);
+        alt = flags & FLAG_ALT;
+      }
       mbar_arrive(bars + 8u * (L::B_IEMPTY + ie));
       if (++ie == NINFO) { ie = 0; ie_par ^= 1u; }
       if (end) break;
@@ -551,11 +389,60 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       o_par ^= 1u;
       tc_fence_after();
     }
-    const int rows = min(p.T, sq - tok0) * p.g;  // of this tile (may be <= 0)
+    const int rows = min(p.tile.T, sq - tok0) * p.g;  // of this tile (may be <= 0)
     const bool row_ok = r < rows;
+    const int my_tok = token_of(r);
+    const long long part = (long long)slot_out * UNIT_ROWS + (alt ? 0 : t * BM) + r;
+    if (alt) {
+      // Both Q tiles hold results of the same rows: they exchange m and l through shared memory (d = 128:
+      // the staging area, d = 64: the Q buffer, whose reads are over), then each warpgroup joins and
+      // writes half of the columns, reading both accumulators.  They meet before the exchange is read
+      // and again before either goes on to the next unit.
+      constexpr int XCH = L::STAGE_O ? L::OFF_Q : L::OFF_STAGE, XCH_T = L::STAGE_O ? L::Q_TILE_BYTES : 4 * 32 * 128;
+      uint8_t* xch = gbase + XCH + (L::STAGE_O ? (k % L::QBUF) * L::Q_BUF_BYTES : 0);
+      reinterpret_cast<float2*>(xch + t * XCH_T)[r] = make_float2(m, l);
+      if (!meet(false)) return;
+      const float2 other = reinterpret_cast<const float2*>(xch + (1 - t) * XCH_T)[r];
+      const float mm = fmaxf(m, other.x);
+      const float f_own = m == -INFINITY ? 0.f : ex2_approx(m - mm), f_other = other.x == -INFINITY ? 0.f : ex2_approx(other.x - mm);
+      const float ll = l * f_own + other.y * f_other;
+      const float inv = slot_out >= 0 ? 1.f : ll > 0.f ? 1.f / ll : 0.f;
+      const float fa = (t ? f_other : f_own) * inv, fb = (t ? f_own : f_other) * inv;
+      const uint32_t both = tmem + lane_off + L::O_COL + t * (D / 2);
+      const int head = h * p.g + r - my_tok * p.g;
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t oa[16], ob[16];
+        tmem_ld32x32b_x16_wait(both + ch * 16, oa);
+        tmem_ld32x32b_x16_wait(both + L::O_STRIDE + ch * 16, ob);
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = fmaf(fa, __uint_as_float(oa[e]), fb * __uint_as_float(ob[e]));
+        const int col = t * (D / 2) + ch * 16;
+        if (row_ok && slot_out >= 0) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(p.tile.part_o + part * D + col + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else if (row_ok) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + (long long)(row0 + tok0 + my_tok) * p.o_row + (long long)head * p.o_head + col);
+          dst[0] = make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+          dst[1] = make_uint4(pack2<BF16>(x[8], x[9]), pack2<BF16>(x[10], x[11]), pack2<BF16>(x[12], x[13]), pack2<BF16>(x[14], x[15]));
+        }
+        __syncwarp();
+      }
+      if (t == 0 && row_ok) {
+        if (slot_out >= 0) p.tile.part_ml[part] = make_float2(mm, ll);
+        else if (p.lse) p.lse[(long long)head * p.total_q + row0 + tok0 + my_tok] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
+      }
+      if (!meet(true)) return;
+      if constexpr (L::STAGE_O) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8u * (L::B_QEMPTY + (k % L::QBUF)));
+      }
+      continue;
+    }
     if (slot_out >= 0) {
-      const long long at = (long long)slot_out * UNIT_ROWS + t * BM + r;
-      float* dst = p.part_o + at * D;
+      float* dst = p.tile.part_o + part * D;
 #pragma unroll
       for (int ch = 0; ch < D / 16; ++ch) {
         uint32_t ob[16];
@@ -571,7 +458,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
             *reinterpret_cast<uint4*>(dst + ch * 16 + x * 4) = make_uint4(ob[4 * x], ob[4 * x + 1], ob[4 * x + 2], ob[4 * x + 3]);
         }
       }
-      if (row_ok) p.part_ml[at] = make_float2(m, l);
+      if (row_ok) p.tile.part_ml[part] = make_float2(m, l);
       if (L::STAGE_O && lane == 0) mbar_arrive(bars + 8u * (L::B_QEMPTY + (k % L::QBUF)));
       continue;
     }
@@ -612,7 +499,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
         const int q = kk * 4 + lane / 8, cc = lane % 8, row = quarter * 32 + q;
         if (row < rows) {
           const uint4 val = staged ? *reinterpret_cast<const uint4*>(stage + q * 128 + ((cc ^ (q & 7)) * 16)) : make_uint4(0u, 0u, 0u, 0u);
-          const int tok = row / p.g, head = h * p.g + row - tok * p.g;
+          const int tok = token_of(row), head = h * p.g + row - tok * p.g;
           *reinterpret_cast<uint4*>(p.o + (long long)(row0 + tok0 + tok) * p.o_row + (long long)head * p.o_head + hh * 64 + cc * 8) = val;
         }
       }
@@ -660,6 +547,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_launch_dependents();
   grid_dependency_wait();  // the plan
 
   if (warp < 4) {
@@ -683,70 +571,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
   }
 }
 
-// ------------------------------------------------------------------ join
-// One warp per row of a cut unit: out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k.  Memory-bound (the parts
-// were just written and are largely in L2).
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) tile_join_kernel(const __grid_constant__ TileParams p) {
-  constexpr int E = D / 32;
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int rows = p.queue->njoins * UNIT_ROWS, nwarps = gridDim.x * 8;
-  for (int x = blockIdx.x * 8 + (threadIdx.x >> 5); x < rows; x += nwarps) {
-    const int row = x % UNIT_ROWS, rest = x / UNIT_ROWS;
-    const TileJoin jn = p.joins[rest];
-    const TileUnit un = p.units[jn.unit];
-    const int h = jn.h, t = row / BM, r = row % BM;
-    int row0, sq, sk;
-    request_span(p, un.b, row0, sq, sk);
-    const int tok0 = (un.blk * QT + t) * p.T;
-    if (r >= min(p.T, sq - tok0) * p.g) continue;
-    float m = -INFINITY, l = 0.f, acc[E] = {};
-    for (int k = 0; k < jn.parts; ++k) {
-      const long long at = (long long)(k == 0 ? 2 * jn.run + 1 : 2 * (jn.run + k)) * UNIT_ROWS + row;
-      const float2 ml = p.part_ml[at];
-      const float* src = p.part_o + at * D + lane * E;
-      float v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = src[e];
-      const float mn = fmaxf(m, ml.x);
-      const float fa = m == -INFINITY ? 0.f : ex2_approx(m - mn), fb = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
-      l = l * fa + ml.y * fb;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * fa + v[e] * fb;
-      m = mn;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int tok = r / p.g, head = h * p.g + r - tok * p.g;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (long long)(row0 + tok0 + tok) * p.o_row + (long long)head * p.o_head + lane * E);
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[(long long)head * p.total_q + row0 + tok0 + tok] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
-  }
-}
-
 // ------------------------------------------------------------------ host side
-struct TilePlan {
-  int T, max_units, max_runs;
-  size_t off_units, off_joins, off_ml, off_o, bytes;
-  TilePlan(const attn_fwd_paged_params_t& a, int sms) {
-    const int g = a.Hq / a.Hkv;
-    T = BM / g;
-    const int longest = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
-    // units of a head: every request's tokens over 2 T, rounded up
-    const long long by_rows = (long long)a.total_q / (QT * T) + a.B;
-    const long long by_len = (long long)a.B * ((longest + QT * T - 1) / (QT * T));
-    max_units = (int)(by_rows < by_len ? by_rows : by_len);  // by_rows <= total_q / 2 + B
-    max_runs = MAX_SPLIT * sms;
-    const size_t slots = 2 * (size_t)max_runs;
-    off_units = 256;
-    off_joins = off_units + round256((size_t)(max_units + 1) * sizeof(TileUnit));
-    off_ml = off_joins + round256((size_t)max_runs * sizeof(TileJoin));
-    off_o = off_ml + round256(slots * UNIT_ROWS * sizeof(float2));
-    bytes = off_o + round256(slots * UNIT_ROWS * a.d * sizeof(float));
-  }
-};
-
 template <int D, bool BF16>
 int launch_tiles(const TileParams& p, int sms, int dev, cudaStream_t st) {
   using L = TileLayout<D>;
@@ -754,61 +579,40 @@ int launch_tiles(const TileParams& p, int sms, int dev, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_set{0};  // bit per device
   const unsigned long long bit = 1ull << dev;
   if (!(attr_set.load() & bit)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_ALLOC) != cudaSuccess ||
-        cudaFuncSetAttribute(tile_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 66 * 1024) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_ALLOC) != cudaSuccess)
       return ATTN_ERR_CUDA;
     attr_set.fetch_or(bit);
   }
-  tile_plan_kernel<<<1, PLAN_THREADS, ((size_t)p.B + 1) * sizeof(int), st>>>(p, sms);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms);
-  cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = L::SMEM_ALLOC;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return ATTN_ERR_CUDA;
-  cfg.gridDim = dim3(4 * sms);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, tile_join_kernel<D, BF16>, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_dependent(kern, dim3(sms), NTHREADS, L::SMEM_ALLOC, st, p);
 }
 
 }  // namespace
 
-size_t tile_workspace(const attn_fwd_paged_params_t& a, int sms) { return TilePlan(a, sms).bytes; }
-
-int tile_launch(const PagedParams& base, const attn_fwd_paged_params_t& a, void* workspace, int sms, int dev, cudaStream_t st) {
-  const TilePlan plan(a, sms);
+int tile_launch(const PagedParams& base, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
   TileParams p = {};
   static_cast<PagedParams&>(p) = base;
   const bool bf16 = a.dtype == ATTN_BF16;
-  p.T = plan.T;
   p.box_rows = 128;
   while (a.page_size % p.box_rows != 0) p.box_rows /= 2;
   // (the stride of a dimension of one entry is of no account: any valid one does)
   const auto stride = [&](long long s, int n) { return n > 1 ? s * 2 : (long long)a.d * 2; };
-  const Map4 q{{a.d, p.g, a.total_q, a.Hkv},
-               {stride(a.q_head_stride, p.g), stride(a.q_row_stride, a.total_q), stride(a.q_head_stride * p.g, a.Hkv)},
-               {64, p.g, p.T, 1}};
-  const Map4 kv{{a.d, a.page_size, a.Hkv, a.num_pages},
-                {a.cache_row_stride * 2, stride(a.cache_head_stride, a.Hkv), stride(a.cache_page_stride, a.num_pages)},
-                {64, p.box_rows, 1, 1}};
+  const Map5 q{{a.d, p.g, a.total_q, a.Hkv, 1},
+               {stride(a.q_head_stride, p.g), stride(a.q_row_stride, a.total_q), stride(a.q_head_stride * p.g, a.Hkv), a.d * 2ll},
+               {64, p.g, p.tile.T, 1, 1}};
+  // 64 columns, 8 rows, halves, groups of 8 rows, and page and head in the smaller of their strides
+  const long long sp = a.num_pages > 1 ? a.cache_page_stride : 0, sh = a.Hkv > 1 ? a.cache_head_stride : 0;
+  const long long unit = sp && sh ? (sp < sh ? sp : sh) : sp + sh;
+  p.z_page = unit ? (int)(sp / unit) : 0;
+  p.z_head = unit ? (int)(sh / unit) : 0;
+  p.z_extent = (a.num_pages - 1) * p.z_page + (a.Hkv - 1) * p.z_head + 1;
+  const Map5 kv{{64, 8, a.d / 64, a.page_size / 8, p.z_extent},
+                {a.cache_row_stride * 2, 128, a.cache_row_stride * 16, unit ? unit * 2 : a.d * 2ll},
+                {64, 8, a.d / 64, p.box_rows / 8, 1}};
   int rc;
-  if ((rc = host_map4(&p.tm_q, a.q, bf16, q)) != ATTN_OK || (rc = host_map4(&p.tm_k, a.k_cache, bf16, kv)) != ATTN_OK ||
-      (rc = host_map4(&p.tm_v, a.v_cache, bf16, kv)) != ATTN_OK)
+  if ((rc = host_map5(&p.tm_q, a.q, bf16, q)) != ATTN_OK || (rc = host_map5(&p.tm_k, a.k_cache, bf16, kv)) != ATTN_OK ||
+      (rc = host_map5(&p.tm_v, a.v_cache, bf16, kv)) != ATTN_OK)
     return rc;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.queue = reinterpret_cast<TileQueue*>(ws);
-  p.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);
-  p.joins = reinterpret_cast<TileJoin*>(ws + plan.off_joins);
-  p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
-  p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
-  p.max_units = plan.max_units;
+  p.g_inverse = 65536u / p.g + 1;
   p.inject = host_take_inject();
   if (a.d == 64) return bf16 ? launch_tiles<64, true>(p, sms, dev, st) : launch_tiles<64, false>(p, sms, dev, st);
   return bf16 ? launch_tiles<128, true>(p, sms, dev, st) : launch_tiles<128, false>(p, sms, dev, st);

@@ -36,9 +36,13 @@ struct InfoHdr {
 };
 static_assert(sizeof(InfoHdr) == 32, "descriptor slot size");
 
-template <int D, int MODE, class HDR = InfoHdr>
+// GROUPED: the 64-column halves of K / V rows stand side by side for every 8 rows (128-byte swizzle
+// atoms of 1024 bytes) instead of one half-tile behind the other, so that one TMA box brings both.
+template <int D, int MODE, class HDR = InfoHdr, bool GROUPED = false>
 struct Layout {
   using Hdr = HDR;
+  static constexpr int KV_HALF = GROUPED ? 1024 : BN * 128;  // from a half to the next
+  static constexpr int KV_SBO = GROUPED ? 1024 * (D / 64) : 1024;  // from 8 rows to the next 8
   static_assert(D == 64 || D == 128, "head dim");
   static constexpr int HALVES = D / 64;                  // 128-byte swizzle spans per row
   static constexpr int Q_TILE_BYTES = BM * D * 2;
@@ -92,7 +96,7 @@ struct Layout {
                        B_IEMPTY = B_IFULL + NINFO,
                        B_STILE = B_IEMPTY + NINFO, B_PREADY = B_STILE + S_SLOTS,
                        B_ODONE = B_PREADY + QT, B_OPV = B_ODONE + QT, B_DRAIN = B_OPV + QT,
-                       NBAR = B_DRAIN + 1;
+                       B_XCHG = B_DRAIN + 1, NBAR = B_XCHG + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM_ALLOC = BYTES + 1024;  // slack for 1024-byte alignment
@@ -152,9 +156,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// Initialises the barriers of a layout (one thread).
+// Initialises the barriers of a layout (one thread).  `readers`: threads that read the tile descriptors
+// beside the MMA warp's one and the softmax threads.
 template <class L>
-__device__ __forceinline__ void init_barriers(uint32_t bars) {
+__device__ __forceinline__ void init_barriers(uint32_t bars, int readers = 0) {
   for (int qb2 = 0; qb2 < L::QBUF; ++qb2) {
     mbar_init(bars + 8u * (L::B_QFULL + qb2), 1);
     mbar_init(bars + 8u * (L::B_QEMPTY + qb2), L::QEMPTY_COUNT);
@@ -169,7 +174,7 @@ __device__ __forceinline__ void init_barriers(uint32_t bars) {
   }
   for (int e = 0; e < NINFO; ++e) {
     mbar_init(bars + 8u * (L::B_IFULL + e), 1);                 // load-warp lane 0
-    mbar_init(bars + 8u * (L::B_IEMPTY + e), 1 + QT * BM);      // MMA thread + softmax threads
+    mbar_init(bars + 8u * (L::B_IEMPTY + e), 1 + QT * BM + readers);  // MMA thread + softmax threads
   }
   for (int sl = 0; sl < L::S_SLOTS; ++sl) mbar_init(bars + 8u * (L::B_STILE + sl), 1);
   for (int t = 0; t < QT; ++t) {
@@ -178,6 +183,7 @@ __device__ __forceinline__ void init_barriers(uint32_t bars) {
     mbar_init(bars + 8u * (L::B_OPV + t), 1);
   }
   mbar_init(bars + 8u * L::B_DRAIN, 1);
+  mbar_init(bars + 8u * L::B_XCHG, QT * BM);
 }
 
 // ------------------------------------------------------------------ MMA issuer (warp 1)
@@ -195,8 +201,8 @@ __device__ __forceinline__ void init_barriers(uint32_t bars) {
 //             OPV(t), which the softmax waits for before it rescales O_t.
 // Each ring slot of K / V is released by a commit right after its last reader.
 // `env` is what differs between the kernels: env.unit(descriptor) at a unit's start, env.computed(t, j,
-// lane) for every (Q tile, key tile) block, and, where Env::SCRUB, env.scrub(descriptor flags, j, V
-// tile, lane) once V(j) has landed and before any P.V reads it.
+// lane) for every (Q tile, key tile) block, where Env::ALTERNATE Env::alternate(flags) (see below), and, where
+// Env::SCRUB, env.scrub(flags, V tile, lane) once V(j) has landed and before any P.V reads it.
 template <int D, bool BF16, class L, class Env>
 __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, uint8_t* gbase,
                                          volatile int* abort_flag, uint32_t tmem, int lane) {
@@ -225,7 +231,7 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
     tc_fence_after();
 
     bool have_prev = false, pv0 = false, pv1 = false;
-    int prev_flags = 0, prev_vslot = 0, prev_j = 0;
+    int prev_flags = 0, prev_vslot = 0;
     uint32_t prev_vpar = 0;
     while (true) {
       if (!bwait_warp(bars + 8u * (L::B_IFULL + ie), ie_par, abort_flag, to)) goto drain;
@@ -244,90 +250,96 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
       if (have_prev) {
         if (!bwait_warp(bars + 8u * (L::B_VFULL + prev_vslot), prev_vpar, abort_flag, to)) goto drain;
         tc_fence_after();
-        if constexpr (Env::SCRUB) env.scrub(prev_flags, prev_j, gbase + L::OFF_V + prev_vslot * L::KV_TILE_BYTES, lane);
+        if constexpr (Env::SCRUB) env.scrub(prev_flags, gbase + L::OFF_V + prev_vslot * L::KV_TILE_BYTES, lane);
       }
       bool k_ready = false;
+      int new_slot0 = 0, new_slot1 = 1;
 
+      // d = 64 issues a Q tile's Q.K^T before its P.V, d = 128 its P.V first.  Where key tiles go to the
+      // two Q tiles by turns (Env::alternate), Q tile 1's Q.K^T comes before all, so that it does not
+      // wait for Q tile 0's P of the key tile before (the other way round the order has it so already).
 #pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        int& pslot = t ? pslot1 : pslot0;
-        int new_slot = t;
-#pragma unroll
-        for (int step = 0; step < 2; ++step) {
-          // d = 64 issues this tile's Q.K^T first, d = 128 its P.V first
-          if ((step == 0) == L::RING) {
-            if (!end && ((flags >> t) & 1)) {
-              if (!k_ready) {
-                if (!bwait_warp(bars + 8u * (L::B_KFULL + cur_kslot), cur_kpar, abort_flag, to)) goto drain;
-                tc_fence_after();
-                k_ready = true;
-              }
-              if constexpr (L::RING) {
-                new_slot = nqk;
-                nqk = nqk == L::S_SLOTS - 1 ? 0 : nqk + 1;
-              }
-              const uint32_t s_col = tmem + new_slot * 128;
-              const uint32_t qbase = base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES;
-              const uint32_t kbase = base + L::OFF_K + cur_kslot * L::KV_TILE_BYTES;
-              // Q and K as K-major operands: 16 elements (32 bytes) per step inside a
-              // 128-byte swizzle row, the next 64 elements one half-tile further.
-              if constexpr (D == 64) {
-                // d = 64 issues twice the instructions per flop: the descriptors are built
-                // once and stepped through their start-address field (address >> 4 in the
-                // low 14 bits; every offset here keeps it below 2^14)
-                const uint64_t qd = sdesc_sw128(qbase, 16, 1024), kd = sdesc_sw128(kbase, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-                  mma_ss_elect(s_col, qd + off, kd + off, ID_QK, kk > 0 ? 1u : 0u);
-                }
-              } else {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
-                  mma_ss_elect(s_col, sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + off, 16, 1024),
-                               ID_QK, kk > 0 ? 1u : 0u);
-                }
-              }
-              tc_commit_elect(bars + 8u * (L::B_STILE + new_slot));
-              env.computed(t, j, lane);
-              __syncwarp();
-            }
-          } else {
-            if (have_prev && ((prev_flags >> t) & 1)) {
-              uint32_t& pp = t ? p_par1 : p_par0;
-              if (!bwait_warp(bars + 8u * (L::B_PREADY + t), pp, abort_flag, to)) goto drain;
-              pp ^= 1u;
+      for (int step = Env::ALTERNATE ? -1 : 0; step < 4; ++step) {
+        const int t = step < 0 ? 1 : step >> 1;
+        bool mine = true;
+        if constexpr (Env::ALTERNATE) {
+          if (step < 0) mine = Env::alternate(flags);
+          if (step == (L::RING ? 2 : 3)) mine = !Env::alternate(flags);
+        }
+        if (step < 0 || ((step & 1) == 0) == L::RING) {
+          if (mine && !end && ((flags >> t) & 1)) {
+            if (!k_ready) {
+              if (!bwait_warp(bars + 8u * (L::B_KFULL + cur_kslot), cur_kpar, abort_flag, to)) goto drain;
               tc_fence_after();
-              bool& started = t ? pv1 : pv0;
-              const uint32_t p_col = tmem + (L::RING ? pslot : t) * 128;
-              const uint32_t vbase = base + L::OFF_V + prev_vslot * L::KV_TILE_BYTES;
-              // V tile as the MN-major B operand: 16 keys per step (2048 bytes), the two
-              // 64-column halves of d are KV_TILE_BYTES/2 apart, 8-key groups 1024 apart.
-              if constexpr (D == 64) {
-                const uint64_t vd = sdesc_sw128(vbase, BN * 128, 1024);
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                  mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4),
-                               ID_PV, (started || kk > 0) ? 1u : 0u);
-              } else {
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                  mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8,
-                               sdesc_sw128(vbase + kk * 16 * 128, BN * 128, 1024), ID_PV,
-                               (started || kk > 0) ? 1u : 0u);
-              }
-              started = true;
-              if constexpr (L::RING) tc_commit_elect(bars + 8u * (L::B_OPV + t));
+              k_ready = true;
             }
-            // end of unit: O_t is complete once its last P.V is -- signal it now, so softmax t
-            // starts its epilogue without waiting for the other Q tile's P.V
-            if (end && (t ? pv1 : pv0)) tc_commit_elect(bars + 8u * (L::B_ODONE + t));
-            if (t == QT - 1 && have_prev) tc_commit_elect(bars + 8u * (L::B_VEMPTY + prev_vslot));
+            if constexpr (L::RING) {
+              (t ? new_slot1 : new_slot0) = nqk;
+              nqk = nqk == L::S_SLOTS - 1 ? 0 : nqk + 1;
+            }
+            const int new_slot = t ? new_slot1 : new_slot0;
+            const uint32_t s_col = tmem + new_slot * 128;
+            const uint32_t qbase = base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES;
+            const uint32_t kbase = base + L::OFF_K + cur_kslot * L::KV_TILE_BYTES;
+            // Q and K as K-major operands: 16 elements (32 bytes) per step inside a
+            // 128-byte swizzle row, the next 64 elements one half-tile further.
+            if constexpr (D == 64) {
+              // d = 64 issues twice the instructions per flop: the descriptors are built
+              // once and stepped through their start-address field (address >> 4 in the
+              // low 14 bits; every offset here keeps it below 2^14)
+              const uint64_t qd = sdesc_sw128(qbase, 16, 1024), kd = sdesc_sw128(kbase, 16, L::KV_SBO);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+                mma_ss_elect(s_col, qd + off, kd + off, ID_QK, kk > 0 ? 1u : 0u);
+              }
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
+                const uint32_t koff = (kk >> 2) * L::KV_HALF + (kk & 3) * 32;
+                mma_ss_elect(s_col, sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + koff, 16, L::KV_SBO),
+                             ID_QK, kk > 0 ? 1u : 0u);
+              }
+            }
+            tc_commit_elect(bars + 8u * (L::B_STILE + new_slot));
+            env.computed(t, j, lane);
+            __syncwarp();
           }
+        } else {
+          if (have_prev && ((prev_flags >> t) & 1)) {
+            uint32_t& pp = t ? p_par1 : p_par0;
+            if (!bwait_warp(bars + 8u * (L::B_PREADY + t), pp, abort_flag, to)) goto drain;
+            pp ^= 1u;
+            tc_fence_after();
+            bool& started = t ? pv1 : pv0;
+            const uint32_t p_col = tmem + (L::RING ? (t ? pslot1 : pslot0) : t) * 128;
+            const uint32_t vbase = base + L::OFF_V + prev_vslot * L::KV_TILE_BYTES;
+            // V tile as the MN-major B operand: 16 keys per step (two groups of 8), the two
+            // 64-column halves of d KV_HALF apart, 8-key groups KV_SBO.
+            if constexpr (D == 64) {
+              const uint64_t vd = sdesc_sw128(vbase, L::KV_HALF, L::KV_SBO);
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8, vd + (uint64_t)(kk * 2 * L::KV_SBO >> 4),
+                             ID_PV, (started || kk > 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8,
+                             sdesc_sw128(vbase + kk * 2 * L::KV_SBO, L::KV_HALF, L::KV_SBO), ID_PV,
+                             (started || kk > 0) ? 1u : 0u);
+            }
+            started = true;
+            if constexpr (L::RING) tc_commit_elect(bars + 8u * (L::B_OPV + t));
+          }
+          // end of unit: O_t is complete once its last P.V is -- signal it now, so softmax t
+          // starts its epilogue without waiting for the other Q tile's P.V
+          if (end && (t ? pv1 : pv0)) tc_commit_elect(bars + 8u * (L::B_ODONE + t));
+          if (t == QT - 1 && have_prev) tc_commit_elect(bars + 8u * (L::B_VEMPTY + prev_vslot));
         }
         if constexpr (L::RING) {
-          if (!end && ((flags >> t) & 1)) pslot = new_slot;
+          if ((step & 1) && step > 0 && !end && ((flags >> t) & 1)) (t ? pslot1 : pslot0) = t ? new_slot1 : new_slot0;
         }
       }
       if (!end) tc_commit_elect(bars + 8u * (L::B_KEMPTY + cur_kslot));
@@ -336,7 +348,6 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
       if (end) break;
       have_prev = true;
       prev_flags = flags;
-      prev_j = j;
       prev_vslot = cur_vslot;
       prev_vpar = cur_vpar;
     }

@@ -46,7 +46,7 @@ REFUSALS = (
     [("attend", {k: v}, -1) for k in ATTEND if k.endswith("_stride") and k != "table_stride" for v in (60, -64)] +
     [("attend", kw, st) for kw, st in (
         (dict(B=0), -1), (dict(B=16385), -1), (dict(cache_row_stride=0), -1), (dict(cache_page_stride=0), -1), (dict(cache_head_stride=0), -1),
-        (dict(q_head_stride=0), -1), (dict(q_row_stride=0), -1), (dict(o_head_stride=0), -1), (dict(o_row_stride=0), -1), (dict(Hq=3), -1), (dict(Hkv=0), -1), (dict(d=80), -2), (dict(dtype=7), -2), (dict(total_q=0), -1),
+        (dict(cache_page_stride=1536), -2), (dict(num_pages=1 << 27, cache_head_stride=64), -2), (dict(q_head_stride=0), -1), (dict(q_row_stride=0), -1), (dict(o_head_stride=0), -1), (dict(o_row_stride=0), -1), (dict(Hq=3), -1), (dict(Hkv=0), -1), (dict(d=80), -2), (dict(dtype=7), -2), (dict(total_q=0), -1),
         (dict(max_seqlen_q=0), -1), (dict(num_pages=0), -1), (dict(page_size=0), -1), (dict(page_size=8), -1), (dict(page_size=40), -1),
         (dict(table_width=0), -1), (dict(table_stride=3), -1), (dict(window_left=-2), -1), (dict(window_right=-2), -1),
         (dict(scale=0.0), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(Hq=258, Hkv=2), -2),
