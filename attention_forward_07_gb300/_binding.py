@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 ATTN_F16 = 0
@@ -117,13 +118,14 @@ def library():
         lib.attn_fwd_noalloc.restype = i
         lib.attn_fwd_ex.argtypes = [ctypes.POINTER(FwdParams)]
         lib.attn_fwd_ex.restype = i
-        lib.attn_paged_tables.argtypes = [ctypes.POINTER(PagedTablesParams)]
+        # (parameter blocks as bytes or by reference)
+        lib.attn_paged_tables.argtypes = [p]
         lib.attn_paged_tables.restype = i
-        lib.attn_paged_append.argtypes = [ctypes.POINTER(PagedAppendParams)]
+        lib.attn_paged_append.argtypes = [p]
         lib.attn_paged_append.restype = i
-        lib.attn_fwd_paged.argtypes = [ctypes.POINTER(FwdPagedParams)]
+        lib.attn_fwd_paged.argtypes = [p]
         lib.attn_fwd_paged.restype = i
-        lib.attn_paged_workspace.argtypes = [ctypes.POINTER(FwdPagedParams), ctypes.POINTER(ctypes.c_ulonglong)]
+        lib.attn_paged_workspace.argtypes = [p, ctypes.POINTER(ctypes.c_ulonglong)]
         lib.attn_paged_workspace.restype = i
         lib.attn_check.argtypes = [p]
         lib.attn_check.restype = i
@@ -261,51 +263,79 @@ def attn_fwd_packed(q, k, v, o, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_se
         raise AttnError(rc, "attn_fwd_ex")
 
 
-def _paged_launch(call, device, stream):
-    """Runs call(stream handle) with `device` current, on `stream` or torch's current stream there."""
+# The paged operators are called once or more per layer and decoding step, where a microsecond counts: their parameter blocks
+# are packed as bytes (in the layout of the structures above), and each tensor is asked only for what is checked.
+_TABLES = struct.Struct("@10P7iP")
+_APPEND = struct.Struct("@5P7q6iP")
+_ATTEND = struct.Struct("@9PQ7q13ifiP")
+_workspace_sizes = {}
+
+
+def _on_device(index, fn, block):
+    """Status of fn(block), called with CUDA device `index` current."""
     import torch
-    if device.type != "cuda":
+    if torch.cuda.current_device() == index:
+        return fn(block)
+    with torch.cuda.device(index):
+        return fn(block)
+
+
+def _paged_stream(torch, index, stream):
+    """(handle, whether it is torch's current stream) of `stream`, or of the current stream of CUDA device `index`."""
+    if index < 0:
         raise ValueError("the paged operators take CUDA tensors")
+    current = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"the tensors are on {device}, the stream on {stream.device}")
-    if torch.cuda.current_device() == device.index:
-        return call(stream)
-    with torch.cuda.device(device):
-        return call(stream)
+        return current, True
+    if stream.device.index != index:
+        raise ValueError(f"the tensors are on device {index}, the stream on {stream.device}")
+    return stream.cuda_stream, stream.cuda_stream == current
 
 
-def _index_ptr(t, name, n, device):
-    """Address of a contiguous int32 vector of n entries on `device`."""
-    import torch
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on {device}")
+def _get_raw_stream():
+    try:
+        from torch._C import _cuda_getCurrentRawStream
+        return _cuda_getCurrentRawStream
+    except ImportError:  # a torch without it: current_stream() does the same, more slowly
+        return None
+
+
+_raw_stream = _get_raw_stream()
+
+
+def _vector(t, i32, index, n, name):
+    """Address of a contiguous int32 vector of n entries on CUDA device `index`."""
+    if t.dtype is not i32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on CUDA device {index}")
     return t.data_ptr()
 
 
-def _table_strides(t, B, device):
-    import torch
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 2 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_table must be int32 [{B}, pages] on {device}, each row contiguous")
-    return t.shape[1], t.stride(0) if B > 1 else t.shape[1]
+def _table(t, i32, index, B):
+    """(address, width, row stride) of a block table."""
+    if t.dtype is not i32 or t.get_device() != index or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError(f"block_table must be int32 [{B}, pages] on CUDA device {index}")
+    width, (row, col) = t.shape[1], t.stride()
+    if width > 1 and col != 1:
+        raise ValueError("each row of block_table must be contiguous")
+    return t.data_ptr(), width, row if B > 1 else width
 
 
-def _rows_strides(t, name, shape, dtype, device):
+def _rows(t, dtype, index, shape, name):
     """(row, head) strides of a packed [H, rows, d] tensor."""
-    if t.dtype != dtype or t.device != device or t.shape != shape or t.stride(2) != 1:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, its last dimension contiguous")
-    return t.stride(1), t.stride(0)
+    head, row, last = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or last != 1:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on CUDA device {index}, its last dimension contiguous")
+    return row, head
 
 
-def _cache_strides(k_cache, v_cache, dtype, device):
-    """(page, head, row) strides of [num_pages, Hkv, page_size, d] caches."""
-    s = k_cache.stride()
-    if (k_cache.dim() != 4 or k_cache.dtype != dtype or v_cache.dtype != dtype or k_cache.device != device or
-            v_cache.device != device or v_cache.shape != k_cache.shape or v_cache.stride() != s or s[3] != 1):
-        raise ValueError(f"k_cache and v_cache must be {dtype} [num_pages, Hkv, page_size, d] on {device}, of the same strides, "
-                         "their last dimension contiguous")
-    return s[0], s[1], s[2]
+def _caches(k, v, dtype, index):
+    """(page, head, row, last) strides of [num_pages, Hkv, page_size, d] caches."""
+    s = k.stride()
+    if (len(s) != 4 or s[3] != 1 or k.dtype is not dtype or v.dtype is not dtype or k.get_device() != index or
+            v.get_device() != index or v.shape != k.shape or v.stride() != s):
+        raise ValueError(f"k_cache and v_cache must be {dtype} [num_pages, Hkv, page_size, d] on CUDA device {index}, of the same "
+                         "strides, their last dimension contiguous")
+    return s
 
 
 def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages, cu_seqlens_q, seqlens_k,
@@ -316,24 +346,19 @@ def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, p
     pages added are filled in), free_pages [F] with free_count [1] (taken from the end) -> cu_seqlens_q [B+1],
     seqlens_k [B], slots and positions [max rows] (-1 behind the last new row), free_count_out [1] (default: free_count
     itself).  See include/attn.h."""
-    dev = ctx_lens.device
-    B = ctx_lens.shape[0]
-    width, stride = _table_strides(block_table, B, dev)
-    rows, nfree = slots.shape[0], free_pages.shape[0]
-    if free_count_out is None:
-        free_count_out = free_count
-    prm = PagedTablesParams(_index_ptr(ctx_lens, "ctx_lens", B, dev), _index_ptr(new_lens, "new_lens", B, dev),
-                            block_table.data_ptr(), _index_ptr(free_pages, "free_pages", nfree, dev),
-                            _index_ptr(free_count, "free_count", 1, dev), _index_ptr(free_count_out, "free_count_out", 1, dev),
-                            _index_ptr(cu_seqlens_q, "cu_seqlens_q", B + 1, dev), _index_ptr(seqlens_k, "seqlens_k", B, dev),
-                            _index_ptr(slots, "slots", rows, dev),
-                            None if positions is None else _index_ptr(positions, "positions", rows, dev),
-                            B, width, stride, nfree, rows, page_size, num_pages)
-
-    def call(st):
-        prm.stream = st.cuda_stream
-        return library().attn_paged_tables(ctypes.byref(prm))
-    rc = _paged_launch(call, dev, stream)
+    import torch
+    i32, index = torch.int32, ctx_lens.get_device()
+    B, rows, free = ctx_lens.shape[0], slots.shape[0], free_pages.shape[0]
+    table, width, stride = _table(block_table, i32, index, B)
+    count = _vector(free_count, i32, index, 1, "free_count")
+    args = (_vector(ctx_lens, i32, index, B, "ctx_lens"), _vector(new_lens, i32, index, B, "new_lens"), table,
+            _vector(free_pages, i32, index, free, "free_pages"), count,
+            count if free_count_out is None else _vector(free_count_out, i32, index, 1, "free_count_out"),
+            _vector(cu_seqlens_q, i32, index, B + 1, "cu_seqlens_q"), _vector(seqlens_k, i32, index, B, "seqlens_k"),
+            _vector(slots, i32, index, rows, "slots"), 0 if positions is None else _vector(positions, i32, index, rows, "positions"),
+            B, width, stride, free, rows, page_size, num_pages)
+    handle, _ = _paged_stream(torch, index, stream)
+    rc = _on_device(index, (_lib or library()).attn_paged_tables, _TABLES.pack(*args, handle))
     if rc != 0:
         raise AttnError(rc, "attn_paged_tables")
 
@@ -341,27 +366,24 @@ def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, p
 def attn_paged_append(k_new, v_new, k_cache, v_cache, slots, stream=None):
     """Write new rows k_new, v_new [Hkv, rows, d] to their slots (int32 [rows]; negative: left out) of the caches
     [num_pages, Hkv, page_size, d].  Any strides whose last dimension is contiguous; see include/attn.h."""
-    dev, dtype = k_new.device, k_new.dtype
+    import torch
+    dtype, index = k_new.dtype, k_new.get_device()
     code = _dtype_code(k_new)
-    cs = _cache_strides(k_cache, v_cache, dtype, dev)
+    page, head, row, _ = _caches(k_cache, v_cache, dtype, index)
     num_pages, Hkv, page_size, d = k_cache.shape
     rows = slots.shape[0]
+    shape = (Hkv, rows, d)
+    k_row, k_head = _rows(k_new, dtype, index, shape, "k_new")
+    v_row, v_head = _rows(v_new, dtype, index, shape, "v_new")
+    at = _vector(slots, torch.int32, index, rows, "slots")
+    handle, _ = _paged_stream(torch, index, stream)
     if rows == 0:
         return
-    shape = (Hkv, rows, d)
-    prm = PagedAppendParams(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                            _index_ptr(slots, "slots", rows, dev), *_rows_strides(k_new, "k_new", shape, dtype, dev),
-                            *_rows_strides(v_new, "v_new", shape, dtype, dev), *cs, rows, Hkv, d, num_pages, page_size, code)
-
-    def call(st):
-        prm.stream = st.cuda_stream
-        return library().attn_paged_append(ctypes.byref(prm))
-    rc = _paged_launch(call, dev, stream)
+    rc = _on_device(index, (_lib or library()).attn_paged_append,
+                    _APPEND.pack(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), at, k_row, k_head, v_row,
+                                 v_head, page, head, row, rows, Hkv, d, num_pages, page_size, code, handle))
     if rc != 0:
         raise AttnError(rc, "attn_paged_append")
-
-
-_workspace_sizes = {}
 
 
 def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, lse=None, causal=False,
@@ -372,48 +394,57 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     chunks, mixed freely.  workspace: a uint8 tensor of attn_paged_workspace() bytes for calls that do not run at the same
     time; None takes one from torch's allocator.  See include/attn.h."""
     import torch
-    dev, dtype = q.device, q.dtype
+    dtype, index = q.dtype, q.get_device()
     code = _dtype_code(q)
-    Hq, total_q, d = shape = q.shape
-    cs = _cache_strides(k_cache, v_cache, dtype, dev)
+    shape = q.shape
+    q_row, q_head = _rows(q, dtype, index, shape, "q")
+    o_row, o_head = _rows(o, dtype, index, shape, "o")
+    page, head, row, _ = _caches(k_cache, v_cache, dtype, index)
+    Hq, total_q, d = shape
     num_pages, Hkv, page_size, dk = k_cache.shape
     if dk != d:
         raise ValueError("q and the caches disagree on d")
-    B = seqlens_k.shape[0]
-    width, tstride = _table_strides(block_table, B, dev)
-    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != shape[:2] or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous fp32 {(Hq, total_q)} on {dev}")
+    i32, B = torch.int32, seqlens_k.shape[0]
+    table, width, table_stride = _table(block_table, i32, index, B)
+    cu = _vector(cu_seqlens_q, i32, index, B + 1, "cu_seqlens_q")
+    lens = _vector(seqlens_k, i32, index, B, "seqlens_k")
+    lse_at = 0
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (Hq, total_q) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous fp32 {(Hq, total_q)} on CUDA device {index}")
+        lse_at = lse.data_ptr()
+    handle, current = _paged_stream(torch, index, stream)
     if total_q == 0:
         return
-    prm = FwdPagedParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-                         block_table.data_ptr(), _index_ptr(cu_seqlens_q, "cu_seqlens_q", B + 1, dev),
-                         _index_ptr(seqlens_k, "seqlens_k", B, dev), None, 0, *_rows_strides(q, "q", shape, dtype, dev),
-                         *_rows_strides(o, "o", shape, dtype, dev), *cs, B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size,
-                         width, tstride, int(bool(causal)), window_left, window_right, d ** -0.5 if scale is None else scale, code)
-
-    def call(st):
-        ws = workspace
-        if ws is None:
-            key = (dev.index, B, Hq, Hkv, d, total_q, max_seqlen_q)
-            n = _workspace_sizes.get(key)
-            if n is None:
-                n = _workspace_sizes[key] = _paged_workspace(prm)
-            ws = torch.empty(n, dtype=torch.uint8, device=dev)
-            if st != torch.cuda.current_stream(dev):
-                ws.record_stream(st)
-        elif ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {dev}")
-        prm.workspace = ws.data_ptr()
-        prm.workspace_bytes = ws.numel() * ws.element_size()
-        prm.stream = st.cuda_stream
-        return library().attn_fwd_paged(ctypes.byref(prm))
-    rc = _paged_launch(call, dev, stream)
+    if workspace is None:
+        key = (index, B, Hq, Hkv, d, total_q, max_seqlen_q)
+        n = _workspace_sizes.get(key)
+        if n is None:
+            if len(_workspace_sizes) >= 4096:
+                _workspace_sizes.clear()
+            n = _workspace_sizes[key] = _on_device(index, _workspace_bytes, (B, Hq, Hkv, d, total_q, max_seqlen_q))
+        if current:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        else:  # from the launch stream's own pool, whose blocks are handed on in that stream's order
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on CUDA device {index}")
+    else:
+        n = workspace.numel() * workspace.element_size()
+    rc = _on_device(index, (_lib or library()).attn_fwd_paged,
+                    _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), lse_at, table, cu, lens,
+                                 workspace.data_ptr(), n, q_row, q_head, o_row, o_head, page, head, row, B, Hq, Hkv, d, total_q,
+                                 max_seqlen_q, num_pages, page_size, width, table_stride, 1 if causal else 0, window_left, window_right,
+                                 d ** -0.5 if scale is None else scale, code, handle))
     if rc != 0:
         raise AttnError(rc, "attn_fwd_paged")
 
 
-def _paged_workspace(prm) -> int:
+def _workspace_bytes(shape) -> int:
+    B, Hq, Hkv, d, total_q, max_seqlen_q = shape
     n = ctypes.c_ulonglong(0)
+    prm = FwdPagedParams(B=B, Hq=Hq, Hkv=Hkv, d=d, total_q=total_q, max_seqlen_q=max_seqlen_q)
     rc = library().attn_paged_workspace(ctypes.byref(prm), ctypes.byref(n))
     if rc != 0:
         raise AttnError(rc, "attn_paged_workspace")
@@ -422,7 +453,7 @@ def _paged_workspace(prm) -> int:
 
 def attn_paged_workspace(B, Hq, Hkv, d, total_q, max_seqlen_q) -> int:
     """Bytes of workspace attn_fwd_paged wants on the current device."""
-    return _paged_workspace(FwdPagedParams(B=B, Hq=Hq, Hkv=Hkv, d=d, total_q=total_q, max_seqlen_q=max_seqlen_q))
+    return _workspace_bytes((B, Hq, Hkv, d, total_q, max_seqlen_q))
 
 
 def attn_check(stream=None) -> int:

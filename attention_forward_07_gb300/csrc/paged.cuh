@@ -20,7 +20,7 @@ constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a un
 struct TileQueue {
   unsigned int next;    // next queue entry (a CTA starts with that of its own number)
   int whole, runs;      // entries: whole (unit, head) pairs, then runs
-  int njoins;           // cut (unit, head) pairs
+  int njoins;
   int units;
   long long line0, line;  // where the runs' line begins, its length
 };
@@ -30,16 +30,18 @@ struct TileUnit {
   long long cum;  // weights of the units before
   int row0, sq, sk, pad;
 };
-struct TileJoin {
-  int unit, h;
-  int run, parts;  // slots 2 run + 1, 2 (run + 1), 2 (run + 2), ...
+struct TileJoin {  // up to JOIN_ROWS packed rows of a cut (unit, head) pair
+  int row0, row, rows;  // request's first query row, first packed row, rows
+  int h, run, parts;    // pieces in slots 2 run + 1, 2 (run + 1), 2 (run + 2), ...
+  int in, pad;          // first row within the slot
 };
+constexpr int JOIN_ROWS = 16;
 
 // Scratch of the tcgen05 path.
 struct TileWork {
   TileQueue* queue;
   TileUnit* units;   // [max_units + 1], longest first
-  TileJoin* joins;   // [max runs]: every cut pair holds a run's beginning
+  TileJoin* joins;   // [max runs * 256 / JOIN_ROWS]: every cut pair holds a run's beginning
   float* part_o;     // [2 max runs][256][D]: unscaled O of a piece
   float2* part_ml;   // [2 max runs][256]: its exponent base (exp2 domain) and sum of weights
   int T;             // tokens of a Q tile

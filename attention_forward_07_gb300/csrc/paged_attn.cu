@@ -25,8 +25,9 @@ namespace {
 
 // An item whose tiles CTA c begins and others finish: the partial results to join.
 struct Split {
-  int b, h, blk;  // b < 0: none
-  int parts;      // slots 2c + 1, 2(c + 1), 2(c + 2), ...
+  int b, h;   // b < 0: none
+  int parts;  // slots 2c + 1, 2(c + 1), 2(c + 2), ...
+  int pad;
 };
 
 struct RowsParams : PagedParams {
@@ -37,15 +38,16 @@ struct RowsParams : PagedParams {
 };
 
 // ------------------------------------------------------------------ few rows: the memory-bound path
-// An item is (request, K/V head, block of 16 packed rows), row r of a request's K/V head being query
-// token r / g, query head r % g of the group: one pass over the keys serves the whole group.  Each
+// An item is (request, K/V head) with at most 16 packed rows, row r being query token r / g, query head r % g
+// of the group: one pass over the keys serves the whole group.  Each
 // key costs 4 d bytes and 16 * 4 d flops, far below the machine's ratio, so the keys' stream from memory is
 // the floor and everything else has to hide behind it:
 //  * the items' key tiles, laid end to end, are cut into equal runs, one per CTA, whatever the
 //    lengths: no CTA has more to read than another.  Items cut across CTAs leave partial results
-//    (at most two to a CTA) that rows_join_kernel puts together;
+//    (at most two to a CTA) that join_kernel puts together;
 //  * the four warps of a CTA take a quarter of each tile's keys each, with a ring of asynchronous copies,
-//    a running maximum, sum and accumulator of their own: nothing synchronises them before the item's end;
+//    a running maximum, sum and accumulator of their own: nothing synchronises them before the item's end,
+//    and the copies go on into the next item meanwhile;
 //  * a lane holds the places of the next 32 page rows, so the table is read once per 32 copies;
 //  * mma.sync with the keys as the N side: 16 rows are its smallest M, and its operands come by
 //    ldmatrix straight from the copied rows (128-byte tcgen05 tiles would be an eighth full).
@@ -60,43 +62,41 @@ struct Rows {
   static constexpr int SMEM = WARPS * NST * STAGE;
   static constexpr int CTAS_PER_SM = 2;
   static constexpr int MIN_TILES = 2;             // tiles a CTA takes at least
-  static_assert(NST * STAGE >= 16 * D * 4, "a warp's ring holds its accumulator at the end");
+  static_assert(STAGE >= 16 * D * 4, "a stage holds a warp's accumulator at the item's end");
+  static_assert(NTHREADS == 128, "the plan and block_scan are written for four warps");
 };
 
-// What the runs' arithmetic needs to know of a request.
+// What this path needs to know of a request: first query row, packed rows (0: not this path's), keys
+// [lo, hi) that any of its rows keeps and the tiles [t0, t1) that hold them (one tile of nothing where no
+// key is kept: the item still writes its rows).
 struct RowsItem {
-  int row0, sq, sk, off, R, nblk;
+  int row0, R, off, sk;
+  int lo, hi, t0, t1;
 };
 template <int D>
 __device__ __forceinline__ RowsItem rows_request(const RowsParams& p, int b) {
   RowsItem it;
-  request_span(p, b, it.row0, it.sq, it.sk);
-  it.off = it.sk - it.sq;
-  it.R = it.sq * p.g;
-  it.nblk = it.R <= ROWS_MAX && it.R > 0 ? 1 : 0;
+  int sq;
+  request_span(p, b, it.row0, sq, it.sk);
+  it.off = it.sk - sq;
+  it.R = sq * p.g;
+  it.lo = row_lo(p, 0, it.off);
+  it.hi = row_hi(p, sq - 1, it.off, it.sk);
+  if (it.hi <= it.lo) it.lo = it.hi = 0;
+  it.t0 = it.lo / Rows<D>::TK;
+  it.t1 = it.hi > it.lo ? (it.hi - 1) / Rows<D>::TK + 1 : it.t0 + 1;
+  if (it.R > ROWS_MAX || it.R == 0) it.R = it.t0 = it.t1 = 0;
   return it;
 }
-// Keys [lo, hi) that any row of block blk keeps and the tiles [t0, t1) that hold them (one tile of
-// nothing where no key is kept: the item still writes its rows).
+// The item after head h of request b.
 template <int D>
-__device__ __forceinline__ void rows_range(const RowsParams& p, const RowsItem& it, int blk, int& lo, int& hi, int& t0, int& t1) {
-  const int i0 = blk * 16 / p.g, i1 = (min(blk * 16 + 16, it.R) - 1) / p.g;
-  lo = row_lo(p, i0, it.off);
-  hi = row_hi(p, i1, it.off, it.sk);
-  if (hi <= lo) lo = hi = 0;
-  t0 = lo / Rows<D>::TK;
-  t1 = hi > lo ? (hi - 1) / Rows<D>::TK + 1 : t0 + 1;
+__device__ __forceinline__ void rows_next(const RowsParams& p, int& b, int& h, RowsItem& it) {
+  if (++h < p.Hkv) return;
+  h = 0;
+  do it = rows_request<D>(p, ++b);
+  while (it.R == 0);
 }
-template <int D>
-__device__ __forceinline__ long long rows_weight(const RowsParams& p, const RowsItem& it) {
-  long long w = 0;
-  for (int blk = 0; blk < it.nblk; ++blk) {
-    int lo, hi, t0, t1;
-    rows_range<D>(p, it, blk, lo, hi, t0, t1);
-    w += t1 - t0;
-  }
-  return w * p.Hkv;
-}
+
 // ------------------------------------------------------------------ plan
 // What the tcgen05 path works off, by one CTA of 128 threads while the others run the few-row path.  Units
 // (of one head) are numbered request by request, requests of the other path having none, and sorted by
@@ -253,7 +253,16 @@ __device__ __forceinline__ void tile_plan(const PagedParams& p, int* pre) {
     const int s = (int)(x / p.Hkv), h = (int)(x - (long long)s * p.Hkv);
     const long long at = line_of(x) - line0;
     const int first = run_of(line, runs, at), last = run_of(line, runs, at + tw.units[s].w - 1);
-    if (first != last) tw.joins[atomicAdd(&joins_s, 1)] = TileJoin{s, h, first, last - first + 1};
+    if (first == last) continue;
+    const TileUnit un = tw.units[s];
+    for (int t = 0; t < TILE_QT; ++t) {
+      const int tok0 = (un.blk * TILE_QT + t) * tw.T, rows = min(tw.T, un.sq - tok0) * p.g;
+      if (rows <= 0) break;
+      const int n = (rows + JOIN_ROWS - 1) / JOIN_ROWS, to = atomicAdd(&joins_s, n);
+      for (int k = 0; k < n; ++k)
+        tw.joins[to + k] = TileJoin{un.row0, tok0 * p.g + k * JOIN_ROWS, min(rows - k * JOIN_ROWS, JOIN_ROWS), h,
+                                    first, last - first + 1, t * TILE_ROWS + k * JOIN_ROWS, 0};
+    }
   }
   __syncthreads();
   if (tid == 0) *tw.queue = TileQueue{(unsigned int)sms, whole, runs, joins_s, units, line0, line};
@@ -296,82 +305,108 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
     tile_plan(p, reinterpret_cast<int*>(smem));
     return;
   }
-  __shared__ long long warp_sum[C::WARPS];
-  __shared__ int4 start_s;            // b, h, blk, tile of the run's first tile
+  __shared__ long long warp_sum[PLAN_WARPS];
+  __shared__ int3 start_s;            // request, head and tile that the run begins with
   __shared__ float2 ml_s[C::WARPS][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- this CTA's run: sum the weights, find where it begins
   const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS;
   const int rb0 = min(tid * per, p.B), rb1 = min(rb0 + per, p.B);
-  long long own = 0;
-  for (int b = rb0; b < rb1; ++b) own += rows_weight<D>(p, rows_request<D>(p, b));
-  long long incl = own;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, s);
-    if (lane >= s) incl += x;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long n = 0, before = incl - own;
-#pragma unroll
-  for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) before += warp_sum[w];
-    n += warp_sum[w];
-  }
+  const auto weight = [&](const RowsItem& it) { return (long long)(it.t1 - it.t0) * p.Hkv; };
+  long long own = 0, n;
+  for (int b = rb0; b < rb1; ++b) own += weight(rows_request<D>(p, b));
+  const long long before = block_scan(own, warp_sum, n);
   const int ctas = (int)min((long long)p.rows_grid, (n + C::MIN_TILES - 1) / C::MIN_TILES);
   const int cta = (int)blockIdx.x - ((int)gridDim.x - p.rows_grid);
   if (tid == 0) p.split[cta].b = -1;
   if (cta >= ctas) return;
-  const long long run0 = run_begin(n, ctas, cta), run1 = run_begin(n, ctas, cta + 1);
+  const long long run0 = run_begin(n, ctas, cta);
+  const int run = (int)(run_begin(n, ctas, cta + 1) - run0);  // tiles
   if (run0 >= before && run0 < before + own) {
     long long at = before;
-    int b = rb0;
-    RowsItem it;
-    for (;; ++b) {
-      it = rows_request<D>(p, b);
-      const long long w = rows_weight<D>(p, it);
+    for (int b = rb0;; ++b) {
+      const RowsItem it = rows_request<D>(p, b);
+      const long long w = weight(it);
       if (run0 < at + w) {
-        const long long per_head = w / p.Hkv;
-        int h = (int)((run0 - at) / per_head), blk = 0;
-        long long rest = (run0 - at) - h * per_head;
-        for (;; ++blk) {
-          int lo, hi, t0, t1;
-          rows_range<D>(p, it, blk, lo, hi, t0, t1);
-          if (rest < t1 - t0) {
-            start_s = make_int4(b, h, blk, t0 + (int)rest);
-            break;
-          }
-          rest -= t1 - t0;
-        }
+        const int tiles = it.t1 - it.t0, h = (int)((run0 - at) / tiles);
+        start_s = make_int3(b, h, it.t0 + (int)(run0 - at - (long long)h * tiles));
         break;
       }
       at += w;
     }
   }
   __syncthreads();
-  int b = start_s.x, h = start_s.y, blk = start_s.z, tile = start_s.w;
-  RowsItem it = rows_request<D>(p, b);
 
   const uint32_t ring = smem_u32(smem) + warp * (C::NST * C::STAGE);
-  float* ringf = reinterpret_cast<float*>(smem + warp * (C::NST * C::STAGE));
   constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks of a row, rows of one copy of the warp
   const int crow = lane / CPR, cchunk = lane % CPR;
   const int fr = lane >> 2, fc = (lane & 3) * 2;  // fragment row and column pair
 
-  for (long long pos = run0; pos < run1;) {
-    int lo, hi, t0, t1;
-    rows_range<D>(p, it, blk, lo, hi, t0, t1);
-    const int ntiles = (int)min((long long)(t1 - tile), run1 - pos);
-    const bool begins = tile == t0, ends = tile + ntiles == t1;
+  // ---- the copies run ahead of the products, across items: their own place in the run
+  int b = start_s.x, h = start_s.y, tile = start_s.z;
+  RowsItem it = rows_request<D>(p, b);
+  int cb = b, ch = h, ctile = tile, cleft = run, ccount = 0, cslot = 0;
+  RowsItem cit = it;
+  long long place = -1;  // lane's entry of the item's next 32 groups: element offset of its first row, -1 = none
+  const auto issue = [&] {
+    if (cleft > 0) {
+      if (ctile == cit.t1) {
+        rows_next<D>(p, cb, ch, cit);
+        ctile = cit.t0;
+        ccount = 0;
+      }
+      if (ccount % (32 / C::NG) == 0) {
+        const int t = ctile + lane / C::NG, key = t * C::TK + warp * C::KPW + (lane % C::NG) * 16;
+        place = -1;
+        if (t < ctile + cleft && key < cit.hi && key + 16 > cit.lo) {
+          const int idx = key / p.page_size;
+          const int pg = __ldg(p.table + (long long)cb * p.table_stride + idx);
+          if ((unsigned)pg < (unsigned)p.num_pages)
+            place = (long long)pg * p.c_page + (long long)(key - idx * p.page_size) * p.c_row;
+          else
+            atomicOr(p.status, STATUS_PAGE);
+        }
+      }
+      const uint32_t st = ring + cslot * C::STAGE;
+      const int key0 = ctile * C::TK + warp * C::KPW;
+      const uint16_t* kh = p.k + ch * p.c_head;
+      const uint16_t* vh = p.v + ch * p.c_head;
+#pragma unroll
+      for (int gq = 0; gq < C::NG; ++gq) {
+        const long long at = __shfl_sync(0xffffffffu, place, (ccount * C::NG + gq) % 32);
+#pragma unroll
+        for (int x = 0; x < 16 / RPI; ++x) {
+          const int r = gq * 16 + x * RPI + crow;
+          const int key = key0 + r;
+          const bool ok = at >= 0 && key >= cit.lo && key < cit.hi;
+          const long long src = ok ? at + (long long)(x * RPI + crow) * p.c_row + cchunk * 8 : 0;
+          const uint32_t dst = st + r * (D * 2) + ((cchunk ^ (r & 7)) * 16);
+          copy16(dst, kh + src, ok ? 16u : 0u);
+          copy16(dst + C::KPW * D * 2, vh + src, ok ? 16u : 0u);
+        }
+      }
+      ++ctile;
+      ++ccount;
+      --cleft;
+      if (++cslot == C::NST) cslot = 0;
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < C::NST - 1; ++s) issue();
 
-    // Q fragments: rows fr and fr + 8 of the block (rows past the last one are copies of it)
+  int slot = 0;
+  for (int left = run; left > 0;) {
+    const int ntiles = min(it.t1 - tile, left);
+    const bool begins = tile == it.t0, ends = tile + ntiles == it.t1;
+
+    // Q fragments: rows fr and fr + 8 (rows past the last one are copies of it)
     uint32_t qf[D / 16][4];
     int klo[2], khi[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int r = min(blk * 16 + fr + 8 * x, it.R - 1);
+      const int r = min(fr + 8 * x, it.R - 1);
       const int i = r / p.g;
       klo[x] = row_lo(p, i, it.off);
       khi[x] = row_hi(p, i, it.off, it.sk);
@@ -383,61 +418,23 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
       }
     }
     // tiles whose every key is kept by every row need no mask
-    const int lo_all = row_lo(p, (min(blk * 16 + 16, it.R) - 1) / p.g, it.off), hi_all = row_hi(p, blk * 16 / p.g, it.off, it.sk);
-
-    const uint16_t* kh = p.k + h * p.c_head;
-    const uint16_t* vh = p.v + h * p.c_head;
-    const int* row = p.table + (long long)b * p.table_stride;
-    long long place = -1;  // lane's entry of the next 32 groups: element offset of its first row, -1 = none
-    const auto issue = [&](int s) {
-      if (s < ntiles) {
-        if ((s * C::NG) % 32 == 0) {
-          const int e = s + lane / C::NG;  // the lane's tile
-          const int key = (tile + e) * C::TK + warp * C::KPW + (lane % C::NG) * 16;
-          place = -1;
-          if (e < ntiles && key < hi && key + 16 > lo) {
-            const int idx = key / p.page_size;
-            const int pg = __ldg(row + idx);
-            if ((unsigned)pg < (unsigned)p.num_pages)
-              place = (long long)pg * p.c_page + (long long)(key - idx * p.page_size) * p.c_row;
-            else
-              atomicOr(p.status, STATUS_PAGE);
-          }
-        }
-        const uint32_t st = ring + (s % C::NST) * C::STAGE;
-        const int key0 = (tile + s) * C::TK + warp * C::KPW;
-#pragma unroll
-        for (int gq = 0; gq < C::NG; ++gq) {
-          const long long at = __shfl_sync(0xffffffffu, place, (s * C::NG + gq) % 32);
-#pragma unroll
-          for (int x = 0; x < 16 / RPI; ++x) {
-            const int r = gq * 16 + x * RPI + crow;
-            const int key = key0 + r;
-            const bool ok = at >= 0 && key >= lo && key < hi;
-            const long long src = ok ? at + (long long)(x * RPI + crow) * p.c_row + cchunk * 8 : 0;
-            const uint32_t dst = st + r * (D * 2) + ((cchunk ^ (r & 7)) * 16);
-            copy16(dst, kh + src, ok ? 16u : 0u);
-            copy16(dst + C::KPW * D * 2, vh + src, ok ? 16u : 0u);
-          }
-        }
-      }
-      copy_commit();
-    };
+    const int lo_all = row_lo(p, (it.R - 1) / p.g, it.off), hi_all = row_hi(p, 0, it.off, it.sk);
 
     float o[D / 8][4];
 #pragma unroll
     for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float* exchange = nullptr;  // the slot of the last stage, which no copy takes before the join
 
-#pragma unroll
-    for (int s = 0; s < C::NST - 1; ++s) issue(s);
     for (int s = 0; s < ntiles; ++s) {
       copy_wait<C::NST - 2>();
       __syncwarp();
-      issue(s + C::NST - 1);
-      const uint32_t st = ring + (s % C::NST) * C::STAGE;
+      issue();
+      const uint32_t st = ring + slot * C::STAGE;
+      exchange = reinterpret_cast<float*>(smem + slot * C::STAGE);
+      if (++slot == C::NST) slot = 0;
       const int key0 = (tile + s) * C::TK + warp * C::KPW;
-      if (key0 >= hi || key0 + C::KPW <= lo) continue;  // no key of this warp's quarter
+      if (key0 >= it.hi || key0 + C::KPW <= it.lo) continue;  // no key of this warp's quarter
 
       // S = Q K^T: 16 rows x KPW keys
       float sc[2 * C::NG][4];
@@ -518,10 +515,11 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
         }
       }
     }
-    copy_wait<0>();
-    __syncwarp();
+    __syncwarp();  // every lane has read the last stage
 
-    // ---- join the four warps through their rings: row r's 8-column chunk c at chunk c ^ (r & 7)
+    // ---- join the four warps, each through the slot of its last stage: row r's 8-column chunk c at chunk
+    // c ^ (r & 7)
+    float* mine = exchange + warp * (C::NST * C::STAGE / 4);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -530,11 +528,11 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
       if ((lane & 3) == 0) ml_s[warp][r] = make_float2(m[x], l[x]);
 #pragma unroll
       for (int y = 0; y < D / 8; ++y)
-        *reinterpret_cast<float2*>(ringf + r * D + ((y ^ (r & 7)) * 8) + fc) = make_float2(o[y][2 * x], o[y][2 * x + 1]);
+        *reinterpret_cast<float2*>(mine + r * D + ((y ^ (r & 7)) * 8) + fc) = make_float2(o[y][2 * x], o[y][2 * x + 1]);
     }
     __syncthreads();
-    {
-      const int r = tid / 8;
+    const int r = tid / 8;
+    if (r < it.R) {
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml_s[w][r].x);
@@ -545,9 +543,8 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
         ll += f[w] * ml_s[w][r].y;
       }
       const bool whole = begins && ends;
-      const int slot = 2 * cta + (begins ? 1 : 0);
-      const int rr = blk * 16 + r;
-      const int i = rr / p.g, hq = h * p.g + rr - i * p.g;
+      const int at = (2 * cta + (begins ? 1 : 0)) * 16 + r;  // (a part's place)
+      const int i = r / p.g, hq = h * p.g + r - i * p.g;
       const float inv = ll > 0.f ? 1.f / ll : 0.f;
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
@@ -555,7 +552,7 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
         float acc[8] = {};
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) {
-          const float4* src = reinterpret_cast<const float4*>(smem + w * (C::NST * C::STAGE)) + (r * D + phys * 8) / 4;
+          const float4* src = reinterpret_cast<const float4*>(exchange + w * (C::NST * C::STAGE / 4) + r * D + phys * 8);
           const float4 a = src[0], c = src[1];
           acc[0] = fmaf(f[w], a.x, acc[0]);
           acc[1] = fmaf(f[w], a.y, acc[1]);
@@ -567,41 +564,32 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
           acc[7] = fmaf(f[w], c.w, acc[7]);
         }
         if (whole) {
-          if (rr < it.R)
-            *reinterpret_cast<uint4*>(p.o + (long long)(it.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
-                make_uint4(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv),
-                           pack2<BF16>(acc[4] * inv, acc[5] * inv), pack2<BF16>(acc[6] * inv, acc[7] * inv));
+          *reinterpret_cast<uint4*>(p.o + (long long)(it.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
+              make_uint4(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv),
+                         pack2<BF16>(acc[4] * inv, acc[5] * inv), pack2<BF16>(acc[6] * inv, acc[7] * inv));
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)slot * 16 + r) * D + col);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (long long)at * D + col);
           dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
           dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         }
       }
       if ((tid & 7) == 0) {
-        if (!whole) p.part_ml[slot * 16 + r] = make_float2(mm, ll);
-        else if (rr < it.R && p.lse)
-          p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
-      }
-      if (begins && !ends && tid == 0) {
-        // the CTAs that hold the item's other tiles: up to the one whose run reaches its end
-        p.split[cta] = Split{b, h, blk, run_of(n, ctas, pos + (t1 - tile) - 1) - cta + 1};
+        if (!whole) p.part_ml[at] = make_float2(mm, ll);
+        else if (p.lse) p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
       }
     }
-    __syncthreads();  // the rings are free again
+    if (begins && !ends && tid == 0) {
+      // the CTAs that hold the item's other tiles: up to the one whose run reaches its end
+      const long long last = run0 + (run - left) + (it.t1 - tile) - 1;
+      p.split[cta] = Split{b, h, run_of(n, ctas, last) - cta + 1, 0};
+    }
+    __syncthreads();  // the exchange has been read
 
-    pos += ntiles;
-    if (pos >= run1) break;
-    // next item: the head's next block, the next head, the next request with rows
-    if (++blk == it.nblk) {
-      blk = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        do it = rows_request<D>(p, ++b);
-        while (it.nblk == 0);
-      }
+    left -= ntiles;
+    if (left > 0) {
+      rows_next<D>(p, b, h, it);
+      tile = it.t0;
     }
-    rows_range<D>(p, it, blk, lo, hi, t0, t1);
-    tile = t0;
   }
 }
 
@@ -611,7 +599,7 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
 // A CTA takes a cut item of the few-row path (at most 16 rows) or 16 rows of a cut unit of the tcgen05 path;
 // its warps share out the rows, and where there are fewer rows than warps, a row's parts.  The parts were
 // just written and are mostly in L2; four are in flight at a time.
-constexpr int JOIN_WARPS = 16;
+constexpr int JOIN_WARPS = JOIN_ROWS;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_constant__ RowsParams p) {
@@ -622,10 +610,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
   grid_launch_dependents();
   grid_dependency_wait();
   const int items = p.rows_grid;
-  const int total = items + (p.tile.max_units > 0 ? p.tile.queue->njoins * (TILE_QT * TILE_ROWS / JOIN_WARPS) : 0);
+  const int total = items + (p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
     int rows, row0, h, parts, first, stride, slot0;  // part k of row r: record (k ? slot0 + k * stride : first) + r
-    int tok0;
+    int prow;  // first packed row
     const float* part_o;
     const float2* part_ml;
     if (x < items) {
@@ -634,7 +622,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
       int sq, sk;
       request_span(p, sp.b, row0, sq, sk);
       rows = sq * p.g;
-      tok0 = 0;
+      prow = 0;
       h = sp.h;
       parts = sp.parts;
       first = (2 * x + 1) * 16;
@@ -643,21 +631,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
       part_o = p.part_o;
       part_ml = p.part_ml;
     } else {
-      constexpr int CHUNKS = TILE_QT * TILE_ROWS / JOIN_WARPS;
-      const int y = x - items, chunk = y % CHUNKS;
-      const TileJoin jn = p.tile.joins[y / CHUNKS];
-      const TileUnit un = p.tile.units[jn.unit];
-      const int t = chunk / (CHUNKS / TILE_QT), r0 = chunk % (CHUNKS / TILE_QT) * JOIN_WARPS;  // Q tile, first row in it
-      row0 = un.row0;
-      tok0 = (un.blk * TILE_QT + t) * p.tile.T;
-      rows = min(min(p.tile.T, un.sq - tok0) * p.g - r0, JOIN_WARPS);
-      if (rows <= 0) continue;
-      tok0 = tok0 * p.g + r0;  // (as packed row)
+      const TileJoin jn = p.tile.joins[x - items];
+      row0 = jn.row0;
+      prow = jn.row;
+      rows = jn.rows;
       h = jn.h;
       parts = jn.parts;
-      const int in = t * TILE_ROWS + r0;
-      first = (2 * jn.run + 1) * (TILE_QT * TILE_ROWS) + in;
-      slot0 = 2 * jn.run * (TILE_QT * TILE_ROWS) + in;
+      first = (2 * jn.run + 1) * (TILE_QT * TILE_ROWS) + jn.in;
+      slot0 = 2 * jn.run * (TILE_QT * TILE_ROWS) + jn.in;
       stride = 2 * TILE_QT * TILE_ROWS;
       part_o = p.tile.part_o;
       part_ml = p.tile.part_ml;
@@ -721,7 +702,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
     }
     if (sub != 0 || r >= rows) continue;
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int rr = tok0 + r, i = rr / p.g, hq = h * p.g + rr - i * p.g;
+    const int rr = prow + r, i = rr / p.g, hq = h * p.g + rr - i * p.g;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (long long)(row0 + i) * p.o_row + (long long)hq * p.o_head + lane * E);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
@@ -756,7 +737,7 @@ struct Plan {
     const size_t max_runs = (size_t)MAX_SPLIT * sms, pieces = 2 * max_runs * TILE_QT * TILE_ROWS;
     off_units = off_queue + 256;
     off_joins = off_units + round256((size_t)(max_units + 1) * sizeof(TileUnit));
-    off_tile_ml = off_joins + round256(max_runs * sizeof(TileJoin));
+    off_tile_ml = off_joins + round256(max_runs * (TILE_QT * TILE_ROWS / JOIN_ROWS) * sizeof(TileJoin));
     off_tile_o = off_tile_ml + round256(pieces * sizeof(float2));
     bytes = off_tile_o + round256(pieces * a.d * sizeof(float));
   }

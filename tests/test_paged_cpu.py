@@ -65,6 +65,14 @@ def test_refusals(lib, op, kw, status):
     assert _call(lib, op, kw) == status
 
 
+def test_packed_blocks_have_the_structures_layout():
+    for fmt, cls in ((bd._TABLES, bd.PagedTablesParams), (bd._APPEND, bd.PagedAppendParams), (bd._ATTEND, bd.FwdPagedParams)):
+        assert fmt.size == ctypes.sizeof(cls)
+        values = [float(i) if kind is ctypes.c_float else i + 1 for i, (_, kind) in enumerate(cls._fields_)]
+        got = cls.from_buffer_copy(fmt.pack(*values))
+        assert [getattr(got, name) for name, _ in cls._fields_] == values
+
+
 def test_null_parameters(lib):
     n = ctypes.c_ulonglong(0)
     assert lib.attn_paged_tables(None) == lib.attn_paged_append(None) == lib.attn_fwd_paged(None) == -1
