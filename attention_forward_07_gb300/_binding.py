@@ -264,78 +264,67 @@ def attn_fwd_packed(q, k, v, o, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_se
 
 
 # The paged operators are called once or more per layer and decoding step, where a microsecond counts: their parameter blocks
-# are packed as bytes (in the layout of the structures above), and each tensor is asked only for what is checked.
+# are packed as bytes (in the layout of the structures above), each tensor is asked only for what is checked, all checks of a
+# call stand in one condition, and what is wrong is worked out only once that has failed.
 _TABLES = struct.Struct("@10P7iP")
 _APPEND = struct.Struct("@5P7q6iP")
 _ATTEND = struct.Struct("@9PQ7q13ifiP")
 _workspace_sizes = {}
+_torch = None
+_raw_stream = None
 
 
-def _on_device(index, fn, block):
-    """Status of fn(block), called with CUDA device `index` current."""
-    import torch
-    if torch.cuda.current_device() == index:
-        return fn(block)
-    with torch.cuda.device(index):
-        return fn(block)
+def _with_torch():
+    """torch, imported on first use (with it the cheapest way it has to name a device's current stream)."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _torch = torch
+    return _torch
 
 
-def _paged_stream(torch, index, stream):
-    """(handle, whether it is torch's current stream) of `stream`, or of the current stream of CUDA device `index`."""
+def _stream_on(index, stream):
+    """Handle of `stream`, checked to be on CUDA device `index`."""
+    if stream.device.index != index:
+        raise ValueError(f"the tensors are on CUDA device {index}, the stream is on {stream.device}")
+    return stream.cuda_stream
+
+
+def _launch(index, fn, block):
+    """Calls fn(block) with CUDA device `index` current; raises on a status other than 0."""
+    if _torch.cuda.current_device() == index:
+        rc = fn(block)
+    else:
+        with _torch.cuda.device(index):
+            rc = fn(block)
+    if rc != 0:
+        raise AttnError(rc, fn.__name__)
+
+
+def _refuse(index, vectors=(), table=None, rows=(), caches=None, others=()):
+    """Raises for the first of the tensors that is not as its caller wants it.  vectors: (tensor, entries, name); table:
+    (tensor, B); rows: (tensor, shape, dtype, name); caches: (k, v, dtype, d); others: (wrong, what is wanted)."""
+    i32 = _torch.int32
     if index < 0:
         raise ValueError("the paged operators take CUDA tensors")
-    current = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
-    if stream is None:
-        return current, True
-    if stream.device.index != index:
-        raise ValueError(f"the tensors are on device {index}, the stream on {stream.device}")
-    return stream.cuda_stream, stream.cuda_stream == current
-
-
-def _get_raw_stream():
-    try:
-        from torch._C import _cuda_getCurrentRawStream
-        return _cuda_getCurrentRawStream
-    except ImportError:  # a torch without it: current_stream() does the same, more slowly
-        return None
-
-
-_raw_stream = _get_raw_stream()
-
-
-def _vector(t, i32, index, n, name):
-    """Address of a contiguous int32 vector of n entries on CUDA device `index`."""
-    if t.dtype is not i32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on CUDA device {index}")
-    return t.data_ptr()
-
-
-def _table(t, i32, index, B):
-    """(address, width, row stride) of a block table."""
-    if t.dtype is not i32 or t.get_device() != index or t.dim() != 2 or t.shape[0] != B:
-        raise ValueError(f"block_table must be int32 [{B}, pages] on CUDA device {index}")
-    width, (row, col) = t.shape[1], t.stride()
-    if width > 1 and col != 1:
-        raise ValueError("each row of block_table must be contiguous")
-    return t.data_ptr(), width, row if B > 1 else width
-
-
-def _rows(t, dtype, index, shape, name):
-    """(row, head) strides of a packed [H, rows, d] tensor."""
-    head, row, last = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or last != 1:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on CUDA device {index}, its last dimension contiguous")
-    return row, head
-
-
-def _caches(k, v, dtype, index):
-    """(page, head, row, last) strides of [num_pages, Hkv, page_size, d] caches."""
-    s = k.stride()
-    if (len(s) != 4 or s[3] != 1 or k.dtype is not dtype or v.dtype is not dtype or k.get_device() != index or
-            v.get_device() != index or v.shape != k.shape or v.stride() != s):
-        raise ValueError(f"k_cache and v_cache must be {dtype} [num_pages, Hkv, page_size, d] on CUDA device {index}, of the same "
-                         "strides, their last dimension contiguous")
-    return s
+    for t, n, name in vectors:
+        if t.dtype is not i32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on CUDA device {index}")
+    if table is not None:
+        raise_if = table[0].dtype is not i32 or table[0].get_device() != index or table[0].dim() != 2 or table[0].shape[0] != table[1]
+        if raise_if or (table[0].shape[1] > 1 and table[0].stride(1) != 1):
+            raise ValueError(f"block_table must be int32 [{table[1]}, pages] on CUDA device {index}, each row contiguous")
+    for t, shape, dtype, name in rows:
+        if t.dtype is not dtype or t.get_device() != index or t.shape != shape or t.stride(-1) != 1:
+            raise ValueError(f"{name} must be {dtype} {tuple(shape)} on CUDA device {index}, its last dimension contiguous")
+    if caches is not None:
+        k, v, dtype, d = caches
+        raise ValueError(f"k_cache and v_cache must be {dtype} [num_pages, Hkv, page_size, {d}] on CUDA device {index}, of the same "
+                         f"strides, their last dimension contiguous; got {tuple(k.shape)} and {tuple(v.shape)}")
+    for wrong, wanted in others:
+        if wrong:
+            raise ValueError(wanted)
 
 
 def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages, cu_seqlens_q, seqlens_k,
@@ -346,44 +335,50 @@ def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, p
     pages added are filled in), free_pages [F] with free_count [1] (taken from the end) -> cu_seqlens_q [B+1],
     seqlens_k [B], slots and positions [max rows] (-1 behind the last new row), free_count_out [1] (default: free_count
     itself).  See include/attn.h."""
-    import torch
+    torch = _torch or _with_torch()
     i32, index = torch.int32, ctx_lens.get_device()
-    B, rows, free = ctx_lens.shape[0], slots.shape[0], free_pages.shape[0]
-    table, width, stride = _table(block_table, i32, index, B)
-    count = _vector(free_count, i32, index, 1, "free_count")
-    args = (_vector(ctx_lens, i32, index, B, "ctx_lens"), _vector(new_lens, i32, index, B, "new_lens"), table,
-            _vector(free_pages, i32, index, free, "free_pages"), count,
-            count if free_count_out is None else _vector(free_count_out, i32, index, 1, "free_count_out"),
-            _vector(cu_seqlens_q, i32, index, B + 1, "cu_seqlens_q"), _vector(seqlens_k, i32, index, B, "seqlens_k"),
-            _vector(slots, i32, index, rows, "slots"), 0 if positions is None else _vector(positions, i32, index, rows, "positions"),
-            B, width, stride, free, rows, page_size, num_pages)
-    handle, _ = _paged_stream(torch, index, stream)
-    rc = _on_device(index, (_lib or library()).attn_paged_tables, _TABLES.pack(*args, handle))
-    if rc != 0:
-        raise AttnError(rc, "attn_paged_tables")
+    (B,), (rows,), (free,) = ctx_lens.shape, slots.shape, free_pages.shape
+    if free_count_out is None:
+        free_count_out = free_count
+    vectors = ((ctx_lens, B, "ctx_lens"), (new_lens, B, "new_lens"), (free_pages, free, "free_pages"), (free_count, 1, "free_count"),
+               (free_count_out, 1, "free_count_out"), (cu_seqlens_q, B + 1, "cu_seqlens_q"), (seqlens_k, B, "seqlens_k"),
+               (slots, rows, "slots")) + (() if positions is None else ((positions, rows, "positions"),))
+    for t, n, _ in vectors:
+        if t.dtype is not i32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+            _refuse(index, vectors)
+    if (index < 0 or block_table.dtype is not i32 or block_table.get_device() != index or block_table.dim() != 2 or
+            block_table.shape[0] != B or (block_table.stride(1) != 1 and block_table.shape[1] > 1)):
+        _refuse(index, table=(block_table, B))
+    width = block_table.shape[1]
+    _launch(index, (_lib or library()).attn_paged_tables,
+            _TABLES.pack(ctx_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                         free_count_out.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), slots.data_ptr(),
+                         0 if positions is None else positions.data_ptr(), B, width, block_table.stride(0) if B > 1 else width, free,
+                         rows, page_size, num_pages, _raw_stream(index) if stream is None else _stream_on(index, stream)))
 
 
 def attn_paged_append(k_new, v_new, k_cache, v_cache, slots, stream=None):
     """Write new rows k_new, v_new [Hkv, rows, d] to their slots (int32 [rows]; negative: left out) of the caches
     [num_pages, Hkv, page_size, d].  Any strides whose last dimension is contiguous; see include/attn.h."""
-    import torch
+    torch = _torch or _with_torch()
     dtype, index = k_new.dtype, k_new.get_device()
     code = _dtype_code(k_new)
-    page, head, row, _ = _caches(k_cache, v_cache, dtype, index)
+    cs, ks, vs = k_cache.stride(), k_new.stride(), v_new.stride()
+    (rows,) = slots.shape
+    if (index < 0 or len(cs) != 4 or k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != index or
+            v_cache.get_device() != index or v_cache.shape != k_cache.shape or v_cache.stride() != cs or cs[3] != 1):
+        _refuse(index, caches=(k_cache, v_cache, dtype, "d"))
     num_pages, Hkv, page_size, d = k_cache.shape
-    rows = slots.shape[0]
     shape = (Hkv, rows, d)
-    k_row, k_head = _rows(k_new, dtype, index, shape, "k_new")
-    v_row, v_head = _rows(v_new, dtype, index, shape, "v_new")
-    at = _vector(slots, torch.int32, index, rows, "slots")
-    handle, _ = _paged_stream(torch, index, stream)
+    if (v_new.dtype is not dtype or v_new.get_device() != index or k_new.shape != shape or v_new.shape != shape or ks[2] != 1 or
+            vs[2] != 1 or slots.dtype is not torch.int32 or slots.get_device() != index or not slots.is_contiguous()):
+        _refuse(index, ((slots, rows, "slots"),), rows=((k_new, shape, dtype, "k_new"), (v_new, shape, dtype, "v_new")))
+    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
     if rows == 0:
         return
-    rc = _on_device(index, (_lib or library()).attn_paged_append,
-                    _APPEND.pack(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), at, k_row, k_head, v_row,
-                                 v_head, page, head, row, rows, Hkv, d, num_pages, page_size, code, handle))
-    if rc != 0:
-        raise AttnError(rc, "attn_paged_append")
+    _launch(index, (_lib or library()).attn_paged_append,
+            _APPEND.pack(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(), ks[1], ks[0], vs[1],
+                         vs[0], cs[0], cs[1], cs[2], rows, Hkv, d, num_pages, page_size, code, handle))
 
 
 def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, lse=None, causal=False,
@@ -393,27 +388,29 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     int32 [B+1], seqlens_k int32 [B] (keys per request, the new rows' own included).  One token per request, a few or whole
     chunks, mixed freely.  workspace: a uint8 tensor of attn_paged_workspace() bytes for calls that do not run at the same
     time; None takes one from torch's allocator.  See include/attn.h."""
-    import torch
-    dtype, index = q.dtype, q.get_device()
+    torch = _torch or _with_torch()
+    dtype, index, i32 = q.dtype, q.get_device(), torch.int32
     code = _dtype_code(q)
-    shape = q.shape
-    q_row, q_head = _rows(q, dtype, index, shape, "q")
-    o_row, o_head = _rows(o, dtype, index, shape, "o")
-    page, head, row, _ = _caches(k_cache, v_cache, dtype, index)
+    shape, qs, ost, cs = q.shape, q.stride(), o.stride(), k_cache.stride()
     Hq, total_q, d = shape
-    num_pages, Hkv, page_size, dk = k_cache.shape
-    if dk != d:
-        raise ValueError("q and the caches disagree on d")
-    i32, B = torch.int32, seqlens_k.shape[0]
-    table, width, table_stride = _table(block_table, i32, index, B)
-    cu = _vector(cu_seqlens_q, i32, index, B + 1, "cu_seqlens_q")
-    lens = _vector(seqlens_k, i32, index, B, "seqlens_k")
-    lse_at = 0
-    if lse is not None:
-        if lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (Hq, total_q) or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous fp32 {(Hq, total_q)} on CUDA device {index}")
-        lse_at = lse.data_ptr()
-    handle, current = _paged_stream(torch, index, stream)
+    (B,) = seqlens_k.shape
+    if (index < 0 or len(cs) != 4 or k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != index or
+            v_cache.get_device() != index or v_cache.shape != k_cache.shape or v_cache.stride() != cs or cs[3] != 1 or
+            k_cache.shape[3] != d):
+        _refuse(index, caches=(k_cache, v_cache, dtype, d))
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    if (o.dtype is not dtype or o.get_device() != index or o.shape != shape or qs[2] != 1 or ost[2] != 1 or
+            cu_seqlens_q.dtype is not i32 or cu_seqlens_q.get_device() != index or cu_seqlens_q.shape != (B + 1,) or
+            not cu_seqlens_q.is_contiguous() or seqlens_k.dtype is not i32 or seqlens_k.get_device() != index or
+            not seqlens_k.is_contiguous() or block_table.dtype is not i32 or block_table.get_device() != index or
+            block_table.dim() != 2 or block_table.shape[0] != B or (block_table.stride(1) != 1 and block_table.shape[1] > 1) or
+            (lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (Hq, total_q) or
+                                  not lse.is_contiguous()))):
+        _refuse(index, ((cu_seqlens_q, B + 1, "cu_seqlens_q"), (seqlens_k, B, "seqlens_k")), (block_table, B),
+                ((q, shape, dtype, "q"), (o, shape, dtype, "o")),
+                others=((True, f"lse must be contiguous fp32 {(Hq, total_q)} on CUDA device {index}"),))
+    current = _raw_stream(index)
+    handle = current if stream is None else _stream_on(index, stream)
     if total_q == 0:
         return
     if workspace is None:
@@ -422,23 +419,24 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
         if n is None:
             if len(_workspace_sizes) >= 4096:
                 _workspace_sizes.clear()
-            n = _workspace_sizes[key] = _on_device(index, _workspace_bytes, (B, Hq, Hkv, d, total_q, max_seqlen_q))
-        if current:
+            with torch.cuda.device(index):
+                n = _workspace_sizes[key] = _workspace_bytes(key[1:])
+        if handle == current:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
         else:  # from the launch stream's own pool, whose blocks are handed on in that stream's order
             with torch.cuda.stream(stream):
                 workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on CUDA device {index}")
     else:
         n = workspace.numel() * workspace.element_size()
-    rc = _on_device(index, (_lib or library()).attn_fwd_paged,
-                    _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), lse_at, table, cu, lens,
-                                 workspace.data_ptr(), n, q_row, q_head, o_row, o_head, page, head, row, B, Hq, Hkv, d, total_q,
-                                 max_seqlen_q, num_pages, page_size, width, table_stride, 1 if causal else 0, window_left, window_right,
-                                 d ** -0.5 if scale is None else scale, code, handle))
-    if rc != 0:
-        raise AttnError(rc, "attn_fwd_paged")
+        _refuse(index, others=((workspace.get_device() != index or not workspace.is_contiguous(),
+                                f"workspace must be contiguous and on CUDA device {index}"),))
+    width = block_table.shape[1]
+    _launch(index, (_lib or library()).attn_fwd_paged,
+            _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                         block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), workspace.data_ptr(), n, qs[1], qs[0],
+                         ost[1], ost[0], cs[0], cs[1], cs[2], B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size, width,
+                         block_table.stride(0) if B > 1 else width, 1 if causal else 0, window_left, window_right,
+                         d ** -0.5 if scale is None else scale, code, handle))
 
 
 def _workspace_bytes(shape) -> int:

@@ -466,7 +466,7 @@ namespace attn {
 // What the MMA warp does for this kernel beside its multiplications: it records the computed blocks.
 template <int MODE>
 struct FwdEnv {
-  static constexpr bool SCRUB = false, ALTERNATE = false;
+  static constexpr bool SCRUB = false, BY_TURNS = false;
   const Params& p;
   int b, hq, qb;
   __device__ __forceinline__ void unit(volatile InfoHdr& h) {

@@ -27,7 +27,6 @@ namespace {
 
 constexpr int FLAG_SCRUB = 16;  // the key tile holds rows that no query row of the request sees: those outside
                                 // [flags >> 8 & 255, flags >> 16 & 255)
-constexpr int FLAG_ALT = 32;    // both Q tiles hold the unit's one tile of rows and take its key tiles by turns
 
 struct TileParams : PagedParams {
   CUtensorMap tm_q, tm_k, tm_v;
@@ -81,7 +80,7 @@ struct TileBox {
 };
 
 // ------------------------------------------------------------------ load warp
-template <int D>
+template <int D, bool TURNS>
 __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t base, uint8_t* gbase, volatile int* abort_flag, int lane) {
   using L = TileLayout<D>;
   const uint32_t to = p.timeout_us;
@@ -178,9 +177,6 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
       jlo[t] = a / BN;
       jhi[t] = (e + BN - 1) / BN;
     }
-    // One tile of rows only: both Q tiles take it and its key tiles by turns, so that one's products
-    // run while the other's softmax does.
-    const bool alt = !rows1 && tiles > 1;
     int scrub_lo, scrub_hi;
     request_keys(p, sq, sk, scrub_lo, scrub_hi);
     const int tok0 = pt.blk * QT * p.tile.T;
@@ -191,14 +187,14 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
     if (!inject) {
       if (lane == 0) {
         const uint32_t fb = bars + 8u * (L::B_QFULL + qbuf);
-        mbar_expect_tx(fb, (uint32_t)((rows1 || alt ? 2 : 1) * p.tile.T * p.g * D * 2));
+        mbar_expect_tx(fb, (uint32_t)((rows1 || TURNS ? 2 : 1) * p.tile.T * p.g * D * 2));
 #pragma unroll
         for (int t = 0; t < QT; ++t)
 #pragma unroll
           for (int hh = 0; hh < L::HALVES; ++hh)
-            if (t == 0 || rows1 || alt)
+            if (t == 0 || rows1 || TURNS)
               tma_load_5d(base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES + hh * BM * 128, &p.tm_q, fb, hh * 64, 0,
-                          row0 + tok0 + (alt ? 0 : t * p.tile.T), h, 0);
+                          row0 + tok0 + (TURNS ? 0 : t * p.tile.T), h, 0);
       }
       q_pend |= 1u << qbuf;
       q_pend_par = (q_pend_par & ~(1u << qbuf)) | ((((q_empty_par >> qbuf) & 1u)) << qbuf);
@@ -219,14 +215,14 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
     for (int j = j0; j < j1; ++j) {
       bool a0 = j >= jlo[0] && j < jhi[0], a1 = j >= jlo[1] && j < jhi[1];
       if (!a0 && !a1) continue;
-      if (alt) {
+      if constexpr (TURNS) {
         a1 = (j - j0) & 1;
         a0 = !a1;
       }
       const TileBox box(p, pt.b, h, j, lo, hi, lane);  // looked up while the slots are still taken
       if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
       if (lane == 0) {
-        int flags = (a0 ? 1 : 0) | (a1 ? 2 : 0) | (alt ? FLAG_ALT : 0);
+        int flags = (a0 ? 1 : 0) | (a1 ? 2 : 0);
         const int r0 = max(scrub_lo - j * BN, 0), r1 = min(scrub_hi - j * BN, BN);
         if (r0 > 0 || r1 < BN) flags |= FLAG_SCRUB | r0 << 8 | r1 << 16;
         describe(j, flags);
@@ -248,7 +244,7 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
     }
     fetch();
     if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
-    if (lane == 0) describe(-1, FLAG_END | (alt ? FLAG_ALT : 0));
+    if (lane == 0) describe(-1, FLAG_END);
     __syncwarp();
     if (++ie == NINFO) { ie = 0; ie_par ^= 1u; }
   }
@@ -270,10 +266,9 @@ drain:
 // What the MMA warp does beside its multiplications: it zeroes the rows of a V tile that no query row
 // of the request sees (past the last key, ahead of the window), which may hold anything; their weights are
 // 0, and 0 * NaN would not be.
-template <int D>
+template <int D, bool TURNS>
 struct TileEnv {
-  static constexpr bool SCRUB = true, ALTERNATE = true;
-  static __device__ __forceinline__ bool alternate(int flags) { return flags & FLAG_ALT; }
+  static constexpr bool SCRUB = true, BY_TURNS = TURNS;
   __device__ __forceinline__ void unit(volatile TileHdr&) {}
   __device__ __forceinline__ void computed(int, int, int) {}
   __device__ __forceinline__ void scrub(int flags, uint8_t* v, int lane) {
@@ -291,7 +286,7 @@ struct TileEnv {
 };
 
 // ------------------------------------------------------------------ softmax warpgroup t
-template <int D, bool BF16>
+template <int D, bool BF16, bool TURNS>
 __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t base, uint8_t* gbase, volatile int* abort_flag, uint32_t tmem,
                                                   int t, int quarter, int lane) {
   using L = TileLayout<D>;
@@ -322,7 +317,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       mbar_arrive(bars + 8u * (L::B_IEMPTY + ie));
       break;
     }
-    const auto first_token = [&](int e) { return (hdr[e].blk * QT + (hdr[e].flags & FLAG_ALT ? 0 : t)) * p.tile.T; };
+    const auto first_token = [&](int e) { return (hdr[e].blk * QT + (TURNS ? 0 : t)) * p.tile.T; };
     int klo, khi;
     {
       const int sq = hdr[ie].sq, sk = hdr[ie].sk, i = min(first_token(ie) + token_of(min(r, p.tile.T * p.g - 1)), sq - 1);
@@ -330,7 +325,6 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       khi = row_hi(p, i, sk - sq, sk);
     }
     int row0 = 0, sq = 0, h = 0, slot_out = 0, tok0 = 0;  // the unit's place, read at its end
-    bool alt = false;
     float m = -INFINITY, l = 0.f;
     int nact = 0;
 
@@ -346,7 +340,6 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
         h = hdr[ie].h;
         slot_out = hdr[ie].slot;
         tok0 = first_token(ie);
-        alt = flags & FLAG_ALT;
       }
       mbar_arrive(bars + 8u * (L::B_IEMPTY + ie));
       if (++ie == NINFO) { ie = 0; ie_par ^= 1u; }
@@ -392,14 +385,17 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
     const int rows = min(p.tile.T, sq - tok0) * p.g;  // of this tile (may be <= 0)
     const bool row_ok = r < rows;
     const int my_tok = token_of(r);
-    const long long part = (long long)slot_out * UNIT_ROWS + (alt ? 0 : t * BM) + r;
-    if (alt) {
+    const long long part = (long long)slot_out * UNIT_ROWS + (TURNS ? 0 : t * BM) + r;
+    if constexpr (TURNS) {
       // Both Q tiles hold results of the same rows: they exchange m and l through shared memory (d = 128:
       // the staging area, d = 64: the Q buffer, whose reads are over), then each warpgroup joins and
       // writes half of the columns, reading both accumulators.  They meet before the exchange is read
       // and again before either goes on to the next unit.
       constexpr int XCH = L::STAGE_O ? L::OFF_Q : L::OFF_STAGE, XCH_T = L::STAGE_O ? L::Q_TILE_BYTES : 4 * 32 * 128;
       uint8_t* xch = gbase + XCH + (L::STAGE_O ? (k % L::QBUF) * L::Q_BUF_BYTES : 0);
+      if constexpr (L::STAGE_O) {  // (a Q tile that computed nothing may still be loading)
+        if (nact == 0 && !bwait_warp(bars + 8u * (L::B_QFULL + (k % L::QBUF)), (uint32_t)(k / L::QBUF) & 1u, abort_flag, to)) return;
+      }
       reinterpret_cast<float2*>(xch + t * XCH_T)[r] = make_float2(m, l);
       if (!meet(false)) return;
       const float2 other = reinterpret_cast<const float2*>(xch + (1 - t) * XCH_T)[r];
@@ -417,7 +413,8 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
         tmem_ld32x32b_x16_wait(both + L::O_STRIDE + ch * 16, ob);
         float x[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = fmaf(fa, __uint_as_float(oa[e]), fb * __uint_as_float(ob[e]));
+        for (int e = 0; e < 16; ++e)  // (an accumulator that nothing has gone into holds anything)
+          x[e] = (fa != 0.f ? fa * __uint_as_float(oa[e]) : 0.f) + (fb != 0.f ? fb * __uint_as_float(ob[e]) : 0.f);
         const int col = t * (D / 2) + ch * 16;
         if (row_ok && slot_out >= 0) {
 #pragma unroll
@@ -516,7 +513,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int D, bool BF16>
+template <int D, bool BF16, bool TURNS>
 __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_constant__ TileParams p) {
   using L = TileLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -553,14 +550,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
   if (warp < 4) {
     setmaxnreg_dec<L::REGS_LOADMMA>();
     if (warp == 0) {
-      tile_load_role<D>(p, base, gbase, abort_flag, lane);
+      tile_load_role<D, TURNS>(p, base, gbase, abort_flag, lane);
     } else if (warp == 1) {
-      TileEnv<D> env;
+      TileEnv<D, TURNS> env;
       mma_role<D, BF16, L>(env, p.timeout_us, base, gbase, abort_flag, tmem, lane);
     }
   } else {
     setmaxnreg_inc<L::REGS_SOFTMAX>();
-    tile_softmax_role<D, BF16>(p, base, gbase, abort_flag, tmem, (warp - 4) >> 2, warp & 3, lane);
+    tile_softmax_role<D, BF16, TURNS>(p, base, gbase, abort_flag, tmem, (warp - 4) >> 2, warp & 3, lane);
   }
 
   tc_fence_before();
@@ -572,10 +569,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ host side
-template <int D, bool BF16>
+template <int D, bool BF16, bool TURNS>
 int launch_tiles(const TileParams& p, int sms, int dev, cudaStream_t st) {
   using L = TileLayout<D>;
-  auto kern = paged_tile_kernel<D, BF16>;
+  auto kern = paged_tile_kernel<D, BF16, TURNS>;
   static std::atomic<unsigned long long> attr_set{0};  // bit per device
   const unsigned long long bit = 1ull << dev;
   if (!(attr_set.load() & bit)) {
@@ -614,8 +611,17 @@ int tile_launch(const PagedParams& base, const attn_fwd_paged_params_t& a, int s
     return rc;
   p.g_inverse = 65536u / p.g + 1;
   p.inject = host_take_inject();
-  if (a.d == 64) return bf16 ? launch_tiles<64, true>(p, sms, dev, st) : launch_tiles<64, false>(p, sms, dev, st);
-  return bf16 ? launch_tiles<128, true>(p, sms, dev, st) : launch_tiles<128, false>(p, sms, dev, st);
+  // Where no request has more rows than one Q tile, both Q tiles take the same rows and the key tiles by turns,
+  // so that one's products run while the other's softmax does.  24 requests of 3 - 6 tokens x 8 heads
+  // against up to 6k keys: 45 us by turns, 51 with the second Q tile idle.
+  const bool turns = p.max_q <= p.tile.T;
+  const auto go = [&](auto launch) { return launch(p, sms, dev, st); };
+  if (a.d == 64) {
+    if (turns) return go(bf16 ? launch_tiles<64, true, true> : launch_tiles<64, false, true>);
+    return go(bf16 ? launch_tiles<64, true, false> : launch_tiles<64, false, false>);
+  }
+  if (turns) return go(bf16 ? launch_tiles<128, true, true> : launch_tiles<128, false, true>);
+  return go(bf16 ? launch_tiles<128, true, false> : launch_tiles<128, false, false>);
 }
 
 }  // namespace attn

@@ -201,8 +201,7 @@ __device__ __forceinline__ void init_barriers(uint32_t bars, int readers = 0) {
 //             OPV(t), which the softmax waits for before it rescales O_t.
 // Each ring slot of K / V is released by a commit right after its last reader.
 // `env` is what differs between the kernels: env.unit(descriptor) at a unit's start, env.computed(t, j,
-// lane) for every (Q tile, key tile) block, where Env::ALTERNATE Env::alternate(flags) (see below), and, where
-// Env::SCRUB, env.scrub(flags, V tile, lane) once V(j) has landed and before any P.V reads it.
+// lane) for every (Q tile, key tile) block, Env::BY_TURNS (see below), and, where Env::SCRUB, env.scrub(flags, V tile, lane) once V(j) has landed and before any P.V reads it.
 template <int D, bool BF16, class L, class Env>
 __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, uint8_t* gbase,
                                          volatile int* abort_flag, uint32_t tmem, int lane) {
@@ -256,18 +255,14 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
       int new_slot0 = 0, new_slot1 = 1;
 
       // d = 64 issues a Q tile's Q.K^T before its P.V, d = 128 its P.V first.  Where key tiles go to the
-      // two Q tiles by turns (Env::alternate), Q tile 1's Q.K^T comes before all, so that it does not
+      // two Q tiles by turns (Env::BY_TURNS), Q tile 1's Q.K^T comes before all, so that it does not
       // wait for Q tile 0's P of the key tile before (the other way round the order has it so already).
 #pragma unroll
-      for (int step = Env::ALTERNATE ? -1 : 0; step < 4; ++step) {
+      for (int step = Env::BY_TURNS ? -1 : 0; step < 4; ++step) {
+        if (Env::BY_TURNS && step == (L::RING ? 2 : 3)) continue;
         const int t = step < 0 ? 1 : step >> 1;
-        bool mine = true;
-        if constexpr (Env::ALTERNATE) {
-          if (step < 0) mine = Env::alternate(flags);
-          if (step == (L::RING ? 2 : 3)) mine = !Env::alternate(flags);
-        }
         if (step < 0 || ((step & 1) == 0) == L::RING) {
-          if (mine && !end && ((flags >> t) & 1)) {
+          if (!end && ((flags >> t) & 1)) {
             if (!k_ready) {
               if (!bwait_warp(bars + 8u * (L::B_KFULL + cur_kslot), cur_kpar, abort_flag, to)) goto drain;
               tc_fence_after();
@@ -339,7 +334,8 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
           if (t == QT - 1 && have_prev) tc_commit_elect(bars + 8u * (L::B_VEMPTY + prev_vslot));
         }
         if constexpr (L::RING) {
-          if ((step & 1) && step > 0 && !end && ((flags >> t) & 1)) (t ? pslot1 : pslot0) = t ? new_slot1 : new_slot0;
+          if (step == 1 && !end && (flags & 1)) pslot0 = new_slot0;
+          if (step == 3 && !end && (flags & 2)) pslot1 = new_slot1;
         }
       }
       if (!end) tc_commit_elect(bars + 8u * (L::B_KEMPTY + cur_kslot));
