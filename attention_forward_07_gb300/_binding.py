@@ -269,7 +269,6 @@ def attn_fwd_packed(q, k, v, o, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_se
 _TABLES = struct.Struct("@10P7iP")
 _APPEND = struct.Struct("@5P7q6iP")
 _ATTEND = struct.Struct("@9PQ7q13ifiP")
-_workspace_sizes = {}
 _torch = None
 _raw_stream = None
 
@@ -387,7 +386,7 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     strides whose last dimension is contiguous), lse fp32 [Hq, total_q] or None; block_table int32 [B, W], cu_seqlens_q
     int32 [B+1], seqlens_k int32 [B] (keys per request, the new rows' own included).  One token per request, a few or whole
     chunks, mixed freely.  workspace: a uint8 tensor of attn_paged_workspace() bytes for calls that do not run at the same
-    time; None takes one from torch's allocator.  See include/attn.h."""
+    time; None uses the stream's own, or under graph capture one of the graph's memory pool.  See include/attn.h."""
     torch = _torch or _with_torch()
     dtype, index, i32 = q.dtype, q.get_device(), torch.int32
     code = _dtype_code(q)
@@ -409,31 +408,22 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
         _refuse(index, ((cu_seqlens_q, B + 1, "cu_seqlens_q"), (seqlens_k, B, "seqlens_k")), (block_table, B),
                 ((q, shape, dtype, "q"), (o, shape, dtype, "o")),
                 others=((True, f"lse must be contiguous fp32 {(Hq, total_q)} on CUDA device {index}"),))
-    current = _raw_stream(index)
-    handle = current if stream is None else _stream_on(index, stream)
+    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
     if total_q == 0:
         return
-    if workspace is None:
-        key = (index, B, Hq, Hkv, d, total_q, max_seqlen_q)
-        n = _workspace_sizes.get(key)
-        if n is None:
-            if len(_workspace_sizes) >= 4096:
-                _workspace_sizes.clear()
-            with torch.cuda.device(index):
-                n = _workspace_sizes[key] = _workspace_bytes(key[1:])
-        if handle == current:
+    at = n = 0  # no workspace: the library's own of the stream
+    if workspace is None and torch.cuda.is_current_stream_capturing():
+        with torch.cuda.device(index):  # from the graph's memory pool
+            n = _workspace_bytes((B, Hq, Hkv, d, total_q, max_seqlen_q))
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        else:  # from the launch stream's own pool, whose blocks are handed on in that stream's order
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    else:
-        n = workspace.numel() * workspace.element_size()
+    if workspace is not None:
+        n, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         _refuse(index, others=((workspace.get_device() != index or not workspace.is_contiguous(),
                                 f"workspace must be contiguous and on CUDA device {index}"),))
     width = block_table.shape[1]
     _launch(index, (_lib or library()).attn_fwd_paged,
             _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(),
-                         block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), workspace.data_ptr(), n, qs[1], qs[0],
+                         block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), at, n, qs[1], qs[0],
                          ost[1], ost[0], cs[0], cs[1], cs[2], B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size, width,
                          block_table.stride(0) if B > 1 else width, 1 if causal else 0, window_left, window_right,
                          d ** -0.5 if scale is None else scale, code, handle))
@@ -463,7 +453,7 @@ def attn_check(stream=None) -> int:
 
 
 def attn_release_workspace(stream=None) -> None:
-    """Free the custom-mask workspace the library holds for `stream` (stream-ordered)."""
+    """Free the workspace the library holds for `stream` (stream-ordered)."""
     rc = library().attn_release_workspace(_stream_handle(stream))
     if rc != 0:
         raise AttnError(rc, "attn_release_workspace")

@@ -1547,6 +1547,14 @@ int host_map5(CUtensorMap* m, const void* ptr, bool bf16, const Map5& t) {
   });
 }
 
+int host_workspace(int dev, void* stream, size_t bytes, std::unique_lock<std::mutex>& hold, void** ws) {
+  StreamState& s = *stream_state(dev, stream, true);
+  hold = std::unique_lock<std::mutex>(s.m);
+  const int rc = ensure_workspace(s, bytes, reinterpret_cast<cudaStream_t>(stream));
+  *ws = s.ws;
+  return rc;
+}
+
 int host_status_word(int dev, void* stream, unsigned int** word) {
   void* base = nullptr;
   if (cudaGetSymbolAddress(&base, g_attn_status) != cudaSuccess || !base) return ATTN_ERR_CUDA;

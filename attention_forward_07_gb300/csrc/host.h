@@ -2,7 +2,9 @@
 #pragma once
 #include <cuda.h>
 
+#include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 namespace attn {
 
@@ -28,5 +30,9 @@ int host_map5(CUtensorMap* m, const void* ptr, bool bf16, const Map5& t);
 
 // Device address of the status word of `stream` (what attn_check reads and clears).
 int host_status_word(int dev, void* stream, unsigned int** word);
+
+// The workspace that the library keeps for `stream`, grown to `bytes` where needed (stream-ordered).  `hold`
+// keeps other calls on the stream from it until the caller has enqueued what uses it.
+int host_workspace(int dev, void* stream, size_t bytes, std::unique_lock<std::mutex>& hold, void** ws);
 
 }  // namespace attn

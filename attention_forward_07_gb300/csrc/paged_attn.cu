@@ -753,7 +753,7 @@ int check_shape(const attn_fwd_paged_params_t& a) {
 }
 
 int check(const attn_fwd_paged_params_t& a) {
-  if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.block_table || !a.cu_seqlens_q || !a.seqlens_k || !a.workspace)
+  if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.block_table || !a.cu_seqlens_q || !a.seqlens_k)
     return ATTN_ERR_INVALID;
   int rc = check_shape(a);
   if (rc != ATTN_OK) return rc;
@@ -826,7 +826,7 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
   int sms = 0, dev = 0;
   if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
   const Plan plan(a, sms);
-  if (a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
+  if (a.workspace && a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
   RowsParams p = {};
   p.q = static_cast<const uint16_t*>(a.q);
   p.k = static_cast<const uint16_t*>(a.k_cache);
@@ -857,11 +857,20 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
   p.er = a.causal ? 0 : a.window_right;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+  void* scratch = a.workspace;
+  std::unique_lock<std::mutex> hold;  // until the launches are enqueued
+  if (!scratch) {
+    // a captured call would share the stream's workspace with whatever runs beside its replays
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) return ATTN_ERR_INVALID;
+    if ((rc = host_workspace(dev, a.stream, plan.bytes, hold, &scratch)) != ATTN_OK) return rc;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(scratch);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   p.split = reinterpret_cast<Split*>(ws + plan.off_split);
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
   p.timeout_us = host_timeout_us();
   p.rows_grid = plan.rows_grid;
   p.tile.T = plan.T;

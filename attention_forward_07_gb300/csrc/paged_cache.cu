@@ -8,6 +8,8 @@
 
 #include "attn.h"
 #include "host.h"
+#include "paged.cuh"
+#include "ptx.cuh"
 
 namespace attn {
 namespace {
@@ -20,7 +22,8 @@ namespace {
 //
 // One launch and no state between calls: every CTA sums all lengths by itself (a block-wide scan
 // of two counters, kept in shared memory), then the threads of all CTAs share out the pages and
-// the rows and find their request by bisection.  A slot on a page added in this call comes
+// the rows (four neighbours to a thread where there are more rows than threads) and find their request
+// by bisection.  A slot on a page added in this call comes
 // straight from the free list, so no CTA waits for another's table entries.  The CTAs are one
 // cluster, and its barrier orders the reads of free_count before its one write, which may be in
 // place.  What bounds it is latency: the chain lengths -> scan -> bisection -> free list -> slot.
@@ -50,14 +53,16 @@ __device__ __forceinline__ int holder(const int* pre, int B, int x) {
 
 __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __grid_constant__ TablesParams p) {
   const attn_paged_tables_params_t& a = p.a;
-  extern __shared__ int pre[];       // rows_pre[B + 1], need_pre[B + 1]
+  extern __shared__ int pre[];       // rows_pre[B + 1], need_pre[B + 1], ctx[B]
   __shared__ int2 warp_sum[32];
   const int B = a.B, P = a.page_size;
   int* rows_pre = pre;
   int* need_pre = pre + B + 1;
+  int* ctx_s = pre + 2 * (B + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int count = min(max(*a.free_count, 0), a.max_free);
-  const int count_in = *a.free_count;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int count_in = *a.free_count, count = min(max(count_in, 0), a.max_free);
   __syncthreads();
   cluster_arrive();  // free_count is read (the wait stands before its write)
 
@@ -67,6 +72,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
   int2 sum = make_int2(0, 0);
   for (int b = b0; b < b1; ++b) {
     const int ctx = max(__ldg(a.ctx_lens + b), 0), add = max(__ldg(a.new_lens + b), 0);
+    ctx_s[b] = ctx;
     rows_pre[b] = sum.x;
     need_pre[b] = sum.y;
     sum.x += add;
@@ -108,29 +114,46 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
     for (int b = tid; b <= B; b += TABLES_THREADS) a.cu_seqlens_q[b] = rows_pre[b];
   for (int n = gid; n < need; n += nthr) {
     const int b = holder(need_pre, B, n);
-    const int i = (max(__ldg(a.ctx_lens + b), 0) + P - 1) / P + (n - need_pre[b]);
+    const int i = (ctx_s[b] + P - 1) / P + (n - need_pre[b]);
     const int id = free_page(n);
     const bool fits = (unsigned)i < (unsigned)a.table_width;
     if (fits) a.block_table[(long long)b * a.table_stride + i] = id;
     bad |= id < 0 || !fits;
   }
-  for (int t = gid; t < a.max_rows; t += nthr) {
-    int slot = -1, pos = -1;
-    if (t < total) {
-      const int b = holder(rows_pre, B, t);
-      const int ctx = max(__ldg(a.ctx_lens + b), 0), held = (ctx + P - 1) / P;
-      pos = ctx + (t - rows_pre[b]);
-      const int i = pos / P;
-      int id = -1;
-      if ((unsigned)i < (unsigned)a.table_width) {
-        id = i < held ? a.block_table[(long long)b * a.table_stride + i] : free_page(need_pre[b] + i - held);
-        if (id >= a.num_pages) id = -1;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+  const int each = a.max_rows > nthr ? 4 : 1;
+  for (int t0 = each * gid; t0 < a.max_rows; t0 += each * nthr) {
+    int slot[4] = {-1, -1, -1, -1}, at[4] = {-1, -1, -1, -1};
+    int b = -1, page = -1, id = -1;  // request, page (of the request) and its id, of the row before
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = t0 + k;
+      if (k >= each || t >= min(total, a.max_rows)) break;
+      if (b < 0) b = holder(rows_pre, B, t);
+      while (t >= rows_pre[b + 1]) ++b, page = -1;
+      const int pos = ctx_s[b] + (t - rows_pre[b]), i = pos / P;
+      if (i != page) {
+        page = i;
+        id = -1;
+        if ((unsigned)i < (unsigned)a.table_width) {
+          const int held = (ctx_s[b] + P - 1) / P;
+          id = i < held ? a.block_table[(long long)b * a.table_stride + i] : free_page(need_pre[b] + i - held);
+          if (id >= a.num_pages) id = -1;
+        }
       }
-      if (id >= 0) slot = id * P + (pos - i * P);
+      at[k] = pos;
+      if (id >= 0) slot[k] = id * P + (pos - i * P);
       else bad = true;
     }
-    a.slots[t] = slot;
-    if (a.positions) a.positions[t] = pos;
+    if (each == 4 && wide && t0 + 4 <= a.max_rows) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(at[0], at[1], at[2], at[3]);
+    } else {
+      for (int k = 0; k < each && t0 + k < a.max_rows; ++k) {
+        a.slots[t0 + k] = slot[k];
+        if (a.positions) a.positions[t0 + k] = at[k];
+      }
+    }
   }
   if (bad) atomicOr(p.status, STATUS_PAGE);
   cluster_wait();
@@ -155,6 +178,8 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS) paged_append_kernel(const _
   const int lane = threadIdx.x & 31;
   const int nwarps = gridDim.x * APPEND_WARPS;
   const int per_side = a.Hkv * CPR;
+  grid_launch_dependents();
+  grid_dependency_wait();
   for (int t = blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5); t < a.rows; t += nwarps) {
     const int slot = __ldg(a.slots + t);
     const int page = slot / a.page_size;
@@ -209,7 +234,7 @@ int attn_paged_tables(const attn_paged_tables_params_t* params) {
                           (const void*)a.free_count, (const void*)a.free_count_out, (const void*)a.cu_seqlens_q,
                           (const void*)a.seqlens_k, (const void*)a.slots, (const void*)a.positions})
     if (misaligned(ptr, 4)) return ATTN_ERR_INVALID;
-  if (a.B < 1 || a.B > TABLES_MAX_B || a.table_width < 1 || a.table_stride < a.table_width || a.max_free < 0 || a.max_rows < 1 ||
+  if (a.B < 1 || a.B > TABLES_MAX_B || a.table_width < 1 || a.table_stride < a.table_width || a.max_free < 0 || a.max_rows < 1 || a.max_rows > (1 << 30) ||
       a.page_size < 16 || a.page_size % 16 != 0 || a.num_pages < 1 || (long long)a.num_pages * a.page_size > INT_MAX)
     return ATTN_ERR_INVALID;
   int sms = 0, dev = 0;
@@ -217,7 +242,7 @@ int attn_paged_tables(const attn_paged_tables_params_t* params) {
   if (rc != ATTN_OK) return rc;
   TablesParams p{a, nullptr};
   if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-  const size_t smem = 2 * ((size_t)a.B + 1) * sizeof(int);
+  const size_t smem = (3 * (size_t)a.B + 2) * sizeof(int);
   if (smem > 47 * 1024 &&
       cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
@@ -229,12 +254,14 @@ int attn_paged_tables(const attn_paged_tables_params_t* params) {
   cfg.blockDim = dim3(TABLES_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(a.stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, paged_tables_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -260,11 +287,9 @@ int attn_paged_append(const attn_paged_append_params_t* params) {
   AppendParams p{a, nullptr};
   if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
   const long long want = ((long long)a.rows + APPEND_WARPS - 1) / APPEND_WARPS;
-  const int grid = (int)(want < 16ll * sms ? want : 16ll * sms);
+  const int grid = (int)(want < (1 << 30) ? want : (1 << 30));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
-  if (a.d == 64) paged_append_kernel<64><<<grid, 32 * APPEND_WARPS, 0, st>>>(p);
-  else paged_append_kernel<128><<<grid, 32 * APPEND_WARPS, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_dependent(a.d == 64 ? paged_append_kernel<64> : paged_append_kernel<128>, dim3(grid), 32 * APPEND_WARPS, 0, st, p);
 }
 
 }  // extern "C"

@@ -59,9 +59,10 @@
  *     of one shape therefore allocate nothing after the first.  Variable-length
  *     batches (attn_fwd_ex with per-entry lengths or packed offsets) use the same
  *     workspace for their work order, B*ceil(max Sq/256) ints after the mask
- *     scratch (256-byte aligned).  The workspace is held until
+ *     scratch (256-byte aligned), and so does attn_fwd_paged without a workspace of the caller's.
+ *     The workspace is held until
  *     attn_release_workspace(stream) or process exit: release it before
- *     destroying a stream that has run custom masks or variable-length batches.
+ *     destroying a stream that has run custom masks, variable-length batches or paged attention.
  *   - Errors: arguments are validated before any launch (ATTN_ERR_INVALID /
  *     ATTN_ERR_UNSUPPORTED, nothing launched); a failed launch returns
  *     ATTN_ERR_CUDA.  The work is asynchronous: a kernel that gives up on a
@@ -245,7 +246,7 @@ int attn_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float
  * of the page that request b's new tokens start in) is out of range, the slots concerned
  * are -1 and so are the table entries that exist; rows past max_rows get no slot.  Each of these
  * sets ATTN_ERR_PAGE.  cu_seqlens_q and seqlens_k are as if all had been well; *free_count_out
- * is never below 0.  No output overlaps an input but free_count_out.  1 <= B <= 16384; num_pages*page_size, and the sums of the lengths, fit 31 bits.
+ * is never below 0.  No output overlaps an input but free_count_out.  1 <= B <= 16384, max_rows <= 2^30; num_pages*page_size, and the sums of the lengths, fit 31 bits.
  */
 typedef struct {
     const int *ctx_lens, *new_lens; /* [B] */
@@ -300,10 +301,12 @@ int attn_paged_append(const attn_paged_append_params_t *params);
  * window, or on pages listed for none of its keys, may hold anything; those that one of its query
  * rows sees hold finite values.  A page id out of range sets ATTN_ERR_PAGE; its keys then count as
  * zeros.
- * workspace: device memory, 256-byte aligned, of at least the size that
+ * workspace: NULL, or device memory, 256-byte aligned, of at least the size that
  * attn_paged_workspace gives for the same parameters; its contents are of no account before and
- * after the call, and calls that may run at the same time (two captured graphs among
- * them) each take their own.
+ * after the call, and calls that may run at the same time (two captured graphs among them) each
+ * take their own.  With NULL the call uses the stream's workspace (see the conventions), which
+ * later calls on the stream share in stream order; a call that is being captured into a graph
+ * brings its own (NULL is ATTN_ERR_INVALID there).
  */
 typedef struct {
     const void *q, *k_cache, *v_cache;
@@ -344,7 +347,7 @@ int attn_check(void *stream);
 
 /*
  * attn_release_workspace -- free (in stream order, cudaFreeAsync on `stream`) the
- * custom-mask workspace the library holds for `stream` on the current device, if
+ * workspace the library holds for `stream` on the current device, if
  * any.  Call it before destroying a stream that ran custom masks; a later call on
  * the stream simply allocates a new one.  ATTN_OK, or ATTN_ERR_CUDA.
  */

@@ -33,14 +33,14 @@ ATTEND = dict(q=P, k_cache=P, v_cache=P, o=P, block_table=P, cu_seqlens_q=P, seq
 REFUSALS = (
     [("tables", {k: 0}, -1) for k in TABLES if TABLES[k] == P] +
     [("tables", {k: P + 2}, -1) for k in TABLES if TABLES[k] == P] +
-    [("tables", kw, -1) for kw in (dict(B=0), dict(B=16385), dict(table_width=0), dict(table_stride=3), dict(max_free=-1), dict(max_rows=0),
+    [("tables", kw, -1) for kw in (dict(B=0), dict(B=16385), dict(table_width=0), dict(table_stride=3), dict(max_free=-1), dict(max_rows=0), dict(max_rows=(1 << 30) + 1),
                                    dict(page_size=8), dict(page_size=24), dict(num_pages=0), dict(num_pages=INT_MAX), dict(positions=P + 1))] +
     [("append", {k: 0}, -1) for k in ("k_new", "v_new", "k_cache", "v_cache", "slots")] +
     [("append", {k: P + 8}, -1) for k in ("k_new", "v_new", "k_cache", "v_cache")] +
     [("append", {k: v}, -1) for k in APPEND if k.endswith("stride") for v in (60, -64)] +
     [("append", kw, st) for kw, st in ((dict(d=96), -2), (dict(dtype=2), -2), (dict(rows=0), -1), (dict(Hkv=0), -1), (dict(slots=P + 1), -1),
                                        (dict(page_size=20), -1), (dict(num_pages=INT_MAX), -1))] +
-    [("attend", {k: 0}, -1) for k in ATTEND if ATTEND[k] == P] +
+    [("attend", {k: 0}, -1) for k in ATTEND if ATTEND[k] == P and k != "workspace"] +
     [("attend", {k: P + 8}, -1) for k in ("q", "k_cache", "v_cache", "o", "workspace")] +
     [("attend", {k: P + 2}, -1) for k in ("lse", "block_table", "cu_seqlens_q", "seqlens_k")] +
     [("attend", {k: v}, -1) for k in ATTEND if k.endswith("_stride") and k != "table_stride" for v in (60, -64)] +
