@@ -14,6 +14,7 @@
 namespace attn {
 
 constexpr int ROWS_MAX = 16;
+constexpr int ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile
 
 // Written by the plan.  Line coordinates count key tiles over all (unit, head) pairs in order, heads inside.

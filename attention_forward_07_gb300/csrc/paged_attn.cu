@@ -31,10 +31,11 @@ struct Split {
 };
 
 struct RowsParams : PagedParams {
-  float* part_o;    // [2 * rows_grid][16][D] partial sums of V, not normalised
-  float2* part_ml;  // [2 * rows_grid][16] their exponent base (exp2 domain) and sum of weights
+  float* part_o;    // [2 * rows_grid][slot_rows][D] partial sums of V, not normalised
+  float2* part_ml;  // [2 * rows_grid][slot_rows] their exponent base (exp2 domain) and sum of weights
   Split* split;     // [rows_grid]
   int rows_grid;    // CTAs of this path
+  int slot_rows;    // rows of a slot: 16 or 32
 };
 
 // ------------------------------------------------------------------ few rows: the memory-bound path
@@ -51,18 +52,21 @@ struct RowsParams : PagedParams {
 //  * a lane holds the places of the next 32 page rows, so the table is read once per 32 copies;
 //  * mma.sync with the keys as the N side: 16 rows are its smallest M, and its operands come by
 //    ldmatrix straight from the copied rows (128-byte tcgen05 tiles would be an eighth full).
-template <int D>
+template <int D, int MT>
 struct Rows {
   static constexpr int WARPS = 4, NTHREADS = 32 * WARPS;
+  static constexpr int ROWS = 16 * MT;            // packed rows of an item at most
   static constexpr int KPW = D == 128 ? 16 : 32;  // keys of a warp's stage: 8 KiB of K and V
   static constexpr int NG = KPW / 16;             // groups of 16 keys: each lies in one page
   static constexpr int TK = WARPS * KPW;          // keys of a tile
   static constexpr int NST = 3;
   static constexpr int STAGE = 2 * KPW * D * 2;
-  static constexpr int SMEM = WARPS * NST * STAGE;
+  // Q operands in registers, or, where they and the accumulators would not fit, in shared memory
+  static constexpr bool Q_SMEM = MT * D > 128;
+  static constexpr int OFF_Q = WARPS * NST * STAGE;
+  static constexpr int SMEM = OFF_Q + (Q_SMEM ? ROWS * D * 2 : 0);
   static constexpr int CTAS_PER_SM = 2;
-  static constexpr int MIN_TILES = 2;             // tiles a CTA takes at least
-  static_assert(STAGE >= 16 * D * 4, "a stage holds a warp's accumulator at the item's end");
+  static_assert(STAGE >= 16 * D * 4, "a stage holds a 16-row accumulator of the warp at the item's end");
   static_assert(NTHREADS == 128, "the plan and block_scan are written for four warps");
 };
 
@@ -73,7 +77,7 @@ struct RowsItem {
   int row0, R, off, sk;
   int lo, hi, t0, t1;
 };
-template <int D>
+template <class C>
 __device__ __forceinline__ RowsItem rows_request(const RowsParams& p, int b) {
   RowsItem it;
   int sq;
@@ -83,17 +87,17 @@ __device__ __forceinline__ RowsItem rows_request(const RowsParams& p, int b) {
   it.lo = row_lo(p, 0, it.off);
   it.hi = row_hi(p, sq - 1, it.off, it.sk);
   if (it.hi <= it.lo) it.lo = it.hi = 0;
-  it.t0 = it.lo / Rows<D>::TK;
-  it.t1 = it.hi > it.lo ? (it.hi - 1) / Rows<D>::TK + 1 : it.t0 + 1;
-  if (it.R > ROWS_MAX || it.R == 0) it.R = it.t0 = it.t1 = 0;
+  it.t0 = it.lo / C::TK;
+  it.t1 = it.hi > it.lo ? (it.hi - 1) / C::TK + 1 : it.t0 + 1;
+  if (it.R > C::ROWS || it.R == 0) it.R = it.t0 = it.t1 = 0;
   return it;
 }
 // The item after head h of request b.
-template <int D>
+template <class C>
 __device__ __forceinline__ void rows_next(const RowsParams& p, int& b, int& h, RowsItem& it) {
   if (++h < p.Hkv) return;
   h = 0;
-  do it = rows_request<D>(p, ++b);
+  do it = rows_request<C>(p, ++b);
   while (it.R == 0);
 }
 
@@ -295,9 +299,9 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_kernel(const __grid_constant__ RowsParams p) {
-  using C = Rows<D>;
+template <int D, int MT, bool BF16>
+__global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_SM) rows_kernel(const __grid_constant__ RowsParams p) {
+  using C = Rows<D, MT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   grid_launch_dependents();
   grid_dependency_wait();
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
   }
   __shared__ long long warp_sum[PLAN_WARPS];
   __shared__ int3 start_s;            // request, head and tile that the run begins with
-  __shared__ float2 ml_s[C::WARPS][16];
+  __shared__ float2 ml_s[C::WARPS][C::ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- this CTA's run: sum the weights, find where it begins
@@ -315,9 +319,9 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
   const int rb0 = min(tid * per, p.B), rb1 = min(rb0 + per, p.B);
   const auto weight = [&](const RowsItem& it) { return (long long)(it.t1 - it.t0) * p.Hkv; };
   long long own = 0, n;
-  for (int b = rb0; b < rb1; ++b) own += weight(rows_request<D>(p, b));
+  for (int b = rb0; b < rb1; ++b) own += weight(rows_request<C>(p, b));
   const long long before = block_scan(own, warp_sum, n);
-  const int ctas = (int)min((long long)p.rows_grid, (n + C::MIN_TILES - 1) / C::MIN_TILES);
+  const int ctas = (int)min((long long)p.rows_grid, n);
   const int cta = (int)blockIdx.x - ((int)gridDim.x - p.rows_grid);
   if (tid == 0) p.split[cta].b = -1;
   if (cta >= ctas) return;
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
   if (run0 >= before && run0 < before + own) {
     long long at = before;
     for (int b = rb0;; ++b) {
-      const RowsItem it = rows_request<D>(p, b);
+      const RowsItem it = rows_request<C>(p, b);
       const long long w = weight(it);
       if (run0 < at + w) {
         const int tiles = it.t1 - it.t0, h = (int)((run0 - at) / tiles);
@@ -345,14 +349,14 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
 
   // ---- the copies run ahead of the products, across items: their own place in the run
   int b = start_s.x, h = start_s.y, tile = start_s.z;
-  RowsItem it = rows_request<D>(p, b);
+  RowsItem it = rows_request<C>(p, b);
   int cb = b, ch = h, ctile = tile, cleft = run, ccount = 0, cslot = 0;
   RowsItem cit = it;
   long long place = -1;  // lane's entry of the item's next 32 groups: element offset of its first row, -1 = none
   const auto issue = [&] {
     if (cleft > 0) {
       if (ctile == cit.t1) {
-        rows_next<D>(p, cb, ch, cit);
+        rows_next<C>(p, cb, ch, cit);
         ctile = cit.t0;
         ccount = 0;
       }
@@ -401,29 +405,48 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
     const int ntiles = min(it.t1 - tile, left);
     const bool begins = tile == it.t0, ends = tile + ntiles == it.t1;
 
-    // Q fragments: rows fr and fr + 8 (rows past the last one are copies of it)
-    uint32_t qf[D / 16][4];
-    int klo[2], khi[2];
+    // Q operands of each 16-row tile (rows past the last one are copies of it), and the keys of rows fr, fr + 8
+    const auto q_row = [&](int r) {
+      const int rr = min(r, it.R - 1), i = rr / p.g;
+      return p.q + (long long)(it.row0 + i) * p.q_row + (long long)(h * p.g + rr - i * p.g) * p.q_head;
+    };
+    uint32_t qf[C::Q_SMEM ? 1 : MT][D / 16][4];
+    int klo[MT][2], khi[MT][2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = min(fr + 8 * x, it.R - 1);
-      const int i = r / p.g;
-      klo[x] = row_lo(p, i, it.off);
-      khi[x] = row_hi(p, i, it.off, it.sk);
-      const uint16_t* src = p.q + (long long)(it.row0 + i) * p.q_row + (long long)(h * p.g + r - i * p.g) * p.q_head + fc;
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        qf[s][x] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16));
-        qf[s][x + 2] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16 + 8));
+      for (int x = 0; x < 2; ++x) {
+        const int r = mt * 16 + fr + 8 * x, i = min(r, it.R - 1) / p.g;
+        klo[mt][x] = row_lo(p, i, it.off);
+        khi[mt][x] = row_hi(p, i, it.off, it.sk);
+        if constexpr (!C::Q_SMEM) {
+          const uint16_t* src = q_row(r) + fc;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            qf[mt][s][x] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16));
+            qf[mt][s][x + 2] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16 + 8));
+          }
+        }
       }
+    if constexpr (C::Q_SMEM) {
+      for (int e = tid; e < C::ROWS * CPR; e += C::NTHREADS) {
+        const int r = e / CPR, c = e % CPR;
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + r * (D * 2) + ((c ^ (r & 7)) * 16)) = __ldg(reinterpret_cast<const uint4*>(q_row(r)) + c);
+      }
+      __syncthreads();
     }
     // tiles whose every key is kept by every row need no mask
     const int lo_all = row_lo(p, (it.R - 1) / p.g, it.off), hi_all = row_hi(p, 0, it.off, it.sk);
 
-    float o[D / 8][4];
+    float o[MT][D / 8][4];
+    float m[MT][2], l[MT][2];
 #pragma unroll
-    for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) o[mt][x][0] = o[mt][x][1] = o[mt][x][2] = o[mt][x][3] = 0.f;
+    }
     float* exchange = nullptr;  // the slot of the last stage, which no copy takes before the join
 
     for (int s = 0; s < ntiles; ++s) {
@@ -436,146 +459,180 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
       const int key0 = (tile + s) * C::TK + warp * C::KPW;
       if (key0 >= it.hi || key0 + C::KPW <= it.lo) continue;  // no key of this warp's quarter
 
-      // S = Q K^T: 16 rows x KPW keys
-      float sc[2 * C::NG][4];
+      // S = Q K^T: ROWS rows x KPW keys
+      float sc[MT][2 * C::NG][4];
 #pragma unroll
-      for (int x = 0; x < 2 * C::NG; ++x) sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int x = 0; x < 2 * C::NG; ++x) sc[mt][x][0] = sc[mt][x][1] = sc[mt][x][2] = sc[mt][x][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t qa[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if constexpr (C::Q_SMEM) {
+            const int r = mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * ks + (lane >> 4);
+            ldsm_x4(smem_u32(smem) + C::OFF_Q + r * (D * 2) + ((c ^ (r & 7)) * 16), qa[mt]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qa[mt][e] = qf[mt][ks][e];
+          }
+        }
 #pragma unroll
         for (int gq = 0; gq < C::NG; ++gq) {
           uint32_t kf[4];
           const int r = gq * 16 + (lane >> 4) * 8 + (lane & 7), c = 2 * ks + ((lane >> 3) & 1);
           ldsm_x4(st + r * (D * 2) + ((c ^ (r & 7)) * 16), kf);
-          mma_16816<BF16>(sc[2 * gq], qf[ks], kf[0], kf[1]);
-          mma_16816<BF16>(sc[2 * gq + 1], qf[ks], kf[2], kf[3]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_16816<BF16>(sc[mt][2 * gq], qa[mt], kf[0], kf[1]);
+            mma_16816<BF16>(sc[mt][2 * gq + 1], qa[mt], kf[2], kf[3]);
+          }
         }
       }
-      if (key0 < lo_all || key0 + C::KPW > hi_all) {
+      uint32_t pf[MT][C::NG][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (key0 < lo_all || key0 + C::KPW > hi_all) {
+#pragma unroll
+          for (int x = 0; x < 2 * C::NG; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + x * 8 + fc + (e & 1);
+              if (key < klo[mt][e >> 1] || key >= khi[mt][e >> 1]) sc[mt][x][e] = -INFINITY;
+            }
+        }
+        // running maximum (exp2 domain): it moves only when it grows by more than 8, so the
+        // accumulator is rarely rescaled and weights stay below 2^8
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < 2 * C::NG; ++x) {
+          mx[0] = fmaxf(mx[0], fmaxf(sc[mt][x][0], sc[mt][x][1]));
+          mx[1] = fmaxf(mx[1], fmaxf(sc[mt][x][2], sc[mt][x][3]));
+        }
+        bool grow = false;
+        float mn[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2)) * p.scale_log2;
+          mn[x] = mx[x] > m[mt][x] + 8.f ? mx[x] : m[mt][x];
+          grow |= mn[x] != m[mt][x];
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float alpha = mn[x] == m[mt][x] ? 1.f : ex2_approx(m[mt][x] - mn[x]);
+            l[mt][x] *= alpha;
+            m[mt][x] = mn[x];
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y) {
+              o[mt][y][2 * x] *= alpha;
+              o[mt][y][2 * x + 1] *= alpha;
+            }
+          }
+        }
+        const float mu[2] = {m[mt][0] == -INFINITY ? 0.f : m[mt][0], m[mt][1] == -INFINITY ? 0.f : m[mt][1]};
 #pragma unroll
         for (int x = 0; x < 2 * C::NG; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = key0 + x * 8 + fc + (e & 1);
-            if (key < klo[e >> 1] || key >= khi[e >> 1]) sc[x][e] = -INFINITY;
+            sc[mt][x][e] = ex2_approx(fmaf(sc[mt][x][e], p.scale_log2, -mu[e >> 1]));
+            l[mt][e >> 1] += sc[mt][x][e];
           }
-      }
-      // running maximum (exp2 domain): it moves only when it grows by more than 8, so the
-      // accumulator is rarely rescaled and weights stay below 2^8
-      float mx[2] = {-INFINITY, -INFINITY};
+        // the weights rounded to the values' type, as a matrix instruction takes them; the sum l keeps them
+        // in 32 bits
 #pragma unroll
-      for (int x = 0; x < 2 * C::NG; ++x) {
-        mx[0] = fmaxf(mx[0], fmaxf(sc[x][0], sc[x][1]));
-        mx[1] = fmaxf(mx[1], fmaxf(sc[x][2], sc[x][3]));
-      }
-      bool grow = false;
-      float mn[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2)) * p.scale_log2;
-        mn[x] = mx[x] > m[x] + 8.f ? mx[x] : m[x];
-        grow |= mn[x] != m[x];
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float alpha = mn[x] == m[x] ? 1.f : ex2_approx(m[x] - mn[x]);
-          l[x] *= alpha;
-          m[x] = mn[x];
-#pragma unroll
-          for (int y = 0; y < D / 8; ++y) {
-            o[y][2 * x] *= alpha;
-            o[y][2 * x + 1] *= alpha;
-          }
+        for (int gq = 0; gq < C::NG; ++gq) {
+          pf[mt][gq][0] = pack2<BF16>(sc[mt][2 * gq][0], sc[mt][2 * gq][1]);
+          pf[mt][gq][1] = pack2<BF16>(sc[mt][2 * gq][2], sc[mt][2 * gq][3]);
+          pf[mt][gq][2] = pack2<BF16>(sc[mt][2 * gq + 1][0], sc[mt][2 * gq + 1][1]);
+          pf[mt][gq][3] = pack2<BF16>(sc[mt][2 * gq + 1][2], sc[mt][2 * gq + 1][3]);
         }
       }
-      const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-#pragma unroll
-      for (int x = 0; x < 2 * C::NG; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[x][e] = ex2_approx(fmaf(sc[x][e], p.scale_log2, -mu[e >> 1]));
-          l[e >> 1] += sc[x][e];
-        }
-      // O += P V, the weights rounded to the values' type (as a matrix instruction takes them; the
-      // sum l keeps them in 32 bits)
+      // O += P V
 #pragma unroll
       for (int gq = 0; gq < C::NG; ++gq) {
-        const uint32_t pf[4] = {pack2<BF16>(sc[2 * gq][0], sc[2 * gq][1]), pack2<BF16>(sc[2 * gq][2], sc[2 * gq][3]),
-                                pack2<BF16>(sc[2 * gq + 1][0], sc[2 * gq + 1][1]), pack2<BF16>(sc[2 * gq + 1][2], sc[2 * gq + 1][3])};
         const int r = gq * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           uint32_t vf[4];
           const int c = 2 * x + (lane >> 4);
           ldsm_x4_trans(st + C::KPW * D * 2 + r * (D * 2) + ((c ^ (r & 7)) * 16), vf);
-          mma_16816<BF16>(o[2 * x], pf, vf[0], vf[1]);
-          mma_16816<BF16>(o[2 * x + 1], pf, vf[2], vf[3]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_16816<BF16>(o[mt][2 * x], pf[mt][gq], vf[0], vf[1]);
+            mma_16816<BF16>(o[mt][2 * x + 1], pf[mt][gq], vf[2], vf[3]);
+          }
         }
       }
     }
     __syncwarp();  // every lane has read the last stage
 
-    // ---- join the four warps, each through the slot of its last stage: row r's 8-column chunk c at chunk
-    // c ^ (r & 7)
+    // ---- join the four warps, 16 rows at a time, each through the slot of its last stage: row r's 8-column
+    // chunk c at chunk c ^ (r & 7)
     float* mine = exchange + warp * (C::NST * C::STAGE / 4);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      const int r = fr + 8 * x;
-      if ((lane & 3) == 0) ml_s[warp][r] = make_float2(m[x], l[x]);
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt > 0) __syncthreads();  // the 16 rows before have been read
 #pragma unroll
-      for (int y = 0; y < D / 8; ++y)
-        *reinterpret_cast<float2*>(mine + r * D + ((y ^ (r & 7)) * 8) + fc) = make_float2(o[y][2 * x], o[y][2 * x + 1]);
-    }
-    __syncthreads();
-    const int r = tid / 8;
-    if (r < it.R) {
-      float mm = -INFINITY;
+      for (int x = 0; x < 2; ++x) {
+        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
+        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
+        const int r = fr + 8 * x;
+        if (mt * 16 + r >= it.R) continue;
+        if ((lane & 3) == 0) ml_s[warp][mt * 16 + r] = make_float2(m[mt][x], l[mt][x]);
 #pragma unroll
-      for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml_s[w][r].x);
-      float f[C::WARPS], ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < C::WARPS; ++w) {
-        f[w] = ml_s[w][r].x == -INFINITY ? 0.f : ex2_approx(ml_s[w][r].x - mm);
-        ll += f[w] * ml_s[w][r].y;
+        for (int y = 0; y < D / 8; ++y)
+          *reinterpret_cast<float2*>(mine + r * D + ((y ^ (r & 7)) * 8) + fc) = make_float2(o[mt][y][2 * x], o[mt][y][2 * x + 1]);
       }
-      const bool whole = begins && ends;
-      const int at = (2 * cta + (begins ? 1 : 0)) * 16 + r;  // (a part's place)
-      const int i = r / p.g, hq = h * p.g + r - i * p.g;
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      __syncthreads();
+      const int rs = tid / 8, r = mt * 16 + rs;
+      if (r < it.R) {
+        float mm = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        const int phys = (tid & 7) + 8 * j, col = (phys ^ (r & 7)) * 8;
-        float acc[8] = {};
+        for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml_s[w][r].x);
+        float f[C::WARPS], ll = 0.f;
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) {
-          const float4* src = reinterpret_cast<const float4*>(exchange + w * (C::NST * C::STAGE / 4) + r * D + phys * 8);
-          const float4 a = src[0], c = src[1];
-          acc[0] = fmaf(f[w], a.x, acc[0]);
-          acc[1] = fmaf(f[w], a.y, acc[1]);
-          acc[2] = fmaf(f[w], a.z, acc[2]);
-          acc[3] = fmaf(f[w], a.w, acc[3]);
-          acc[4] = fmaf(f[w], c.x, acc[4]);
-          acc[5] = fmaf(f[w], c.y, acc[5]);
-          acc[6] = fmaf(f[w], c.z, acc[6]);
-          acc[7] = fmaf(f[w], c.w, acc[7]);
+          f[w] = ml_s[w][r].x == -INFINITY ? 0.f : ex2_approx(ml_s[w][r].x - mm);
+          ll += f[w] * ml_s[w][r].y;
         }
-        if (whole) {
-          *reinterpret_cast<uint4*>(p.o + (long long)(it.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
-              make_uint4(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv),
-                         pack2<BF16>(acc[4] * inv, acc[5] * inv), pack2<BF16>(acc[6] * inv, acc[7] * inv));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (long long)at * D + col);
-          dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        const bool whole = begins && ends;
+        const int at = (2 * cta + (begins ? 1 : 0)) * C::ROWS + r;  // (a part's place)
+        const int i = r / p.g, hq = h * p.g + r - i * p.g;
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          const int phys = (tid & 7) + 8 * j, col = (phys ^ (rs & 7)) * 8;
+          float acc[8] = {};
+#pragma unroll
+          for (int w = 0; w < C::WARPS; ++w) {
+            const float4* src = reinterpret_cast<const float4*>(exchange + w * (C::NST * C::STAGE / 4) + rs * D + phys * 8);
+            const float4 a = src[0], c = src[1];
+            acc[0] = fmaf(f[w], a.x, acc[0]);
+            acc[1] = fmaf(f[w], a.y, acc[1]);
+            acc[2] = fmaf(f[w], a.z, acc[2]);
+            acc[3] = fmaf(f[w], a.w, acc[3]);
+            acc[4] = fmaf(f[w], c.x, acc[4]);
+            acc[5] = fmaf(f[w], c.y, acc[5]);
+            acc[6] = fmaf(f[w], c.z, acc[6]);
+            acc[7] = fmaf(f[w], c.w, acc[7]);
+          }
+          if (whole) {
+            *reinterpret_cast<uint4*>(p.o + (long long)(it.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
+                make_uint4(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv),
+                           pack2<BF16>(acc[4] * inv, acc[5] * inv), pack2<BF16>(acc[6] * inv, acc[7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + (long long)at * D + col);
+            dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+          }
         }
-      }
-      if ((tid & 7) == 0) {
-        if (!whole) p.part_ml[at] = make_float2(mm, ll);
-        else if (p.lse) p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
+        if ((tid & 7) == 0) {
+          if (!whole) p.part_ml[at] = make_float2(mm, ll);
+          else if (p.lse) p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
+        }
       }
     }
     if (begins && !ends && tid == 0) {
@@ -587,7 +644,7 @@ __global__ void __launch_bounds__(Rows<D>::NTHREADS, Rows<D>::CTAS_PER_SM) rows_
 
     left -= ntiles;
     if (left > 0) {
-      rows_next<D>(p, b, h, it);
+      rows_next<C>(p, b, h, it);
       tile = it.t0;
     }
   }
@@ -609,7 +666,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int items = p.rows_grid;
+  const int halves = p.slot_rows / JOIN_ROWS, items = p.rows_grid * halves;
   const int total = items + (p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
     int rows, row0, h, parts, first, stride, slot0;  // part k of row r: record (k ? slot0 + k * stride : first) + r
@@ -617,17 +674,19 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
     const float* part_o;
     const float2* part_ml;
     if (x < items) {
-      const Split sp = p.split[x];
+      const int c = x / halves;
+      const Split sp = p.split[c];
       if (sp.b < 0) continue;
       int sq, sk;
       request_span(p, sp.b, row0, sq, sk);
-      rows = sq * p.g;
-      prow = 0;
+      prow = x % halves * JOIN_ROWS;
+      rows = min(sq * p.g - prow, JOIN_ROWS);
+      if (rows <= 0) continue;
       h = sp.h;
       parts = sp.parts;
-      first = (2 * x + 1) * 16;
-      slot0 = 2 * x * 16;
-      stride = 2 * 16;
+      first = (2 * c + 1) * p.slot_rows + prow;
+      slot0 = 2 * c * p.slot_rows + prow;
+      stride = 2 * p.slot_rows;
       part_o = p.part_o;
       part_ml = p.part_ml;
     } else {
@@ -714,18 +773,20 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
 // Workspace: the few-row path's partial results, then, where a request may take the tcgen05 path, that
 // path's scratch.
 struct Plan {
-  int rows_grid, T, max_units;
+  int rows_grid, slot_rows, T, max_units;
   size_t off_ml, off_split, off_queue, off_units, off_joins, off_tile_ml, off_tile_o, bytes;
   Plan(const attn_fwd_paged_params_t& a, int sms) {
     const int g = a.Hq / a.Hkv;
     rows_grid = 2 * sms;
-    const size_t slots = 2 * (size_t)rows_grid * 16;
+    const int longest = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+    const long long most = (long long)longest * g;  // packed rows of a request
+    slot_rows = most > ROWS_MAX && most <= ROWS_ONLY ? 32 : 16;
+    const size_t slots = 2 * (size_t)rows_grid * slot_rows;
     off_ml = round256(slots * a.d * sizeof(float));
     off_split = off_ml + round256(slots * sizeof(float2));
     off_queue = off_split + round256((size_t)rows_grid * sizeof(Split));
     T = TILE_ROWS / g;
-    const int longest = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
-    if ((long long)longest * g <= ROWS_MAX) {
+    if (most <= ROWS_ONLY) {
       max_units = 0;
       bytes = off_queue;
       return;
@@ -784,18 +845,18 @@ int check(const attn_fwd_paged_params_t& a) {
   return ATTN_OK;
 }
 
-template <int D, bool BF16>
+template <int D, int MT, bool BF16>
 int launch(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& plan, int sms, int dev, cudaStream_t st) {
-  using C = Rows<D>;
+  using C = Rows<D, MT>;
   static std::atomic<unsigned long long> attr_set{0};  // bit per device
   const unsigned long long bit = 1ull << dev;
   if (!(attr_set.load() & bit)) {
-    if (cudaFuncSetAttribute(rows_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(rows_kernel<D, MT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
       return ATTN_ERR_CUDA;
     attr_set.fetch_or(bit);
   }
   const bool tiles = p.tile.max_units > 0;
-  int rc = launch_dependent(rows_kernel<D, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
+  int rc = launch_dependent(rows_kernel<D, MT, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
   if (rc == ATTN_OK && tiles) rc = tile_launch(p, a, sms, dev, st);
   if (rc != ATTN_OK) return rc;
   return launch_dependent(join_kernel<D, BF16>, dim3(plan.rows_grid), 32 * JOIN_WARPS, 0, st, p);
@@ -883,9 +944,15 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
     p.tile.part_ml = reinterpret_cast<float2*>(ws + plan.off_tile_ml);
     p.tile.part_o = reinterpret_cast<float*>(ws + plan.off_tile_o);
   }
+  p.slot_rows = plan.slot_rows;
   const bool bf16 = a.dtype == ATTN_BF16;
-  if (a.d == 64) return bf16 ? launch<64, true>(p, a, plan, sms, dev, st) : launch<64, false>(p, a, plan, sms, dev, st);
-  return bf16 ? launch<128, true>(p, a, plan, sms, dev, st) : launch<128, false>(p, a, plan, sms, dev, st);
+  const auto go = [&](auto launch) { return launch(p, a, plan, sms, dev, st); };
+  if (plan.slot_rows == 16) {
+    if (a.d == 64) return go(bf16 ? launch<64, 1, true> : launch<64, 1, false>);
+    return go(bf16 ? launch<128, 1, true> : launch<128, 1, false>);
+  }
+  if (a.d == 64) return go(bf16 ? launch<64, 2, true> : launch<64, 2, false>);
+  return go(bf16 ? launch<128, 2, true> : launch<128, 2, false>);
 }
 
 }  // extern "C"
