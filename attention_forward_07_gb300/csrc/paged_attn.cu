@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
         const bool whole = begins && ends;
         const int at = (2 * cta + (begins ? 1 : 0)) * C::ROWS + r;  // (a part's place)
         const int i = r / p.g, hq = h * p.g + r - i * p.g;
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
           const int phys = (tid & 7) + 8 * j, col = (phys ^ (rs & 7)) * 8;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
         }
         if ((tid & 7) == 0) {
           if (!whole) p.part_ml[at] = make_float2(mm, ll);
-          else if (p.lse) p.lse[(long long)hq * p.total_q + it.row0 + i] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
+          else if (p.lse) p.lse[(long long)hq * p.total_q + it.row0 + i] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
         }
       }
     }
@@ -760,12 +760,12 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
       }
     }
     if (sub != 0 || r >= rows) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int rr = prow + r, i = rr / p.g, hq = h * p.g + rr - i * p.g;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (long long)(row0 + i) * p.o_row + (long long)hq * p.o_head + lane * E);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[(long long)hq * p.total_q + row0 + i] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[(long long)hq * p.total_q + row0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
   }
 }
 

@@ -281,6 +281,8 @@ int attn_paged_append(const attn_paged_append_params_t* params) {
   for (long long s : {a.k_row_stride, a.k_head_stride, a.v_row_stride, a.v_head_stride, a.cache_page_stride, a.cache_head_stride,
                       a.cache_row_stride})
     if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID;
+  if (a.cache_row_stride == 0 || (a.num_pages > 1 && a.cache_page_stride == 0) || (a.Hkv > 1 && a.cache_head_stride == 0))
+    return ATTN_ERR_INVALID;
   int sms = 0, dev = 0;
   int rc = host_device(sms, dev);
   if (rc != ATTN_OK) return rc;

@@ -402,7 +402,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       const float mm = fmaxf(m, other.x);
       const float f_own = m == -INFINITY ? 0.f : ex2_approx(m - mm), f_other = other.x == -INFINITY ? 0.f : ex2_approx(other.x - mm);
       const float ll = l * f_own + other.y * f_other;
-      const float inv = slot_out >= 0 ? 1.f : ll > 0.f ? 1.f / ll : 0.f;
+      const float inv = slot_out >= 0 ? 1.f : ll == 0.f ? 0.f : 1.f / ll;
       const float fa = (t ? f_other : f_own) * inv, fb = (t ? f_own : f_other) * inv;
       const uint32_t both = tmem + lane_off + L::O_COL + t * (D / 2);
       const int head = h * p.g + r - my_tok * p.g;
@@ -428,7 +428,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       }
       if (t == 0 && row_ok) {
         if (slot_out >= 0) p.tile.part_ml[part] = make_float2(mm, ll);
-        else if (p.lse) p.lse[(long long)head * p.total_q + row0 + tok0 + my_tok] = ll > 0.f ? (mm + log2f(ll)) * LN2 : -INFINITY;
+        else if (p.lse) p.lse[(long long)head * p.total_q + row0 + tok0 + my_tok] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
       }
       if (!meet(true)) return;
       if constexpr (L::STAGE_O) {
@@ -459,7 +459,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       if (L::STAGE_O && lane == 0) mbar_arrive(bars + 8u * (L::B_QEMPTY + (k % L::QBUF)));
       continue;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     // The warp's 32 rows go through a slice of shared memory, 128 bytes of every row at a time (d = 64: the
     // unit's Q buffer, whose last reader is done; a tile that computed nothing has not waited for its Q
     // load, and writes zeros without it), and are written out a whole 128-byte segment to eight lanes.
@@ -508,7 +508,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       if (lane == 0) mbar_arrive(bars + 8u * (L::B_QEMPTY + (k % L::QBUF)));
     }
     if (row_ok && p.lse)
-      p.lse[(long long)(h * p.g + r - my_tok * p.g) * p.total_q + row0 + tok0 + my_tok] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+      p.lse[(long long)(h * p.g + r - my_tok * p.g) * p.total_q + row0 + tok0 + my_tok] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
   }
 }
 

@@ -215,7 +215,9 @@ int attn_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float
  * their heads one after the other ([num_pages][Hkv][page_size][d]) or their rows one after
  * the other ([num_pages][page_size][Hkv][d]), inside larger buffers or not.  New rows, q and
  * o are packed, request after request, with a row and a head stride of their own.  Strides
- * are multiples of 8, pointers to rows 16-byte aligned; page_size is a multiple of 16.
+ * are multiples of 8 and not negative (those of a cache's dimensions of more than one entry
+ * positive), pointers to rows 16-byte aligned; page_size is a multiple of 16.  No output of a
+ * call overlaps an input of it, unless said so.
  * Slot s is row s % page_size of page s / page_size.
  * block_table: int32, row b at block_table + b*table_stride, table_width entries: request
  * b's token at position p is in page block_table[b][p / page_size], row p % page_size.
@@ -246,7 +248,7 @@ int attn_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float
  * of the page that request b's new tokens start in) is out of range, the slots concerned
  * are -1 and so are the table entries that exist; rows past max_rows get no slot.  Each of these
  * sets ATTN_ERR_PAGE.  cu_seqlens_q and seqlens_k are as if all had been well; *free_count_out
- * is never below 0.  No output overlaps an input but free_count_out.  1 <= B <= 16384, max_rows <= 2^30; num_pages*page_size, and the sums of the lengths, fit 31 bits.
+ * is never below 0.  1 <= B <= 16384, 1 <= max_rows <= 2^30; num_pages*page_size, and the sums of the lengths, fit 31 bits.
  */
 typedef struct {
     const int *ctx_lens, *new_lens; /* [B] */

@@ -177,10 +177,18 @@ CASES = [
     ([1, 1], [300, 257], 32, 1, 128, "bf16", 256, True, -1, -1, {}),                  # 32 heads of one K/V head
     ([1], [150], 128, 1, 64, "f16", 16, True, -1, -1, {}),                            # 128 of them
     ([1, 1], [600, 33], 4, 1, 64, "bf16", 16, True, 0, -1, {}),                       # a window of one key
+    ([1], [3000], 1, 1, 64, "bf16", 16, True, -1, -1, {}),                            # one item over many runs
     # a few tokens per request
     ([3, 5, 2, 4], [200, 5, 66, 1000], 8, 2, 128, "bf16", 16, True, -1, -1, {}),
     ([4, 1, 6], [300, 64, 100], 8, 1, 64, "f16", 128, True, 50, -1, {}),
     ([2, 7], [128, 129], 4, 4, 128, "f16", 16, False, 40, 2, {}),
+    ([4, 1, 3, 2], [500, 64, 100, 2], 8, 1, 128, "f16", 16, True, -1, -1, {}),        # up to 32 rows of a head
+    ([4, 4, 0], [700, 63, 10], 8, 1, 64, "bf16", 48, True, 90, -1, dict(cache="tokens")),
+    ([2, 9], [2, 300], 3, 1, 128, "bf16", 32, False, -1, 4, dict(rows="heads")),
+    ([5, 2], [150, 400], 128, 1, 64, "f16", 16, True, -1, -1, {}),                    # more heads than a tile's half
+    ([3], [77], 100, 1, 128, "bf16", 16, True, -1, -1, {}),
+    ([16, 7, 1], [900, 300, 40], 8, 1, 128, "f16", 64, True, -1, -1, {}),             # one tile of rows, many key tiles
+    ([20, 1], [64, 1000], 6, 1, 64, "bf16", 16, True, 200, -1, {}),
     # chunks
     ([100, 33], [100, 500], 4, 2, 128, "bf16", 16, True, -1, -1, {}),
     ([129], [129], 2, 1, 64, "f16", 16, True, -1, -1, {}),
@@ -468,3 +476,87 @@ def test_a_wait_that_runs_out_is_reported():
     o, lse = _attend(bt, True, -1, -1, 0.1)
     af.attn_check()
     bt.check(o.cpu(), lse.cpu(), True, -1, -1, 0.1)
+
+
+@pytest.mark.parametrize("lq", [[1, 1, 2], [3, 1, 8], [150, 1, 40]])
+def test_nan_in_a_query_row_stays_in_it(lq):
+    """A NaN that a row does see comes out as NaN, in O and LSE, and in no other row."""
+    bt = Batch(lq, [900, 70, 300], 4, 2, 128, "bf16", 16, seed=21)
+    clean, _ = _attend(bt, True, -1, -1, 0.1)
+    bt.q[1, 0, 5] = float("nan")
+    o, lse = _attend(bt, True, -1, -1, 0.1)
+    af.attn_check()
+    assert torch.all(torch.isnan(o[1, 0])) and torch.isnan(lse[1, 0])
+    o[1, 0] = clean[1, 0]
+    assert torch.equal(o[:, :int(bt.cu[-1])], clean[:, :int(bt.cu[-1])])
+
+
+def test_the_streams_workspace_and_maps_are_reused():
+    """Without a workspace of the caller's, repeated calls allocate nothing and encode nothing after the first of a
+    shape; a released workspace comes back; a captured call gets none of it."""
+    s = torch.cuda.Stream()
+    small, big = Batch([1, 1], [300, 90], 8, 2, 128, "f16", 16, seed=22), Batch([1, 200], [300, 900], 8, 2, 128, "f16", 16, seed=23)
+    af.attn_release_workspace(s)
+    with torch.cuda.stream(s):
+        devs = [b.device() for b in (small, big)]
+        tabs = [(b.table.cuda(), b.cu.cuda(), b.lens.cuda()) for b in (small, big)]
+        seen = []
+        for which in (0, 0, 1, 1, 0, 1):
+            b, d, t = (small, big)[which], devs[which], tabs[which]
+            af.attn_fwd_paged(*d[:4], *t, b.max_q, lse=d[4], causal=True, scale=0.1)
+            seen.append(af.debug_counters())
+        af.attn_check(s)
+        assert [c["workspace_allocs"] - seen[0]["workspace_allocs"] for c in seen] == [0, 0, 1, 1, 1, 1]
+        assert seen[3]["map_encodes"] == seen[2]["map_encodes"] == seen[-1]["map_encodes"]
+        af.attn_release_workspace(s)
+        af.attn_fwd_paged(*devs[1][:4], *tabs[1], big.max_q, lse=devs[1][4], causal=True, scale=0.1)
+        af.attn_check(s)
+    for b, d in zip((small, big), devs):
+        b.check(d[3].cpu(), d[4].cpu(), True, -1, -1, 0.1)
+    af.attn_release_workspace(s)
+    g = torch.cuda.CUDAGraph()
+    n = af.debug_counters()["workspace_allocs"]
+    with torch.cuda.graph(g, stream=s):
+        af.attn_fwd_paged(*devs[0][:4], *tabs[0], small.max_q, lse=devs[0][4], causal=True, scale=0.1)
+    assert af.debug_counters()["workspace_allocs"] == n
+    g.replay()
+    torch.cuda.synchronize()
+    small.check(devs[0][3].cpu(), devs[0][4].cpu(), True, -1, -1, 0.1)
+
+
+def test_a_workspace_that_is_too_small_is_refused():
+    bt = Batch([1, 60], [300, 90], 8, 2, 128, "f16", 16, seed=24)
+    n = af.attn_paged_workspace(2, 8, 2, 128, 61, 60)
+    with pytest.raises(af.AttnError) as e:
+        _attend(bt, True, -1, -1, 0.1, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == -1
+    with pytest.raises(ValueError):
+        _attend(bt, True, -1, -1, 0.1, workspace=torch.empty(n, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        _attend(bt, True, -1, -1, 0.1, workspace=torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2])
+
+
+def test_threads_on_one_stream_and_on_their_own():
+    """Host threads that call at the same time, sharing a stream (and its workspace) or not."""
+    import threading
+    bts = [Batch([1, 1, 1], [900, 30, 400], 8, 2, 128, "bf16", 16, seed=25), Batch([130, 1], [400, 600], 8, 2, 128, "bf16", 16, seed=26),
+           Batch([2, 4], [64, 1000], 8, 2, 64, "f16", 32, seed=27), Batch([9, 3], [300, 500], 8, 2, 64, "bf16", 16, seed=28)]
+    devs = [b.device() for b in bts]
+    tabs = [(b.table.cuda(), b.cu.cuda(), b.lens.cuda()) for b in bts]
+    torch.cuda.synchronize()
+    for streams in ([torch.cuda.Stream()] * 4, [torch.cuda.Stream() for _ in range(4)]):
+        def work(i):
+            for _ in range(20):
+                af.attn_fwd_paged(*devs[i][:4], *tabs[i], bts[i].max_q, lse=devs[i][4], causal=True, scale=0.1, stream=streams[i])
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        for s in streams:
+            af.attn_check(s)
+        for b, d in zip(bts, devs):
+            b.check(d[3].cpu(), d[4].cpu(), True, -1, -1, 0.1)
+            d[3].fill_(float("nan"))
+            d[4].fill_(float("nan"))
+        torch.cuda.synchronize()

@@ -38,7 +38,7 @@ REFUSALS = (
     [("append", {k: 0}, -1) for k in ("k_new", "v_new", "k_cache", "v_cache", "slots")] +
     [("append", {k: P + 8}, -1) for k in ("k_new", "v_new", "k_cache", "v_cache")] +
     [("append", {k: v}, -1) for k in APPEND if k.endswith("stride") for v in (60, -64)] +
-    [("append", kw, st) for kw, st in ((dict(d=96), -2), (dict(dtype=2), -2), (dict(rows=0), -1), (dict(Hkv=0), -1), (dict(slots=P + 1), -1),
+    [("append", kw, st) for kw, st in ((dict(cache_row_stride=0), -1), (dict(cache_page_stride=0), -1), (dict(cache_head_stride=0), -1), (dict(d=96), -2), (dict(dtype=2), -2), (dict(rows=0), -1), (dict(Hkv=0), -1), (dict(slots=P + 1), -1),
                                        (dict(page_size=20), -1), (dict(num_pages=INT_MAX), -1))] +
     [("attend", {k: 0}, -1) for k in ATTEND if ATTEND[k] == P and k != "workspace"] +
     [("attend", {k: P + 8}, -1) for k in ("q", "k_cache", "v_cache", "o", "workspace")] +
