@@ -336,22 +336,27 @@ def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, p
     itself).  See include/attn.h."""
     torch = _torch or _with_torch()
     i32, index = torch.int32, ctx_lens.get_device()
-    (B,), (rows,), (free,) = ctx_lens.shape, slots.shape, free_pages.shape
-    if free_count_out is None:
-        free_count_out = free_count
-    vectors = ((ctx_lens, B, "ctx_lens"), (new_lens, B, "new_lens"), (free_pages, free, "free_pages"), (free_count, 1, "free_count"),
-               (free_count_out, 1, "free_count_out"), (cu_seqlens_q, B + 1, "cu_seqlens_q"), (seqlens_k, B, "seqlens_k"),
-               (slots, rows, "slots")) + (() if positions is None else ((positions, rows, "positions"),))
-    for t, n, _ in vectors:
-        if t.dtype is not i32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
-            _refuse(index, vectors)
-    if (index < 0 or block_table.dtype is not i32 or block_table.get_device() != index or block_table.dim() != 2 or
-            block_table.shape[0] != B or (block_table.stride(1) != 1 and block_table.shape[1] > 1)):
-        _refuse(index, table=(block_table, B))
-    width = block_table.shape[1]
+    one, many, after = ctx_lens.shape, slots.shape, cu_seqlens_q.shape
+    (B,), (rows,), (free,) = one, many, free_pages.shape
+    left = free_count if free_count_out is None else free_count_out
+    width = block_table.shape[-1]
+    if (index < 0 or not ctx_lens.dtype is new_lens.dtype is free_pages.dtype is free_count.dtype is left.dtype is cu_seqlens_q.dtype is
+            seqlens_k.dtype is slots.dtype is block_table.dtype is i32 or
+            not index == new_lens.get_device() == free_pages.get_device() == free_count.get_device() == left.get_device() ==
+            cu_seqlens_q.get_device() == seqlens_k.get_device() == slots.get_device() == block_table.get_device() or
+            not (ctx_lens.is_contiguous() and new_lens.is_contiguous() and free_pages.is_contiguous() and cu_seqlens_q.is_contiguous() and
+                 seqlens_k.is_contiguous() and slots.is_contiguous()) or
+            new_lens.shape != one or seqlens_k.shape != one or free_count.shape != (1,) or left.shape != (1,) or after != (B + 1,) or
+            block_table.dim() != 2 or block_table.shape[0] != B or (block_table.stride(1) != 1 and width > 1) or
+            (positions is not None and (positions.dtype is not i32 or positions.get_device() != index or positions.shape != many or
+                                        not positions.is_contiguous()))):
+        _refuse(index, ((ctx_lens, B, "ctx_lens"), (new_lens, B, "new_lens"), (free_pages, free, "free_pages"),
+                        (free_count, 1, "free_count"), (left, 1, "free_count_out"), (cu_seqlens_q, B + 1, "cu_seqlens_q"),
+                        (seqlens_k, B, "seqlens_k"), (slots, rows, "slots")) +
+                (() if positions is None else ((positions, rows, "positions"),)), (block_table, B))
     _launch(index, (_lib or library()).attn_paged_tables,
             _TABLES.pack(ctx_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-                         free_count_out.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), slots.data_ptr(),
+                         left.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), slots.data_ptr(),
                          0 if positions is None else positions.data_ptr(), B, width, block_table.stride(0) if B > 1 else width, free,
                          rows, page_size, num_pages, _raw_stream(index) if stream is None else _stream_on(index, stream)))
 

@@ -97,20 +97,23 @@ __device__ __forceinline__ int run_of(long long line, int n, long long x) { retu
 // Launches the tcgen05 path's attention kernel.
 int tile_launch(const PagedParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st);
 
-// Launches a kernel that may start before the one ahead of it on the stream has finished; it waits for
-// that one (griddepcontrol.wait) before it touches memory.
+// Launches a kernel (in clusters of `cluster` CTAs) that may start before the one ahead of it on the stream has
+// finished; it waits for that one (griddepcontrol.wait) before it touches memory.
 template <class P>
-int launch_dependent(void (*kern)(P), dim3 grid, unsigned int threads, size_t smem, cudaStream_t st, const P& p) {
+int launch_dependent(void (*kern)(P), dim3 grid, unsigned int threads, size_t smem, cudaStream_t st, const P& p, int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -249,20 +249,8 @@ int attn_paged_tables(const attn_paged_tables_params_t* params) {
   // a CTA for every four rows of its threads, up to the portable cluster of eight
   int ctas = 1;
   while (ctas < 8 && (long long)ctas * 4 * TABLES_THREADS < a.max_rows) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(TABLES_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(a.stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, paged_tables_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+  return launch_dependent(paged_tables_kernel, dim3(ctas), TABLES_THREADS, smem, st, p, ctas);
 }
 
 int attn_paged_append(const attn_paged_append_params_t* params) {

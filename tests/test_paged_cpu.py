@@ -121,6 +121,33 @@ def test_the_binding_refuses_what_it_can_see():
         af.attn_paged_tables(i(2), i(3), i(2, 4), i(9), i(1), 16, 9, i(3), i(2), i(5))
 
 
+def test_every_tensor_of_the_tables_is_looked_at(monkeypatch):
+    """Each wrong type, length, stride or rank of each argument is refused (the launch itself is replaced)."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    good = dict(ctx_lens=i(2), new_lens=i(2), block_table=i(2, 4), free_pages=i(9), free_count=i(1), cu_seqlens_q=i(3), seqlens_k=i(2),
+                slots=i(5), positions=i(5), free_count_out=i(1))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    bd._with_torch()
+    monkeypatch.setattr(bd, "_raw_stream", lambda index: 0)
+    launched = []
+    monkeypatch.setattr(bd, "_launch", lambda index, fn, block: launched.append(block))
+    af.attn_paged_tables(**good, page_size=16, num_pages=9)
+    assert len(launched) == 1
+    for name, t in good.items():
+        longer = i(*[n + 1 for n in t.shape])
+        wrong = [t.long(), t[None], i(*[2 * n + 2 for n in t.shape])[tuple(slice(0, 2 * n, 2) for n in t.shape)]]
+        if name not in ("free_pages", "slots"):  # (whose own length is what they hold)
+            wrong.append(longer if name != "block_table" else i(3, 4))
+        for bad in wrong:
+            if name in ("free_count", "free_count_out") and bad.shape == (1,) and bad.dtype is torch.int32:
+                continue  # one entry has no stride
+            if name == "slots" and bad.dtype is torch.int32 and bad.is_contiguous() and bad.dim() == 1:
+                continue
+            with pytest.raises(ValueError):
+                af.attn_paged_tables(**dict(good, **{name: bad}), page_size=16, num_pages=9)
+    assert len(launched) == 1
+
+
 # ---- the plain forms themselves, against the oracle and by hand
 def test_plain_attention_against_the_oracle():
     import oracle
