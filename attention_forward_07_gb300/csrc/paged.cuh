@@ -1,7 +1,12 @@
 // paged.cuh -- what the two paths of attn_fwd_paged share.  A request whose K/V heads have at most
 // ROWS_MAX packed rows (query tokens times group size) takes the memory-bound path of
 // paged_attn.cu, a longer one the tcgen05 path of paged_tile.cu; each path's kernels pass over the
-// other's requests, so the lengths need not be known on the host.
+// other's requests, so the lengths need not be known on the host.  Two rules move the border:
+//  * where max_seqlen_q allows no request more than ROWS_ONLY rows, all take the memory-bound path, with
+//    32 rows to an item.  24 requests of 32 rows against 4000 keys (d = 128 / 64): 53 / 21 us, by the
+//    tcgen05 path 55 / 31; above 32 rows the order turns (48 rows: 78 us against 57 at d = 128);
+//  * few-row requests beside chunks join the chunks' units while they have few key tiles altogether
+//    (FOLD_TILES in paged_attn.cu).
 #pragma once
 #include <cuda_runtime.h>
 
@@ -13,11 +18,14 @@
 
 namespace attn {
 
-constexpr int ROWS_MAX = 16;
-constexpr int ROWS_ONLY = 32;
+constexpr int ROWS_MAX = 16, ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile
 
-// Written by the plan.  Line coordinates count key tiles over all (unit, head) pairs in order, heads inside.
+// Written by the plan.  Line coordinates count steps over all (unit, head) pairs in order, heads inside: a
+// pair is UNIT_COST steps for its start and end, then a step for each key tile.  (Measured with 1 / 2 / 3 / 4:
+// checking 3 - 6 tokens of 24 requests 43.1 / 41.0 / 39.0 / 39.6 us, a mixed batch of 13 requests 77.4 /
+// 74.3 / 66.7 / 66.0, four prompts of 4k 438 / 438 / 436 / 431.)
+constexpr int UNIT_COST = 4;
 struct TileQueue {
   unsigned int next;    // next queue entry (a CTA starts with that of its own number)
   int whole, runs;      // entries: whole (unit, head) pairs, then runs
@@ -28,7 +36,7 @@ struct TileQueue {
 struct TileUnit {
   int b, blk;
   int j0, w;      // key tiles j0 .. j0 + w - 1 (one where no key is seen: the unit still writes its rows)
-  long long cum;  // weights of the units before
+  long long cum;  // steps of the units before
   int row0, sq, sk, pad;
 };
 struct TileJoin {  // up to JOIN_ROWS packed rows of a cut (unit, head) pair
@@ -90,7 +98,7 @@ __device__ __forceinline__ bool tile_keys(const PagedParams& p, int sq, int sk, 
   return true;
 }
 
-// First tile of run i out of n over a line of tiles, and the run that holds tile x of it.
+// First step of run i out of n over a line, and the run that holds step x of it.
 __host__ __device__ __forceinline__ long long run_begin(long long line, int n, int i) { return line * i / n; }
 __device__ __forceinline__ int run_of(long long line, int n, long long x) { return (int)(((x + 1) * n - 1) / line); }
 

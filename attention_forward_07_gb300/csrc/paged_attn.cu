@@ -39,10 +39,10 @@ struct RowsParams : PagedParams {
 };
 
 // ------------------------------------------------------------------ few rows: the memory-bound path
-// An item is (request, K/V head) with at most 16 packed rows, row r being query token r / g, query head r % g
-// of the group: one pass over the keys serves the whole group.  Each
-// key costs 4 d bytes and 16 * 4 d flops, far below the machine's ratio, so the keys' stream from memory is
-// the floor and everything else has to hide behind it:
+// An item is (request, K/V head) with at most 16 MT packed rows, row r being query token r / g, query head
+// r % g of the group: one pass over the keys serves the whole group.  Each key costs 4 d bytes and at most
+// 16 MT * 4 d flops, below the machine's ratio, so the keys' stream from memory is the floor and
+// everything else has to hide behind it:
 //  * the items' key tiles, laid end to end, are cut into equal runs, one per CTA, whatever the
 //    lengths: no CTA has more to read than another.  Items cut across CTAs leave partial results
 //    (at most two to a CTA) that join_kernel puts together;
@@ -51,7 +51,11 @@ struct RowsParams : PagedParams {
 //    and the copies go on into the next item meanwhile;
 //  * a lane holds the places of the next 32 page rows, so the table is read once per 32 copies;
 //  * mma.sync with the keys as the N side: 16 rows are its smallest M, and its operands come by
-//    ldmatrix straight from the copied rows (128-byte tcgen05 tiles would be an eighth full).
+//    ldmatrix straight from the copied rows (a tcgen05 tile's 128 rows would be an eighth full).
+// Measured: 61 requests of 500 - 8000 keys, 32/8 heads, d = 128, bf16: 110 - 112 us, 6.2 TB/s of keys and values
+// (0.92 of measured copy bandwidth); 3 of 60 - 106 thousand: 95 us, 6.0 TB/s; one of 1001: 9.1 us, latency (of
+// launches, lengths -> table -> keys, and the join).  Ring depth, CTAs and keys to a stage were swept: 2 stages
+// and 3 CTAs 112 us, 2 and 4 (128 registers, spills) 166, 8 KiB in half the keys 126, this 110.
 template <int D, int MT>
 struct Rows {
   static constexpr int WARPS = 4, NTHREADS = 32 * WARPS;
@@ -66,6 +70,7 @@ struct Rows {
   static constexpr int OFF_Q = WARPS * NST * STAGE;
   static constexpr int SMEM = OFF_Q + (Q_SMEM ? ROWS * D * 2 : 0);
   static constexpr int CTAS_PER_SM = 2;
+  static constexpr int FOLD_TILES = D == 128 ? 128 : 12;  // (few_tiles_too)
   static_assert(STAGE >= 16 * D * 4, "a stage holds a 16-row accumulator of the warp at the item's end");
   static_assert(NTHREADS == 128, "the plan and block_scan are written for four warps");
 };
@@ -92,6 +97,18 @@ __device__ __forceinline__ RowsItem rows_request(const RowsParams& p, int b) {
   if (it.R > C::ROWS || it.R == 0) it.R = it.t0 = it.t1 = 0;
   return it;
 }
+// Its tiles, over all heads.
+__device__ __forceinline__ long long rows_weight(const RowsParams& p, const RowsItem& it) { return (long long)(it.t1 - it.t0) * p.Hkv; }
+// Whether the tcgen05 path takes the few-row requests as well, of `tiles` tiles (32 KiB each) altogether.  Two
+// passes over the machine cost a start and an end each, one pass reads these keys more slowly (its step takes a
+// 128-row tile's time), half as fast again at d = 64.  d = 128, 30 requests of 2000 keys beside a chunk of 512
+// rows (50 tiles an SM): 98 us apart, 76 together; 16 of 8000 beside 2000 rows (108): 207 and 147; 64 of
+// 4000 beside 256 (215): 198 and 224.  d = 64, 16 of 2000 beside 300 (7): 35 and 33; 30 of 2000 beside 512
+// (13): 43 and 49.
+template <class C>
+__device__ __forceinline__ bool few_tiles_too(const RowsParams& p, long long tiles) {
+  return p.tile.max_units > 0 && tiles < (long long)C::FOLD_TILES * p.tile.sms;
+}
 // The item after head h of request b.
 template <class C>
 __device__ __forceinline__ void rows_next(const RowsParams& p, int& b, int& h, RowsItem& it) {
@@ -107,7 +124,7 @@ __device__ __forceinline__ void rows_next(const RowsParams& p, int& b, int& h, R
 // weight into 32 classes, stably, so that equal inputs give equal cuts.  Bound by latency: one pass over the
 // requests, then one over the units for each of weigh, sort, sum.
 constexpr int PLAN_THREADS = 128, PLAN_WARPS = PLAN_THREADS / 32;
-constexpr int MIN_RUN = 4;   // tiles of a run at least
+constexpr int MIN_RUN = 4 + UNIT_COST;  // steps of a run at least
 constexpr int MAX_SPLIT = 3; // runs per SM at most
 
 // Exclusive sum over the block's threads of x, and the total.
@@ -134,7 +151,8 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {
 }
 
 // `pre` holds B + 1 ints of shared memory (units before each request).
-__device__ __forceinline__ void tile_plan(const PagedParams& p, int* pre) {
+template <class C>
+__device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
   __shared__ int sum_s[PLAN_WARPS], rank_s[PLAN_WARPS][33];
   __shared__ long long sum64_s[PLAN_WARPS];
   __shared__ int wmax_s, wmin_s, joins_s;
@@ -145,11 +163,15 @@ __device__ __forceinline__ void tile_plan(const PagedParams& p, int* pre) {
   const int per = (p.B + PLAN_THREADS - 1) / PLAN_THREADS;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   int own = 0, total;
+  long long few = 0, few_all;
+  for (int b = b0; b < b1; ++b) few += rows_weight(p, rows_request<C>(p, b));
+  block_scan(few, sum64_s, few_all);
+  const bool all_here = few_tiles_too<C>(p, few_all);
   for (int b = b0; b < b1; ++b) {
     int row0, sq, sk;
     request_span(p, b, row0, sq, sk);
     pre[b] = own;
-    own += sq * p.g > ROWS_MAX ? (sq + unit_tokens - 1) / unit_tokens : 0;
+    own += all_here || sq * p.g > ROWS_MAX ? (sq + unit_tokens - 1) / unit_tokens : 0;
   }
   if (tid == 0) wmax_s = joins_s = 0, wmin_s = INT_MAX;
   for (int x = lane; x < 33; x += 32) rank_s[warp][x] = 0;
@@ -227,25 +249,25 @@ __device__ __forceinline__ void tile_plan(const PagedParams& p, int* pre) {
     if (c < 32) tw.units[to] = x;
   }
   __syncthreads();
-  // weights before each unit, in the sorted order
+  // steps before each unit, in the sorted order
   const int chunk = (units + PLAN_THREADS - 1) / PLAN_THREADS;
   const int s0 = min(tid * chunk, units), s1 = min(s0 + chunk, units);
   long long weight = 0, all;
-  for (int s = s0; s < s1; ++s) weight += tw.units[s].w;
+  for (int s = s0; s < s1; ++s) weight += tw.units[s].w + UNIT_COST;
   long long cum = block_scan(weight, sum64_s, all);
   for (int s = s0; s < s1; ++s) {
     tw.units[s].cum = cum;
-    cum += tw.units[s].w;
+    cum += tw.units[s].w + UNIT_COST;
   }
   if (tid == 0) tw.units[units].cum = all;
   __syncthreads();
 
   // Whole pairs: full waves of the longest, where none is longer than an SM's share.
   const long long pairs = (long long)units * p.Hkv, share = all * p.Hkv / sms;
-  const int whole = wmax <= share ? (int)(pairs / sms * sms) : 0;
+  const int whole = wmax + UNIT_COST <= share ? (int)(pairs / sms * sms) : 0;
   const auto line_of = [&](long long x) {
     const int s = (int)(x / p.Hkv);
-    return tw.units[s].cum * p.Hkv + (s < units ? (x - (long long)s * p.Hkv) * tw.units[s].w : 0);
+    return tw.units[s].cum * p.Hkv + (s < units ? (x - (long long)s * p.Hkv) * (tw.units[s].w + UNIT_COST) : 0);
   };
   const long long line0 = line_of(whole), line = all * p.Hkv - line0;
   // Runs: one per SM; more where the whole pairs before them differ, so that the SMs that are done
@@ -256,7 +278,7 @@ __device__ __forceinline__ void tile_plan(const PagedParams& p, int* pre) {
   for (long long x = whole + tid; x < pairs; x += PLAN_THREADS) {
     const int s = (int)(x / p.Hkv), h = (int)(x - (long long)s * p.Hkv);
     const long long at = line_of(x) - line0;
-    const int first = run_of(line, runs, at), last = run_of(line, runs, at + tw.units[s].w - 1);
+    const int first = run_of(line, runs, at + UNIT_COST), last = run_of(line, runs, at + UNIT_COST + tw.units[s].w - 1);
     if (first == last) continue;
     const TileUnit un = tw.units[s];
     for (int t = 0; t < TILE_QT; ++t) {
@@ -306,7 +328,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
   grid_launch_dependents();
   grid_dependency_wait();
   if (p.tile.max_units > 0 && blockIdx.x == 0) {
-    tile_plan(p, reinterpret_cast<int*>(smem));
+    tile_plan<C>(p, reinterpret_cast<int*>(smem));
     return;
   }
   __shared__ long long warp_sum[PLAN_WARPS];
@@ -317,21 +339,20 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
   // ---- this CTA's run: sum the weights, find where it begins
   const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS;
   const int rb0 = min(tid * per, p.B), rb1 = min(rb0 + per, p.B);
-  const auto weight = [&](const RowsItem& it) { return (long long)(it.t1 - it.t0) * p.Hkv; };
   long long own = 0, n;
-  for (int b = rb0; b < rb1; ++b) own += weight(rows_request<C>(p, b));
+  for (int b = rb0; b < rb1; ++b) own += rows_weight(p, rows_request<C>(p, b));
   const long long before = block_scan(own, warp_sum, n);
   const int ctas = (int)min((long long)p.rows_grid, n);
   const int cta = (int)blockIdx.x - ((int)gridDim.x - p.rows_grid);
   if (tid == 0) p.split[cta].b = -1;
-  if (cta >= ctas) return;
+  if (cta >= ctas || few_tiles_too<C>(p, n)) return;
   const long long run0 = run_begin(n, ctas, cta);
   const int run = (int)(run_begin(n, ctas, cta + 1) - run0);  // tiles
   if (run0 >= before && run0 < before + own) {
     long long at = before;
     for (int b = rb0;; ++b) {
       const RowsItem it = rows_request<C>(p, b);
-      const long long w = weight(it);
+      const long long w = rows_weight(p, it);
       if (run0 < at + w) {
         const int tiles = it.t1 - it.t0, h = (int)((run0 - at) / tiles);
         start_s = make_int3(b, h, it.t0 + (int)(run0 - at - (long long)h * tiles));

