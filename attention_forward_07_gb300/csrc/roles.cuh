@@ -252,90 +252,94 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
         if constexpr (Env::SCRUB) env.scrub(prev_flags, gbase + L::OFF_V + prev_vslot * L::KV_TILE_BYTES, lane);
       }
       bool k_ready = false;
-      int new_slot0 = 0, new_slot1 = 1;
+      int ahead = 0;  // by turns: the slot of Q tile 1's Q.K^T
 
       // d = 64 issues a Q tile's Q.K^T before its P.V, d = 128 its P.V first.  Where key tiles go to the
-      // two Q tiles by turns (Env::BY_TURNS), Q tile 1's Q.K^T comes before all, so that it does not
-      // wait for Q tile 0's P of the key tile before (the other way round the order has it so already).
+      // two Q tiles by turns (Env::BY_TURNS), Q tile 1's Q.K^T comes before all (turn -1), so that it does
+      // not wait for Q tile 0's P of the key tile before (the other way round the order has it so already).
 #pragma unroll
-      for (int step = Env::BY_TURNS ? -1 : 0; step < 4; ++step) {
-        if (Env::BY_TURNS && step == (L::RING ? 2 : 3)) continue;
-        const int t = step < 0 ? 1 : step >> 1;
-        if (step < 0 || ((step & 1) == 0) == L::RING) {
-          if (!end && ((flags >> t) & 1)) {
-            if (!k_ready) {
-              if (!bwait_warp(bars + 8u * (L::B_KFULL + cur_kslot), cur_kpar, abort_flag, to)) goto drain;
+      for (int turn = Env::BY_TURNS ? -1 : 0; turn < QT; ++turn) {
+        const int t = turn < 0 ? 1 : turn;
+        int& pslot = t ? pslot1 : pslot0;
+        int new_slot = Env::BY_TURNS && turn == 1 ? ahead : t;
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+          if ((step == 0) == L::RING) {
+            if (Env::BY_TURNS && turn == 1) continue;
+            if (!end && ((flags >> t) & 1)) {
+              if (!k_ready) {
+                if (!bwait_warp(bars + 8u * (L::B_KFULL + cur_kslot), cur_kpar, abort_flag, to)) goto drain;
+                tc_fence_after();
+                k_ready = true;
+              }
+              if constexpr (L::RING) {
+                new_slot = nqk;
+                nqk = nqk == L::S_SLOTS - 1 ? 0 : nqk + 1;
+              }
+              const uint32_t s_col = tmem + new_slot * 128;
+              const uint32_t qbase = base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES;
+              const uint32_t kbase = base + L::OFF_K + cur_kslot * L::KV_TILE_BYTES;
+              // Q and K as K-major operands: 16 elements (32 bytes) per step inside a
+              // 128-byte swizzle row, the next 64 elements one half-tile further.
+              if constexpr (D == 64) {
+                // d = 64 issues twice the instructions per flop: the descriptors are built
+                // once and stepped through their start-address field (address >> 4 in the
+                // low 14 bits; every offset here keeps it below 2^14)
+                const uint64_t qd = sdesc_sw128(qbase, 16, 1024), kd = sdesc_sw128(kbase, 16, L::KV_SBO);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+                  mma_ss_elect(s_col, qd + off, kd + off, ID_QK, kk > 0 ? 1u : 0u);
+                }
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
+                  const uint32_t koff = (kk >> 2) * L::KV_HALF + (kk & 3) * 32;
+                  mma_ss_elect(s_col, sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + koff, 16, L::KV_SBO),
+                               ID_QK, kk > 0 ? 1u : 0u);
+                }
+              }
+              tc_commit_elect(bars + 8u * (L::B_STILE + new_slot));
+              env.computed(t, j, lane);
+              __syncwarp();
+            }
+          } else if (turn >= 0) {
+            if (have_prev && ((prev_flags >> t) & 1)) {
+              uint32_t& pp = t ? p_par1 : p_par0;
+              if (!bwait_warp(bars + 8u * (L::B_PREADY + t), pp, abort_flag, to)) goto drain;
+              pp ^= 1u;
               tc_fence_after();
-              k_ready = true;
-            }
-            if constexpr (L::RING) {
-              (t ? new_slot1 : new_slot0) = nqk;
-              nqk = nqk == L::S_SLOTS - 1 ? 0 : nqk + 1;
-            }
-            const int new_slot = t ? new_slot1 : new_slot0;
-            const uint32_t s_col = tmem + new_slot * 128;
-            const uint32_t qbase = base + L::OFF_Q + qbuf * L::Q_BUF_BYTES + t * L::Q_TILE_BYTES;
-            const uint32_t kbase = base + L::OFF_K + cur_kslot * L::KV_TILE_BYTES;
-            // Q and K as K-major operands: 16 elements (32 bytes) per step inside a
-            // 128-byte swizzle row, the next 64 elements one half-tile further.
-            if constexpr (D == 64) {
-              // d = 64 issues twice the instructions per flop: the descriptors are built
-              // once and stepped through their start-address field (address >> 4 in the
-              // low 14 bits; every offset here keeps it below 2^14)
-              const uint64_t qd = sdesc_sw128(qbase, 16, 1024), kd = sdesc_sw128(kbase, 16, L::KV_SBO);
+              bool& started = t ? pv1 : pv0;
+              const uint32_t p_col = tmem + (L::RING ? pslot : t) * 128;
+              const uint32_t vbase = base + L::OFF_V + prev_vslot * L::KV_TILE_BYTES;
+              // V tile as the MN-major B operand: 16 keys per step (two groups of 8), the two
+              // 64-column halves of d KV_HALF apart, 8-key groups KV_SBO.
+              if constexpr (D == 64) {
+                const uint64_t vd = sdesc_sw128(vbase, L::KV_HALF, L::KV_SBO);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-                mma_ss_elect(s_col, qd + off, kd + off, ID_QK, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < BN / 16; ++kk)
+                  mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8, vd + (uint64_t)(kk * 2 * L::KV_SBO >> 4),
+                               ID_PV, (started || kk > 0) ? 1u : 0u);
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                  mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8,
+                               sdesc_sw128(vbase + kk * 2 * L::KV_SBO, L::KV_HALF, L::KV_SBO), ID_PV,
+                               (started || kk > 0) ? 1u : 0u);
               }
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
-                const uint32_t koff = (kk >> 2) * L::KV_HALF + (kk & 3) * 32;
-                mma_ss_elect(s_col, sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + koff, 16, L::KV_SBO),
-                             ID_QK, kk > 0 ? 1u : 0u);
-              }
+              started = true;
+              if constexpr (L::RING) tc_commit_elect(bars + 8u * (L::B_OPV + t));
             }
-            tc_commit_elect(bars + 8u * (L::B_STILE + new_slot));
-            env.computed(t, j, lane);
-            __syncwarp();
+            // end of unit: O_t is complete once its last P.V is -- signal it now, so softmax t
+            // starts its epilogue without waiting for the other Q tile's P.V
+            if (end && (t ? pv1 : pv0)) tc_commit_elect(bars + 8u * (L::B_ODONE + t));
+            if (t == QT - 1 && have_prev) tc_commit_elect(bars + 8u * (L::B_VEMPTY + prev_vslot));
           }
-        } else {
-          if (have_prev && ((prev_flags >> t) & 1)) {
-            uint32_t& pp = t ? p_par1 : p_par0;
-            if (!bwait_warp(bars + 8u * (L::B_PREADY + t), pp, abort_flag, to)) goto drain;
-            pp ^= 1u;
-            tc_fence_after();
-            bool& started = t ? pv1 : pv0;
-            const uint32_t p_col = tmem + (L::RING ? (t ? pslot1 : pslot0) : t) * 128;
-            const uint32_t vbase = base + L::OFF_V + prev_vslot * L::KV_TILE_BYTES;
-            // V tile as the MN-major B operand: 16 keys per step (two groups of 8), the two
-            // 64-column halves of d KV_HALF apart, 8-key groups KV_SBO.
-            if constexpr (D == 64) {
-              const uint64_t vd = sdesc_sw128(vbase, L::KV_HALF, L::KV_SBO);
-#pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8, vd + (uint64_t)(kk * 2 * L::KV_SBO >> 4),
-                             ID_PV, (started || kk > 0) ? 1u : 0u);
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                mma_ts_elect(tmem + L::O_COL + t * L::O_STRIDE, p_col + kk * 8,
-                             sdesc_sw128(vbase + kk * 2 * L::KV_SBO, L::KV_HALF, L::KV_SBO), ID_PV,
-                             (started || kk > 0) ? 1u : 0u);
-            }
-            started = true;
-            if constexpr (L::RING) tc_commit_elect(bars + 8u * (L::B_OPV + t));
-          }
-          // end of unit: O_t is complete once its last P.V is -- signal it now, so softmax t
-          // starts its epilogue without waiting for the other Q tile's P.V
-          if (end && (t ? pv1 : pv0)) tc_commit_elect(bars + 8u * (L::B_ODONE + t));
-          if (t == QT - 1 && have_prev) tc_commit_elect(bars + 8u * (L::B_VEMPTY + prev_vslot));
         }
+        if (turn < 0) ahead = new_slot;
         if constexpr (L::RING) {
-          if (step == 1 && !end && (flags & 1)) pslot0 = new_slot0;
-          if (step == 3 && !end && (flags & 2)) pslot1 = new_slot1;
+          if (turn >= 0 && !end && ((flags >> t) & 1)) pslot = new_slot;
         }
       }
       if (!end) tc_commit_elect(bars + 8u * (L::B_KEMPTY + cur_kslot));
