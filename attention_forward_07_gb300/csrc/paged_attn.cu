@@ -275,12 +275,20 @@ __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
   const long long len = line / sms + 1;
   const int split = whole ? (int)min((long long)MAX_SPLIT, 1 + 2ll * (wmax - wmin_s) / len) : 1;
   const int runs = line ? (int)max(1ll, min((long long)split * sms, line / MIN_RUN)) : 0;
-  for (long long x = whole + tid; x < pairs; x += PLAN_THREADS) {
-    const int s = (int)(x / p.Hkv), h = (int)(x - (long long)s * p.Hkv);
-    const long long at = line_of(x) - line0;
-    const int first = run_of(line, runs, at + UNIT_COST), last = run_of(line, runs, at + UNIT_COST + tw.units[s].w - 1);
-    if (first == last) continue;
-    const TileUnit un = tw.units[s];
+  // The cut pairs, each found by the run that takes its second piece.
+  for (int r = 1 + tid; r < runs; r += PLAN_THREADS) {
+    const long long begin = run_begin(line, runs, r);
+    int lo = whole / p.Hkv, hi = units;  // the last unit whose pairs begin at or before the run
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tw.units[mid].cum * p.Hkv <= line0 + begin) lo = mid;
+      else hi = mid;
+    }
+    const TileUnit un = tw.units[lo];
+    const int steps = un.w + UNIT_COST, h = (int)((line0 + begin - un.cum * p.Hkv) / steps);
+    const long long at = un.cum * p.Hkv + (long long)h * steps - line0;  // where the pair begins
+    const int first = run_of(line, runs, at + UNIT_COST), last = run_of(line, runs, at + steps - 1);
+    if (r != first + 1 || r > last) continue;
     for (int t = 0; t < TILE_QT; ++t) {
       const int tok0 = (un.blk * TILE_QT + t) * tw.T, rows = min(tw.T, un.sq - tok0) * p.g;
       if (rows <= 0) break;

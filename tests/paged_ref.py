@@ -76,10 +76,10 @@ def attention(q, k_cache, v_cache, table, cu, lens, max_q, causal, wl, wr, scale
         seen = keep.any(0)
         kb = torch.zeros((Hkv, sk, d), dtype=torch.float64)
         vb = torch.zeros((Hkv, sk, d), dtype=torch.float64)
-        for key in torch.nonzero(seen).flatten().tolist():
-            pg = int(table[b, key // page])
-            kb[:, key] = k_cache[pg, :, key % page].double()
-            vb[:, key] = v_cache[pg, :, key % page].double()
+        key = torch.nonzero(seen).flatten()
+        pg = torch.as_tensor(table)[b, key // page].long()
+        kb[:, key] = k_cache[pg, :, key % page].double().transpose(0, 1)
+        vb[:, key] = v_cache[pg, :, key % page].double().transpose(0, 1)
         for hq in range(Hq):
             qq = q[hq, rows].double()
             s = (qq @ kb[hq // g].T) * scale

@@ -222,6 +222,48 @@ def test_attention(case):
     bt.check(o.cpu(), lse.cpu(), causal, wl, wr, scale, what=str(case))
 
 
+@pytest.mark.parametrize("d,Hkv,lq,lk", [
+    (64, 4, [1] * 8 + [90, 2, 4] + [1] * 8, [4200] * 8 + [300, 900, 77] + [4100, 1, 4000, 3000, 4500, 3900, 4400, 4300]),
+    (128, 8, [1] * 24 + [200] + [1] * 16, [4600] * 24 + [900] + [4500] * 16)])
+def test_many_decoding_requests_beside_a_chunk(d, Hkv, lq, lk):
+    """Enough keys of few-row requests that they take a path of their own beside the chunk; checked on some requests."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    page, Hq, B = 16, 2 * Hkv, len(lq)
+    need = [pages(n, page) for n in lk]
+    num = sum(need)
+    k, v = (torch.randn((num, Hkv, page, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn((Hq, sum(lq), d), generator=g, device="cuda", dtype=torch.bfloat16)
+    perm = torch.randperm(num, generator=g, device="cuda").int().cpu()
+    table = torch.full((B, max(need)), -1, dtype=torch.int32)
+    at = np.concatenate([[0], np.cumsum(need)])
+    for b in range(B):
+        table[b, :need[b]] = perm[at[b]:at[b + 1]]
+    cu = np.concatenate([[0], np.cumsum(lq)])
+    o, lse = torch.full_like(q, float("nan")), torch.full((Hq, q.shape[1]), float("nan"), device="cuda")
+    af.attn_fwd_paged(q, k, v, o, table.cuda(), _i32(cu), _i32(lk), max(lq), lse=lse, causal=True, scale=0.1)
+    af.attn_check()
+    assert torch.all(torch.isfinite(o.float())) and torch.all(torch.isfinite(lse))
+    for b in (0, 7, 8, 9, 10, 12, B - 8, B - 1) if d == 64 else (0, 23, 24, B - 1):
+        rows, ids = slice(cu[b], cu[b + 1]), table[b, :need[b]].long()
+        own = torch.arange(need[b], dtype=torch.int32)[None]
+        kb, vb, qb = (x.cpu() for x in (k[ids.cuda()], v[ids.cuda()], q[:, rows]))
+        ro, rl, A, S = attention(qb, kb, vb, own, [0, lq[b]], [lk[b]], lq[b], True, -1, -1, float(np.float32(0.1)))
+        to, tl = tolerances(torch.bfloat16, d, lk[b], ro, rl, A, S)
+        assert torch.all((o[:, rows].cpu().double() - ro).abs() <= to), f"request {b}"
+        assert torch.all((lse[:, rows].cpu().double() - rl).abs() <= tl), f"request {b}"
+
+
+def test_one_long_request_among_many_short_ones():
+    """A unit longer than an SM's share: everything is cut into runs."""
+    lq = [40] + [21] * 30
+    lk = [9000] + [30 + 3 * i for i in range(30)]
+    for d, Hq, Hkv in ((128, 2, 1), (64, 8, 2)):
+        bt = Batch(lq, lk, Hq, Hkv, d, "bf16", 32, seed=33)
+        o, lse = _attend(bt, True, -1, -1, 0.1)
+        af.attn_check()
+        bt.check(o.cpu(), lse.cpu(), True, -1, -1, 0.1)
+
+
 @pytest.mark.parametrize("lq,lk,d,page,wl", [([1, 1, 1], [65, 17, 300], 128, 16, -1), ([1, 1], [333, 90], 64, 64, 40),
                                              ([70, 3], [200, 39], 128, 32, -1), ([150, 90], [400, 90], 64, 48, 33),
                                              ([200], [517], 128, 256, 64)])
