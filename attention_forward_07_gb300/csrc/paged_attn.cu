@@ -70,6 +70,10 @@ struct Rows {
   static constexpr int OFF_Q = WARPS * NST * STAGE;
   static constexpr int SMEM = OFF_Q + (Q_SMEM ? ROWS * D * 2 : 0);
   static constexpr int CTAS_PER_SM = 2;
+  // Weights in two parts (see the product with V): 61 requests x 8k keys 112.5 us, with one part 111.5, and its
+  // error the output rounding's alone (bf16 0.0017 of the norm, 0.0023 with one part).  With 32 rows at d =
+  // 128 the products no longer hide behind the keys (64 requests x 2000 keys 121 us against 102).
+  static constexpr bool TWO_PARTS = MT == 1 || D == 64;
   static constexpr int FOLD_TILES = D == 128 ? 128 : 12;  // (few_tiles_too)
   static_assert(STAGE >= 16 * D * 4, "a stage holds a 16-row accumulator of the warp at the item's end");
   static_assert(NTHREADS == 128, "the plan and block_scan are written for four warps");
@@ -319,6 +323,17 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+template <bool BF16>
+__device__ __forceinline__ void unpack2(uint32_t x, float& lo, float& hi) {
+  if constexpr (BF16) {
+    lo = __uint_as_float(x << 16);
+    hi = __uint_as_float(x & 0xFFFF0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+    lo = f.x;
+    hi = f.y;
+  }
+}
 // 16 bytes into shared memory, zeros where `bytes` is 0 (src is then not read).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -519,7 +534,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
           }
         }
       }
-      uint32_t pf[MT][C::NG][4];
+      uint32_t pf[MT][C::NG][4], pl[C::TWO_PARTS ? MT : 1][C::NG][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         if (key0 < lo_all || key0 + C::KPW > hi_all) {
@@ -569,15 +584,22 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
             sc[mt][x][e] = ex2_approx(fmaf(sc[mt][x][e], p.scale_log2, -mu[e >> 1]));
             l[mt][e >> 1] += sc[mt][x][e];
           }
-        // the weights rounded to the values' type, as a matrix instruction takes them; the sum l keeps them
-        // in 32 bits
+        // A matrix instruction takes the weights in the values' type.  That rounding alone would cost as
+        // much as the output's own, so what it leaves goes through a second instruction, and they count to
+        // twice as many bits (TWO_PARTS; else it is accepted).  The sum l has them in 32 bits.
 #pragma unroll
-        for (int gq = 0; gq < C::NG; ++gq) {
-          pf[mt][gq][0] = pack2<BF16>(sc[mt][2 * gq][0], sc[mt][2 * gq][1]);
-          pf[mt][gq][1] = pack2<BF16>(sc[mt][2 * gq][2], sc[mt][2 * gq][3]);
-          pf[mt][gq][2] = pack2<BF16>(sc[mt][2 * gq + 1][0], sc[mt][2 * gq + 1][1]);
-          pf[mt][gq][3] = pack2<BF16>(sc[mt][2 * gq + 1][2], sc[mt][2 * gq + 1][3]);
-        }
+        for (int gq = 0; gq < C::NG; ++gq)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& a = sc[mt][2 * gq + (e >> 1)][(e & 1) * 2];
+            float& c = sc[mt][2 * gq + (e >> 1)][(e & 1) * 2 + 1];
+            pf[mt][gq][e] = pack2<BF16>(a, c);
+            if constexpr (C::TWO_PARTS) {
+              float ah, ch;
+              unpack2<BF16>(pf[mt][gq][e], ah, ch);
+              pl[mt][gq][e] = pack2<BF16>(a - ah, c - ch);
+            }
+          }
       }
       // O += P V
 #pragma unroll
@@ -592,6 +614,10 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
           for (int mt = 0; mt < MT; ++mt) {
             mma_16816<BF16>(o[mt][2 * x], pf[mt][gq], vf[0], vf[1]);
             mma_16816<BF16>(o[mt][2 * x + 1], pf[mt][gq], vf[2], vf[3]);
+            if constexpr (C::TWO_PARTS) {
+              mma_16816<BF16>(o[mt][2 * x], pl[mt][gq], vf[0], vf[1]);
+              mma_16816<BF16>(o[mt][2 * x + 1], pl[mt][gq], vf[2], vf[3]);
+            }
           }
         }
       }
