@@ -8,6 +8,7 @@
 //  * few-row requests beside chunks join the chunks' units while they have few key tiles altogether
 //    (FOLD_TILES in paged_attn.cu).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -18,6 +19,8 @@
 
 namespace attn {
 
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr long long MAX_STRIDE = 1ll << 38;  // elements: no memory holds two entries that far apart, and tensor maps end there
 constexpr int ROWS_MAX = 16, ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile
 
@@ -102,8 +105,17 @@ __device__ __forceinline__ bool tile_keys(const PagedParams& p, int sq, int sk, 
 __host__ __device__ __forceinline__ long long run_begin(long long line, int n, int i) { return line * i / n; }
 __device__ __forceinline__ int run_of(long long line, int n, long long x) { return (int)(((x + 1) * n - 1) / line); }
 
-// Launches the tcgen05 path's attention kernel.
-int tile_launch(const PagedParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st);
+// Parameters of the tcgen05 path's kernel.
+struct TileParams : PagedParams {
+  CUtensorMap tm_q, tm_k, tm_v;
+  int box_rows;   // rows of one K/V box
+  int z_page, z_head, z_extent;  // the maps' page-and-head coordinate: page * z_page + h * z_head, below z_extent
+  unsigned int g_inverse;  // 65536 / g + 1: row / g = row * g_inverse >> 16 for rows below 128
+  int inject;
+};
+// Fills them in (ahead of any launch: a tensor map may fail), and launches the kernel.
+int tile_prepare(const PagedParams& base, const attn_fwd_paged_params_t& a, TileParams& p);
+int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st);
 
 // Launches a kernel (in clusters of `cluster` CTAs) that may start before the one ahead of it on the stream has
 // finished; it waits for that one (griddepcontrol.wait) before it touches memory.

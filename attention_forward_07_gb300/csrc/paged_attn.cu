@@ -878,7 +878,7 @@ int check(const attn_fwd_paged_params_t& a) {
       a.page_size % 16 != 0 || (long long)a.table_width * a.page_size > INT_MAX - 4096 ||
       (long long)a.total_q * a.Hq > INT_MAX - (1 << 27) || a.window_left < -1 || a.window_right < -1)
     return ATTN_ERR_INVALID;
-  if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return ATTN_ERR_INVALID;
+  if (!(a.scale > 0.f) || !std::isfinite(a.scale * LOG2E)) return ATTN_ERR_INVALID;
   for (const void* ptr : {a.q, a.k_cache, a.v_cache, (const void*)a.o})
     if (misaligned(ptr, 16)) return ATTN_ERR_INVALID;
   for (const void* ptr : {(const void*)a.lse, (const void*)a.block_table, (const void*)a.cu_seqlens_q, (const void*)a.seqlens_k})
@@ -886,7 +886,9 @@ int check(const attn_fwd_paged_params_t& a) {
   if (misaligned(a.workspace, 256)) return ATTN_ERR_INVALID;
   for (long long s : {a.q_row_stride, a.q_head_stride, a.o_row_stride, a.o_head_stride, a.cache_page_stride, a.cache_head_stride,
                       a.cache_row_stride})
-    if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID;
+    if (s < 0 || s % 8 != 0 || s > MAX_STRIDE) return ATTN_ERR_INVALID;
+  // one handle stands for a stream of every thread, which the library cannot keep a workspace for
+  if (!a.workspace && a.stream == reinterpret_cast<void*>(cudaStreamPerThread)) return ATTN_ERR_INVALID;
   // the strides of dimensions with more than one entry
   if (a.cache_row_stride == 0 || (a.num_pages > 1 && a.cache_page_stride == 0) || (a.Hkv > 1 && a.cache_head_stride == 0) ||
       (a.Hq > 1 && (a.q_head_stride == 0 || a.o_head_stride == 0)) || (a.total_q > 1 && (a.q_row_stride == 0 || a.o_row_stride == 0)))
@@ -911,8 +913,10 @@ int launch(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& pl
     attr_set.fetch_or(bit);
   }
   const bool tiles = p.tile.max_units > 0;
-  int rc = launch_dependent(rows_kernel<D, MT, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
-  if (rc == ATTN_OK && tiles) rc = tile_launch(p, a, sms, dev, st);
+  TileParams tp = {};
+  int rc = tiles ? tile_prepare(p, a, tp) : ATTN_OK;
+  if (rc == ATTN_OK) rc = launch_dependent(rows_kernel<D, MT, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
+  if (rc == ATTN_OK && tiles) rc = tile_launch(tp, a, sms, dev, st);
   if (rc != ATTN_OK) return rc;
   return launch_dependent(join_kernel<D, BF16>, dim3(plan.rows_grid), 32 * JOIN_WARPS, 0, st, p);
 }
@@ -971,7 +975,7 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
   p.table_stride = a.table_stride;
   p.wl = a.window_left;
   p.er = a.causal ? 0 : a.window_right;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = a.scale * LOG2E;
   if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
   void* scratch = a.workspace;

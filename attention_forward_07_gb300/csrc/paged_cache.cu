@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
     }
   }
   if (bad) atomicOr(p.status, STATUS_PAGE);
+  __syncwarp();
   cluster_wait();
   if (gid == 0) *a.free_count_out = max(count - need, 0);
 }
@@ -263,12 +264,12 @@ int attn_paged_append(const attn_paged_append_params_t* params) {
   if (misaligned(a.slots, 4)) return ATTN_ERR_INVALID;
   if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
-  if (a.rows < 1 || a.Hkv < 1 || a.Hkv > (1 << 16) || a.num_pages < 1 || a.page_size < 16 || a.page_size % 16 != 0 ||
+  if (a.rows < 1 || a.rows > (1 << 30) || a.Hkv < 1 || a.Hkv > (1 << 16) || a.num_pages < 1 || a.page_size < 16 || a.page_size % 16 != 0 ||
       (long long)a.num_pages * a.page_size > INT_MAX)
     return ATTN_ERR_INVALID;
   for (long long s : {a.k_row_stride, a.k_head_stride, a.v_row_stride, a.v_head_stride, a.cache_page_stride, a.cache_head_stride,
                       a.cache_row_stride})
-    if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID;
+    if (s < 0 || s % 8 != 0 || s > MAX_STRIDE) return ATTN_ERR_INVALID;
   if (a.cache_row_stride == 0 || (a.num_pages > 1 && a.cache_page_stride == 0) || (a.Hkv > 1 && a.cache_head_stride == 0))
     return ATTN_ERR_INVALID;
   int sms = 0, dev = 0;
@@ -276,8 +277,7 @@ int attn_paged_append(const attn_paged_append_params_t* params) {
   if (rc != ATTN_OK) return rc;
   AppendParams p{a, nullptr};
   if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-  const long long want = ((long long)a.rows + APPEND_WARPS - 1) / APPEND_WARPS;
-  const int grid = (int)(want < (1 << 30) ? want : (1 << 30));
+  const int grid = (a.rows + APPEND_WARPS - 1) / APPEND_WARPS;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
   return launch_dependent(a.d == 64 ? paged_append_kernel<64> : paged_append_kernel<128>, dim3(grid), 32 * APPEND_WARPS, 0, st, p);
 }

@@ -33,14 +33,6 @@ namespace {
 constexpr int FLAG_SCRUB = 16;  // the key tile holds rows that no query row of the request sees: those outside
                                 // [flags >> 8 & 255, flags >> 16 & 255)
 
-struct TileParams : PagedParams {
-  CUtensorMap tm_q, tm_k, tm_v;
-  int box_rows;   // rows of one K/V box
-  int z_page, z_head, z_extent;  // the maps' page-and-head coordinate: page * z_page + h * z_head, below z_extent
-  unsigned int g_inverse;  // 65536 / g + 1: row / g = row * g_inverse >> 16 for rows below 128
-  int inject;
-};
-
 struct TileHdr {
   int j, flags;
   int row0, sq, sk;
@@ -594,8 +586,7 @@ int launch_tiles(const TileParams& p, int sms, int dev, cudaStream_t st) {
 
 }  // namespace
 
-int tile_launch(const PagedParams& base, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
-  TileParams p = {};
+int tile_prepare(const PagedParams& base, const attn_fwd_paged_params_t& a, TileParams& p) {
   static_cast<PagedParams&>(p) = base;
   const bool bf16 = a.dtype == ATTN_BF16;
   p.box_rows = 128;
@@ -620,6 +611,11 @@ int tile_launch(const PagedParams& base, const attn_fwd_paged_params_t& a, int s
     return rc;
   p.g_inverse = 65536u / p.g + 1;
   p.inject = host_take_inject();
+  return ATTN_OK;
+}
+
+int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
+  const bool bf16 = a.dtype == ATTN_BF16;
   // Where no request has more rows than one Q tile, both Q tiles take the same rows and the key tiles by turns,
   // so that one's products run while the other's softmax does.  24 requests of 3 - 6 tokens x 8 heads
   // against up to 6k keys: 45 us by turns, 51 with the second Q tile idle.

@@ -215,8 +215,8 @@ int attn_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float
  * their heads one after the other ([num_pages][Hkv][page_size][d]) or their rows one after
  * the other ([num_pages][page_size][Hkv][d]), inside larger buffers or not.  New rows, q and
  * o are packed, request after request, with a row and a head stride of their own.  Strides
- * are multiples of 8 and not negative (those of a cache's dimensions of more than one entry
- * positive), pointers to rows 16-byte aligned; page_size is a multiple of 16.  No output of a
+ * are multiples of 8, not negative (those of a cache's dimensions of more than one entry
+ * positive) and at most 2^38, pointers to rows 16-byte aligned; page_size is a multiple of 16.  No output of a
  * call overlaps an input of it, unless said so.
  * Slot s is row s % page_size of page s / page_size.
  * block_table: int32, row b at block_table + b*table_stride, table_width entries: request
@@ -271,7 +271,7 @@ int attn_paged_tables(const attn_paged_tables_params_t *params);
  * attn_paged_tables marks them); one at or past num_pages*page_size too, with ATTN_ERR_PAGE.
  * Slots are distinct (the rows of a slot that is named twice would overwrite each other in
  * no particular order).  k_new, v_new: element (h, t, x) at h*head + t*row + x of their own
- * strides; they do not overlap the cache.  num_pages*page_size fits 31 bits.
+ * strides; they do not overlap the cache.  rows <= 2^30; num_pages*page_size fits 31 bits.
  */
 typedef struct {
     const void *k_new, *v_new;
@@ -308,7 +308,8 @@ int attn_paged_append(const attn_paged_append_params_t *params);
  * after the call, and calls that may run at the same time (two captured graphs among them) each
  * take their own.  With NULL the call uses the stream's workspace (see the conventions), which
  * later calls on the stream share in stream order; a call that is being captured into a graph
- * brings its own (NULL is ATTN_ERR_INVALID there).
+ * brings its own, and so does one on cudaStreamPerThread, one handle for a stream of every thread
+ * (NULL is ATTN_ERR_INVALID there).
  */
 typedef struct {
     const void *q, *k_cache, *v_cache;

@@ -1,5 +1,9 @@
 """The paged-cache operators on the GPU against their plain 64-bit forms (paged_ref.py): tables
 and slot maps, the append, attention over pages, and the three together as a serving loop runs them."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -602,3 +606,32 @@ def test_threads_on_one_stream_and_on_their_own():
             d[3].fill_(float("nan"))
             d[4].fill_(float("nan"))
         torch.cuda.synchronize()
+
+
+def test_a_process_whose_first_calls_are_captured():
+    """Nothing that the library sets up on its first call stands in the way of a capture."""
+    code = (
+        "import torch, attention_forward_07_gb300 as af\n"
+        "i = lambda *s: torch.zeros(s, dtype=torch.int32, device='cuda')\n"
+        "q, kc = (torch.randn(s, device='cuda', dtype=torch.bfloat16) for s in ((8, 40, 64), (9, 2, 16, 64)))\n"
+        "vc, o, new = kc.flip(0).contiguous(), torch.empty_like(q), torch.randn((2, 40, 64), device='cuda', dtype=torch.bfloat16)\n"
+        "ctx, n, table, free, cnt = i(2), torch.tensor([1, 39], dtype=torch.int32, device='cuda'), i(2, 4), torch.arange(9, dtype=torch.int32, device='cuda'), i(1) + 9\n"
+        "left, cu, lens, slots = i(1), i(3), i(2), i(40)\n"
+        "ws = torch.empty(af.attn_paged_workspace(2, 8, 2, 64, 40, 39), dtype=torch.uint8, device='cuda')\n"
+        "def step():\n"
+        "    af.attn_paged_tables(ctx, n, table, free, cnt, 16, 9, cu, lens, slots, free_count_out=left)\n"
+        "    af.attn_paged_append(new, new, kc, vc, slots)\n"
+        "    af.attn_fwd_paged(q, kc, vc, o, table, cu, lens, 39, causal=True, scale=0.125, workspace=ws)\n"
+        "torch.cuda.synchronize()\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    step()\n"
+        "g.replay()\n"
+        "torch.cuda.synchronize()\n"
+        "first = o.clone()\n"
+        "step()\n"
+        "torch.cuda.synchronize()\n"
+        "assert torch.equal(first, o) and left.item() == 5 and first.float().abs().sum() > 0\n"
+        "print('captured')\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "captured", r.stderr[-2000:]

@@ -50,7 +50,12 @@ REFUSALS = (
         (dict(max_seqlen_q=0), -1), (dict(num_pages=0), -1), (dict(page_size=0), -1), (dict(page_size=8), -1), (dict(page_size=40), -1),
         (dict(table_width=0), -1), (dict(table_stride=3), -1), (dict(window_left=-2), -1), (dict(window_right=-2), -1),
         (dict(scale=0.0), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(Hq=258, Hkv=2), -2),
-        (dict(table_width=1 << 27, table_stride=1 << 27), -1), (dict(Hq=128, Hkv=1, total_q=1 << 25), -1))])
+        (dict(table_width=1 << 27, table_stride=1 << 27), -1), (dict(Hq=128, Hkv=1, total_q=1 << 25), -1))] +
+    # a scale whose exponent-of-two form is infinite, strides that no memory spans, a row count past the row counter,
+    # the library's workspace for a handle (2: the calling thread's default stream) that is a stream per thread
+    [("attend", dict(scale=3e38), -1), ("append", dict(rows=(1 << 30) + 1), -1), ("attend", dict(workspace=0, stream=2), -1)] +
+    [(op, {k: (1 << 38) + 8}, -1) for op, base in (("append", APPEND), ("attend", ATTEND)) for k in base
+     if k.endswith("_stride") and k != "table_stride"])
 
 
 def _call(lib, op, kw):
