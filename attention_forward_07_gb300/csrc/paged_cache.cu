@@ -27,6 +27,8 @@ namespace {
 // straight from the free list, so no CTA waits for another's table entries.  The CTAs are one
 // cluster, and its barrier orders the reads of free_count before its one write, which may be in
 // place.  What bounds it is latency: the chain lengths -> scan -> bisection -> free list -> slot.
+// Measured: 64 requests that grow by a token 4.1 us; 509 requests, 12 prompts of up to 8000 tokens among
+// them (0.45 MB to read and write, 0.07 us of bandwidth) 9.5 us.
 constexpr int TABLES_THREADS = 1024;
 constexpr int TABLES_MAX_B = 16384;
 
@@ -165,6 +167,8 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
 // cache[slot / P][h][slot % P][:] = new[h][t][:].  One warp takes a row t, reads its slot once
 // (the division by P is the row's, not each chunk's) and moves the row's 2 * Hkv * d / 8 chunks of 16
 // bytes of K and V, up to eight in flight to a lane.  Memory-bound: every byte is read and written once.
+// Measured: 16.9 thousand rows of 8 heads, d = 128: 23.7 us, 5.84 TB/s (0.86 of measured copy bandwidth);
+// 64 rows: 2.8 us, a launch's time.
 constexpr int APPEND_WARPS = 4;
 
 struct AppendParams {

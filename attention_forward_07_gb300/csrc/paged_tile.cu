@@ -12,7 +12,12 @@
 // few units still fill the machine.  The results of cut units (at most two pieces to a run) are joined by
 // join_kernel.
 //
-// Bound by: the tensor path for chunks.  2037 rows x 32 heads against 32k keys, d = 128, pages of 16: 0.72 ms, 1440
+// The weights enter the second product rounded to the values' type, as in attn_fwd: half a step each,
+// which adds as much to the error as the output's own rounding (bf16 0.0023 of the norm, 0.0017 without).
+// A second product with what the rounding leaves would cost chunks half as much again, and a few tokens of 24
+// requests 54 us against 41.
+//
+// Bound by: the tensor path for chunks.  2037 rows x 32 heads against 32k keys, d = 128, pages of 16: 0.725 ms, 1430
 // TFLOP/s (0.75 of the measured burst peak; contiguous attn_fwd_ex on the same shape 0.76 ms); four prompts
 // of 4k rows 0.43 ms, 1260 TFLOP/s, of which a unit's start and end (one Q buffer at d = 128) take a tenth.
 #include <cuda_runtime.h>
