@@ -24,7 +24,7 @@ constexpr long long MAX_STRIDE = 1ll << 38;  // elements: no memory holds two en
 constexpr int ROWS_MAX = 16, ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile
 
-// Written by the plan.  Line coordinates count steps over all (unit, head) pairs in order, heads inside: a
+// Written by the plan (the joins by the tcgen05 kernel).  Line coordinates count steps over all (unit, head) pairs in order, heads inside: a
 // pair is UNIT_COST steps for its start and end, then a step for each key tile.  (Measured with 1 / 2 / 3 / 4:
 // checking 3 - 6 tokens of 24 requests 43.1 / 41.0 / 39.0 / 39.6 us, a mixed batch of 13 requests 77.4 /
 // 74.3 / 66.7 / 66.0, four prompts of 4k 438 / 438 / 436 / 431.)
@@ -32,7 +32,7 @@ constexpr int UNIT_COST = 4;
 struct TileQueue {
   unsigned int next;    // next queue entry (a CTA starts with that of its own number)
   int whole, runs;      // entries: whole (unit, head) pairs, then runs
-  int njoins;
+  int njoins;             // counted by the tcgen05 kernel
   int units;
   long long line0, line;  // where the runs' line begins, its length
 };

@@ -77,6 +77,7 @@ struct Rows {
   static constexpr bool TWO_PARTS = MT == 1 || D == 64;
   static constexpr int FOLD_TILES = D == 128 ? 128 : 12;  // (few_tiles_too)
   static_assert(STAGE >= 16 * D * 4, "a stage holds a 16-row accumulator of the warp at the item's end");
+  static_assert(sizeof(TileUnit) % 8 == 0, "units are copied 8 bytes at a time");
   static_assert(NTHREADS == 128, "the plan and block_scan are written for four warps");
 };
 
@@ -127,7 +128,8 @@ __device__ __forceinline__ void rows_next(const RowsParams& p, int& b, int& h, R
 // What the tcgen05 path works off, by one CTA of 128 threads while the others run the few-row path.  Units
 // (of one head) are numbered request by request, requests of the other path having none, and sorted by
 // weight into 32 classes, stably, so that equal inputs give equal cuts.  Bound by latency: one pass over the
-// requests, then one over the units for each of weigh, sort, sum.
+// requests, then one over the units for each of weigh, sort, sum; the units stay in shared memory for these
+// where they fit.
 constexpr int PLAN_THREADS = 128, PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int MIN_RUN = 4 + UNIT_COST;  // steps of a run at least
 constexpr int MAX_SPLIT = 3; // runs per SM at most
@@ -155,12 +157,13 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {
   return before + incl - x;
 }
 
-// `pre` holds B + 1 ints of shared memory (units before each request).
+// `pre` is the CTA's shared memory: units before each request (B + 1 ints), then, where there is room, the
+// units twice, as numbered and as sorted.
 template <class C>
 __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
   __shared__ int sum_s[PLAN_WARPS], rank_s[PLAN_WARPS][33];
   __shared__ long long sum64_s[PLAN_WARPS];
-  __shared__ int wmax_s, wmin_s, joins_s;
+  __shared__ int wmax_s, wmin_s;
   const TileWork& tw = p.tile;
   const int sms = tw.sms;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -178,14 +181,18 @@ __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
     pre[b] = own;
     own += all_here || sq * p.g > ROWS_MAX ? (sq + unit_tokens - 1) / unit_tokens : 0;
   }
-  if (tid == 0) wmax_s = joins_s = 0, wmin_s = INT_MAX;
+  if (tid == 0) wmax_s = 0, wmin_s = INT_MAX;
   for (int x = lane; x < 33; x += 32) rank_s[warp][x] = 0;
   const int before = block_scan(own, sum_s, total);
   for (int b = b0; b < b1; ++b) pre[b] += before;
   if (tid == 0) pre[p.B] = total;
   __syncthreads();
   const int units = min(total, tw.max_units);  // (more only where the row offsets overlap)
-  const auto unit_at = [&](int u) {
+  const int at_units = (p.B + 1 + 3) & ~3;       // (ints)
+  const bool near = (size_t)at_units * 4 + (size_t)(2 * units + 1) * sizeof(TileUnit) <= (size_t)C::SMEM;
+  TileUnit* const sorted = near ? reinterpret_cast<TileUnit*>(pre + at_units) : tw.units;
+  TileUnit* const numbered = sorted + units + 1;  // (only where near)
+  const auto weigh = [&](int u) {
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -211,9 +218,10 @@ __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
   const int u0 = min(warp * stretch, units), u1 = min(u0 + stretch, units);
   int wmax = 0, wmin = INT_MAX;
   for (int u = u0 + lane; u < u1; u += 32) {
-    const int w = unit_at(u).w;
-    wmax = max(wmax, w);
-    wmin = min(wmin, w);
+    const TileUnit x = weigh(u);
+    if (near) numbered[u] = x;
+    wmax = max(wmax, x.w);
+    wmin = min(wmin, x.w);
   }
   wmax = __reduce_max_sync(0xffffffffu, wmax);
   wmin = __reduce_min_sync(0xffffffffu, wmin);
@@ -223,7 +231,8 @@ __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
   }
   __syncthreads();
   wmax = max(wmax_s, 1);
-  const auto class_of = [&](int w) { return 31 - (int)((long long)(w - 1) * 32 / wmax); };
+  const auto unit_at = [&](int u) { return near ? numbered[u] : weigh(u); };
+  const auto class_of = [&](int w) { return 31 - (int)((unsigned)(w - 1) * 32u / (unsigned)wmax); };  // (w <= 2^24)
   for (int at = u0; at < u1; at += 32) {
     const int c = at + lane < u1 ? class_of(unit_at(at + lane).w) : 32;  // (class 32: no unit)
     const unsigned int same = __match_any_sync(0xffffffffu, c);
@@ -251,28 +260,31 @@ __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
     __syncwarp();
     if (lane == __ffs(same) - 1) rank_s[warp][c] += __popc(same);
     __syncwarp();
-    if (c < 32) tw.units[to] = x;
+    if (c < 32) sorted[to] = x;
   }
   __syncthreads();
   // steps before each unit, in the sorted order
   const int chunk = (units + PLAN_THREADS - 1) / PLAN_THREADS;
   const int s0 = min(tid * chunk, units), s1 = min(s0 + chunk, units);
   long long weight = 0, all;
-  for (int s = s0; s < s1; ++s) weight += tw.units[s].w + UNIT_COST;
+  for (int s = s0; s < s1; ++s) weight += sorted[s].w + UNIT_COST;
   long long cum = block_scan(weight, sum64_s, all);
   for (int s = s0; s < s1; ++s) {
-    tw.units[s].cum = cum;
-    cum += tw.units[s].w + UNIT_COST;
+    sorted[s].cum = cum;
+    cum += sorted[s].w + UNIT_COST;
   }
-  if (tid == 0) tw.units[units].cum = all;
+  if (tid == 0) sorted[units].cum = all;
   __syncthreads();
+  if (near)
+    for (int e = tid; e < (units + 1) * (int)(sizeof(TileUnit) / 8); e += PLAN_THREADS)
+      reinterpret_cast<uint2*>(tw.units)[e] = reinterpret_cast<const uint2*>(sorted)[e];
 
   // Whole pairs: full waves of the longest, where none is longer than an SM's share.
   const long long pairs = (long long)units * p.Hkv, share = all * p.Hkv / sms;
   const int whole = wmax + UNIT_COST <= share ? (int)(pairs / sms * sms) : 0;
   const auto line_of = [&](long long x) {
     const int s = (int)(x / p.Hkv);
-    return tw.units[s].cum * p.Hkv + (s < units ? (x - (long long)s * p.Hkv) * (tw.units[s].w + UNIT_COST) : 0);
+    return sorted[s].cum * p.Hkv + (s < units ? (x - (long long)s * p.Hkv) * (sorted[s].w + UNIT_COST) : 0);
   };
   const long long line0 = line_of(whole), line = all * p.Hkv - line0;
   // Runs: one per SM; more where the whole pairs before them differ, so that the SMs that are done
@@ -280,31 +292,7 @@ __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
   const long long len = line / sms + 1;
   const int split = whole ? (int)min((long long)MAX_SPLIT, 1 + 2ll * (wmax - wmin_s) / len) : 1;
   const int runs = line ? (int)max(1ll, min((long long)split * sms, line / MIN_RUN)) : 0;
-  // The cut pairs, each found by the run that takes its second piece.
-  for (int r = 1 + tid; r < runs; r += PLAN_THREADS) {
-    const long long begin = run_begin(line, runs, r);
-    int lo = whole / p.Hkv, hi = units;  // the last unit whose pairs begin at or before the run
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tw.units[mid].cum * p.Hkv <= line0 + begin) lo = mid;
-      else hi = mid;
-    }
-    const TileUnit un = tw.units[lo];
-    const int steps = un.w + UNIT_COST, h = (int)((line0 + begin - un.cum * p.Hkv) / steps);
-    const long long at = un.cum * p.Hkv + (long long)h * steps - line0;  // where the pair begins
-    const int first = run_of(line, runs, at + UNIT_COST), last = run_of(line, runs, at + steps - 1);
-    if (r != first + 1 || r > last) continue;
-    for (int t = 0; t < TILE_QT; ++t) {
-      const int tok0 = (un.blk * TILE_QT + t) * tw.T, rows = min(tw.T, un.sq - tok0) * p.g;
-      if (rows <= 0) break;
-      const int n = (rows + JOIN_ROWS - 1) / JOIN_ROWS, to = atomicAdd(&joins_s, n);
-      for (int k = 0; k < n; ++k)
-        tw.joins[to + k] = TileJoin{un.row0, tok0 * p.g + k * JOIN_ROWS, min(rows - k * JOIN_ROWS, JOIN_ROWS), h,
-                                    first, last - first + 1, t * TILE_ROWS + k * JOIN_ROWS, 0};
-    }
-  }
-  __syncthreads();
-  if (tid == 0) *tw.queue = TileQueue{(unsigned int)sms, whole, runs, joins_s, units, line0, line};
+  if (tid == 0) *tw.queue = TileQueue{(unsigned int)sms, whole, runs, 0, units, line0, line};
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
