@@ -25,9 +25,8 @@ namespace {
 
 // An item whose tiles CTA c begins and others finish: the partial results to join.
 struct Split {
-  int b, h;   // b < 0: none
-  int parts;  // slots 2c + 1, 2(c + 1), 2(c + 2), ...
-  int pad;
+  int row0, rows;  // the request's first query row, its packed rows (0: no such item)
+  int h, parts;    // slots 2c + 1, 2(c + 1), 2(c + 2), ...
 };
 
 struct RowsParams : PagedParams {
@@ -356,7 +355,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
   const long long before = block_scan(own, warp_sum, n);
   const int ctas = (int)min((long long)p.rows_grid, n);
   const int cta = (int)blockIdx.x - ((int)gridDim.x - p.rows_grid);
-  if (tid == 0) p.split[cta].b = -1;
+  if (tid == 0) p.split[cta].rows = 0;
   if (cta >= ctas || few_tiles_too<C>(p, n)) return;
   const long long run0 = run_begin(n, ctas, cta);
   const int run = (int)(run_begin(n, ctas, cta + 1) - run0);  // tiles
@@ -682,7 +681,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
     if (begins && !ends && tid == 0) {
       // the CTAs that hold the item's other tiles: up to the one whose run reaches its end
       const long long last = run0 + (run - left) + (it.t1 - tile) - 1;
-      p.split[cta] = Split{b, h, run_of(n, ctas, last) - cta + 1, 0};
+      p.split[cta] = Split{it.row0, it.R, h, run_of(n, ctas, last) - cta + 1};
     }
     __syncthreads();  // the exchange has been read
 
@@ -720,12 +719,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
     if (x < items) {
       const int c = x / halves;
       const Split sp = p.split[c];
-      if (sp.b < 0) continue;
-      int sq, sk;
-      request_span(p, sp.b, row0, sq, sk);
       prow = x % halves * JOIN_ROWS;
-      rows = min(sq * p.g - prow, JOIN_ROWS);
+      rows = min(sp.rows - prow, JOIN_ROWS);
       if (rows <= 0) continue;
+      row0 = sp.row0;
       h = sp.h;
       parts = sp.parts;
       first = (2 * c + 1) * p.slot_rows + prow;

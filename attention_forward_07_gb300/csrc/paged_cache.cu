@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -20,15 +21,15 @@ namespace {
 // free[count - 1 - n], request b's page held_b + i is the (N_b + i)-th, and new row t of request
 // b is at position ctx_b + t - C_b.
 //
-// One launch and no state between calls: every CTA sums all lengths by itself (a block-wide scan
+// One launch and nothing kept between calls: every CTA sums all lengths by itself (a block-wide scan
 // of two counters, kept in shared memory), then the threads of all CTAs share out the pages and
 // the rows (four neighbours to a thread where there are more rows than threads) and find their request
 // by bisection.  A slot on a page added in this call comes
 // straight from the free list, so no CTA waits for another's table entries.  The CTAs are one
 // cluster, and its barrier orders the reads of free_count before its one write, which may be in
 // place.  What bounds it is latency: the chain lengths -> scan -> bisection -> free list -> slot.
-// Measured: 64 requests that grow by a token 4.1 us; 509 requests, 12 prompts of up to 8000 tokens among
-// them (0.45 MB to read and write, 0.07 us of bandwidth) 9.5 us.
+// Measured: 64 requests that grow by a token 3.4 us; 509 requests, 12 prompts of up to 8000 tokens among
+// them (0.45 MB to read and write, 0.07 us of bandwidth) 6.8 us.
 constexpr int TABLES_THREADS = 1024;
 constexpr int TABLES_MAX_B = 16384;
 
@@ -65,8 +66,6 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
   grid_launch_dependents();
   grid_dependency_wait();
   const int count_in = *a.free_count, count = min(max(count_in, 0), a.max_free);
-  __syncthreads();
-  cluster_arrive();  // free_count is read (the wait stands before its write)
 
   // block-wide exclusive scan of (new, need), `per` neighbouring requests to a thread
   const int per = (B + TABLES_THREADS - 1) / TABLES_THREADS;
@@ -104,6 +103,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
   const int2 before = make_int2(warp_sum[warp].x + incl.x - sum.x, warp_sum[warp].y + incl.y - sum.y);
   for (int b = b0; b < b1; ++b) rows_pre[b] += before.x, need_pre[b] += before.y;
   __syncthreads();
+  cluster_arrive();  // free_count has been read (the wait stands before its write)
   const int total = rows_pre[B], need = need_pre[B];
 
   bool bad = count_in != count || need > count || total > a.max_rows;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
   const int nthr = gridDim.x * TABLES_THREADS, gid = blockIdx.x * TABLES_THREADS + tid;
   if (blockIdx.x == 0)
     for (int b = tid; b <= B; b += TABLES_THREADS) a.cu_seqlens_q[b] = rows_pre[b];
-  for (int n = gid; n < need; n += nthr) {
+  for (int n = nthr - 1 - gid; n < need; n += nthr) {  // (from the far end: the near threads have rows)
     const int b = holder(need_pre, B, n);
     const int i = (ctx_s[b] + P - 1) / P + (n - need_pre[b]);
     const int id = free_page(n);
@@ -221,6 +221,37 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS) paged_append_kernel(const _
   }
 }
 
+size_t tables_smem(int B) { return (3 * (size_t)B + 2) * sizeof(int); }
+
+// CTAs of a cluster of paged_tables_kernel at most: 16 where the device has that many SMs side by side for it
+// (509 requests, 45 thousand rows: 7.5 us against 9.5 with the portable 8, a step's worth of rows less to a thread).  Asked once per device.
+int widest_cluster(int dev, int& ctas) {
+  static std::atomic<int> known[64];
+  if ((ctas = known[dev].load()) != 0) return ATTN_OK;
+  const size_t smem = tables_smem(TABLES_MAX_B);
+  if (cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(TABLES_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  ctas = 8;
+  if (cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&clusters, paged_tables_kernel, &cfg) == cudaSuccess && clusters > 0)
+    ctas = 16;
+  else
+    cudaGetLastError();  // (the answer was no)
+  known[dev].store(ctas);
+  return ATTN_OK;
+}
+
 bool misaligned(const void* ptr, unsigned int to) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
 
 }  // namespace
@@ -247,13 +278,12 @@ int attn_paged_tables(const attn_paged_tables_params_t* params) {
   if (rc != ATTN_OK) return rc;
   TablesParams p{a, nullptr};
   if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-  const size_t smem = (3 * (size_t)a.B + 2) * sizeof(int);
-  if (smem > 47 * 1024 &&
-      cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return ATTN_ERR_CUDA;
-  // a CTA for every four rows of its threads, up to the portable cluster of eight
+  int widest = 0;
+  if ((rc = widest_cluster(dev, widest)) != ATTN_OK) return rc;
+  const size_t smem = tables_smem(a.B);
+  // a CTA for every four rows of its threads, up to the widest cluster
   int ctas = 1;
-  while (ctas < 8 && (long long)ctas * 4 * TABLES_THREADS < a.max_rows) ctas *= 2;
+  while (ctas < widest && (long long)ctas * 4 * TABLES_THREADS < a.max_rows) ctas *= 2;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
   return launch_dependent(paged_tables_kernel, dim3(ctas), TABLES_THREADS, smem, st, p, ctas);
 }
