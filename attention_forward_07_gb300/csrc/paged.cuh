@@ -137,6 +137,16 @@ int launch_dependent(void (*kern)(P), dim3 grid, unsigned int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// A C entry's body: what it throws (host memory that has run out, a mutex that fails) becomes a status.
+template <class F>
+int entry(F body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return ATTN_ERR_CUDA;
+  }
+}
+
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace attn

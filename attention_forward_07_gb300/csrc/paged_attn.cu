@@ -913,91 +913,95 @@ int launch(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& pl
 extern "C" {
 
 int attn_paged_workspace(const attn_fwd_paged_params_t* params, unsigned long long* bytes) {
-  using namespace attn;
-  if (!params || !bytes) return ATTN_ERR_INVALID;
-  int rc = check_shape(*params);
-  if (rc != ATTN_OK) return rc;
-  int sms = 0, dev = 0;
-  if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
-  *bytes = Plan(*params, sms).bytes;
-  return ATTN_OK;
+  return attn::entry([&]() -> int {
+    using namespace attn;
+    if (!params || !bytes) return ATTN_ERR_INVALID;
+    int rc = check_shape(*params);
+    if (rc != ATTN_OK) return rc;
+    int sms = 0, dev = 0;
+    if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
+    *bytes = Plan(*params, sms).bytes;
+    return ATTN_OK;
+  });
 }
 
 int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
-  using namespace attn;
-  if (!params) return ATTN_ERR_INVALID;
-  const attn_fwd_paged_params_t& a = *params;
-  int rc = check(a);
-  if (rc != ATTN_OK) return rc;
-  int sms = 0, dev = 0;
-  if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
-  const Plan plan(a, sms);
-  if (a.workspace && a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
-  RowsParams p = {};
-  p.q = static_cast<const uint16_t*>(a.q);
-  p.k = static_cast<const uint16_t*>(a.k_cache);
-  p.v = static_cast<const uint16_t*>(a.v_cache);
-  p.o = static_cast<uint16_t*>(a.o);
-  p.lse = a.lse;
-  p.table = a.block_table;
-  p.cu_q = a.cu_seqlens_q;
-  p.lens_k = a.seqlens_k;
-  p.q_row = a.q_row_stride;
-  p.q_head = a.q_head_stride;
-  p.o_row = a.o_row_stride;
-  p.o_head = a.o_head_stride;
-  p.c_page = a.cache_page_stride;
-  p.c_head = a.cache_head_stride;
-  p.c_row = a.cache_row_stride;
-  p.B = a.B;
-  p.Hq = a.Hq;
-  p.Hkv = a.Hkv;
-  p.g = a.Hq / a.Hkv;
-  p.total_q = a.total_q;
-  p.max_q = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
-  p.num_pages = a.num_pages;
-  p.page_size = a.page_size;
-  p.width = a.table_width;
-  p.table_stride = a.table_stride;
-  p.wl = a.window_left;
-  p.er = a.causal ? 0 : a.window_right;
-  p.scale_log2 = a.scale * LOG2E;
-  if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
-  void* scratch = a.workspace;
-  std::unique_lock<std::mutex> hold;  // until the launches are enqueued
-  if (!scratch) {
-    // a captured call would share the stream's workspace with whatever runs beside its replays
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (capture != cudaStreamCaptureStatusNone) return ATTN_ERR_INVALID;
-    if ((rc = host_workspace(dev, a.stream, plan.bytes, hold, &scratch)) != ATTN_OK) return rc;
-  }
-  uint8_t* ws = static_cast<uint8_t*>(scratch);
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
-  p.split = reinterpret_cast<Split*>(ws + plan.off_split);
-  p.timeout_us = host_timeout_us();
-  p.rows_grid = plan.rows_grid;
-  p.tile.T = plan.T;
-  p.tile.max_units = plan.max_units;
-  p.tile.sms = sms;
-  if (plan.max_units > 0) {
-    p.tile.queue = reinterpret_cast<TileQueue*>(ws + plan.off_queue);
-    p.tile.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);
-    p.tile.joins = reinterpret_cast<TileJoin*>(ws + plan.off_joins);
-    p.tile.part_ml = reinterpret_cast<float2*>(ws + plan.off_tile_ml);
-    p.tile.part_o = reinterpret_cast<float*>(ws + plan.off_tile_o);
-  }
-  p.slot_rows = plan.slot_rows;
-  const bool bf16 = a.dtype == ATTN_BF16;
-  const auto go = [&](auto launch) { return launch(p, a, plan, sms, dev, st); };
-  if (plan.slot_rows == 16) {
-    if (a.d == 64) return go(bf16 ? launch<64, 1, true> : launch<64, 1, false>);
-    return go(bf16 ? launch<128, 1, true> : launch<128, 1, false>);
-  }
-  if (a.d == 64) return go(bf16 ? launch<64, 2, true> : launch<64, 2, false>);
-  return go(bf16 ? launch<128, 2, true> : launch<128, 2, false>);
+  return attn::entry([&]() -> int {
+    using namespace attn;
+    if (!params) return ATTN_ERR_INVALID;
+    const attn_fwd_paged_params_t& a = *params;
+    int rc = check(a);
+    if (rc != ATTN_OK) return rc;
+    int sms = 0, dev = 0;
+    if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
+    const Plan plan(a, sms);
+    if (a.workspace && a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
+    RowsParams p = {};
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.k = static_cast<const uint16_t*>(a.k_cache);
+    p.v = static_cast<const uint16_t*>(a.v_cache);
+    p.o = static_cast<uint16_t*>(a.o);
+    p.lse = a.lse;
+    p.table = a.block_table;
+    p.cu_q = a.cu_seqlens_q;
+    p.lens_k = a.seqlens_k;
+    p.q_row = a.q_row_stride;
+    p.q_head = a.q_head_stride;
+    p.o_row = a.o_row_stride;
+    p.o_head = a.o_head_stride;
+    p.c_page = a.cache_page_stride;
+    p.c_head = a.cache_head_stride;
+    p.c_row = a.cache_row_stride;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.g = a.Hq / a.Hkv;
+    p.total_q = a.total_q;
+    p.max_q = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+    p.num_pages = a.num_pages;
+    p.page_size = a.page_size;
+    p.width = a.table_width;
+    p.table_stride = a.table_stride;
+    p.wl = a.window_left;
+    p.er = a.causal ? 0 : a.window_right;
+    p.scale_log2 = a.scale * LOG2E;
+    if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+    void* scratch = a.workspace;
+    std::unique_lock<std::mutex> hold;  // until the launches are enqueued
+    if (!scratch) {
+      // a captured call would share the stream's workspace with whatever runs beside its replays
+      cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+      if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return ATTN_ERR_CUDA;
+      if (capture != cudaStreamCaptureStatusNone) return ATTN_ERR_INVALID;
+      if ((rc = host_workspace(dev, a.stream, plan.bytes, hold, &scratch)) != ATTN_OK) return rc;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(scratch);
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+    p.split = reinterpret_cast<Split*>(ws + plan.off_split);
+    p.timeout_us = host_timeout_us();
+    p.rows_grid = plan.rows_grid;
+    p.tile.T = plan.T;
+    p.tile.max_units = plan.max_units;
+    p.tile.sms = sms;
+    if (plan.max_units > 0) {
+      p.tile.queue = reinterpret_cast<TileQueue*>(ws + plan.off_queue);
+      p.tile.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);
+      p.tile.joins = reinterpret_cast<TileJoin*>(ws + plan.off_joins);
+      p.tile.part_ml = reinterpret_cast<float2*>(ws + plan.off_tile_ml);
+      p.tile.part_o = reinterpret_cast<float*>(ws + plan.off_tile_o);
+    }
+    p.slot_rows = plan.slot_rows;
+    const bool bf16 = a.dtype == ATTN_BF16;
+    const auto go = [&](auto launch) { return launch(p, a, plan, sms, dev, st); };
+    if (plan.slot_rows == 16) {
+      if (a.d == 64) return go(bf16 ? launch<64, 1, true> : launch<64, 1, false>);
+      return go(bf16 ? launch<128, 1, true> : launch<128, 1, false>);
+    }
+    if (a.d == 64) return go(bf16 ? launch<64, 2, true> : launch<64, 2, false>);
+    return go(bf16 ? launch<128, 2, true> : launch<128, 2, false>);
+  });
 }
 
 }  // extern "C"

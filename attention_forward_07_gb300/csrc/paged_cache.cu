@@ -260,60 +260,64 @@ bool misaligned(const void* ptr, unsigned int to) { return (reinterpret_cast<uin
 extern "C" {
 
 int attn_paged_tables(const attn_paged_tables_params_t* params) {
-  using namespace attn;
-  if (!params) return ATTN_ERR_INVALID;
-  const attn_paged_tables_params_t& a = *params;
-  if (!a.ctx_lens || !a.new_lens || !a.block_table || !a.free_pages || !a.free_count || !a.free_count_out || !a.cu_seqlens_q ||
-      !a.seqlens_k || !a.slots)
-    return ATTN_ERR_INVALID;
-  for (const void* ptr : {(const void*)a.ctx_lens, (const void*)a.new_lens, (const void*)a.block_table, (const void*)a.free_pages,
-                          (const void*)a.free_count, (const void*)a.free_count_out, (const void*)a.cu_seqlens_q,
-                          (const void*)a.seqlens_k, (const void*)a.slots, (const void*)a.positions})
-    if (misaligned(ptr, 4)) return ATTN_ERR_INVALID;
-  if (a.B < 1 || a.B > TABLES_MAX_B || a.table_width < 1 || a.table_stride < a.table_width || a.max_free < 0 || a.max_rows < 1 || a.max_rows > (1 << 30) ||
-      a.page_size < 16 || a.page_size % 16 != 0 || a.num_pages < 1 || (long long)a.num_pages * a.page_size > INT_MAX)
-    return ATTN_ERR_INVALID;
-  int sms = 0, dev = 0;
-  int rc = host_device(sms, dev);
-  if (rc != ATTN_OK) return rc;
-  TablesParams p{a, nullptr};
-  if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-  int widest = 0;
-  if ((rc = widest_cluster(dev, widest)) != ATTN_OK) return rc;
-  const size_t smem = tables_smem(a.B);
-  // a CTA for every four rows of its threads, up to the widest cluster
-  int ctas = 1;
-  while (ctas < widest && (long long)ctas * 4 * TABLES_THREADS < a.max_rows) ctas *= 2;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
-  return launch_dependent(paged_tables_kernel, dim3(ctas), TABLES_THREADS, smem, st, p, ctas);
+  return attn::entry([&]() -> int {
+    using namespace attn;
+    if (!params) return ATTN_ERR_INVALID;
+    const attn_paged_tables_params_t& a = *params;
+    if (!a.ctx_lens || !a.new_lens || !a.block_table || !a.free_pages || !a.free_count || !a.free_count_out || !a.cu_seqlens_q ||
+        !a.seqlens_k || !a.slots)
+      return ATTN_ERR_INVALID;
+    for (const void* ptr : {(const void*)a.ctx_lens, (const void*)a.new_lens, (const void*)a.block_table, (const void*)a.free_pages,
+                            (const void*)a.free_count, (const void*)a.free_count_out, (const void*)a.cu_seqlens_q,
+                            (const void*)a.seqlens_k, (const void*)a.slots, (const void*)a.positions})
+      if (misaligned(ptr, 4)) return ATTN_ERR_INVALID;
+    if (a.B < 1 || a.B > TABLES_MAX_B || a.table_width < 1 || a.table_stride < a.table_width || a.max_free < 0 || a.max_rows < 1 || a.max_rows > (1 << 30) ||
+        a.page_size < 16 || a.page_size % 16 != 0 || a.num_pages < 1 || (long long)a.num_pages * a.page_size > INT_MAX)
+      return ATTN_ERR_INVALID;
+    int sms = 0, dev = 0;
+    int rc = host_device(sms, dev);
+    if (rc != ATTN_OK) return rc;
+    TablesParams p{a, nullptr};
+    if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
+    int widest = 0;
+    if ((rc = widest_cluster(dev, widest)) != ATTN_OK) return rc;
+    const size_t smem = tables_smem(a.B);
+    // a CTA for every four rows of its threads, up to the widest cluster
+    int ctas = 1;
+    while (ctas < widest && (long long)ctas * 4 * TABLES_THREADS < a.max_rows) ctas *= 2;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+    return launch_dependent(paged_tables_kernel, dim3(ctas), TABLES_THREADS, smem, st, p, ctas);
+  });
 }
 
 int attn_paged_append(const attn_paged_append_params_t* params) {
-  using namespace attn;
-  if (!params) return ATTN_ERR_INVALID;
-  const attn_paged_append_params_t& a = *params;
-  if (!a.k_new || !a.v_new || !a.k_cache || !a.v_cache || !a.slots) return ATTN_ERR_INVALID;
-  for (const void* ptr : {a.k_new, a.v_new, (const void*)a.k_cache, (const void*)a.v_cache})
-    if (misaligned(ptr, 16)) return ATTN_ERR_INVALID;
-  if (misaligned(a.slots, 4)) return ATTN_ERR_INVALID;
-  if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
-  if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
-  if (a.rows < 1 || a.rows > (1 << 30) || a.Hkv < 1 || a.Hkv > (1 << 16) || a.num_pages < 1 || a.page_size < 16 || a.page_size % 16 != 0 ||
-      (long long)a.num_pages * a.page_size > INT_MAX)
-    return ATTN_ERR_INVALID;
-  for (long long s : {a.k_row_stride, a.k_head_stride, a.v_row_stride, a.v_head_stride, a.cache_page_stride, a.cache_head_stride,
-                      a.cache_row_stride})
-    if (s < 0 || s % 8 != 0 || s > MAX_STRIDE) return ATTN_ERR_INVALID;
-  if (a.cache_row_stride == 0 || (a.num_pages > 1 && a.cache_page_stride == 0) || (a.Hkv > 1 && a.cache_head_stride == 0))
-    return ATTN_ERR_INVALID;
-  int sms = 0, dev = 0;
-  int rc = host_device(sms, dev);
-  if (rc != ATTN_OK) return rc;
-  AppendParams p{a, nullptr};
-  if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-  const int grid = (a.rows + APPEND_WARPS - 1) / APPEND_WARPS;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
-  return launch_dependent(a.d == 64 ? paged_append_kernel<64> : paged_append_kernel<128>, dim3(grid), 32 * APPEND_WARPS, 0, st, p);
+  return attn::entry([&]() -> int {
+    using namespace attn;
+    if (!params) return ATTN_ERR_INVALID;
+    const attn_paged_append_params_t& a = *params;
+    if (!a.k_new || !a.v_new || !a.k_cache || !a.v_cache || !a.slots) return ATTN_ERR_INVALID;
+    for (const void* ptr : {a.k_new, a.v_new, (const void*)a.k_cache, (const void*)a.v_cache})
+      if (misaligned(ptr, 16)) return ATTN_ERR_INVALID;
+    if (misaligned(a.slots, 4)) return ATTN_ERR_INVALID;
+    if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
+    if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+    if (a.rows < 1 || a.rows > (1 << 30) || a.Hkv < 1 || a.Hkv > (1 << 16) || a.num_pages < 1 || a.page_size < 16 || a.page_size % 16 != 0 ||
+        (long long)a.num_pages * a.page_size > INT_MAX)
+      return ATTN_ERR_INVALID;
+    for (long long s : {a.k_row_stride, a.k_head_stride, a.v_row_stride, a.v_head_stride, a.cache_page_stride, a.cache_head_stride,
+                        a.cache_row_stride})
+      if (s < 0 || s % 8 != 0 || s > MAX_STRIDE) return ATTN_ERR_INVALID;
+    if (a.cache_row_stride == 0 || (a.num_pages > 1 && a.cache_page_stride == 0) || (a.Hkv > 1 && a.cache_head_stride == 0))
+      return ATTN_ERR_INVALID;
+    int sms = 0, dev = 0;
+    int rc = host_device(sms, dev);
+    if (rc != ATTN_OK) return rc;
+    AppendParams p{a, nullptr};
+    if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
+    const int grid = (a.rows + APPEND_WARPS - 1) / APPEND_WARPS;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+    return launch_dependent(a.d == 64 ? paged_append_kernel<64> : paged_append_kernel<128>, dim3(grid), 32 * APPEND_WARPS, 0, st, p);
+  });
 }
 
 }  // extern "C"

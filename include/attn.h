@@ -89,7 +89,7 @@ typedef enum {
     ATTN_OK = 0,
     ATTN_ERR_INVALID = -1,     /* a null pointer, a non-positive size, misalignment, bad scale */
     ATTN_ERR_UNSUPPORTED = -2, /* a head dim or dtype the library has no kernel for */
-    ATTN_ERR_CUDA = -3,        /* a CUDA runtime/driver call failed (launch, tensor map) */
+    ATTN_ERR_CUDA = -3,        /* a CUDA runtime/driver call failed (launch, tensor map, memory) */
     ATTN_ERR_TIMEOUT = -4,     /* a kernel barrier wait ran out of time; outputs undefined */
     ATTN_ERR_DEVICE = -5,      /* no usable sm_103 device */
     ATTN_ERR_PAGE = -6         /* a kernel met a page id, slot or page count out of range */
