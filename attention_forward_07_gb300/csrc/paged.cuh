@@ -6,7 +6,9 @@
 //    32 rows to an item.  24 requests of 32 rows against 4000 keys (d = 128 / 64): 53 / 21 us, by the
 //    tcgen05 path 55 / 31; above 32 rows the order turns (48 rows: 78 us against 57 at d = 128);
 //  * few-row requests beside chunks join the chunks' units while they have few key tiles altogether
-//    (FOLD_TILES in paged_attn.cu).
+//    (FOLD_TILES in paged_attn.cu);
+//  * where no request has more rows than a Q tile, and they have more than ROWS_MAX on the average, all
+//    take the tcgen05 path, which then needs neither the other path's kernel nor its plan (NO_PLAN_B).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -21,6 +23,7 @@ namespace attn {
 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr long long MAX_STRIDE = 1ll << 38;  // elements: no memory holds two entries that far apart, and tensor maps end there
+constexpr int NO_PLAN_B = 512;  // requests at most whose lengths every CTA looks at (16 to a lane)
 constexpr int ROWS_MAX = 16, ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile
 
@@ -29,6 +32,7 @@ constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a un
 // checking 3 - 6 tokens of 24 requests 43.1 / 41.0 / 39.0 / 39.6 us, a mixed batch of 13 requests 77.4 /
 // 74.3 / 66.7 / 66.0, four prompts of 4k 438 / 438 / 436 / 431.)
 constexpr int UNIT_COST = 4;
+constexpr int MIN_RUN = 4 + UNIT_COST;  // steps of a run at least
 struct TileQueue {
   unsigned int next;    // next queue entry (a CTA starts with that of its own number)
   int whole, runs;      // entries: whole (unit, head) pairs, then runs
@@ -48,6 +52,7 @@ struct TileJoin {  // up to JOIN_ROWS packed rows of a cut (unit, head) pair
   int in, pad;          // first row within the slot
 };
 constexpr int JOIN_ROWS = 16;
+constexpr int JOINS_OF_RUN = TILE_ROWS / JOIN_ROWS;  // without a plan
 
 // Scratch of the tcgen05 path.
 struct TileWork {
@@ -59,6 +64,7 @@ struct TileWork {
   int T;             // tokens of a Q tile
   int max_units;     // 0: no request takes this path
   int sms;
+  int no_plan;       // every CTA finds its run by itself (NO_PLAN_B), and lists joins at places of its own
 };
 
 struct PagedParams {

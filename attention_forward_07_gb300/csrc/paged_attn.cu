@@ -130,7 +130,6 @@ __device__ __forceinline__ void rows_next(const RowsParams& p, int& b, int& h, R
 // requests, then one over the units for each of weigh, sort, sum; the units stay in shared memory for these
 // where they fit.
 constexpr int PLAN_THREADS = 128, PLAN_WARPS = PLAN_THREADS / 32;
-constexpr int MIN_RUN = 4 + UNIT_COST;  // steps of a run at least
 constexpr int MAX_SPLIT = 3; // runs per SM at most
 
 // Exclusive sum over the block's threads of x, and the total.
@@ -709,8 +708,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int halves = p.slot_rows / JOIN_ROWS, items = p.rows_grid * halves;
-  const int total = items + (p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
+  const int halves = p.slot_rows / JOIN_ROWS, items = p.tile.no_plan ? 0 : p.rows_grid * halves;
+  const int total = items + (p.tile.no_plan ? p.tile.sms * JOINS_OF_RUN : p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
     int rows, row0, h, parts, first, stride, slot0;  // part k of row r: record (k ? slot0 + k * stride : first) + r
     int prow;  // first packed row
@@ -735,6 +734,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
       row0 = jn.row0;
       prow = jn.row;
       rows = jn.rows;
+      if (rows <= 0) continue;
       h = jn.h;
       parts = jn.parts;
       first = (2 * jn.run + 1) * (TILE_QT * TILE_ROWS) + jn.in;
@@ -901,10 +901,11 @@ int launch(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& pl
   const bool tiles = p.tile.max_units > 0;
   TileParams tp = {};
   int rc = tiles ? tile_prepare(p, a, tp) : ATTN_OK;
-  if (rc == ATTN_OK) rc = launch_dependent(rows_kernel<D, MT, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
+  if (rc == ATTN_OK && !p.tile.no_plan) rc = launch_dependent(rows_kernel<D, MT, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
   if (rc == ATTN_OK && tiles) rc = tile_launch(tp, a, sms, dev, st);
   if (rc != ATTN_OK) return rc;
-  return launch_dependent(join_kernel<D, BF16>, dim3(plan.rows_grid), 32 * JOIN_WARPS, 0, st, p);
+  const int joins = p.tile.no_plan ? sms * JOINS_OF_RUN : plan.rows_grid;
+  return launch_dependent(join_kernel<D, BF16>, dim3(joins), 32 * JOIN_WARPS, 0, st, p);
 }
 
 }  // namespace
@@ -985,6 +986,7 @@ int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
     p.tile.T = plan.T;
     p.tile.max_units = plan.max_units;
     p.tile.sms = sms;
+    p.tile.no_plan = plan.max_units > 0 && p.max_q <= plan.T && a.B <= NO_PLAN_B && (long long)a.total_q * p.g > (long long)ROWS_MAX * a.B;
     if (plan.max_units > 0) {
       p.tile.queue = reinterpret_cast<TileQueue*>(ws + plan.off_queue);
       p.tile.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);

@@ -93,9 +93,86 @@ __device__ __forceinline__ int unit_holding(const TileParams& p, int whole, long
   return lo;
 }
 
+// ------------------------------------------------------------------ runs without a plan
+// Where no request has more rows than a Q tile, every request is one unit, and the units in their own order
+// do for equal runs, one to a CTA: each finds its own from the lengths, and the plan's kernel is not needed
+// (24 requests of 3 - 6 tokens x 8 heads against up to 6k keys: 34.5 us, with the plan 39.3; 4 requests of
+// 6 tokens against 16k: 38 and 45).  A run's beginning: request, head, steps of the pair that lie before it.
+struct RunStart {
+  int b, h, runs;
+  long long in, line, pos, left;  // (pos: the run's first step, left: its steps)
+};
+__device__ __forceinline__ bool request_unit(const TileParams& p, int b, TileUnit& x) {
+  int k0, k1;
+  request_span(p, b, x.row0, x.sq, x.sk);
+  tile_keys(p, x.sq, x.sk, 0, 0, TILE_QT, k0, k1);
+  x.b = b;
+  x.blk = 0;
+  x.j0 = k0 / TILE_KEYS;
+  x.w = max((k1 + TILE_KEYS - 1) / TILE_KEYS - x.j0, 1);
+  return x.sq > 0;
+}
+// By a warp; false where there are fewer runs.
+__device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane, RunStart& r) {
+  const int per = (p.B + 31) / 32, b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B);
+  TileUnit x;
+  long long own = 0;
+  for (int b = b0; b < b1; ++b)
+    if (request_unit(p, b, x)) own += x.w + UNIT_COST;
+  own *= p.Hkv;
+  long long incl = own;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, s);
+    if (lane >= s) incl += y;
+  }
+  r.line = __shfl_sync(0xffffffffu, incl, 31);
+  r.runs = r.line ? (int)max(1ll, min((long long)p.tile.sms, r.line / MIN_RUN)) : 0;
+  if (run >= r.runs) return false;
+  r.pos = run_begin(r.line, r.runs, run);
+  r.left = run_begin(r.line, r.runs, run + 1) - r.pos;
+  const bool mine = r.pos >= incl - own && r.pos < incl;
+  r.b = r.h = 0;
+  r.in = 0;
+  if (mine) {
+    long long at = incl - own;
+    for (int b = b0; b < b1; ++b) {
+      if (!request_unit(p, b, x)) continue;
+      const int steps = x.w + UNIT_COST;
+      if (r.pos < at + (long long)steps * p.Hkv) {
+        r.b = b;
+        r.h = (int)((r.pos - at) / steps);
+        r.in = r.pos - at - (long long)r.h * steps;
+        break;
+      }
+      at += (long long)steps * p.Hkv;
+    }
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  r.b = __shfl_sync(0xffffffffu, r.b, from);
+  r.h = __shfl_sync(0xffffffffu, r.h, from);
+  r.in = __shfl_sync(0xffffffffu, r.in, from);
+  return true;
+}
+
 // ------------------------------------------------------------------ join list
 // One warp of each CTA lists the cut pairs for join_kernel while the others work (the plan, which all wait
 // for, was 2.5 - 4 us longer with it).  Each pair is found by the run that takes its second piece.
+__device__ __forceinline__ void run_join_list(const TileParams& p, int lane) {  // (without a plan)
+  const int r = blockIdx.x;
+  TileJoin* list = p.tile.joins + r * JOINS_OF_RUN;
+  RunStart rs;
+  TileJoin jn = {};
+  if (run_start(p, r, lane, rs)) {
+    TileUnit un;
+    request_unit(p, rs.b, un);
+    const long long at = rs.pos - rs.in;  // where the pair begins
+    const int first = run_of(rs.line, rs.runs, at + UNIT_COST), last = run_of(rs.line, rs.runs, at + un.w + UNIT_COST - 1);
+    if (r == first + 1 && r <= last)
+      jn = TileJoin{un.row0, lane * JOIN_ROWS, max(min(un.sq * p.g - lane * JOIN_ROWS, JOIN_ROWS), 0), rs.h, first, last - first + 1, lane * JOIN_ROWS, 0};
+  }
+  if (lane < JOINS_OF_RUN) list[lane] = jn;
+}
 __device__ __forceinline__ void tile_join_list(const TileParams& p, int lane) {
   TileQueue* q = p.tile.queue;
   const int whole = q->whole, runs = q->runs;
@@ -137,7 +214,9 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
   uint32_t kpar = 1, vpar = 1, ie_par = 1;
   uint32_t kpend = 0, kpend_par = 0, vpend = 0, vpend_par = 0;
   bool inject = p.inject != 0;
-  const unsigned int whole = p.tile.queue->whole, entries = whole + p.tile.queue->runs;
+  const bool no_plan = TURNS && p.tile.no_plan;
+  bool begun = false;  // (without a plan)
+  const unsigned int whole = no_plan ? 0 : p.tile.queue->whole, entries = no_plan ? 0 : whole + p.tile.queue->runs;
 
   // The first entry is the CTA's own number, later ones come from the queue, one ahead and no more (an SM
   // that held two would leave another without).  While a unit's first tiles load, the next entry and,
@@ -154,8 +233,8 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
   };
   int s = 0, h = 0, run = 0;  // unit (in the plan's order), head; run being worked off
   long long left = 0;         // steps of the run that are left
+  TileUnit pt;
   for (int k = 0;; ++k) {
-    TileUnit pt;
     int slot = -1, from = 0, tiles = 0;  // this piece: tiles from .. from + tiles of the unit
     while (tiles == 0) {
       long long in = 0;  // steps of the pair that lie before the run
@@ -164,11 +243,15 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
         if (++h == p.Hkv) {
           h = 0;
           ++s;
+          if (no_plan)
+            while (s < p.B && !request_unit(p, s, pt)) ++s;
         }
-        pt = p.tile.units[s];
+        if (!no_plan) pt = p.tile.units[s];
       } else {
         const unsigned int x = x_next;
-        if (x >= entries) {
+        RunStart rs;
+        const bool more = no_plan ? !begun && run_start(p, blockIdx.x, lane, rs) : x < entries;
+        if (!more) {
           if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
           if (lane == 0) {
             hdr[ie].j = -1;
@@ -178,24 +261,34 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
           __syncwarp();
           return;
         }
-        pt = u_next;
-        if (lane == 0) raw = atomicAdd(&p.tile.queue->next, 1u);
-        asked = true;
-        if (x < whole) {
-          h = (int)(x % p.Hkv);
-          tiles = pt.w;
-          break;
+        if (no_plan) {
+          run = blockIdx.x;
+          s = rs.b;
+          h = rs.h;
+          in = rs.in;
+          left = rs.left;
+          request_unit(p, s, pt);
+          begun = true;
+        } else {
+          pt = u_next;
+          if (lane == 0) raw = atomicAdd(&p.tile.queue->next, 1u);
+          asked = true;
+          if (x < whole) {
+            h = (int)(x % p.Hkv);
+            tiles = pt.w;
+            break;
+          }
+          run = (int)(x - whole);
+          const int runs = (int)(entries - whole);
+          const long long line = p.tile.queue->line, at = run_begin(line, runs, run);
+          left = run_begin(line, runs, run + 1) - at;
+          const long long pos = p.tile.queue->line0 + at;
+          s = unit_holding(p, (int)whole, pos, lane);
+          pt = p.tile.units[s];
+          in = pos - pt.cum * p.Hkv;
+          h = (int)(in / (pt.w + UNIT_COST));
+          in -= (long long)h * (pt.w + UNIT_COST);
         }
-        run = (int)(x - whole);
-        const int runs = (int)(entries - whole);
-        const long long line = p.tile.queue->line, at = run_begin(line, runs, run);
-        left = run_begin(line, runs, run + 1) - at;
-        const long long pos = p.tile.queue->line0 + at;
-        s = unit_holding(p, (int)whole, pos, lane);
-        pt = p.tile.units[s];
-        in = pos - pt.cum * p.Hkv;
-        h = (int)(in / (pt.w + UNIT_COST));
-        in -= (long long)h * (pt.w + UNIT_COST);
       }
       // the run's steps of the pair; none of its tiles where the run ends ahead of them
       const long long out = min(in + left, (long long)(pt.w + UNIT_COST));
@@ -597,7 +690,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
       TileEnv<D, TURNS> env;
       mma_role<D, BF16, L>(env, p.timeout_us, base, gbase, abort_flag, tmem, lane);
     } else if (warp == 2) {
-      tile_join_list(p, lane);
+      if (TURNS && p.tile.no_plan) run_join_list(p, lane);
+      else tile_join_list(p, lane);
     }
   } else {
     setmaxnreg_inc<L::REGS_SOFTMAX>();
@@ -661,7 +755,7 @@ int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, 
   const bool bf16 = a.dtype == ATTN_BF16;
   // Where no request has more rows than one Q tile, both Q tiles take the same rows and the key tiles by turns,
   // so that one's products run while the other's softmax does.  24 requests of 3 - 6 tokens x 8 heads
-  // against up to 6k keys: 45 us by turns, 51 with the second Q tile idle.
+  // against up to 6k keys, when their start took longer: 45 us by turns, 51 with the second Q tile idle.
   const bool turns = p.max_q <= p.tile.T;
   const auto go = [&](auto launch) { return launch(p, sms, dev, st); };
   if (a.d == 64) {

@@ -268,6 +268,19 @@ def test_one_long_request_among_many_short_ones():
         bt.check(o.cpu(), lse.cpu(), True, -1, -1, 0.1)
 
 
+@pytest.mark.parametrize("wl", [-1, 50])
+@pytest.mark.parametrize("B,new,Hkv,d", [(1, [7], 2, 128), (33, [3, 0, 5, 7], 1, 64), (70, [3, 0, 5, 7], 2, 128), (512, [0, 5, 3], 1, 128),
+                                         (513, [3, 0, 5, 7], 1, 64), (60, [5, 1, 1, 1], 2, 64), (61, [1, 6, 1, 1, 0], 1, 128)])
+def test_a_few_tokens_of_many_requests(B, new, Hkv, d, wl):
+    """Requests of one tile of rows at most, with a plan and without (up to 512 of more than 16 rows on the average)."""
+    lq = [new[b % len(new)] for b in range(B)]
+    lk = [(977 * b) % (3000 if B < 40 else 400 if B < 100 else 150) + lq[b] * (b % 5 != 0) for b in range(B)]
+    bt = Batch(lq, lk, 8 * Hkv, Hkv, d, "bf16", 16, seed=B + d)
+    o, lse = _attend(bt, True, wl, -1, 0.1)
+    af.attn_check()
+    bt.check(o.cpu(), lse.cpu(), True, wl, -1, 0.1)
+
+
 @pytest.mark.parametrize("lq,lk,d,page,wl", [([1, 1, 1], [65, 17, 300], 128, 16, -1), ([1, 1], [333, 90], 64, 64, 40),
                                              ([70, 3], [200, 39], 128, 32, -1), ([150, 90], [400, 90], 64, 48, 33),
                                              ([200], [517], 128, 256, 64)])
