@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS) paged_append_kernel(const _
 size_t tables_smem(int B) { return (3 * (size_t)B + 2) * sizeof(int); }
 
 // CTAs of a cluster of paged_tables_kernel at most: 16 where the device has that many SMs side by side for it
-// (509 requests, 45 thousand rows: 7.5 us against 9.5 with the portable 8, a step's worth of rows less to a thread).  Asked once per device.
+// (509 requests, 52 thousand rows: 7.5 us against 9.5 with the portable 8, a step's worth of rows less to a thread).  Asked once per device.
 int widest_cluster(int dev, int& ctas) {
   static std::atomic<int> known[64];
   if ((ctas = known[dev].load()) != 0) return ATTN_OK;
