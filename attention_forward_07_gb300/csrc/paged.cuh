@@ -59,7 +59,7 @@ struct TileWork {
   TileQueue* queue;
   TileUnit* units;   // [max_units + 1], longest first
   TileJoin* joins;   // [max runs * 256 / JOIN_ROWS]: every cut pair holds a run's beginning
-  float* part_o;     // [2 max runs][256][D]: unscaled O of a piece
+  float* part_o;     // [2 max runs][D / 4][256][4]: unscaled O of a piece (part_at)
   float2* part_ml;   // [2 max runs][256]: its exponent base (exp2 domain) and sum of weights
   int T;             // tokens of a Q tile
   int max_units;     // 0: no request takes this path
@@ -105,6 +105,13 @@ __device__ __forceinline__ bool tile_keys(const PagedParams& p, int sq, int sk, 
   const int a = row_lo(p, i0, sk - sq), e = row_hi(p, i1, sk - sq, sk);
   if (e > a) lo = a, hi = e;
   return true;
+}
+
+// Where four columns of a row of a slot begin.  A thread of the tcgen05 kernel has a row, so neighbouring rows
+// lie side by side (with the columns of a row side by side a full piece took 6 - 11k cycles to write).
+template <int D>
+__device__ __forceinline__ long long part_at(int slot, int row, int col) {
+  return (((long long)slot * (D / 4) + col / 4) * (TILE_QT * TILE_ROWS) + row) * 4;
 }
 
 // First step of run i out of n over a line, and the run that holds step x of it.

@@ -695,10 +695,52 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
 // ------------------------------------------------------------------ join
 // Puts the partial results of cut items and units together: for a row of theirs
 //     m = max m_k, O = sum 2^(m_k - m) O_k / sum 2^(m_k - m) l_k, LSE = ln2 (m + log2 sum).
-// A CTA takes a cut item of the few-row path (at most 16 rows) or 16 rows of a cut unit of the tcgen05 path;
-// its warps share out the rows, and where there are fewer rows than warps, a row's parts.  The parts were
-// just written and are mostly in L2; four are in flight at a time.
-constexpr int JOIN_WARPS = JOIN_ROWS;
+// A CTA takes 16 rows of a cut item of the few-row path, whose warps share out the rows, and where there are
+// fewer rows than warps, a row's parts; or 16 rows of a cut unit of the tcgen05 path, four columns of a
+// row to a thread, as that path writes them.  The parts were just written and are mostly in L2; four are in
+// flight at a time.
+constexpr int JOIN_WARPS = JOIN_ROWS, JOIN_AHEAD = 4;
+
+template <int D, bool BF16>
+__device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& jn) {
+  const int r = threadIdx.x % JOIN_ROWS, col = threadIdx.x / JOIN_ROWS * 4;
+  static_assert(D / 4 <= 32 * JOIN_WARPS / JOIN_ROWS, "a thread to four columns of a row");
+  if (r >= jn.rows || col >= D) return;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < jn.parts; k0 += JOIN_AHEAD) {
+    float2 ml[JOIN_AHEAD];
+    float4 v[JOIN_AHEAD];
+#pragma unroll
+    for (int a = 0; a < JOIN_AHEAD; ++a) {
+      const int k = k0 + a, slot = 2 * (jn.run + k) + (k == 0);
+      ml[a] = make_float2(-INFINITY, 0.f);
+      v[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < jn.parts) {
+        ml[a] = p.tile.part_ml[(long long)slot * (TILE_QT * TILE_ROWS) + jn.in + r];
+        v[a] = *reinterpret_cast<const float4*>(p.tile.part_o + part_at<D>(slot, jn.in + r, col));
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int a = 0; a < JOIN_AHEAD; ++a) mn = fmaxf(mn, ml[a].x);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+    l *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int a = 0; a < JOIN_AHEAD; ++a) {
+      const float fa = ml[a].x == -INFINITY ? 0.f : ex2_approx(ml[a].x - mn);
+      l = fmaf(ml[a].y, fa, l);
+      acc = make_float4(fmaf(v[a].x, fa, acc.x), fmaf(v[a].y, fa, acc.y), fmaf(v[a].z, fa, acc.z), fmaf(v[a].w, fa, acc.w));
+    }
+    m = mn;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int rr = jn.row + r, i = rr / p.g, hq = jn.h * p.g + rr - i * p.g;
+  *reinterpret_cast<uint2*>(p.o + (long long)(jn.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
+      make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+  if (col == 0 && p.lse) p.lse[(long long)hq * p.total_q + jn.row0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_constant__ RowsParams p) {
@@ -711,44 +753,22 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
   const int halves = p.slot_rows / JOIN_ROWS, items = p.tile.no_plan ? 0 : p.rows_grid * halves;
   const int total = items + (p.tile.no_plan ? p.tile.sms * JOINS_OF_RUN : p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
-    int rows, row0, h, parts, first, stride, slot0;  // part k of row r: record (k ? slot0 + k * stride : first) + r
-    int prow;  // first packed row
-    const float* part_o;
-    const float2* part_ml;
-    if (x < items) {
-      const int c = x / halves;
-      const Split sp = p.split[c];
-      prow = x % halves * JOIN_ROWS;
-      rows = min(sp.rows - prow, JOIN_ROWS);
-      if (rows <= 0) continue;
-      row0 = sp.row0;
-      h = sp.h;
-      parts = sp.parts;
-      first = (2 * c + 1) * p.slot_rows + prow;
-      slot0 = 2 * c * p.slot_rows + prow;
-      stride = 2 * p.slot_rows;
-      part_o = p.part_o;
-      part_ml = p.part_ml;
-    } else {
-      const TileJoin jn = p.tile.joins[x - items];
-      row0 = jn.row0;
-      prow = jn.row;
-      rows = jn.rows;
-      if (rows <= 0) continue;
-      h = jn.h;
-      parts = jn.parts;
-      first = (2 * jn.run + 1) * (TILE_QT * TILE_ROWS) + jn.in;
-      slot0 = 2 * jn.run * (TILE_QT * TILE_ROWS) + jn.in;
-      stride = 2 * TILE_QT * TILE_ROWS;
-      part_o = p.tile.part_o;
-      part_ml = p.tile.part_ml;
+    if (x >= items) {
+      join_unit<D, BF16>(p, p.tile.joins[x - items]);
+      continue;
     }
+    const int c = x / halves, prow = x % halves * JOIN_ROWS;
+    const Split sp = p.split[c];
+    const int rows = min(sp.rows - prow, JOIN_ROWS), row0 = sp.row0, h = sp.h, parts = sp.parts;
+    if (rows <= 0) continue;
+    // part k of row r: record (k ? slot0 + k * stride : first) + r
+    const int first = (2 * c + 1) * p.slot_rows + prow, slot0 = 2 * c * p.slot_rows + prow, stride = 2 * p.slot_rows;
     int share = 1;  // warps to a row
     while (share * 2 * rows <= JOIN_WARPS) share *= 2;
     const int r = warp / share, sub = warp % share;
     float m = -INFINITY, l = 0.f, acc[E] = {};
     if (r < rows) {
-      constexpr int AHEAD = 4;
+      constexpr int AHEAD = JOIN_AHEAD;
       for (int k0 = sub; k0 < parts; k0 += share * AHEAD) {
         float2 ml[AHEAD];
         float v[AHEAD][E];
@@ -756,9 +776,9 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
         for (int a = 0; a < AHEAD; ++a) {
           const int k = k0 + a * share;
           const long long at = (k ? slot0 + (long long)k * stride : first) + r;
-          ml[a] = k < parts ? part_ml[at] : make_float2(-INFINITY, 0.f);
+          ml[a] = k < parts ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[a][e] = k < parts ? part_o[at * D + lane * E + e] : 0.f;
+          for (int e = 0; e < E; ++e) v[a][e] = k < parts ? p.part_o[at * D + lane * E + e] : 0.f;
         }
         float mn = m;
 #pragma unroll

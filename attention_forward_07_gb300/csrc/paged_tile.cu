@@ -520,7 +520,8 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
     const int rows = min(p.tile.T, sq - tok0) * p.g;  // of this tile (may be <= 0)
     const bool row_ok = r < rows;
     const int my_tok = token_of(r);
-    const long long part = (long long)slot_out * UNIT_ROWS + (TURNS ? 0 : t * BM) + r;
+    const int part_row = (TURNS ? 0 : t * BM) + r;
+    const long long part = (long long)slot_out * UNIT_ROWS + part_row;
     if constexpr (TURNS) {
       // Both Q tiles hold results of the same rows: they exchange m and l through shared memory (d = 128:
       // the staging area, d = 64: the Q buffer, whose reads are over), then each warpgroup joins and
@@ -553,7 +554,8 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
         const int col = t * (D / 2) + ch * 16;
         if (row_ok && slot_out >= 0) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(p.tile.part_o + part * D + col + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(p.tile.part_o + part_at<D>(slot_out, part_row, col + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         } else if (row_ok) {
           uint4* dst = reinterpret_cast<uint4*>(p.o + (long long)(row0 + tok0 + my_tok) * p.o_row + (long long)head * p.o_head + col);
           dst[0] = make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
@@ -574,7 +576,6 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       continue;
     }
     if (slot_out >= 0) {
-      float* dst = p.tile.part_o + part * D;
 #pragma unroll
       for (int ch = 0; ch < D / 16; ++ch) {
         uint32_t ob[16];
@@ -587,7 +588,8 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
         if (row_ok) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4*>(dst + ch * 16 + x * 4) = make_uint4(ob[4 * x], ob[4 * x + 1], ob[4 * x + 2], ob[4 * x + 3]);
+            *reinterpret_cast<uint4*>(p.tile.part_o + part_at<D>(slot_out, part_row, ch * 16 + x * 4)) =
+                make_uint4(ob[4 * x], ob[4 * x + 1], ob[4 * x + 2], ob[4 * x + 3]);
         }
       }
       if (row_ok) p.tile.part_ml[part] = make_float2(m, l);
