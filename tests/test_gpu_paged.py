@@ -58,7 +58,7 @@ def _held(ctx, page, W, num_pages, rng):
 
 @pytest.mark.parametrize("B,page,top_ctx,top_new,pad", [
     (1, 16, 1, 1, 0), (1, 16, 40, 0, 3), (3, 48, 100, 70, 5), (64, 16, 900, 1, 0), (33, 256, 3000, 700, 9),
-    (1025, 32, 300, 5, 100), (2500, 16, 60, 30, 1), (16384, 16, 20, 2, 0)])
+    (1025, 32, 300, 5, 100), (2500, 16, 60, 30, 1), (16384, 16, 20, 2, 0), (16384, 16, 20, 9, 2)])
 def test_tables(B, page, top_ctx, top_new, pad):
     rng = np.random.default_rng(B + page)
     ctx = rng.integers(0, top_ctx + 1, B)
