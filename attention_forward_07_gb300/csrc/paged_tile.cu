@@ -603,6 +603,12 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
     const bool staged = !L::STAGE_O || nact > 0;
     uint8_t* stage = L::STAGE_O ? gbase + L::OFF_Q + (k % L::QBUF) * L::Q_BUF_BYTES + (t * 4 + quarter) * (32 * 128)
                                 : gbase + L::OFF_STAGE + (t * 4 + quarter) * (32 * 128);
+    uint16_t* out[8];  // where the lane's segments of rows kk * 4 + lane / 8 go
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const int row = quarter * 32 + kk * 4 + lane / 8, tok = token_of(row), head = h * p.g + row - tok * p.g;
+      out[kk] = p.o + (long long)(row0 + tok0 + tok) * p.o_row + (long long)head * p.o_head + lane % 8 * 8;
+    }
 #pragma unroll
     for (int hh = 0; hh < D / 64; ++hh) {
       if (staged) {
@@ -633,8 +639,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
         const int q = kk * 4 + lane / 8, cc = lane % 8, row = quarter * 32 + q;
         if (row < rows) {
           const uint4 val = staged ? *reinterpret_cast<const uint4*>(stage + q * 128 + ((cc ^ (q & 7)) * 16)) : make_uint4(0u, 0u, 0u, 0u);
-          const int tok = token_of(row), head = h * p.g + row - tok * p.g;
-          *reinterpret_cast<uint4*>(p.o + (long long)(row0 + tok0 + tok) * p.o_row + (long long)head * p.o_head + hh * 64 + cc * 8) = val;
+          *reinterpret_cast<uint4*>(out[kk] + hh * 64) = val;
         }
       }
       __syncwarp();
