@@ -542,7 +542,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       const float fa = (t ? f_other : f_own) * inv, fb = (t ? f_own : f_other) * inv;
       const uint32_t both = tmem + lane_off + L::O_COL + t * (D / 2);
       const int head = h * p.g + r - my_tok * p.g;
-#pragma unroll
+#pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t oa[16], ob[16];
         tmem_ld32x32b_x16_wait(both + ch * 16, oa);
@@ -576,7 +576,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       continue;
     }
     if (slot_out >= 0) {
-#pragma unroll
+#pragma unroll 1
       for (int ch = 0; ch < D / 16; ++ch) {
         uint32_t ob[16];
         if (nact > 0) {
@@ -609,10 +609,10 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       const int row = quarter * 32 + kk * 4 + lane / 8, tok = token_of(row), head = h * p.g + row - tok * p.g;
       out[kk] = p.o + (long long)(row0 + tok0 + tok) * p.o_row + (long long)head * p.o_head + lane % 8 * 8;
     }
-#pragma unroll
+#pragma unroll 1
     for (int hh = 0; hh < D / 64; ++hh) {
       if (staged) {
-#pragma unroll
+#pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t ob[16];
           if (nact > 0) {
