@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
     }
     copy_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < C::NST - 1; ++s) issue();
 
   int slot = 0;

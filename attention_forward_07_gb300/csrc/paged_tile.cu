@@ -96,7 +96,7 @@ __device__ __forceinline__ int unit_holding(const TileParams& p, int whole, long
 // ------------------------------------------------------------------ runs without a plan
 // Where no request has more rows than a Q tile, every request is one unit, and the units in their own order
 // do for equal runs, one to a CTA: each finds its own from the lengths, and the plan's kernel is not needed
-// (24 requests of 3 - 6 tokens x 8 heads against up to 6k keys: 34.5 us, with the plan 39.3; 4 requests of
+// (24 requests of 3 - 6 tokens x 8 heads against up to 6k keys: 34.5 us, with the plan 39.3 (33.4 now); 4 requests of
 // 6 tokens against 16k: 38 and 45).  A run's beginning: request, head, steps of the pair that lie before it.
 struct RunStart {
   int b, h, runs;
@@ -511,7 +511,8 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       ++np;
     }
 
-    // Epilogue.  A whole unit writes O / l and LSE, a part its unscaled O in 32 bits, m and l.
+    // Epilogue.  A whole unit writes O / l and LSE, a part its unscaled O in 32 bits, m and l.  Its loops are not
+    // unrolled: it runs once a unit, and fetching its instructions took longer than a loop's turns do.
     if (nact > 0) {
       if (!bwait_warp(bars + 8u * (L::B_ODONE + t), o_par, abort_flag, to)) return;
       o_par ^= 1u;
