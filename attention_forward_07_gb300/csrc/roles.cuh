@@ -62,6 +62,12 @@ struct Layout {
   // current one.
   static constexpr bool RING = (D == 64);
   static constexpr int S_SLOTS = RING ? 3 : QT;
+  // Barriers that say S is there.  d = 64: two to a Q tile, its Q.K^Ts by turns: softmax t has waited for
+  // the one before the last itself, so the phase it waits for is the next one (with a barrier to a slot it
+  // might have passed over key tiles of the other Q tile alone, and taken an earlier phase for its own), and
+  // the one after the next is not computed before softmax t is done with this one.
+  static constexpr int S_BARS = RING ? 2 * QT : QT;
+  __device__ static __forceinline__ int s_bar(int t, int n) { return RING ? 2 * t + (n & 1) : t; }  // of a Q tile's n-th
   static constexpr int O_COL = RING ? 384 : 256;
   static constexpr int O_STRIDE = RING ? 64 : 128;
   static_assert(S_SLOTS * 128 + QT * O_STRIDE <= TMEM_COLS, "TMEM columns");
@@ -94,7 +100,7 @@ struct Layout {
                        B_KEMPTY = B_KFULL + KSLOT, B_VFULL = B_KEMPTY + KSLOT,
                        B_VEMPTY = B_VFULL + VSLOT, B_IFULL = B_VEMPTY + VSLOT,
                        B_IEMPTY = B_IFULL + NINFO,
-                       B_STILE = B_IEMPTY + NINFO, B_PREADY = B_STILE + S_SLOTS,
+                       B_STILE = B_IEMPTY + NINFO, B_PREADY = B_STILE + S_BARS,
                        B_ODONE = B_PREADY + QT, B_OPV = B_ODONE + QT, B_DRAIN = B_OPV + QT,
                        B_XCHG = B_DRAIN + 1, NBAR = B_XCHG + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -176,7 +182,7 @@ __device__ __forceinline__ void init_barriers(uint32_t bars, int readers = 0) {
     mbar_init(bars + 8u * (L::B_IFULL + e), 1);                 // load-warp lane 0
     mbar_init(bars + 8u * (L::B_IEMPTY + e), 1 + QT * BM + readers);  // MMA thread + softmax threads
   }
-  for (int sl = 0; sl < L::S_SLOTS; ++sl) mbar_init(bars + 8u * (L::B_STILE + sl), 1);
+  for (int sb = 0; sb < L::S_BARS; ++sb) mbar_init(bars + 8u * (L::B_STILE + sb), 1);
   for (int t = 0; t < QT; ++t) {
     mbar_init(bars + 8u * (L::B_PREADY + t), BM);
     mbar_init(bars + 8u * (L::B_ODONE + t), 1);
@@ -214,6 +220,7 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
   uint32_t q_par = 0, ie_par = 0, kpar = 0, vpar = 0, p_par0 = 0, p_par1 = 0;  // q_par: bit per Q buffer
   int kslot = 0, vslot = 0, ie = 0;
   int nqk = 0;                 // d = 64: ring slot of the next Q.K^T
+  uint32_t odd = 0;            // d = 64: bit t: Q tile t has had an odd number of them
   int pslot0 = 0, pslot1 = 0;  // d = 64: ring slot holding P_t of the previous key tile
 
   for (int k = 0;; ++k) {
@@ -300,7 +307,8 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
                                ID_QK, kk > 0 ? 1u : 0u);
                 }
               }
-              tc_commit_elect(bars + 8u * (L::B_STILE + new_slot));
+              tc_commit_elect(bars + 8u * (L::B_STILE + L::s_bar(t, (int)(odd >> t))));
+              if constexpr (L::RING) odd ^= 1u << t;
               env.computed(t, j, lane);
               __syncwarp();
             }

@@ -281,6 +281,31 @@ def test_a_few_tokens_of_many_requests(B, new, Hkv, d, wl):
     bt.check(o.cpu(), lse.cpu(), True, wl, -1, 0.1)
 
 
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,d,dtype,page", [
+    ([30, 1, 887, 5, 276, 29, 13, 308, 21, 558, 51, 110, 23, 512, 7, 855, 10, 18, 229, 2, 10, 7, 1],
+     [49, 2503, 1, 626, 20, 1, 64, 4, 513, 4, 3773, 11, 5, 73, 184, 1006, 8, 13, 1472, 37, 475, 22, 2], 9, 3, 64, "f16", 16),
+    ([129, 248, 9, 164, 1, 4, 5, 111, 240, 3], [481, 14, 1, 58, 617, 619, 28, 965, 27, 11], 96, 3, 64, "bf16", 256),
+    ([2, 283], [6378, 2072], 128, 8, 64, "bf16", 256),
+    ([40, 130, 40, 130] * 6, [700, 900, 650, 130] * 6, 4, 2, 128, "bf16", 32)])
+def test_units_of_one_tile_before_units_of_two(lq, lk, Hq, Hkv, d, dtype, page):
+    """A Q tile that has no key tiles for a whole unit does not take the other one's scores for its own in the
+    next: the softmax of the idle tile is ahead of the products by the whole ring of descriptors."""
+    bt = Batch(lq, lk, Hq, Hkv, d, dtype, page, seed=sum(lq))
+    q, k, v, o, lse = bt.device()
+    args = (k, v, o, bt.table.cuda(), bt.cu.cuda(), bt.lens.cuda(), bt.max_q)
+    first = None
+    for _ in range(30):
+        o.fill_(float("nan"))
+        af.attn_fwd_paged(q, *args, lse=lse, causal=True, scale=0.125)
+        af.attn_check()
+        if first is None:
+            first = o.clone(), lse.clone()
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    if Hq <= 32:
+        bt.check(o.cpu(), lse.cpu(), True, -1, -1, 0.125)
+    assert torch.all(torch.isfinite(o[:, :sum(lq)].float()))
+
+
 @pytest.mark.parametrize("lq,lk,d,page,wl", [([1, 1, 1], [65, 17, 300], 128, 16, -1), ([1, 1], [333, 90], 64, 64, 40),
                                              ([70, 3], [200, 39], 128, 32, -1), ([150, 90], [400, 90], 64, 48, 33),
                                              ([200], [517], 128, 256, 64)])
