@@ -566,13 +566,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t base, uin
       if constexpr (L::RING) {
         const int before = nq + ((t == 1 && (flags & 1)) ? 1 : 0);
         slot = before % L::S_SLOTS;
-        spar = (uint32_t)(np >> 1) & 1u;
+        spar = L::sp_parity(np);
         nq += (flags & 1) + ((flags >> 1) & 1);
       }
       if (!act) continue;
       const uint32_t s_addr = tmem + lane_off + slot * 128;
 
-      if (!bwait_warp(bars + 8u * (L::B_STILE + L::s_bar(t, np)), spar, abort_flag, to)) return;
+      if (!bwait_warp(bars + 8u * (L::B_STILE + L::sp_bar(t, np)), spar, abort_flag, to)) return;
       if constexpr (!L::RING) s_par ^= 1u;
       tc_fence_after();
       const auto make_mask = [&] {
@@ -603,7 +603,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t base, uin
       // and arrive again before the slowest warp has arrived for this one; the warpgroup
       // meets here first
       if constexpr (L::RING) named_bar_sync(1 + t, BM);
-      mbar_arrive(bars + 8u * (L::B_PREADY + t));
+      mbar_arrive(bars + 8u * (L::B_PREADY + L::sp_bar(t, np)));
       ++nact;
       ++np;
     }

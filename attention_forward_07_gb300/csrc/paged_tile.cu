@@ -484,12 +484,12 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       if constexpr (L::RING) {
         const int before = nq + ((t == 1 && (flags & 1)) ? 1 : 0);
         slot = before % L::S_SLOTS;
-        spar = (uint32_t)(np >> 1) & 1u;
+        spar = L::sp_parity(np);
         nq += (flags & 1) + ((flags >> 1) & 1);
       }
       if (!act) continue;
       const uint32_t s_addr = tmem + lane_off + slot * 128;
-      if (!bwait_warp(bars + 8u * (L::B_STILE + L::s_bar(t, np)), spar, abort_flag, to)) return;
+      if (!bwait_warp(bars + 8u * (L::B_STILE + L::sp_bar(t, np)), spar, abort_flag, to)) return;
       if constexpr (!L::RING) s_par ^= 1u;
       tc_fence_after();
       const auto make_mask = [&] {
@@ -506,7 +506,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       if (!softmax_tile<D, BF16, L>(s_addr, o_addr, c, make_mask, bars + 8u * (L::B_OPV + t), np, nact, abort_flag, to, m, l)) return;
       tc_fence_before();
       if constexpr (L::RING) named_bar_sync(1 + t, BM);
-      mbar_arrive(bars + 8u * (L::B_PREADY + t));
+      mbar_arrive(bars + 8u * (L::B_PREADY + L::sp_bar(t, np)));
       ++nact;
       ++np;
     }

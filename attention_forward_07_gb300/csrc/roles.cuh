@@ -62,12 +62,15 @@ struct Layout {
   // current one.
   static constexpr bool RING = (D == 64);
   static constexpr int S_SLOTS = RING ? 3 : QT;
-  // Barriers that say S is there.  d = 64: two to a Q tile, its Q.K^Ts by turns: softmax t has waited for
-  // the one before the last itself, so the phase it waits for is the next one (with a barrier to a slot it
-  // might have passed over key tiles of the other Q tile alone, and taken an earlier phase for its own), and
-  // the one after the next is not computed before softmax t is done with this one.
-  static constexpr int S_BARS = RING ? 2 * QT : QT;
-  __device__ static __forceinline__ int s_bar(int t, int n) { return RING ? 2 * t + (n & 1) : t; }  // of a Q tile's n-th
+  // Barriers that say S or P is there.  A wait tells a phase from the next one by one bit, so it has to be
+  // within a phase of what it waits for.  d = 64: two barriers to a Q tile, its n-th S and P by turns.  Whoever
+  // waits for the n-th has waited for the (n - 2)-th, and the (n + 2)-th is not made before it is done with
+  // the n-th.  (With S barriers to ring slots a softmax might have passed over key tiles of the other Q
+  // tile alone, and taken an earlier phase for its own; with one P barrier to a Q tile the MMA warp, where
+  // it lost time between a Q.K^T and the wait for the P before, found two phases gone by.)
+  static constexpr int SP_BARS = RING ? 2 * QT : QT;
+  __device__ static __forceinline__ int sp_bar(int t, uint32_t n) { return RING ? 2 * t + (int)(n & 1u) : t; }
+  __device__ static __forceinline__ uint32_t sp_parity(uint32_t n) { return (RING ? n >> 1 : n) & 1u; }
   static constexpr int O_COL = RING ? 384 : 256;
   static constexpr int O_STRIDE = RING ? 64 : 128;
   static_assert(S_SLOTS * 128 + QT * O_STRIDE <= TMEM_COLS, "TMEM columns");
@@ -100,8 +103,8 @@ struct Layout {
                        B_KEMPTY = B_KFULL + KSLOT, B_VFULL = B_KEMPTY + KSLOT,
                        B_VEMPTY = B_VFULL + VSLOT, B_IFULL = B_VEMPTY + VSLOT,
                        B_IEMPTY = B_IFULL + NINFO,
-                       B_STILE = B_IEMPTY + NINFO, B_PREADY = B_STILE + S_BARS,
-                       B_ODONE = B_PREADY + QT, B_OPV = B_ODONE + QT, B_DRAIN = B_OPV + QT,
+                       B_STILE = B_IEMPTY + NINFO, B_PREADY = B_STILE + SP_BARS,
+                       B_ODONE = B_PREADY + SP_BARS, B_OPV = B_ODONE + QT, B_DRAIN = B_OPV + QT,
                        B_XCHG = B_DRAIN + 1, NBAR = B_XCHG + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
@@ -182,9 +185,11 @@ __device__ __forceinline__ void init_barriers(uint32_t bars, int readers = 0) {
     mbar_init(bars + 8u * (L::B_IFULL + e), 1);                 // load-warp lane 0
     mbar_init(bars + 8u * (L::B_IEMPTY + e), 1 + QT * BM + readers);  // MMA thread + softmax threads
   }
-  for (int sb = 0; sb < L::S_BARS; ++sb) mbar_init(bars + 8u * (L::B_STILE + sb), 1);
+  for (int b = 0; b < L::SP_BARS; ++b) {
+    mbar_init(bars + 8u * (L::B_STILE + b), 1);
+    mbar_init(bars + 8u * (L::B_PREADY + b), BM);
+  }
   for (int t = 0; t < QT; ++t) {
-    mbar_init(bars + 8u * (L::B_PREADY + t), BM);
     mbar_init(bars + 8u * (L::B_ODONE + t), 1);
     mbar_init(bars + 8u * (L::B_OPV + t), 1);
   }
@@ -217,7 +222,7 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
   constexpr uint32_t ID_QK = idesc_f16acc32(BF16, false, false, BM, BN);
   constexpr uint32_t ID_PV = idesc_f16acc32(BF16, false, true, BM, D);
 
-  uint32_t q_par = 0, ie_par = 0, kpar = 0, vpar = 0, p_par0 = 0, p_par1 = 0;  // q_par: bit per Q buffer
+  uint32_t q_par = 0, ie_par = 0, kpar = 0, vpar = 0, pn0 = 0, pn1 = 0;  // q_par: bit per Q buffer; pn: P tiles taken
   int kslot = 0, vslot = 0, ie = 0;
   int nqk = 0;                 // d = 64: ring slot of the next Q.K^T
   uint32_t odd = 0;            // d = 64: bit t: Q tile t has had an odd number of them
@@ -307,16 +312,16 @@ __device__ __forceinline__ void mma_role(Env& env, uint32_t to, uint32_t base, u
                                ID_QK, kk > 0 ? 1u : 0u);
                 }
               }
-              tc_commit_elect(bars + 8u * (L::B_STILE + L::s_bar(t, (int)(odd >> t))));
+              tc_commit_elect(bars + 8u * (L::B_STILE + L::sp_bar(t, odd >> t)));
               if constexpr (L::RING) odd ^= 1u << t;
               env.computed(t, j, lane);
               __syncwarp();
             }
           } else if (turn >= 0) {
             if (have_prev && ((prev_flags >> t) & 1)) {
-              uint32_t& pp = t ? p_par1 : p_par0;
-              if (!bwait_warp(bars + 8u * (L::B_PREADY + t), pp, abort_flag, to)) goto drain;
-              pp ^= 1u;
+              uint32_t& pn = t ? pn1 : pn0;
+              if (!bwait_warp(bars + 8u * (L::B_PREADY + L::sp_bar(t, pn)), L::sp_parity(pn), abort_flag, to)) goto drain;
+              ++pn;
               tc_fence_after();
               bool& started = t ? pv1 : pv0;
               const uint32_t p_col = tmem + (L::RING ? pslot : t) * 128;

@@ -1,4 +1,4 @@
-"""attn_fwd_packed where entries of one Q tile of rows and of two take turns on an SM."""
+"""attn_fwd_packed where entries of one Q tile of rows and of two take turns on an SM, and calls on several streams."""
 import pytest
 import torch
 
@@ -40,3 +40,28 @@ def test_entries_of_one_tile_among_others(lens, d, dtype):
         assert torch.all((o[:, a:a + sq].double() - want).abs() <= u * want.abs() + (u + 2.0 ** -12) * (1 + u) * size + 1e-7)
         assert torch.all((lse[:, a:a + sq].double() - torch.logsumexp(s, -1)).abs() <= 1e-3)
         a, b = a + sq, b + sk
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_on_three_streams_at_once(d):
+    """Kernels that share the machine lose time anywhere; what each waits for is still told apart."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    calls = []
+    for B, H, S in ((3, 8, 384), (2, 4, 1500), (16, 16, 200)):
+        q, k, v = (torch.randn((B, H, S, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+        o, lse = torch.empty_like(q), torch.empty((B, H, S), device="cuda")
+        af.attn_fwd(q, k, v, o, lse, causal=True, scale=0.1)
+        af.attn_check()
+        calls.append((q, k, v, o, lse, o.clone(), lse.clone()))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for rep in range(60):
+        torch.cuda.synchronize()
+        for i, (q, k, v, o, lse, _, _) in enumerate(calls):
+            with torch.cuda.stream(streams[(i + rep) % 3]):
+                o.zero_()
+                af.attn_fwd(q, k, v, o, lse, causal=True, scale=0.1)
+        for st in streams:
+            af.attn_check(st)
+        for _, _, _, o, lse, o0, lse0 in calls:
+            assert torch.equal(o, o0) and torch.equal(lse, lse0)
+

@@ -673,3 +673,36 @@ def test_a_process_whose_first_calls_are_captured():
         "print('captured')\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.strip() == "captured", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_on_three_streams_at_once(d):
+    """Kernels that share the machine lose time anywhere; what each waits for is still told apart."""
+    shapes = [([693, 210, 40], [1311, 700, 900], 8, 1), ([1] * 30, [1000 + 90 * b for b in range(30)], 32, 8), ([6, 3, 5, 2], [3000, 200, 900, 1], 8, 1),
+              ([300, 1, 1, 1, 120], [900, 3000, 10, 700, 120], 8, 2), ([90] * 9, [700] * 9, 4, 4)]
+    calls = []
+    for lq, lk, Hq, Hkv in shapes:
+        bt = Batch(lq, lk, Hq, Hkv, d, "bf16", 64, seed=sum(lk))
+        q, k, v, o, lse = bt.device()
+        args = (q, k, v, o, bt.table.cuda(), bt.cu.cuda(), bt.lens.cuda(), bt.max_q)
+        af.attn_fwd_paged(*args, lse=lse, causal=True, scale=0.125)
+        af.attn_check()
+        bt.check(o.cpu(), lse.cpu(), True, -1, -1, 0.125)
+        calls.append((args, o, lse, o.clone(), lse.clone()))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for rep in range(60):
+        for _, o, lse, _, _ in calls:
+            o.fill_(float("nan"))
+            lse.zero_()
+        torch.cuda.synchronize()
+        for i in range(len(calls)):
+            args, _, lse, _, _ = calls[(i + rep) % len(calls)]
+            with torch.cuda.stream(streams[(i * 7 + rep) % 3]):
+                af.attn_fwd_paged(*args, lse=lse, causal=True, scale=0.125)
+        for st in streams:
+            af.attn_check(st)
+        for args, o, lse, o0, lse0 in calls:
+            rows = int(args[5][-1])
+            assert torch.equal(o[:, :rows], o0[:, :rows]) and torch.equal(lse[:, :rows], lse0[:, :rows])
+    for st in streams:
+        af.attn_release_workspace(st)
