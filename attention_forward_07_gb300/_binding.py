@@ -391,7 +391,8 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     strides whose last dimension is contiguous), lse fp32 [Hq, total_q] or None; block_table int32 [B, W], cu_seqlens_q
     int32 [B+1], seqlens_k int32 [B] (keys per request, the new rows' own included).  One token per request, a few or whole
     chunks, mixed freely.  workspace: a uint8 tensor of attn_paged_workspace() bytes for calls that do not run at the same
-    time; None uses the stream's own, or under graph capture one of the graph's memory pool.  See include/attn.h."""
+    time; None uses the stream's own, or, while the stream is being captured, one of the call's own from the graph's memory
+    pool.  See include/attn.h."""
     torch = _torch or _with_torch()
     dtype, index, i32 = q.dtype, q.get_device(), torch.int32
     code = _dtype_code(q)
@@ -417,10 +418,17 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     if total_q == 0:
         return
     at = n = 0  # no workspace: the library's own of the stream
-    if workspace is None and torch.cuda.is_current_stream_capturing():
-        with torch.cuda.device(index):  # from the graph's memory pool
-            n = _workspace_bytes((B, Hq, Hkv, d, total_q, max_seqlen_q))
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        # Captured, a call needs one that nothing beside it uses: from the graph's memory pool, taken with the launch
+        # stream current.  A block that is given back is handed out again in the order of the stream it was taken on,
+        # and is this call's alone only if that is the stream that runs it.
+        if (stream is None or handle == _raw_stream(index)) and torch.cuda.current_device() == index:
+            if torch.cuda.is_current_stream_capturing():
+                workspace = _capture_workspace(q, (B, Hq, Hkv, d, total_q, max_seqlen_q))
+        else:
+            with torch.cuda.stream(torch.cuda.current_stream(index) if stream is None else stream):
+                if torch.cuda.is_current_stream_capturing():
+                    workspace = _capture_workspace(q, (B, Hq, Hkv, d, total_q, max_seqlen_q))
     if workspace is not None:
         n, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         _refuse(index, others=((workspace.get_device() != index or not workspace.is_contiguous(),
@@ -432,6 +440,10 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
                          ost[1], ost[0], cs[0], cs[1], cs[2], B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size, width,
                          block_table.stride(0) if B > 1 else width, 1 if causal else 0, window_left, window_right,
                          d ** -0.5 if scale is None else scale, code, handle))
+
+
+def _capture_workspace(q, shape):
+    return _torch.empty(_workspace_bytes(shape), dtype=_torch.uint8, device=q.device)
 
 
 def _workspace_bytes(shape) -> int:

@@ -1,0 +1,64 @@
+"""Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+import attention_forward_07_gb300 as af
+from attention_forward_07_gb300 import _binding as bd
+
+
+# ---- the workspace of a call that is being captured
+class _Streams:
+    """Stands in for torch's streams: a current one, some that are being captured, and what was allocated on which."""
+
+    def __init__(self, monkeypatch, captured):
+        self.current, self.taken, self.blocks = self.make(1), [], []
+        self.captured = captured
+        empty = torch.empty
+
+        @contextlib.contextmanager
+        def stream(s):
+            before, self.current = self.current, s
+            yield
+            self.current = before
+
+        def taking(*a, **kw):
+            if kw.get("dtype") is torch.uint8:
+                self.taken.append((self.current.cuda_stream, a[0]))
+            return empty(*a, **kw)
+
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+        monkeypatch.setattr(torch.cuda, "stream", stream)
+        monkeypatch.setattr(torch.cuda, "device", lambda i: contextlib.nullcontext())
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda i=None: self.current)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.current.cuda_stream in self.captured)
+        monkeypatch.setattr(torch, "empty", taking)
+        bd._with_torch()
+        monkeypatch.setattr(bd, "_raw_stream", lambda i: self.current.cuda_stream)
+        monkeypatch.setattr(bd, "_workspace_bytes", lambda shape: 512)
+        monkeypatch.setattr(bd, "_lib", types.SimpleNamespace(attn_fwd_paged=None))
+        monkeypatch.setattr(bd, "_launch", lambda index, fn, block: self.blocks.append(bd.FwdPagedParams.from_buffer_copy(block)))
+
+    @staticmethod
+    def make(handle):
+        return types.SimpleNamespace(cuda_stream=handle, device=torch.device("cuda", 0))
+
+
+@pytest.mark.parametrize("captured,on,taken_on", [
+    ((), None, None), ((), 2, None),
+    ((1,), None, 1), ((1, 2, 3), 2, 2), ((1, 2, 3), 3, 3),   # streams forked from the one that is captured
+    ((2,), 2, 2),                                            # captured, and not the current one
+    ((1,), 2, None)])                                        # the current one is captured, the launch goes elsewhere
+def test_a_captured_call_takes_its_workspace_on_the_stream_it_runs_on(monkeypatch, captured, on, taken_on):
+    st = _Streams(monkeypatch, captured)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    q, kc = torch.zeros((4, 3, 64)).half(), torch.zeros((4, 2, 16, 64)).half()
+    af.attn_fwd_paged(q, kc, kc, q.clone(), i(2, 4), i(3), i(2), 2, stream=on and st.make(on))
+    (block,) = st.blocks
+    assert (block.stream or 0) == (on or 1)
+    assert st.taken == ([] if taken_on is None else [(taken_on, 512)])
+    assert block.workspace_bytes == (0 if taken_on is None else 512) and (block.workspace is None) == (taken_on is None)
+    assert st.current.cuda_stream == 1
