@@ -599,10 +599,6 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t base, uin
       if (!softmax_tile<D, BF16, L>(s_addr, o_addr, c, make_mask, bars + 8u * (L::B_OPV + t), np, nact, abort_flag, to, m, l))
         return;
       tc_fence_before();
-      // d = 64: the next S may already be there, so a fast warp could start the next tile
-      // and arrive again before the slowest warp has arrived for this one; the warpgroup
-      // meets here first
-      if constexpr (L::RING) named_bar_sync(1 + t, BM);
       mbar_arrive(bars + 8u * (L::B_PREADY + L::sp_bar(t, np)));
       ++nact;
       ++np;

@@ -505,7 +505,6 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       };
       if (!softmax_tile<D, BF16, L>(s_addr, o_addr, c, make_mask, bars + 8u * (L::B_OPV + t), np, nact, abort_flag, to, m, l)) return;
       tc_fence_before();
-      if constexpr (L::RING) named_bar_sync(1 + t, BM);
       mbar_arrive(bars + 8u * (L::B_PREADY + L::sp_bar(t, np)));
       ++nact;
       ++np;

@@ -65,7 +65,10 @@ struct Layout {
   // Barriers that say S or P is there.  A wait tells a phase from the next one by one bit, so it has to be
   // within a phase of what it waits for.  d = 64: two barriers to a Q tile, its n-th S and P by turns.  Whoever
   // waits for the n-th has waited for the (n - 2)-th, and the (n + 2)-th is not made before it is done with
-  // the n-th.  (With S barriers to ring slots a softmax might have passed over key tiles of the other Q
+  // the n-th.  That holds for arrivals as well: a warp that is ahead arrives for its (n + 1)-th P at the other
+  // barrier, and gets no (n + 2)-th S before all have arrived for the n-th P, so the four warps of a
+  // warpgroup need not meet ahead of their arrival (a meeting would wait without limit for a warp that has
+  // given up).  (With S barriers to ring slots a softmax might have passed over key tiles of the other Q
   // tile alone, and taken an earlier phase for its own; with one P barrier to a Q tile the MMA warp, where
   // it lost time between a Q.K^T and the wait for the P before, found two phases gone by.)
   static constexpr int SP_BARS = RING ? 2 * QT : QT;

@@ -1,4 +1,4 @@
-"""Edges of the paged-cache operators on the GPU: captures that fork."""
+"""Edges of the paged-cache operators on the GPU: captures that fork, waits that run out."""
 import numpy as np
 import pytest
 import torch
@@ -53,3 +53,28 @@ def test_calls_on_streams_forked_in_one_capture(d):
             assert torch.equal(args[3][:, :n], o[:, :n]) and torch.equal(kw["lse"][:, :n], lse[:, :n])
     for s in (main, *sides):
         af.attn_check(s)
+
+
+@pytest.mark.parametrize("lq,lk", [([70, 1], [90, 50]), ([300, 20, 1], [2000, 90, 700]), ([5, 3, 4], [2000, 90, 800])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_q_tile_that_never_comes_ends_the_launch_at_either_head_dim(d, lq, lk):
+    """(8 heads to a K/V head: no case has 32 rows at most, which another kernel takes.)  Every wait of the chunk path's roles has a limit, with units of two Q tiles and with key tiles by turns; the
+    call after it is right."""
+    lib = af.library()
+    bt = Batch(lq, lk, 16, 2, d, "bf16", 16, seed=16)
+    args, kw = _device(bt)
+    assert lib.attn_set_wait_timeout_ns(50_000_000) == 0
+    try:
+        assert lib.attn_debug_inject(1) == 0
+        af.attn_fwd_paged(*args, **kw)
+        with pytest.raises(af.AttnError) as e:
+            af.attn_check()
+        assert e.value.status == -4
+    finally:
+        lib.attn_debug_inject(0)
+        lib.attn_set_wait_timeout_ns(0)
+    args[3].fill_(float("nan"))
+    kw["lse"].fill_(float("nan"))
+    af.attn_fwd_paged(*args, **kw)
+    af.attn_check()
+    bt.check(args[3].cpu(), kw["lse"].cpu(), True, -1, -1, 0.125)
