@@ -148,13 +148,13 @@ __device__ __forceinline__ void decode_unit(int u, const Params& p, bool causal,
     // (entry, block) pairs in the work order or in index order, then the head pairs of
     // consecutive K/V heads (an even group size keeps a pair inside one group)
     const int hp = p.Hq >> 1, pi = u / hp;
-    const int pr = p.order ? __ldg(p.order + pi) : pi;
+    const int pr = p.order ? p.order[pi] : pi;
     b = pr / p.nqb;
     qb = pr - b * p.nqb;
     hq = 2 * (u - pi * hp);
   } else if (p.order) {
     const int pi = u / p.Hq;
-    const int pair = __ldg(p.order + pi);
+    const int pair = p.order[pi];
     b = pair / p.nqb;
     qb = pair - b * p.nqb;
     hq = u - pi * p.Hq;
@@ -268,7 +268,7 @@ __device__ __forceinline__ void load_role(const Params& p, uint32_t base, uint8_
     int slot_blk = -1;
     bool unit_empty = false, in_place = true;
     if constexpr (MODE == MASK_CUSTOM) {
-      if (lane < 2 * QT * 4) slot_blk = __ldg(p.rowmap + ((size_t)mb * p.nqb + qb) * 16 + lane);
+      if (lane < 2 * QT * 4) slot_blk = p.rowmap[((size_t)mb * p.nqb + qb) * 16 + lane];
       unit_empty = __shfl_sync(0xffffffffu, slot_blk, 0) < 0;
       // slots that are the unit's own rows (no empty block among them): plain tile loads
       const int own = qb * 16 + lane;
@@ -528,15 +528,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t base, uin
     const int hb0 = (qb * UNIT_ROWS + t * BM + quarter * 32) / 16;
     if constexpr (MODE == MASK_CUSTOM) {
       const int* rm = p.rowmap + ((size_t)mb * p.nqb + qb) * 16 + t * 8 + quarter * 2;
-      blk_a = __ldg(rm);
-      blk_b = __ldg(rm + 1);
+      blk_a = rm[0];
+      blk_b = rm[1];
       const int blk = lane < 16 ? blk_a : blk_b;
       i = blk >= 0 ? blk * 16 + (lane & 15) : -1;
       if constexpr (D == 64) {
         // read now, used by the epilogue (the loads overlap the unit's first tile; d = 128
         // has no registers to spare and reads them at the epilogue)
-        live_a = hb0 >= p.nr16 || __ldg(p.live + (size_t)mb * p.nr16 + hb0) != 0;
-        live_b = hb0 + 1 >= p.nr16 || __ldg(p.live + (size_t)mb * p.nr16 + hb0 + 1) != 0;
+        live_a = hb0 >= p.nr16 || p.live[(size_t)mb * p.nr16 + hb0] != 0;
+        live_b = hb0 + 1 >= p.nr16 || p.live[(size_t)mb * p.nr16 + hb0 + 1] != 0;
       }
     }
     float m = -INFINITY, l = 0.f;
@@ -736,7 +736,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t base, uin
         if constexpr (D == 64) {
           if (hh ? live_b : live_a) continue;  // warp-uniform
         } else {
-          if (hb >= p.nr16 || __ldg(p.live + (size_t)mb * p.nr16 + hb)) continue;  // warp-uniform
+          if (hb >= p.nr16 || p.live[(size_t)mb * p.nr16 + hb]) continue;  // warp-uniform
         }
         uint8_t* ob = reinterpret_cast<uint8_t*>(p.o) + ((size_t)(b * p.Hq + hq) * p.Sq + hb * 16) * ROW_BYTES;
 #pragma unroll
@@ -940,7 +940,7 @@ __device__ __forceinline__ void compact_rows(const uint8_t* f, uint8_t* __restri
 
 // Compaction of one mask row block (one CTA per block, 256 threads) from the pre-pass's flags.
 // Shared memory: nslots (>= nqt * 8 >= nr16) slot entries and nr16 bytes of liveness.
-__global__ void __launch_bounds__(256) mask_compact_kernel(const uint8_t* __restrict__ flags16,
+__global__ void __launch_bounds__(256) mask_compact_kernel(const uint8_t* flags16,
                                                           uint8_t* __restrict__ live, int* __restrict__ rowmap,
                                                           uint8_t* __restrict__ tflags, int nr16, int nkt,
                                                           int nqt, int nslots) {

@@ -84,9 +84,9 @@ struct PagedParams {
 
 // Query rows, keys and first query row of request b, whatever the arrays hold.
 __device__ __forceinline__ void request_span(const PagedParams& p, int b, int& row0, int& sq, int& sk) {
-  row0 = min(max(__ldg(p.cu_q + b), 0), p.total_q);
-  sq = min(min(max(__ldg(p.cu_q + b + 1), row0), p.total_q) - row0, p.max_q);
-  sk = (int)min((long long)max(__ldg(p.lens_k + b), 0), (long long)p.width * p.page_size);
+  row0 = min(max(p.cu_q[b], 0), p.total_q);
+  sq = min(min(max(p.cu_q[b + 1], row0), p.total_q) - row0, p.max_q);
+  sk = (int)min((long long)max(p.lens_k[b], 0), (long long)p.width * p.page_size);
 }
 
 // Keys that query row i (of sq, against sk keys) keeps: [lo, hi).

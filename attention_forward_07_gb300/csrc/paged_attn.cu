@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
         place = -1;
         if (t < ctile + cleft && key < cit.hi && key + 16 > cit.lo) {
           const int idx = key / p.page_size;
-          const int pg = __ldg(p.table + (long long)cb * p.table_stride + idx);
+          const int pg = p.table[(long long)cb * p.table_stride + idx];
           if ((unsigned)pg < (unsigned)p.num_pages)
             place = (long long)pg * p.c_page + (long long)(key - idx * p.page_size) * p.c_row;
           else
@@ -454,15 +454,15 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
           const uint16_t* src = q_row(r) + fc;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
-            qf[mt][s][x] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16));
-            qf[mt][s][x + 2] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 16 + 8));
+            qf[mt][s][x] = *reinterpret_cast<const uint32_t*>(src + s * 16);
+            qf[mt][s][x + 2] = *reinterpret_cast<const uint32_t*>(src + s * 16 + 8);
           }
         }
       }
     if constexpr (C::Q_SMEM) {
       for (int e = tid; e < C::ROWS * CPR; e += C::NTHREADS) {
         const int r = e / CPR, c = e % CPR;
-        *reinterpret_cast<uint4*>(smem + C::OFF_Q + r * (D * 2) + ((c ^ (r & 7)) * 16)) = __ldg(reinterpret_cast<const uint4*>(q_row(r)) + c);
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + r * (D * 2) + ((c ^ (r & 7)) * 16)) = reinterpret_cast<const uint4*>(q_row(r))[c];
       }
       __syncthreads();
     }

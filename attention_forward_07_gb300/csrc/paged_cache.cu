@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   int2 sum = make_int2(0, 0);
   for (int b = b0; b < b1; ++b) {
-    const int ctx = max(__ldg(a.ctx_lens + b), 0), add = max(__ldg(a.new_lens + b), 0);
+    const int ctx = max(a.ctx_lens[b], 0), add = max(a.new_lens[b], 0);
     ctx_s[b] = ctx;
     rows_pre[b] = sum.x;
     need_pre[b] = sum.y;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
 
   bool bad = count_in != count || need > count || total > a.max_rows;
   const auto free_page = [&](int n) {
-    const int id = (unsigned)n < (unsigned)count ? __ldg(a.free_pages + (count - 1 - n)) : -1;
+    const int id = (unsigned)n < (unsigned)count ? a.free_pages[count - 1 - n] : -1;
     return id >= 0 && id < a.num_pages ? id : -1;
   };
   const int nthr = gridDim.x * TABLES_THREADS, gid = blockIdx.x * TABLES_THREADS + tid;
@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
 // (the division by P is the row's, not each chunk's) and moves the row's 2 * Hkv * d / 8 chunks of 16
 // bytes of K and V, up to eight in flight to a lane.  Memory-bound: every byte is read and written once.
 // Measured: 16.9 thousand rows of 8 heads, d = 128: 23.7 us, 5.84 TB/s (0.86 of measured copy bandwidth);
-// 64 rows: 2.8 us, a launch's time.
+// 64 rows: 2.8 us, a launch's time.  All is read past L1, which nothing here uses twice: with plain loads the
+// wait for the kernel ahead empties L1 first, and 64 rows take 3.4 us.
 constexpr int APPEND_WARPS = 4;
 
 struct AppendParams {
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS) paged_append_kernel(const _
   grid_launch_dependents();
   grid_dependency_wait();
   for (int t = blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5); t < a.rows; t += nwarps) {
-    const int slot = __ldg(a.slots + t);
+    const int slot = load_cg(a.slots + t);
     const int page = slot / a.page_size;
     if (slot < 0) continue;
     if (page >= a.num_pages) {
@@ -203,8 +204,8 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS) paged_append_kernel(const _
           const bool v = c >= per_side;
           const int e = v ? c - per_side : c;
           const uint16_t* src = static_cast<const uint16_t*>(v ? a.v_new : a.k_new);
-          x[u] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(e / CPR) * (v ? a.v_head_stride : a.k_head_stride) +
-                                                      (long long)t * (v ? a.v_row_stride : a.k_row_stride) + (e % CPR) * 8));
+          x[u] = load_cg_x4(src + (long long)(e / CPR) * (v ? a.v_head_stride : a.k_head_stride) +
+                            (long long)t * (v ? a.v_row_stride : a.k_row_stride) + (e % CPR) * 8);
         }
       }
 #pragma unroll

@@ -66,7 +66,7 @@ struct TileBox {
     const int key = j * BN + chunk;
     if (chunk < BN && key < hi && key + p.box_rows > lo) {
       const int idx = key / p.page_size;
-      const int page = __ldg(p.table + (long long)b * p.table_stride + idx);
+      const int page = p.table[(long long)b * p.table_stride + idx];
       group = (key - idx * p.page_size) >> 3;
       if ((unsigned)page < (unsigned)p.num_pages) z = page * p.z_page + h * p.z_head;
       else atomicOr(p.status, STATUS_PAGE);

@@ -49,8 +49,21 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 // Waits until the grids this one depends on have completed and their writes are visible
-// (returns at once when the launch had no programmatic dependency).
+// (returns at once when the launch had no programmatic dependency).  What they wrote is read with
+// plain loads or past L1 (load_cg), never with __ldg: that is for data that nothing writes while the kernel
+// lives, and its life begins before the wait ends.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads past L1, kept in order with the waits.
+__device__ __forceinline__ int load_cg(const int* src) {
+  int x;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(x) : "l"(src) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint4 load_cg_x4(const void* src) {  // 16-byte aligned
+  uint4 x;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(src) : "memory");
+  return x;
+}
 
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_map(const void* map) {

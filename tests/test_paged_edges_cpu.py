@@ -1,5 +1,7 @@
-"""Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes."""
+"""Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes, how kernels that start early read."""
 import contextlib
+import os
+import re
 import types
 
 import pytest
@@ -62,3 +64,26 @@ def test_a_captured_call_takes_its_workspace_on_the_stream_it_runs_on(monkeypatc
     assert st.taken == ([] if taken_on is None else [(taken_on, 512)])
     assert block.workspace_bytes == (0 if taken_on is None else 512) and (block.workspace is None) == (taken_on is None)
     assert st.current.cuda_stream == 1
+
+
+# ---- kernels that start before the one ahead has ended
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "attention_forward_07_gb300", "csrc")
+
+
+def _code(name):
+    with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+        return re.sub(r"//.*", "", f.read())
+
+
+@pytest.mark.parametrize("name", ["paged.cuh", "paged_attn.cu", "paged_tile.cu", "paged_cache.cu"])
+def test_the_paged_kernels_read_nothing_as_constant_for_their_life(name):
+    """Any input may be what the kernel ahead on the stream writes, after this one has started."""
+    text = _code(name)
+    assert "__ldg" not in text and ".nc" not in text and "__restrict__" not in text
+
+
+def test_the_forward_reads_its_own_lists_with_plain_loads():
+    """Work order, slot list, liveness and flags come from the dependent kernels ahead."""
+    text = _code("attn_fwd.cu")
+    assert not re.search(r"__ldg\((p\.order|p\.rowmap|rm\b|p\.live|p\.tflags|flags16)", text)
+    assert not re.search(r"const \w+\* __restrict__ (flags16|live|rowmap|tflags|order)\b", text)
