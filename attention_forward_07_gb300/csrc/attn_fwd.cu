@@ -1071,7 +1071,9 @@ std::atomic<unsigned long long> g_ws_allocs{0}, g_map_encodes{0}, g_map_hits{0};
 
 // Tensor maps cached by (kind, address, dims, box rows): a map holds nothing but these, so a
 // cached map is valid for any later call that names the same buffer with the same shape.
-// Least-recently-used replacement over a small table.
+// A model's step comes back to two or three maps of each layer (a hundred layers: 300), so the table
+// holds 4096, in sets of 8 that a key's hash names, the least recently used of a set replaced.  It is
+// an array, as attn_fwd_noalloc may not allocate on the host.
 enum MapKind { MAP_F16 = 0, MAP_BF16 = 1, MAP_WORDS = 2, MAP5_F16 = 3, MAP5_BF16 = 4 };
 struct MapKey {
   int kind;
@@ -1084,21 +1086,36 @@ struct MapKey {
            std::memcmp(&five, &o.five, sizeof five) == 0;
   }
 };
-constexpr int MAP_CACHE = 64;
 struct MapSlot {
   MapKey key;
   CUtensorMap map;
   unsigned long long used = 0;  // 0 = empty
 };
+constexpr int MAP_SET_BITS = 9, MAP_WAYS = 8;
 std::mutex g_map_mutex;
-MapSlot g_maps[MAP_CACHE];
+MapSlot g_maps[1 << MAP_SET_BITS][MAP_WAYS];
 unsigned long long g_map_clock = 0;
+
+MapSlot (&map_set(const MapKey& k))[MAP_WAYS] {
+  unsigned long long words[sizeof(Map5) / 8], h = (unsigned long long)k.kind;
+  static_assert(sizeof(Map5) % 8 == 0, "the rest of a 5-D key in words");
+  std::memcpy(words, &k.five, sizeof words);
+  const auto mix = [&h](unsigned long long x) { h = (h ^ x ^ (h >> 32)) * 0x9E3779B97F4A7C15ull; };
+  mix(reinterpret_cast<uintptr_t>(k.ptr));
+  mix((unsigned long long)k.d0);
+  mix((unsigned long long)k.d1);
+  mix((unsigned long long)k.d2);
+  mix((unsigned long long)k.box_rows);
+  for (unsigned long long w : words) mix(w);
+  return g_maps[h >> (64 - MAP_SET_BITS)];
+}
 
 template <class Encode>
 int cached_map(CUtensorMap* m, const MapKey& key, Encode encode) {
+  MapSlot(&set)[MAP_WAYS] = map_set(key);
   {
     std::lock_guard<std::mutex> lk(g_map_mutex);
-    for (MapSlot& e : g_maps)
+    for (MapSlot& e : set)
       if (e.used && e.key == key) {
         e.used = ++g_map_clock;
         *m = e.map;
@@ -1110,8 +1127,8 @@ int cached_map(CUtensorMap* m, const MapKey& key, Encode encode) {
   if (rc != ATTN_OK) return rc;
   g_map_encodes.fetch_add(1);
   std::lock_guard<std::mutex> lk(g_map_mutex);
-  MapSlot* victim = &g_maps[0];
-  for (MapSlot& e : g_maps)
+  MapSlot* victim = &set[0];
+  for (MapSlot& e : set)
     if (e.used < victim->used) victim = &e;
   victim->key = key;
   victim->map = *m;

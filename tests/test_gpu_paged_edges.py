@@ -1,4 +1,5 @@
-"""Edges of the paged-cache operators on the GPU: captures that fork, waits that run out."""
+"""Edges of the paged-cache operators on the GPU: captures that fork, waits that run out, the
+tensor maps of many layers."""
 import numpy as np
 import pytest
 import torch
@@ -78,3 +79,34 @@ def test_a_q_tile_that_never_comes_ends_the_launch_at_either_head_dim(d, lq, lk)
     af.attn_fwd_paged(*args, **kw)
     af.attn_check()
     bt.check(args[3].cpu(), kw["lse"].cpu(), True, -1, -1, 0.125)
+
+
+def test_the_tensor_maps_of_a_models_layers_are_kept():
+    """A step that goes over the caches of 96 layers makes no tensor map that the step before has made; a flood of other
+    buffers may drop them, and then they are made again."""
+    B, Hq, Hkv, d, page, n = 2, 4, 2, 64, 16, 96
+    bt = Batch([33, 20], [70, 20], Hq, Hkv, d, "f16", page, seed=5)
+    q, k, v, o, lse = bt.device()
+    tabs = bt.table.cuda(), bt.cu.cuda(), bt.lens.cuda()
+    layers = [(torch.empty_like(k).copy_(k), torch.empty_like(v).copy_(v), torch.empty_like(q).copy_(q)) for _ in range(n)]
+
+    def step():
+        before = af.debug_counters()["map_encodes"]
+        for kc, vc, x in layers:
+            o.fill_(float("nan"))
+            af.attn_fwd_paged(x, kc, vc, o, *tabs, bt.max_q, lse=lse, causal=True, scale=0.125)
+        af.attn_check()
+        bt.check(o.cpu(), lse.cpu(), True, -1, -1, 0.125)
+        return af.debug_counters()["map_encodes"] - before
+
+    assert step() <= 3 * n
+    assert step() == 0
+    pool = torch.zeros(k.numel() + 8 * 5000, dtype=k.dtype, device="cuda")
+    before = af.debug_counters()["map_encodes"]
+    for i in range(5000):
+        x = pool[8 * i:8 * i + k.numel()].view(k.shape)
+        af.attn_fwd_paged(q, x, x, o, *tabs, bt.max_q, lse=lse, causal=True, scale=0.125)
+    af.attn_check()
+    assert af.debug_counters()["map_encodes"] - before >= 5000
+    assert 0 < step() <= 3 * n
+    assert step() == 0
