@@ -271,14 +271,17 @@ _APPEND = struct.Struct("@5P7q6iP")
 _ATTEND = struct.Struct("@9PQ7q13ifiP")
 _torch = None
 _raw_stream = None
+_device = None
 
 
 def _with_torch():
-    """torch, imported on first use (with it the cheapest way it has to name a device's current stream)."""
-    global _torch, _raw_stream
+    """torch, imported on first use (with it the cheapest ways it has to name a device's current stream and the current
+    device, once there are CUDA tensors)."""
+    global _torch, _raw_stream, _device
     if _torch is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _torch = torch
     return _torch
 
@@ -292,7 +295,7 @@ def _stream_on(index, stream):
 
 def _launch(index, fn, block):
     """Calls fn(block) with CUDA device `index` current; raises on a status other than 0."""
-    if _torch.cuda.current_device() == index:
+    if _device() == index:
         rc = fn(block)
     else:
         with _torch.cuda.device(index):
@@ -422,7 +425,7 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
         # Captured, a call needs one that nothing beside it uses: from the graph's memory pool, taken with the launch
         # stream current.  A block that is given back is handed out again in the order of the stream it was taken on,
         # and is this call's alone only if that is the stream that runs it.
-        if (stream is None or handle == _raw_stream(index)) and torch.cuda.current_device() == index:
+        if (stream is None or handle == _raw_stream(index)) and _device() == index:
             if torch.cuda.is_current_stream_capturing():
                 workspace = _capture_workspace(q, (B, Hq, Hkv, d, total_q, max_seqlen_q))
         else:

@@ -34,12 +34,12 @@ class _Streams:
         monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
         monkeypatch.setattr(torch.cuda, "stream", stream)
         monkeypatch.setattr(torch.cuda, "device", lambda i: contextlib.nullcontext())
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda i=None: self.current)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.current.cuda_stream in self.captured)
         monkeypatch.setattr(torch, "empty", taking)
         bd._with_torch()
         monkeypatch.setattr(bd, "_raw_stream", lambda i: self.current.cuda_stream)
+        monkeypatch.setattr(bd, "_device", lambda: 0)
         monkeypatch.setattr(bd, "_workspace_bytes", lambda shape: 512)
         monkeypatch.setattr(bd, "_lib", types.SimpleNamespace(attn_fwd_paged=None))
         monkeypatch.setattr(bd, "_launch", lambda index, fn, block: self.blocks.append(bd.FwdPagedParams.from_buffer_copy(block)))
