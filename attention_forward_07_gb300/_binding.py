@@ -336,7 +336,7 @@ def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, p
     int32 device tensors: ctx_lens, new_lens [B] (tokens cached, tokens to come), block_table [B, W] (in / out: the
     pages added are filled in), free_pages [F] with free_count [1] (taken from the end) -> cu_seqlens_q [B+1],
     seqlens_k [B], slots and positions [max rows] (-1 behind the last new row), free_count_out [1] (default: free_count
-    itself).  See include/attn.h."""
+    itself).  free_pages and slots may be empty.  See include/attn.h."""
     torch = _torch or _with_torch()
     i32, index = torch.int32, ctx_lens.get_device()
     one, many, after = ctx_lens.shape, slots.shape, cu_seqlens_q.shape
@@ -358,10 +358,10 @@ def attn_paged_tables(ctx_lens, new_lens, block_table, free_pages, free_count, p
                         (seqlens_k, B, "seqlens_k"), (slots, rows, "slots")) +
                 (() if positions is None else ((positions, rows, "positions"),)), (block_table, B))
     _launch(index, (_lib or library()).attn_paged_tables,
-            _TABLES.pack(ctx_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-                         left.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), slots.data_ptr(),
-                         0 if positions is None else positions.data_ptr(), B, width, block_table.stride(0) if B > 1 else width, free,
-                         rows, page_size, num_pages, _raw_stream(index) if stream is None else _stream_on(index, stream)))
+            _TABLES.pack(ctx_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr() if free else 0,
+                         free_count.data_ptr(), left.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
+                         slots.data_ptr() if rows else 0, 0 if positions is None or not rows else positions.data_ptr(), B, width,
+                         block_table.stride(0) if B > 1 else width, free, rows, page_size, num_pages, _raw_stream(index) if stream is None else _stream_on(index, stream)))
 
 
 def attn_paged_append(k_new, v_new, k_cache, v_cache, slots, stream=None):

@@ -265,14 +265,16 @@ int attn_paged_tables(const attn_paged_tables_params_t* params) {
     using namespace attn;
     if (!params) return ATTN_ERR_INVALID;
     const attn_paged_tables_params_t& a = *params;
-    if (!a.ctx_lens || !a.new_lens || !a.block_table || !a.free_pages || !a.free_count || !a.free_count_out || !a.cu_seqlens_q ||
-        !a.seqlens_k || !a.slots)
+    // (no page list where it holds no page, no slot map where it holds no row)
+    if (!a.ctx_lens || !a.new_lens || !a.block_table || (!a.free_pages && a.max_free != 0) || !a.free_count || !a.free_count_out ||
+        !a.cu_seqlens_q || !a.seqlens_k || (!a.slots && (a.max_rows != 0 || a.positions)))
       return ATTN_ERR_INVALID;
     for (const void* ptr : {(const void*)a.ctx_lens, (const void*)a.new_lens, (const void*)a.block_table, (const void*)a.free_pages,
                             (const void*)a.free_count, (const void*)a.free_count_out, (const void*)a.cu_seqlens_q,
                             (const void*)a.seqlens_k, (const void*)a.slots, (const void*)a.positions})
       if (misaligned(ptr, 4)) return ATTN_ERR_INVALID;
-    if (a.B < 1 || a.B > TABLES_MAX_B || a.table_width < 1 || a.table_stride < a.table_width || a.max_free < 0 || a.max_rows < 1 || a.max_rows > (1 << 30) ||
+    if (a.B < 1 || a.B > TABLES_MAX_B || a.table_width < 1 || a.table_stride < a.table_width || a.max_free < 0 ||
+        a.max_rows < (a.slots ? 1 : 0) || a.max_rows > (1 << 30) ||
         a.page_size < 16 || a.page_size % 16 != 0 || a.num_pages < 1 || (long long)a.num_pages * a.page_size > INT_MAX)
       return ATTN_ERR_INVALID;
     int sms = 0, dev = 0;

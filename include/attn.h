@@ -248,12 +248,13 @@ int attn_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float
  * of the page that request b's new tokens start in) is out of range, the slots concerned
  * are -1 and so are the table entries that exist; rows past max_rows get no slot.  Each of these
  * sets ATTN_ERR_PAGE.  cu_seqlens_q and seqlens_k are as if all had been well; *free_count_out
- * is never below 0.  1 <= B <= 16384, 1 <= max_rows <= 2^30; num_pages*page_size, and the sums of the lengths, fit 31 bits.
+ * is never below 0.  With max_free = 0 free_pages may be NULL; with max_rows = 0 (a step without new
+ * rows) slots and positions are.  1 <= B <= 16384, max_rows <= 2^30; num_pages*page_size, and the sums of the lengths, fit 31 bits.
  */
 typedef struct {
     const int *ctx_lens, *new_lens; /* [B] */
     int *block_table;               /* in / out */
-    const int *free_pages;          /* [max_free] */
+    const int *free_pages;          /* [max_free]; may be NULL if that is 0 */
     const int *free_count;          /* [1], at most max_free (more is cut) */
     int *free_count_out;            /* [1] */
     int *cu_seqlens_q;              /* [B+1] */

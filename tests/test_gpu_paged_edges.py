@@ -1,5 +1,5 @@
 """Edges of the paged-cache operators on the GPU: captures that fork, waits that run out, the
-tensor maps of many layers."""
+tensor maps of many layers, empty lists and maps."""
 import numpy as np
 import pytest
 import torch
@@ -7,6 +7,7 @@ import torch
 import attention_forward_07_gb300 as af
 
 from paged_ref import Batch
+from test_gpu_paged import _check_tables
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,15 @@ def test_the_tensor_maps_of_a_models_layers_are_kept():
     assert af.debug_counters()["map_encodes"] - before >= 5000
     assert 0 < step() <= 3 * n
     assert step() == 0
+
+
+@pytest.mark.parametrize("ctx,new,free,rows,bad", [
+    ([5, 16, 0], [3, 0, 0], 0, 3, False),     # room in the pages held: no free page needed
+    ([5, 16, 0], [0, 0, 0], 4, 0, False),     # no new row at all
+    ([5, 16, 0], [0, 0, 0], 0, 0, False),
+    ([5, 16, 0], [1, 1, 1], 0, 3, True),      # pages wanted, none there
+    ([5, 16, 0], [1, 1, 0], 4, 0, True)])     # rows without a place in the map
+def test_tables_with_an_empty_free_list_or_no_rows(ctx, new, free, rows, bad):
+    table = np.array([[3, -1, -1], [1, -1, -1], [-1, -1, -1]], np.int32)
+    got = _check_tables(np.array(ctx), np.array(new), table, np.array([0, 2, 4, 5][:free], np.int32), free, 16, 6, rows)
+    assert got["bad"] == bad

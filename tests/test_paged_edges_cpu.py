@@ -1,5 +1,7 @@
-"""Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes, how kernels that start early read."""
+"""Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes, how kernels that start early
+read, empty lists and maps."""
 import contextlib
+import ctypes
 import os
 import re
 import types
@@ -9,6 +11,8 @@ import torch
 
 import attention_forward_07_gb300 as af
 from attention_forward_07_gb300 import _binding as bd
+
+from test_paged_cpu import P, TABLES, lib  # noqa: F401
 
 
 # ---- the workspace of a call that is being captured
@@ -87,3 +91,29 @@ def test_the_forward_reads_its_own_lists_with_plain_loads():
     text = _code("attn_fwd.cu")
     assert not re.search(r"__ldg\((p\.order|p\.rowmap|rm\b|p\.live|p\.tflags|flags16)", text)
     assert not re.search(r"const \w+\* __restrict__ (flags16|live|rowmap|tflags|order)\b", text)
+
+
+# ---- empty lists and maps
+@pytest.mark.parametrize("kw,status", [
+    (dict(free_pages=0, max_free=0), -5), (dict(slots=0, max_rows=0), -5), (dict(free_pages=0, max_free=0, slots=0, max_rows=0), -5),
+    (dict(free_pages=0, max_free=1), -1), (dict(slots=0, max_rows=1), -1), (dict(slots=0, max_rows=0, positions=P), -1),
+    (dict(slots=0, max_rows=-1), -1), (dict(slots=P, max_rows=0), -1)], ids=str)
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are none: what is accepted must find no device")
+def test_tables_without_free_pages_or_rows(lib, kw, status):  # noqa: F811
+    assert lib.attn_paged_tables(ctypes.byref(bd.PagedTablesParams(**dict(TABLES, **kw)))) == status
+
+
+@pytest.mark.parametrize("free,rows", [(0, 5), (9, 0), (0, 0)])
+@pytest.mark.parametrize("positions", [False, True])
+def test_empty_tensors_become_null(monkeypatch, free, rows, positions):
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    bd._with_torch()
+    monkeypatch.setattr(bd, "_raw_stream", lambda index: 0)
+    got = []
+    monkeypatch.setattr(bd, "_launch", lambda index, fn, block: got.append(bd.PagedTablesParams.from_buffer_copy(block)))
+    # (slices of longer tensors: an empty slice may have an address)
+    af.attn_paged_tables(i(2), i(2), i(2, 4), i(9)[:free], i(1), 16, 9, i(3), i(2), i(5)[:rows], i(5)[:rows] if positions else None)
+    assert (got[0].max_free, got[0].max_rows) == (free, rows)
+    assert (got[0].free_pages is None) == (free == 0) and (got[0].slots is None) == (rows == 0)
+    assert (got[0].positions is None) == (rows == 0 or not positions)
