@@ -43,6 +43,12 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// ceil(n / P) for every n >= 0 that 31 bits hold (n + P - 1 may not fit).
+__device__ __forceinline__ int pages_of(int n, int P) {
+  const int q = n / P;
+  return q + (q * P != n);
+}
+
 // Last request b with pre[b] <= x (pre[0] = 0, non-decreasing, x < pre[B]): the one that holds x.
 __device__ __forceinline__ int holder(const int* pre, int B, int x) {
   int lo = 0, hi = B;
@@ -77,7 +83,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
     rows_pre[b] = sum.x;
     need_pre[b] = sum.y;
     sum.x += add;
-    sum.y += (ctx + add + P - 1) / P - (ctx + P - 1) / P;
+    sum.y += pages_of(ctx + add, P) - pages_of(ctx, P);
     if (blockIdx.x == 0) a.seqlens_k[b] = ctx + add;
   }
   int2 incl = sum;
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
     for (int b = tid; b <= B; b += TABLES_THREADS) a.cu_seqlens_q[b] = rows_pre[b];
   for (int n = nthr - 1 - gid; n < need; n += nthr) {  // (from the far end: the near threads have rows)
     const int b = holder(need_pre, B, n);
-    const int i = (ctx_s[b] + P - 1) / P + (n - need_pre[b]);
+    const int i = pages_of(ctx_s[b], P) + (n - need_pre[b]);
     const int id = free_page(n);
     const bool fits = (unsigned)i < (unsigned)a.table_width;
     if (fits) a.block_table[(long long)b * a.table_stride + i] = id;
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
         page = i;
         id = -1;
         if ((unsigned)i < (unsigned)a.table_width) {
-          const int held = (ctx_s[b] + P - 1) / P;
+          const int held = pages_of(ctx_s[b], P);
           id = i < held ? a.block_table[(long long)b * a.table_stride + i] : free_page(need_pre[b] + i - held);
           if (id >= a.num_pages) id = -1;
         }

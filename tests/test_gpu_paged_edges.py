@@ -1,5 +1,5 @@
 """Edges of the paged-cache operators on the GPU: captures that fork, waits that run out, the
-tensor maps of many layers, empty lists and maps."""
+tensor maps of many layers, empty lists and maps, the longest lengths."""
 import numpy as np
 import pytest
 import torch
@@ -123,3 +123,15 @@ def test_tables_with_an_empty_free_list_or_no_rows(ctx, new, free, rows, bad):
     table = np.array([[3, -1, -1], [1, -1, -1], [-1, -1, -1]], np.int32)
     got = _check_tables(np.array(ctx), np.array(new), table, np.array([0, 2, 4, 5][:free], np.int32), free, 16, 6, rows)
     assert got["bad"] == bad
+
+
+@pytest.mark.parametrize("ctx,new", [([2 ** 31 - 20, 7], [15, 12]), ([3, 2 ** 31 - 10], [2, 9]), ([0, 2 ** 31 - 1], [17, 0]),
+                                     ([2 ** 31 - 300], [299])])
+@pytest.mark.parametrize("page", [16, 256])
+def test_tables_of_lengths_up_to_31_bits(ctx, new, page):
+    """Lengths whose pages no table holds: reported, counted as all others, and the other requests unharmed."""
+    num_pages = 40
+    table = np.full((len(ctx), 3), -1, np.int32)
+    table[:, 0] = 7
+    got = _check_tables(np.array(ctx), np.array(new), table, np.arange(10, 30, dtype=np.int32), 20, page, num_pages, sum(new) + 2)
+    assert got["bad"] == any(n for c, n in zip(ctx, new) if c > 2 ** 30)
