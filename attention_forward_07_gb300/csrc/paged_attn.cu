@@ -854,7 +854,7 @@ struct Plan {
     }
     // units of a head: every request's tokens over 2 T, rounded up
     const long long by_rows = (long long)a.total_q / (TILE_QT * T) + a.B;  // <= total_q / 2 + B
-    const long long by_len = (long long)a.B * ((longest + TILE_QT * T - 1) / (TILE_QT * T));
+    const long long by_len = a.B * (((long long)longest + TILE_QT * T - 1) / (TILE_QT * T));
     max_units = (int)(by_rows < by_len ? by_rows : by_len);
     const size_t max_runs = (size_t)MAX_SPLIT * sms, pieces = 2 * max_runs * TILE_QT * TILE_ROWS;
     off_units = off_queue + 256;
@@ -871,6 +871,7 @@ int check_shape(const attn_fwd_paged_params_t& a) {
   if (a.B < 1 || a.B > 16384 || a.total_q < 1 || a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv != 0 || a.max_seqlen_q < 1) return ATTN_ERR_INVALID;
   if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (a.Hq / a.Hkv > 128) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)a.total_q * a.Hq > INT_MAX - (1 << 27)) return ATTN_ERR_INVALID;
   return ATTN_OK;
 }
 
@@ -882,7 +883,7 @@ int check(const attn_fwd_paged_params_t& a) {
   if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
   if (a.num_pages < 1 || a.table_width < 1 || a.table_stride < a.table_width || a.page_size < 16 ||
       a.page_size % 16 != 0 || (long long)a.table_width * a.page_size > INT_MAX - 4096 ||
-      (long long)a.total_q * a.Hq > INT_MAX - (1 << 27) || a.window_left < -1 || a.window_right < -1)
+      a.window_left < -1 || a.window_right < -1)
     return ATTN_ERR_INVALID;
   if (!(a.scale > 0.f) || !std::isfinite(a.scale * LOG2E)) return ATTN_ERR_INVALID;
   for (const void* ptr : {a.q, a.k_cache, a.v_cache, (const void*)a.o})

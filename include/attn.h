@@ -297,7 +297,7 @@ int attn_paged_append(const attn_paged_append_params_t *params);
  * (>= 1) are cut to their first max_seqlen_q rows.  Rows of q, o and lse outside every
  * request are neither read into a result nor written.
  * Element (hq, t, x) of q is at t*q_row_stride + hq*q_head_stride + x, of o likewise with its own
- * strides; lse is [Hq][total_q] or NULL.  Hq / Hkv <= 128, B <= 16384.  Strides of dimensions of more
+ * strides; lse is [Hq][total_q] or NULL.  Hq / Hkv <= 128, B <= 16384, total_q * Hq < 2^31 - 2^27.  Strides of dimensions of more
  * than one entry are positive, and of the caches' page and head strides one is a multiple of the
  * other (else ATTN_ERR_UNSUPPORTED).
  * Cache rows that no query row of the request may see, behind its last key, ahead of its

@@ -1,5 +1,5 @@
 """Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes, how kernels that start early
-read, empty lists and maps."""
+read, empty lists and maps, sizes past what is counted."""
 import contextlib
 import ctypes
 import os
@@ -12,7 +12,7 @@ import torch
 import attention_forward_07_gb300 as af
 from attention_forward_07_gb300 import _binding as bd
 
-from test_paged_cpu import P, TABLES, lib  # noqa: F401
+from test_paged_cpu import ATTEND, P, TABLES, lib  # noqa: F401
 
 
 # ---- the workspace of a call that is being captured
@@ -117,3 +117,13 @@ def test_empty_tensors_become_null(monkeypatch, free, rows, positions):
     assert (got[0].max_free, got[0].max_rows) == (free, rows)
     assert (got[0].free_pages is None) == (free == 0) and (got[0].slots is None) == (rows == 0)
     assert (got[0].positions is None) == (rows == 0 or not positions)
+
+
+# ---- sizes past what is counted
+@pytest.mark.parametrize("kw", [dict(total_q=2 ** 31 - 1, max_seqlen_q=2 ** 31 - 1), dict(total_q=2 ** 30, max_seqlen_q=1),
+                                dict(Hq=128, Hkv=1, total_q=1 << 25, max_seqlen_q=64)], ids=str)
+def test_no_workspace_size_for_what_the_attention_refuses(lib, kw):  # noqa: F811
+    n = ctypes.c_ulonglong(77)
+    prm = bd.FwdPagedParams(**dict(ATTEND, **kw))
+    assert lib.attn_paged_workspace(ctypes.byref(prm), ctypes.byref(n)) == -1 and n.value == 77
+    assert lib.attn_fwd_paged(ctypes.byref(prm)) == -1
