@@ -7,8 +7,12 @@
 //    tcgen05 path 55 / 31; above 32 rows the order turns (48 rows: 78 us against 57 at d = 128);
 //  * few-row requests beside chunks join the chunks' units while they have few key tiles altogether
 //    (FOLD_TILES in paged_attn.cu);
-//  * where no request has more rows than a Q tile, and they have more than ROWS_MAX on the average, all
-//    take the tcgen05 path, which then needs neither the other path's kernel nor its plan (NO_PLAN_B).
+//  * where no request may have more rows than a Q tile, and the call gives them room for more than ROWS_MAX on the
+//    average (total_q over B; the lengths themselves are on the device), all take the tcgen05 path, which
+//    then needs neither the other path's kernel nor its plan (NO_PLAN_B).  32 query heads on 4, room for 16
+//    tokens to a request, 4000 keys: with 16 tokens 64 requests take 119 / 105 us (d = 128 / 64), with a plan
+//    124 / 109, 16 requests 44 / 37 and 51 / 40.  Where the room is not used it costs at d = 64: with one
+//    token to a request 64 take 109 / 102, with a plan 115 / 51.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -226,8 +226,8 @@ int attn_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float
  * sequence of these calls can be replayed after the arrays' contents changed.  The calls
  * keep no state between them.  Index arrays are int32, 4-byte aligned, device memory.
  * Bad values in them fault nothing: a page id outside [0, num_pages), a slot at or past
- * num_pages*page_size, a free list that runs out or a table that is too narrow is left out
- * as described with each call, and recorded as ATTN_ERR_PAGE in the stream's status word,
+ * num_pages*page_size, a free list that runs out or, in attn_paged_tables, a table that is too narrow is
+ * left out as described with each call, and recorded as ATTN_ERR_PAGE in the stream's status word,
  * which attn_check(stream) reports.
  */
 
@@ -294,8 +294,15 @@ int attn_paged_append(const attn_paged_append_params_t *params);
  * where they have been appended.  Query i of a request with sq rows and sk keys sits at key
  * position i + sk - sq; causal, window_left and window_right as for attn_fwd_ex, with sk < sq
  * allowed (rows without a key give O = 0, LSE = -inf).  Requests longer than max_seqlen_q
- * (>= 1) are cut to their first max_seqlen_q rows.  Rows of q, o and lse outside every
- * request are neither read into a result nor written.
+ * (>= 1) are cut to their first max_seqlen_q rows.  Neither cut is reported, and positions go by the lengths
+ * after it: keep lengths within both bounds, in replays of a captured call as well.  Rows of q, o and lse
+ * outside every request are neither read into a result nor written.
+ * Roundings: scores, softmax and sums in 32 bits, O rounded once.  The weights go into the product with V in the type
+ * of q, as in attn_fwd (each off by half a step at most).  Where max_seqlen_q * Hq / Hkv <= 16 (32 at d = 64) they
+ * keep twice the bits, and so they may for requests of few rows in other calls: the last bits of such a
+ * request can depend on what it is batched with.
+ * The host does not see the lengths: which kernels serve a call goes by the rows of q, B and max_seqlen_q, so a call with
+ * much more room than its requests use is slower than one that fits.
  * Element (hq, t, x) of q is at t*q_row_stride + hq*q_head_stride + x, of o likewise with its own
  * strides; lse is [Hq][total_q] or NULL.  Hq / Hkv <= 128, B <= 16384, total_q * Hq < 2^31 - 2^27.  Strides of dimensions of more
  * than one entry are positive, and of the caches' page and head strides one is a multiple of the
