@@ -1,11 +1,12 @@
 """Edges of the paged-cache operators on the GPU: captures that fork, waits that run out, the
-tensor maps of many layers, empty lists and maps, the longest lengths."""
+tensor maps of many layers, empty lists and maps, the longest lengths, weights in two parts."""
 import numpy as np
 import pytest
 import torch
 
 import attention_forward_07_gb300 as af
 
+import paged_bounds
 from paged_ref import Batch
 from test_gpu_paged import _check_tables
 
@@ -135,3 +136,16 @@ def test_tables_of_lengths_up_to_31_bits(ctx, new, page):
     table[:, 0] = 7
     got = _check_tables(np.array(ctx), np.array(new), table, np.arange(10, 30, dtype=np.int32), 20, page, num_pages, sum(new) + 2)
     assert got["bad"] == any(n for c, n in zip(ctx, new) if c > 2 ** 30)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", range(len(paged_bounds.CASES)))
+def test_weights_of_few_rows_keep_twice_the_bits(case, dtype):
+    """O within a bound that has no room for weights rounded to the values' type (paged_bounds.py)."""
+    bt = paged_bounds.batch(paged_bounds.CASES[case], dtype, seed=case)
+    q, k, v, o, lse = bt.device()
+    af.attn_fwd_paged(q, k, v, o, bt.table.cuda(), bt.cu.cuda(), bt.lens.cuda(), bt.max_q, lse=lse, causal=True, scale=paged_bounds.SCALE)
+    af.attn_check()
+    for rows, want, bound, *_ in paged_bounds.exact(bt):
+        err = (o[:, rows].cpu().double() - want).abs() - bound
+        assert err.max() <= 0, f"{int((err > 0).sum())} of {err.numel()} over the bound, by {err.max()}"

@@ -1,5 +1,5 @@
 """Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes, how kernels that start early
-read, empty lists and maps, sizes past what is counted."""
+read, empty lists and maps, sizes past what is counted, what tells weights in two parts from weights in one."""
 import contextlib
 import ctypes
 import os
@@ -12,6 +12,7 @@ import torch
 import attention_forward_07_gb300 as af
 from attention_forward_07_gb300 import _binding as bd
 
+import paged_bounds
 from test_paged_cpu import ATTEND, P, TABLES, lib  # noqa: F401
 
 
@@ -127,3 +128,18 @@ def test_no_workspace_size_for_what_the_attention_refuses(lib, kw):  # noqa: F81
     prm = bd.FwdPagedParams(**dict(ATTEND, **kw))
     assert lib.attn_paged_workspace(ctypes.byref(prm), ctypes.byref(n)) == -1 and n.value == 77
     assert lib.attn_fwd_paged(ctypes.byref(prm)) == -1
+
+
+# ---- weights in two parts
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", range(len(paged_bounds.CASES)))
+def test_the_bound_for_two_parts_tells_them_from_one(case, dtype):
+    """Emulated in 64 bits: with the remainder's product O is within the bound, without it far from it."""
+    bt = paged_bounds.batch(paged_bounds.CASES[case], dtype, seed=case)
+    over = {1: 0, 2: 0}
+    n = 0
+    for parts in over:
+        for (rows, o, bound, *_), (_, got) in zip(paged_bounds.exact(bt), paged_bounds.emulated(bt, parts)):
+            over[parts] += int(((got - o).abs() > bound).sum())
+            n += o.numel() if parts == 2 else 0
+    assert over[2] == 0 and over[1] > n // 50
