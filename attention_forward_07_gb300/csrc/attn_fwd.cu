@@ -56,6 +56,7 @@
 #include <memory>
 #include <mutex>
 #include <unordered_map>
+#include <vector>
 
 #include "attn.h"
 #include "host.h"
@@ -1200,6 +1201,8 @@ struct StreamState {
   std::mutex m;
   void* ws = nullptr;
   size_t ws_bytes = 0;
+  bool in_graph = false;    // a captured call works in ws, and so does every replay of it
+  std::vector<void*> kept;  // earlier blocks of which that is true
 };
 std::mutex g_streams_mutex;
 std::unordered_map<StreamKey, std::unique_ptr<StreamState>, StreamKeyHash> g_streams;
@@ -1221,14 +1224,17 @@ StreamState* stream_state(int dev, void* stream, bool create) {
   return raw;
 }
 
-// Makes s.ws hold at least `need` bytes (caller holds s.m).  Grows in whole MiB.
+// Makes s.ws hold at least `need` bytes (caller holds s.m; the stream is not being captured).  Grows in whole
+// MiB.  A block that a graph works in stays where it is.
 int ensure_workspace(StreamState& s, size_t need, cudaStream_t st) {
   if (s.ws_bytes >= need) return ATTN_OK;
   const size_t bytes = (need + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
   if (s.ws) {
-    if (cudaFreeAsync(s.ws, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (s.in_graph) s.kept.push_back(s.ws);
+    else if (cudaFreeAsync(s.ws, st) != cudaSuccess) return ATTN_ERR_CUDA;
     s.ws = nullptr;
     s.ws_bytes = 0;
+    s.in_graph = false;
   }
   void* p = nullptr;
   if (cudaMallocAsync(&p, bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
@@ -1486,16 +1492,34 @@ int fwd_impl(const attn_fwd_params_t& a, bool noalloc = false) {
     return run();
   }
   std::lock_guard<std::mutex> lk(ss->m);
-  if ((rc = ensure_workspace(*ss, need, st)) != ATTN_OK) return rc;
-  if (with_order) {
-    // first, as a plain launch: the mask kernels (if any) start after it has finished
-    int* order = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ss->ws) + order_off);
-    unit_order_kernel<<<1, ORDER_THREADS, (2 * p.nkt + 1) * sizeof(int), st>>>(p, order);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    p.order = order;
+  // A captured call works in the stream's workspace where it is large enough, and keeps it from being freed
+  // (in_graph); otherwise in memory that the graph takes and gives back itself: what is allocated
+  // during a capture is the graph's, and no other call may have it.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return ATTN_ERR_CUDA;
+  const bool of_graph = capture != cudaStreamCaptureStatusNone && ss->ws_bytes < need;
+  void* scratch = nullptr;
+  if (of_graph) {
+    if (cudaMallocAsync(&scratch, need, st) != cudaSuccess) return ATTN_ERR_CUDA;
+  } else {
+    if ((rc = ensure_workspace(*ss, need, st)) != ATTN_OK) return rc;
+    scratch = ss->ws;
+    ss->in_graph |= capture != cudaStreamCaptureStatusNone;
   }
-  if (custom && (rc = prepare_mask(p, a.mask_bits, ss->ws, st, dev)) != ATTN_OK) return rc;
-  return run();
+  const auto launches = [&]() -> int {
+    if (with_order) {
+      // first, as a plain launch: the mask kernels (if any) start after it has finished
+      int* order = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(scratch) + order_off);
+      unit_order_kernel<<<1, ORDER_THREADS, (2 * p.nkt + 1) * sizeof(int), st>>>(p, order);
+      if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+      p.order = order;
+    }
+    if (custom && (rc = prepare_mask(p, a.mask_bits, scratch, st, dev)) != ATTN_OK) return rc;
+    return run();
+  };
+  rc = launches();
+  if (of_graph && cudaFreeAsync(scratch, st) != cudaSuccess && rc == ATTN_OK) rc = ATTN_ERR_CUDA;
+  return rc;
 }
 
 attn_fwd_params_t square_params(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -1641,6 +1665,11 @@ int attn_release_workspace(void* stream) {
     if (cudaFreeAsync(ss->ws, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
     ss->ws = nullptr;
     ss->ws_bytes = 0;
+    ss->in_graph = false;
+  }
+  while (!ss->kept.empty()) {
+    if (cudaFreeAsync(ss->kept.back(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+    ss->kept.pop_back();
   }
   return ATTN_OK;
 }

@@ -63,6 +63,12 @@
  *     The workspace is held until
  *     attn_release_workspace(stream) or process exit: release it before
  *     destroying a stream that has run custom masks, variable-length batches or paged attention.
+ *   - Captured calls: attn_fwd and attn_fwd_ex may be captured into a graph.  A captured call goes on using what the
+ *     library keeps for the stream it was captured on (its work queue, and its workspace where that was large
+ *     enough at the time; otherwise the graph allocates its own): its replays, replays of other graphs captured on
+ *     that stream and calls on the stream take their turns, none at the same time as another.  The workspace
+ *     a graph works in is not freed when a later call needs more, only by attn_release_workspace:
+ *     call that when the graphs are done with.  attn_fwd_paged differs (see there): its replays may run beside anything.
  *   - Errors: arguments are validated before any launch (ATTN_ERR_INVALID /
  *     ATTN_ERR_UNSUPPORTED, nothing launched); a failed launch returns
  *     ATTN_ERR_CUDA.  The work is asynchronous: a kernel that gives up on a
