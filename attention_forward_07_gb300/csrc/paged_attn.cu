@@ -51,8 +51,8 @@ struct RowsParams : PagedParams {
 //  * a lane holds the places of the next 32 page rows, so the table is read once per 32 copies;
 //  * mma.sync with the keys as the N side: 16 rows are its smallest M, and its operands come by
 //    ldmatrix straight from the copied rows (a tcgen05 tile's 128 rows would be an eighth full).
-// Measured: 61 requests of 500 - 7200 keys, 32/8 heads, d = 128, bf16: 112 us, 6.15 TB/s of keys and values
-// (0.91 of measured copy bandwidth); 3 of 84 - 106 thousand: 95 us, 6.0 TB/s; one of 1001: 9.0 us, latency (of
+// Measured: 61 requests of 500 - 7200 keys, 32/8 heads, d = 128, bf16: 113 us, 6.1 TB/s of keys and values
+// (0.90 of measured copy bandwidth); 3 of 84 - 106 thousand: 95 us, 6.0 TB/s; one of 1001: 9.3 us, latency (of
 // launches, lengths -> table -> keys, and the join).  Ring depth, CTAs and keys to a stage were swept, with
 // weights in one part: 2 stages and 3 CTAs 112 us, 2 and 4 (128 registers, spills) 166, 8 KiB in half the
 // keys 126, this 110.

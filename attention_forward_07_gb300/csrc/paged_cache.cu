@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(TABLES_THREADS) paged_tables_kernel(const __gr
 // cache[slot / P][h][slot % P][:] = new[h][t][:].  One warp takes a row t, reads its slot once
 // (the division by P is the row's, not each chunk's) and moves the row's 2 * Hkv * d / 8 chunks of 16
 // bytes of K and V, up to eight in flight to a lane.  Memory-bound: every byte is read and written once.
-// Measured: 16.9 thousand rows of 8 heads, d = 128: 23.7 us, 5.84 TB/s (0.86 of measured copy bandwidth);
+// Measured: 16.9 thousand rows of 8 heads, d = 128: 23.8 us, 5.81 TB/s (0.86 of measured copy bandwidth);
 // 64 rows: 2.8 us, a launch's time.  All is read past L1, which nothing here uses twice: with plain loads the
 // wait for the kernel ahead empties L1 first, and 64 rows take 3.4 us.
 constexpr int APPEND_WARPS = 4;

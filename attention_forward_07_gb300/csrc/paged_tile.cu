@@ -17,9 +17,10 @@
 // A second product with what the rounding leaves would cost chunks half as much again, and a few tokens of 24
 // requests 54 us against 41.
 //
-// Bound by: the tensor path for chunks.  2037 rows x 32 heads against 32k keys, d = 128, pages of 16: 0.69 ms, 1500
-// TFLOP/s (0.79 of the measured burst peak; contiguous attn_fwd_ex on the same shape 0.76 ms); four prompts
-// of 4k rows 0.425 ms, 1280 TFLOP/s, of which a unit's start and end (one Q buffer at d = 128) take a tenth.
+// Bound by: the tensor path for chunks.  2037 rows x 32 heads against 32k keys, d = 128, pages of 16: 0.71 ms, 1450
+// TFLOP/s (0.76 of the measured burst peak; contiguous attn_fwd_ex on the same shape, in turn with it, 0.77 ms); four
+// prompts of 4k rows 0.43 ms, 1280 TFLOP/s, of which a unit's start and end (one Q buffer at d = 128) take a tenth.  At
+// d = 64 the softmax, with as many exponentials for half the flops: the chunk 0.64 ms (contiguous 0.63), the prompts 0.35.
 #include <cuda_runtime.h>
 
 #include <atomic>
