@@ -15,6 +15,7 @@ import threading
 
 ATTN_F16 = 0
 ATTN_BF16 = 1
+ATTN_ERR_INVALID = -1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libattn.so"
@@ -420,33 +421,32 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
     if total_q == 0:
         return
-    at = n = 0  # no workspace: the library's own of the stream
-    if workspace is None:
-        # Captured, a call needs one that nothing beside it uses: from the graph's memory pool, taken with the launch
-        # stream current.  A block that is given back is handed out again in the order of the stream it was taken on,
-        # and is this call's alone only if that is the stream that runs it.
-        if (stream is None or handle == _raw_stream(index)) and _device() == index:
-            if torch.cuda.is_current_stream_capturing():
-                workspace = _capture_workspace(q, (B, Hq, Hkv, d, total_q, max_seqlen_q))
-        else:
-            with torch.cuda.stream(torch.cuda.current_stream(index) if stream is None else stream):
-                if torch.cuda.is_current_stream_capturing():
-                    workspace = _capture_workspace(q, (B, Hq, Hkv, d, total_q, max_seqlen_q))
-    if workspace is not None:
-        n, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-        _refuse(index, others=((workspace.get_device() != index or not workspace.is_contiguous(),
-                                f"workspace must be contiguous and on CUDA device {index}"),))
     width = block_table.shape[1]
-    _launch(index, (_lib or library()).attn_fwd_paged,
-            _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(),
-                         block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), at, n, qs[1], qs[0],
-                         ost[1], ost[0], cs[0], cs[1], cs[2], B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size, width,
-                         block_table.stride(0) if B > 1 else width, 1 if causal else 0, window_left, window_right,
-                         d ** -0.5 if scale is None else scale, code, handle))
+    fn = (_lib or library()).attn_fwd_paged
 
+    def block(at, n):
+        return _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                            block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), at, n, qs[1], qs[0],
+                            ost[1], ost[0], cs[0], cs[1], cs[2], B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size, width,
+                            block_table.stride(0) if B > 1 else width, 1 if causal else 0, window_left, window_right,
+                            d ** -0.5 if scale is None else scale, code, handle)
 
-def _capture_workspace(q, shape):
-    return _torch.empty(_workspace_bytes(shape), dtype=_torch.uint8, device=q.device)
+    if workspace is None:
+        try:
+            return _launch(index, fn, block(0, 0))  # in the library's own of the stream
+        except AttnError as e:
+            if e.status != ATTN_ERR_INVALID:
+                raise
+            # Captured, a call needs one that nothing beside it uses, and the library refuses it without: it gets one from
+            # the graph's memory pool, taken with the launch stream current.  A block that is given back is handed out again
+            # in the order of the stream it was taken on, and is this call's alone only if that is the stream that runs it.
+            with torch.cuda.stream(torch.cuda.current_stream(index) if stream is None else stream):
+                if not torch.cuda.is_current_stream_capturing():
+                    raise
+                workspace = torch.empty(_workspace_bytes((B, Hq, Hkv, d, total_q, max_seqlen_q)), dtype=torch.uint8, device=q.device)
+    _refuse(index, others=((workspace.get_device() != index or not workspace.is_contiguous(),
+                            f"workspace must be contiguous and on CUDA device {index}"),))
+    _launch(index, fn, block(workspace.data_ptr(), workspace.numel() * workspace.element_size()))
 
 
 def _workspace_bytes(shape) -> int:

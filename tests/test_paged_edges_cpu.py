@@ -20,7 +20,8 @@ from test_paged_cpu import ATTEND, P, TABLES, lib  # noqa: F401
 class _Streams:
     """Stands in for torch's streams: a current one, some that are being captured, and what was allocated on which."""
 
-    def __init__(self, monkeypatch, captured):
+    def __init__(self, monkeypatch, captured, status=-1):
+        self.status = status
         self.current, self.taken, self.blocks = self.make(1), [], []
         self.captured = captured
         empty = torch.empty
@@ -46,8 +47,15 @@ class _Streams:
         monkeypatch.setattr(bd, "_raw_stream", lambda i: self.current.cuda_stream)
         monkeypatch.setattr(bd, "_device", lambda: 0)
         monkeypatch.setattr(bd, "_workspace_bytes", lambda shape: 512)
-        monkeypatch.setattr(bd, "_lib", types.SimpleNamespace(attn_fwd_paged=None))
-        monkeypatch.setattr(bd, "_launch", lambda index, fn, block: self.blocks.append(bd.FwdPagedParams.from_buffer_copy(block)))
+        monkeypatch.setattr(bd, "_lib", types.SimpleNamespace(attn_fwd_paged=None, attn_strerror=lambda status: b"refused"))
+        monkeypatch.setattr(bd, "_launch", self.launch)
+
+    def launch(self, index, fn, block):
+        """As the library: no launch on a captured stream without a workspace."""
+        prm = bd.FwdPagedParams.from_buffer_copy(block)
+        if prm.workspace is None and prm.stream in self.captured:
+            raise bd.AttnError(self.status, "attn_fwd_paged")
+        self.blocks.append(prm)
 
     @staticmethod
     def make(handle):
@@ -59,16 +67,39 @@ class _Streams:
     ((1,), None, 1), ((1, 2, 3), 2, 2), ((1, 2, 3), 3, 3),   # streams forked from the one that is captured
     ((2,), 2, 2),                                            # captured, and not the current one
     ((1,), 2, None)])                                        # the current one is captured, the launch goes elsewhere
-def test_a_captured_call_takes_its_workspace_on_the_stream_it_runs_on(monkeypatch, captured, on, taken_on):
+@pytest.mark.parametrize("own", [False, True])
+def test_a_captured_call_takes_its_workspace_on_the_stream_it_runs_on(monkeypatch, captured, on, taken_on, own):
     st = _Streams(monkeypatch, captured)
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     q, kc = torch.zeros((4, 3, 64)).half(), torch.zeros((4, 2, 16, 64)).half()
-    af.attn_fwd_paged(q, kc, kc, q.clone(), i(2, 4), i(3), i(2), 2, stream=on and st.make(on))
+    ws = torch.zeros(768, dtype=torch.uint8) if own else None
+    af.attn_fwd_paged(q, kc, kc, q.clone(), i(2, 4), i(3), i(2), 2, stream=on and st.make(on), workspace=ws)
     (block,) = st.blocks
     assert (block.stream or 0) == (on or 1)
+    if own:  # the caller's, whatever is captured
+        assert not st.taken and (block.workspace, block.workspace_bytes) == (ws.data_ptr(), 768)
+        return
     assert st.taken == ([] if taken_on is None else [(taken_on, 512)])
     assert block.workspace_bytes == (0 if taken_on is None else 512) and (block.workspace is None) == (taken_on is None)
     assert st.current.cuda_stream == 1
+
+
+@pytest.mark.parametrize("captured,status", [((), -1), ((1,), -3)])
+def test_other_refusals_come_through(monkeypatch, captured, status):
+    """What is refused outside a capture, or for another reason, is not tried again."""
+    st = _Streams(monkeypatch, captured, status)
+    tried = []
+
+    def launch(index, fn, block):
+        tried.append(block)
+        raise bd.AttnError(status, "attn_fwd_paged")
+
+    monkeypatch.setattr(bd, "_launch", launch)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    q, kc = torch.zeros((4, 3, 64)).half(), torch.zeros((4, 2, 16, 64)).half()
+    with pytest.raises(af.AttnError) as e:
+        af.attn_fwd_paged(q, kc, kc, q.clone(), i(2, 4), i(3), i(2), 2)
+    assert e.value.status == status and len(tried) == 1 and not st.taken
 
 
 # ---- kernels that start before the one ahead has ended
