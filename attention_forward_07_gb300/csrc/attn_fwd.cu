@@ -1607,71 +1607,81 @@ extern "C" {
 int attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
              const uint32_t* mask_bits, int B, int Hq, int Hkv, int S, int d, int causal,
              float scale, int dtype, void* stream) {
-  return attn::fwd_impl(attn::square_params(q, k, v, o, lse, mask_bits, B, Hq, Hkv, S, d, causal,
-                                            scale, dtype, stream, nullptr));
+  return attn::entry([&] {
+    return attn::fwd_impl(attn::square_params(q, k, v, o, lse, mask_bits, B, Hq, Hkv, S, d, causal,
+                                              scale, dtype, stream, nullptr));
+  });
 }
 
 int attn_fwd_ex(const attn_fwd_params_t* params) {
   if (!params) return ATTN_ERR_INVALID;
-  return attn::fwd_impl(*params);
+  return attn::entry([&] { return attn::fwd_impl(*params); });
 }
 
 int attn_fwd_visited(const void* q, const void* k, const void* v, void* o, float* lse,
                      const uint32_t* mask_bits, int B, int Hq, int Hkv, int S, int d, int causal,
                      float scale, int dtype, void* stream, uint8_t* visited) {
   if (!visited) return ATTN_ERR_INVALID;
-  return attn::fwd_impl(attn::square_params(q, k, v, o, lse, mask_bits, B, Hq, Hkv, S, d, causal,
-                                            scale, dtype, stream, visited));
+  return attn::entry([&] {
+    return attn::fwd_impl(attn::square_params(q, k, v, o, lse, mask_bits, B, Hq, Hkv, S, d, causal,
+                                              scale, dtype, stream, visited));
+  });
 }
 
 int attn_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float* lse,
                      const uint32_t* mask_bits, int B, int Hq, int Hkv, int S, int d, int causal,
                      float scale, int dtype, void* stream) {
-  return attn::fwd_impl(attn::square_params(q, k, v, o, lse, mask_bits, B, Hq, Hkv, S, d, causal,
-                                            scale, dtype, stream, nullptr),
-                        true);
+  return attn::entry([&] {
+    return attn::fwd_impl(attn::square_params(q, k, v, o, lse, mask_bits, B, Hq, Hkv, S, d, causal,
+                                              scale, dtype, stream, nullptr),
+                          true);
+  });
 }
 
 int attn_check(void* stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ATTN_ERR_DEVICE;
-  const attn::StreamState* ss = attn::stream_state(dev, stream, false);
-  const size_t off = (size_t)(ss ? ss->slot : 0) * sizeof(unsigned int);
-  // The status word is read in stream order, after everything enqueued on `stream` so far.
-  unsigned int status = 0;
-  if (cudaMemcpyFromSymbolAsync(&status, g_attn_status, sizeof status, off, cudaMemcpyDeviceToHost, st) !=
-          cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return ATTN_ERR_CUDA;
-  if (status != 0) {
-    const unsigned int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_attn_status, &zero, sizeof zero, off, cudaMemcpyHostToDevice, st) !=
+  return attn::entry([&]() -> int {
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ATTN_ERR_DEVICE;
+    const attn::StreamState* ss = attn::stream_state(dev, stream, false);
+    const size_t off = (size_t)(ss ? ss->slot : 0) * sizeof(unsigned int);
+    // The status word is read in stream order, after everything enqueued on `stream` so far.
+    unsigned int status = 0;
+    if (cudaMemcpyFromSymbolAsync(&status, g_attn_status, sizeof status, off, cudaMemcpyDeviceToHost, st) !=
             cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
       return ATTN_ERR_CUDA;
-    return (status & attn::STATUS_TIMEOUT) ? ATTN_ERR_TIMEOUT : ATTN_ERR_PAGE;
-  }
-  return ATTN_OK;
+    if (status != 0) {
+      const unsigned int zero = 0;
+      if (cudaMemcpyToSymbolAsync(g_attn_status, &zero, sizeof zero, off, cudaMemcpyHostToDevice, st) !=
+              cudaSuccess ||
+          cudaStreamSynchronize(st) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+      return (status & attn::STATUS_TIMEOUT) ? ATTN_ERR_TIMEOUT : ATTN_ERR_PAGE;
+    }
+    return ATTN_OK;
+  });
 }
 
 int attn_release_workspace(void* stream) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ATTN_ERR_DEVICE;
-  attn::StreamState* ss = attn::stream_state(dev, stream, false);
-  if (!ss) return ATTN_OK;
-  std::lock_guard<std::mutex> lk(ss->m);
-  if (ss->ws) {
-    if (cudaFreeAsync(ss->ws, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
-    ss->ws = nullptr;
-    ss->ws_bytes = 0;
-    ss->in_graph = false;
-  }
-  while (!ss->kept.empty()) {
-    if (cudaFreeAsync(ss->kept.back(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
-    ss->kept.pop_back();
-  }
-  return ATTN_OK;
+  return attn::entry([&]() -> int {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ATTN_ERR_DEVICE;
+    attn::StreamState* ss = attn::stream_state(dev, stream, false);
+    if (!ss) return ATTN_OK;
+    std::lock_guard<std::mutex> lk(ss->m);
+    if (ss->ws) {
+      if (cudaFreeAsync(ss->ws, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+      ss->ws = nullptr;
+      ss->ws_bytes = 0;
+      ss->in_graph = false;
+    }
+    while (!ss->kept.empty()) {
+      if (cudaFreeAsync(ss->kept.back(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+      ss->kept.pop_back();
+    }
+    return ATTN_OK;
+  });
 }
 
 int attn_debug_counters(unsigned long long* out, int n) {

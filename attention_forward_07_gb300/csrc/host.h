@@ -6,6 +6,8 @@
 #include <cstdint>
 #include <mutex>
 
+#include "attn.h"
+
 namespace attn {
 
 // Bits of a stream's status word.
@@ -34,5 +36,15 @@ int host_status_word(int dev, void* stream, unsigned int** word);
 // The workspace that the library keeps for `stream`, grown to `bytes` where needed (stream-ordered).  `hold`
 // keeps other calls on the stream from it until the caller has enqueued what uses it.
 int host_workspace(int dev, void* stream, size_t bytes, std::unique_lock<std::mutex>& hold, void** ws);
+
+// A C entry's body: what it throws (host memory that has run out, a mutex that fails) becomes a status.
+template <class F>
+int entry(F body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return ATTN_ERR_CUDA;
+  }
+}
 
 }  // namespace attn

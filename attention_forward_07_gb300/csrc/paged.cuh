@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "attn.h"
+#include "host.h"
 #include "ptx.cuh"
 
 namespace attn {
@@ -152,16 +153,6 @@ int launch_dependent(void (*kern)(P), dim3 grid, unsigned int threads, size_t sm
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-}
-
-// A C entry's body: what it throws (host memory that has run out, a mutex that fails) becomes a status.
-template <class F>
-int entry(F body) noexcept {
-  try {
-    return body();
-  } catch (...) {
-    return ATTN_ERR_CUDA;
-  }
 }
 
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }

@@ -1,5 +1,6 @@
 """Edges of the paged-cache operators that need no GPU: whose workspace a captured call takes, how kernels that start early
-read, empty lists and maps, sizes past what is counted, what tells weights in two parts from weights in one."""
+read, empty lists and maps, sizes past what is counted, what tells weights in two parts from weights in one, and
+that no C entry lets an exception out."""
 import contextlib
 import ctypes
 import os
@@ -174,3 +175,17 @@ def test_the_bound_for_two_parts_tells_them_from_one(case, dtype):
             over[parts] += int(((got - o).abs() > bound).sum())
             n += o.numel() if parts == 2 else 0
     assert over[2] == 0 and over[1] > n // 50
+
+
+# ---- C entries
+def test_c_entries_turn_exceptions_into_a_status():
+    """Whatever allocates on the host or takes a lock runs inside entry(), in all of the library's C functions."""
+    seen = set()
+    for name in ("attn_fwd.cu", "paged_attn.cu", "paged_cache.cu"):
+        text = _code(name)
+        for fn, body in re.findall(r"\nint (attn_\w+)\([^)]*\) {\n(.*?)\n}\n", text[text.index('extern "C"'):], flags=re.S):
+            if re.search(r"fwd_impl|stream_state|host_|Plan\b", body):
+                seen.add(fn)
+                assert re.search(r"return attn::entry\(", body), fn
+    assert seen == {"attn_fwd", "attn_fwd_ex", "attn_fwd_visited", "attn_fwd_noalloc", "attn_check", "attn_release_workspace",
+                    "attn_paged_tables", "attn_paged_append", "attn_fwd_paged", "attn_paged_workspace"}
