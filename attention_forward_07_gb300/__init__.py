@@ -18,11 +18,17 @@ from ._binding import (  # noqa: F401
     attn_fwd_noalloc,
     attn_fwd_packed,
     attn_fwd_paged,
+    attn_fwd_paged_tree,
     attn_fwd_visited,
+    attn_paged_accept,
     attn_paged_append,
+    attn_paged_move,
+    attn_paged_rope,
     attn_paged_tables,
+    attn_paged_tree,
     attn_paged_workspace,
     attn_release_workspace,
+    attn_rope,
     attn_strerror,
     attn_tile_shape,
     debug_counters,

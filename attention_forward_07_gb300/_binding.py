@@ -32,6 +32,11 @@ EXPORTS = (
     "attn_paged_append",
     "attn_fwd_paged",
     "attn_paged_workspace",
+    "attn_rope",
+    "attn_paged_tree",
+    "attn_fwd_paged_tree",
+    "attn_paged_accept",
+    "attn_paged_move",
     "attn_check",
     "attn_release_workspace",
     "attn_debug_counters",
@@ -87,6 +92,46 @@ i: dtype
 p: stream""")
 
 
+class RopeParams(ctypes.Structure):
+    """attn_rope_params_t of include/attn.h."""
+    _fields_ = _fields("""p: q k v q_out k_out k_cache v_cache q_weight k_weight positions slots inv_freq
+l: q_row_stride q_head_stride k_row_stride k_head_stride v_row_stride v_head_stride q_out_row_stride q_out_head_stride
+l: k_out_row_stride k_out_head_stride cache_page_stride cache_head_stride cache_row_stride position_stride
+i: rows Hq Hkv d rot_dim axes interleaved weight_f32 num_pages page_size
+f: eps
+i: dtype
+p: stream""")
+
+
+class PagedTreeParams(ctypes.Structure):
+    """attn_paged_tree_params_t of include/attn.h."""
+    _fields_ = _fields("""p: parents cu_seqlens_q seqlens_k positions tree_mask
+i: B rows mask_words mask_stride window_left
+p: stream""")
+
+
+class FwdPagedTreeParams(ctypes.Structure):
+    """attn_fwd_paged_tree_params_t of include/attn.h."""
+    _fields_ = [("call", FwdPagedParams)] + _fields("""p: tree_mask positions
+i: mask_words mask_stride""")
+
+
+class PagedAcceptParams(ctypes.Structure):
+    """attn_paged_accept_params_t of include/attn.h."""
+    _fields_ = _fields("""p: tokens targets parents confirmed cu_seqlens_q seqlens_k block_table free_pages free_count free_count_out
+p: accepted ctx_lens next_tokens path src_slots dst_slots
+i: B rows max_path table_width table_stride max_free page_size num_pages
+p: stream""")
+
+
+class PagedMoveParams(ctypes.Structure):
+    """attn_paged_move_params_t of include/attn.h."""
+    _fields_ = _fields("""p: k_cache v_cache src_slots dst_slots
+l: cache_layer_stride cache_page_stride cache_head_stride cache_row_stride
+i: layers lists length Hkv d num_pages page_size dtype
+p: stream""")
+
+
 class AttnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -126,6 +171,9 @@ def library():
         lib.attn_paged_append.restype = i
         lib.attn_fwd_paged.argtypes = [p]
         lib.attn_fwd_paged.restype = i
+        for fn in (lib.attn_rope, lib.attn_paged_tree, lib.attn_fwd_paged_tree, lib.attn_paged_accept, lib.attn_paged_move):
+            fn.argtypes = [p]
+            fn.restype = i
         lib.attn_paged_workspace.argtypes = [p, ctypes.POINTER(ctypes.c_ulonglong)]
         lib.attn_paged_workspace.restype = i
         lib.attn_check.argtypes = [p]
@@ -270,6 +318,11 @@ def attn_fwd_packed(q, k, v, o, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_se
 _TABLES = struct.Struct("@10P7iP")
 _APPEND = struct.Struct("@5P7q6iP")
 _ATTEND = struct.Struct("@9PQ7q13ifiP")
+_MASK = struct.Struct("@2P2i")  # what follows _ATTEND in attn_fwd_paged_tree's
+_ROPE = struct.Struct("@12P14q10ifiP")
+_TREE = struct.Struct("@5P5iP")
+_ACCEPT = struct.Struct("@16P8iP")
+_MOVE = struct.Struct("@4P4q8iP")
 _torch = None
 _raw_stream = None
 _device = None
@@ -397,6 +450,33 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     chunks, mixed freely.  workspace: a uint8 tensor of attn_paged_workspace() bytes for calls that do not run at the same
     time; None uses the stream's own, or, while the stream is being captured, one of the call's own from the graph's memory
     pool.  See include/attn.h."""
+    _fwd_paged(None, q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, lse, causal, window_left, window_right, scale,
+               workspace, stream)
+
+
+def attn_fwd_paged_tree(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, tree_mask, positions=None, lse=None,
+                        window_left=-1, scale=None, workspace=None, stream=None):
+    """attn_fwd_paged with a mask among each request's new rows, as for drafted trees: a row sees its context (within
+    window_left of its position) and new row j of its request iff bit j of its row of tree_mask is set (int32 [total_q, words], rows
+    contiguous).  positions: int32 [total_q], wanted with a window.  Requests of more than 32 * words rows are chunks, causal.
+    See include/attn.h."""
+    if (tree_mask.dtype is not (_torch or _with_torch()).int32 or tree_mask.get_device() != q.get_device() or tree_mask.dim() != 2 or
+            tree_mask.shape[0] != q.shape[1] or (tree_mask.stride(1) != 1 and tree_mask.shape[1] > 1)):
+        raise ValueError(f"tree_mask must be int32 [{q.shape[1]}, words] on q's device, each row contiguous")
+    if positions is not None:
+        if (positions.dtype is not _torch.int32 or positions.get_device() != q.get_device() or positions.shape != (q.shape[1],) or
+                not positions.is_contiguous()):
+            raise ValueError(f"positions must be a contiguous int32 vector of {q.shape[1]} entries on q's device")
+    words = tree_mask.shape[1]
+    mask = _MASK.pack(tree_mask.data_ptr(), 0 if positions is None else positions.data_ptr(), words,
+                      tree_mask.stride(0) if tree_mask.shape[0] > 1 else words)
+    _fwd_paged(mask, q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, lse, True, window_left, -1, scale, workspace,
+               stream)
+
+
+def _fwd_paged(mask, q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, lse, causal, window_left, window_right, scale,
+               workspace, stream):
+    """attn_fwd_paged, or, with the packed fields of a mask, attn_fwd_paged_tree."""
     torch = _torch or _with_torch()
     dtype, index, i32 = q.dtype, q.get_device(), torch.int32
     code = _dtype_code(q)
@@ -422,14 +502,16 @@ def attn_fwd_paged(q, k_cache, v_cache, o, block_table, cu_seqlens_q, seqlens_k,
     if total_q == 0:
         return
     width = block_table.shape[1]
-    fn = (_lib or library()).attn_fwd_paged
+    lib = _lib or library()
+    fn = lib.attn_fwd_paged if mask is None else lib.attn_fwd_paged_tree
 
     def block(at, n):
-        return _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        call = _ATTEND.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(),
                             block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), at, n, qs[1], qs[0],
                             ost[1], ost[0], cs[0], cs[1], cs[2], B, Hq, Hkv, d, total_q, max_seqlen_q, num_pages, page_size, width,
                             block_table.stride(0) if B > 1 else width, 1 if causal else 0, window_left, window_right,
                             d ** -0.5 if scale is None else scale, code, handle)
+        return call if mask is None else call + mask
 
     if workspace is None:
         try:
@@ -462,6 +544,176 @@ def _workspace_bytes(shape) -> int:
 def attn_paged_workspace(B, Hq, Hkv, d, total_q, max_seqlen_q) -> int:
     """Bytes of workspace attn_fwd_paged wants on the current device."""
     return _workspace_bytes((B, Hq, Hkv, d, total_q, max_seqlen_q))
+
+
+def _one(t, n):
+    """Whether t is anything but a contiguous vector of n entries."""
+    return t.shape != (n,) or not t.is_contiguous()
+
+
+def _rope(q, k, v, q_out, k_out, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream):
+    torch = _torch or _with_torch()
+    dtype, index, i32 = q.dtype, q.get_device(), torch.int32
+    code = _dtype_code(q)
+    shape = q.shape
+    Hq, rows, d = shape
+    Hkv = k.shape[0]
+    rot = axes = stride = 0
+    if inv_freq is not None:
+        axes, rot = (1, 2 * inv_freq.shape[0]) if inv_freq.dim() == 1 else (inv_freq.shape[0], 2 * inv_freq.shape[1])
+        wanted = (rows,) if positions is not None and positions.dim() == 1 and axes == 1 else (axes, rows)
+        if (positions is None or positions.dtype is not i32 or positions.get_device() != index or positions.shape != wanted or
+                (rows > 1 and positions.stride(-1) != 1)):
+            raise ValueError(f"positions must be int32 {wanted} on CUDA device {index}, each axis contiguous")
+        if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != index or not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq must be contiguous fp32 [pairs] or [axes, pairs] on CUDA device {index}")
+        stride = positions.stride(0) if axes > 1 else rows
+    weight = q_weight if q_weight is not None else k_weight
+    f32 = weight is not None and weight.dtype is torch.float32
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype is not (torch.float32 if f32 else dtype) or w.get_device() != index or _one(w, d)):
+            raise ValueError(f"{name} must be a contiguous vector of {d} entries of {dtype} or (both weights) fp32 on CUDA device {index}")
+    qs, ks, qo = q.stride(), k.stride(), q_out.stride()
+    kv = (Hkv, rows, d)
+    if (index < 0 or q_out.dtype is not dtype or k.dtype is not dtype or q_out.get_device() != index or k.get_device() != index or
+            q_out.shape != shape or k.shape != kv or not qs[2] == ks[2] == qo[2] == 1):
+        _refuse(index, rows=((q, shape, dtype, "q"), (k, kv, dtype, "k"), (q_out, shape, dtype, "q_out")))
+    if slots is None:
+        vs = cs = (0, 0, 0)
+        num_pages = page_size = 0
+        ko = k_out.stride()
+        if k_out.dtype is not dtype or k_out.get_device() != index or k_out.shape != kv or ko[2] != 1:
+            _refuse(index, rows=((k_out, kv, dtype, "k_out"),))
+    else:
+        vs, cs, ko = v.stride(), k_cache.stride(), (0, 0, 0)
+        if (len(cs) != 4 or k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != index or
+                v_cache.get_device() != index or v_cache.shape != k_cache.shape or v_cache.stride() != cs or cs[3] != 1 or
+                k_cache.shape[1] != Hkv or k_cache.shape[3] != d):
+            _refuse(index, caches=(k_cache, v_cache, dtype, d))
+        num_pages, _, page_size, _ = k_cache.shape
+        if (v.dtype is not dtype or v.get_device() != index or v.shape != kv or vs[2] != 1 or slots.dtype is not i32 or
+                slots.get_device() != index or _one(slots, rows)):
+            _refuse(index, ((slots, rows, "slots"),), rows=((v, kv, dtype, "v"),))
+    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
+    if rows == 0:
+        return
+    at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    _launch(index, (_lib or library()).attn_rope,
+            _ROPE.pack(q.data_ptr(), k.data_ptr(), at(v), q_out.data_ptr(), at(k_out), at(k_cache), at(v_cache), at(q_weight), at(k_weight),
+                       at(positions) if axes else 0, at(slots), at(inv_freq), qs[1], qs[0], ks[1], ks[0], vs[1], vs[0], qo[1], qo[0], ko[1],
+                       ko[0], cs[0], cs[1], cs[2], stride, rows, Hq, Hkv, d, rot, axes, 1 if interleaved else 0, 1 if f32 else 0, num_pages,
+                       page_size, eps, code, handle))
+
+
+def attn_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, stream=None):
+    """Norms of queries and keys for each head (where there are weights, [d] of q's type or fp32) and their rotation by position,
+    in one pass: q, q_out [Hq, rows, d], k, k_out [Hkv, rows, d], any strides whose last dimension is contiguous; an output may be
+    its input.  positions int32 [rows] with inv_freq fp32 [pairs], or [axes, rows] with [axes, pairs], whose columns hold a pair's
+    frequency in its axis and 0 elsewhere; pairs are halves' or, interleaved, neighbours', and elements past 2 * pairs are not
+    turned.  inv_freq None: norms alone.  A contiguous [B, H, S, d] of shared positions goes in as view(B * H, S, d).  See include/attn.h."""
+    _rope(q, k, None, q_out, k_out, None, None, None, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream)
+
+
+def attn_paged_rope(q, k, v, q_out, k_cache, v_cache, slots, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                    stream=None):
+    """attn_rope whose keys go, with the values v [Hkv, rows, d], to their slots (int32 [rows]) of the caches [num_pages, Hkv, page_size, d];
+    rows of negative slots are left out, of q_out too.  See include/attn.h."""
+    _rope(q, k, v, q_out, None, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream)
+
+
+def attn_paged_tree(parents, cu_seqlens_q, seqlens_k, positions, tree_mask, window_left=-1, stream=None):
+    """Positions (context + depth) and ancestor masks of drafted trees.  int32 device tensors: parents [rows] (number of the node above
+    among the request's nodes, -1: none), cu_seqlens_q [B+1], seqlens_k [B] -> positions [rows], tree_mask [rows, words].  Requests of
+    more than 32 * words nodes are chunks: chains without a mask.  See include/attn.h."""
+    torch = _torch or _with_torch()
+    i32, index = torch.int32, parents.get_device()
+    (rows,), (B,) = parents.shape, seqlens_k.shape
+    if (index < 0 or not parents.dtype is cu_seqlens_q.dtype is seqlens_k.dtype is positions.dtype is tree_mask.dtype is i32 or
+            not index == cu_seqlens_q.get_device() == seqlens_k.get_device() == positions.get_device() == tree_mask.get_device() or
+            _one(parents, rows) or _one(cu_seqlens_q, B + 1) or _one(seqlens_k, B) or _one(positions, rows) or tree_mask.dim() != 2 or
+            tree_mask.shape[0] != rows or (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1)):
+        _refuse(index, ((parents, rows, "parents"), (cu_seqlens_q, B + 1, "cu_seqlens_q"), (seqlens_k, B, "seqlens_k"),
+                        (positions, rows, "positions")),
+                others=((True, f"tree_mask must be int32 [{rows}, words] on CUDA device {index}, each row contiguous"),))
+    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
+    if rows == 0:
+        return
+    words = tree_mask.shape[1]
+    _launch(index, (_lib or library()).attn_paged_tree,
+            _TREE.pack(parents.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), positions.data_ptr(), tree_mask.data_ptr(), B, rows,
+                       words, tree_mask.stride(0) if rows > 1 else words, window_left, handle))
+
+
+def attn_paged_accept(tokens, targets, parents, cu_seqlens_q, seqlens_k, block_table, free_pages, free_count, page_size, num_pages, accepted,
+                      ctx_lens, next_tokens, path, src_slots, dst_slots, confirmed=None, free_count_out=None, stream=None):
+    """Which nodes of every request's tree the model confirms: from the last known node to the first child whose token is the
+    model's choice behind it, and on from there.
+
+    int32 device tensors: tokens, targets (the model's choice behind each node), parents [rows], cu_seqlens_q [B+1], seqlens_k [B],
+    block_table [B, W], confirmed [B] (leading nodes that are known; None: 1 each) -> accepted, ctx_lens, next_tokens [B], path, src_slots,
+    dst_slots [B, max path] (-1 behind the last; the slots are attn_paged_move's).  Pages without a token go back to free_pages [F] behind
+    its free_count [1] ids, free_count_out [1] (default: free_count itself) counts them; free_pages None: they do not.  See include/attn.h."""
+    torch = _torch or _with_torch()
+    i32, index = torch.int32, tokens.get_device()
+    (rows,), (B,), lists = tokens.shape, seqlens_k.shape, path.shape
+    width = block_table.shape[-1]
+    if (index < 0 or not tokens.dtype is targets.dtype is parents.dtype is cu_seqlens_q.dtype is seqlens_k.dtype is block_table.dtype is
+            accepted.dtype is ctx_lens.dtype is next_tokens.dtype is path.dtype is src_slots.dtype is dst_slots.dtype is i32 or
+            not index == targets.get_device() == parents.get_device() == cu_seqlens_q.get_device() == seqlens_k.get_device() ==
+            block_table.get_device() == accepted.get_device() == ctx_lens.get_device() == next_tokens.get_device() == path.get_device() ==
+            src_slots.get_device() == dst_slots.get_device() or
+            _one(tokens, rows) or _one(targets, rows) or _one(parents, rows) or _one(cu_seqlens_q, B + 1) or _one(seqlens_k, B) or
+            _one(accepted, B) or _one(ctx_lens, B) or _one(next_tokens, B) or len(lists) != 2 or lists[0] != B or
+            not lists == src_slots.shape == dst_slots.shape or
+            not (path.is_contiguous() and src_slots.is_contiguous() and dst_slots.is_contiguous()) or
+            block_table.dim() != 2 or block_table.shape[0] != B or (block_table.stride(1) != 1 and width > 1)):
+        _refuse(index, ((tokens, rows, "tokens"), (targets, rows, "targets"), (parents, rows, "parents"), (cu_seqlens_q, B + 1, "cu_seqlens_q"),
+                        (seqlens_k, B, "seqlens_k"), (accepted, B, "accepted"), (ctx_lens, B, "ctx_lens"), (next_tokens, B, "next_tokens")),
+                (block_table, B), others=((True, f"path, src_slots and dst_slots must be contiguous int32 [{B}, max path] on CUDA device {index}"),))
+    free = 0
+    if free_pages is not None:
+        (free,) = free_pages.shape
+        if free == 0:
+            raise ValueError("free_pages must have room for one page at least (None: no page goes back)")
+        if free_count_out is None:
+            free_count_out = free_count
+        if (free_pages.dtype is not i32 or free_count.dtype is not i32 or free_count_out.dtype is not i32 or
+                not index == free_pages.get_device() == free_count.get_device() == free_count_out.get_device() or
+                _one(free_pages, free) or _one(free_count, 1) or _one(free_count_out, 1)):
+            _refuse(index, ((free_pages, free, "free_pages"), (free_count, 1, "free_count"), (free_count_out, 1, "free_count_out")))
+    if confirmed is not None and (confirmed.dtype is not i32 or confirmed.get_device() != index or _one(confirmed, B)):
+        _refuse(index, ((confirmed, B, "confirmed"),))
+    _launch(index, (_lib or library()).attn_paged_accept,
+            _ACCEPT.pack(tokens.data_ptr() if rows else 0, targets.data_ptr() if rows else 0, parents.data_ptr() if rows else 0, 0 if confirmed is None else confirmed.data_ptr(),
+                         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), free_pages.data_ptr() if free else 0,
+                         free_count.data_ptr() if free else 0, free_count_out.data_ptr() if free else 0, accepted.data_ptr(),
+                         ctx_lens.data_ptr(), next_tokens.data_ptr(), path.data_ptr(), src_slots.data_ptr(), dst_slots.data_ptr(), B, rows,
+                         lists[1], width, block_table.stride(0) if B > 1 else width, free, page_size, num_pages,
+                         _raw_stream(index) if stream is None else _stream_on(index, stream)))
+
+
+def attn_paged_move(k_cache, v_cache, src_slots, dst_slots, stream=None):
+    """Rows of the caches ([num_pages, Hkv, page_size, d], or of all layers at once, [layers, num_pages, Hkv, page_size, d]) go from src_slots
+    to dst_slots (int32 [lists, length]; pairs with a negative slot are left out).  Within a list no source is an earlier pair's
+    destination; lists share no slot that either writes.  See include/attn.h."""
+    torch = _torch or _with_torch()
+    dtype, index, i32 = k_cache.dtype, k_cache.get_device(), torch.int32
+    code = _dtype_code(k_cache)
+    shape, cs, lists = k_cache.shape, k_cache.stride(), src_slots.shape
+    if (index < 0 or len(cs) not in (4, 5) or v_cache.dtype is not dtype or v_cache.get_device() != index or v_cache.shape != shape or
+            v_cache.stride() != cs or cs[-1] != 1):
+        _refuse(index, caches=(k_cache, v_cache, dtype, "d"))
+    if (len(lists) != 2 or dst_slots.shape != lists or not src_slots.dtype is dst_slots.dtype is i32 or
+            not index == src_slots.get_device() == dst_slots.get_device() or not (src_slots.is_contiguous() and dst_slots.is_contiguous())):
+        raise ValueError(f"src_slots and dst_slots must be contiguous int32 [lists, length] on CUDA device {index}")
+    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
+    if lists[0] == 0 or lists[1] == 0 or shape[0] == 0:
+        return
+    layers, layer = (shape[0], cs[0]) if len(cs) == 5 else (1, 0)
+    num_pages, Hkv, page_size, d = shape[-4:]
+    _launch(index, (_lib or library()).attn_paged_move,
+            _MOVE.pack(k_cache.data_ptr(), v_cache.data_ptr(), src_slots.data_ptr(), dst_slots.data_ptr(), layer, cs[-4], cs[-3], cs[-2], layers,
+                       lists[0], lists[1], Hkv, d, num_pages, page_size, code, handle))
 
 
 def attn_check(stream=None) -> int:

@@ -85,6 +85,10 @@ struct PagedParams {
   unsigned int* status;
   uint32_t timeout_us;  // longest barrier wait (microseconds)
   TileWork tile;
+  // attn_fwd_paged_tree: masks of the new rows, [total_q][tree_stride] words of which tree_words count, and positions
+  const uint32_t* tree;
+  const int* pos;
+  int tree_words, tree_stride;
 };
 
 // Query rows, keys and first query row of request b, whatever the arrays hold.
@@ -102,12 +106,24 @@ __device__ __forceinline__ int row_hi(const PagedParams& p, int i, int off, int 
   return p.er < 0 ? sk : (int)min((long long)sk, (long long)i + off + p.er + 1);
 }
 
+// A request with a mask among its new rows; a longer one is a chunk (kernels of attn_fwd_paged_tree; others: none).
+template <bool TREE>
+__device__ __forceinline__ bool has_mask(const PagedParams& p, int sq) { return TREE && sq <= 32 * p.tree_words; }
+// First key of the context that a masked request's query row t may see.
+__device__ __forceinline__ int masked_lo(const PagedParams& p, int t, int off) {
+  return p.wl < 0 ? 0 : (int)max(0ll, (long long)max(p.pos[t], off) - p.wl);
+}
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // Tokens and keys of Q tiles [t0, t1) of block blk: false where it has no token.
+template <bool TREE>
 __device__ __forceinline__ bool tile_keys(const PagedParams& p, int sq, int sk, int blk, int t0, int t1, int& lo, int& hi) {
   const int i0 = (blk * TILE_QT + t0) * p.tile.T, i1 = min((blk * TILE_QT + t1) * p.tile.T, sq) - 1;
   lo = hi = 0;
   if (i0 > i1) return false;
-  const int a = row_lo(p, i0, sk - sq), e = row_hi(p, i1, sk - sq, sk);
+  // (a mask may keep any new row, and its rows' positions begin at the context's end)
+  const bool masked = has_mask<TREE>(p, sq);
+  const int a = row_lo(p, masked ? 0 : i0, sk - sq), e = masked ? sk : row_hi(p, i1, sk - sq, sk);
   if (e > a) lo = a, hi = e;
   return true;
 }
@@ -154,6 +170,9 @@ int launch_dependent(void (*kern)(P), dim3 grid, unsigned int threads, size_t sm
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
+
+// What attn_fwd_paged and attn_fwd_paged_tree (tree not NULL) run.
+int paged_fwd_impl(const attn_fwd_paged_params_t& a, const attn_fwd_paged_tree_params_t* tree);
 
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 

@@ -157,7 +157,7 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {
 
 // `pre` is the CTA's shared memory: units before each request (B + 1 ints), then, where there is room, the
 // units twice, as numbered and as sorted.
-template <class C>
+template <class C, bool TREE>
 __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
   __shared__ int sum_s[PLAN_WARPS], rank_s[PLAN_WARPS][33];
   __shared__ long long sum64_s[PLAN_WARPS];
@@ -202,7 +202,7 @@ __device__ __forceinline__ void tile_plan(const RowsParams& p, int* pre) {
     x.blk = u - pre[lo];
     int row0, sq, sk, k0, k1;
     request_span(p, x.b, row0, sq, sk);
-    tile_keys(p, sq, sk, x.blk, 0, TILE_QT, k0, k1);
+    tile_keys<TREE>(p, sq, sk, x.blk, 0, TILE_QT, k0, k1);
     x.j0 = k0 / TILE_KEYS;
     x.w = max((k1 + TILE_KEYS - 1) / TILE_KEYS - x.j0, 1);
     x.cum = x.pad = 0;
@@ -331,14 +331,14 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D, int MT, bool BF16>
+template <int D, int MT, bool BF16, bool TREE>
 __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_SM) rows_kernel(const __grid_constant__ RowsParams p) {
   using C = Rows<D, MT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   grid_launch_dependents();
   grid_dependency_wait();
   if (p.tile.max_units > 0 && blockIdx.x == 0) {
-    tile_plan<C>(p, reinterpret_cast<int*>(smem));
+    tile_plan<C, TREE>(p, reinterpret_cast<int*>(smem));
     return;
   }
   __shared__ long long warp_sum[PLAN_WARPS];
@@ -443,6 +443,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
     };
     uint32_t qf[C::Q_SMEM ? 1 : MT][D / 16][4];
     int klo[MT][2], khi[MT][2];
+    uint32_t kept[MT][2];  // (TREE) the new rows that they keep: no more than 32 on this path
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -450,6 +451,11 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
         const int r = mt * 16 + fr + 8 * x, i = min(r, it.R - 1) / p.g;
         klo[mt][x] = row_lo(p, i, it.off);
         khi[mt][x] = row_hi(p, i, it.off, it.sk);
+        if constexpr (TREE) {
+          klo[mt][x] = masked_lo(p, it.row0 + i, it.off);
+          khi[mt][x] = it.off;
+          kept[mt][x] = p.tree[(long long)(it.row0 + i) * p.tree_stride] & low_bits(it.R / p.g);
+        }
         if constexpr (!C::Q_SMEM) {
           const uint16_t* src = q_row(r) + fc;
 #pragma unroll
@@ -467,7 +473,14 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
       __syncthreads();
     }
     // tiles whose every key is kept by every row need no mask
-    const int lo_all = row_lo(p, (it.R - 1) / p.g, it.off), hi_all = row_hi(p, 0, it.off, it.sk);
+    int lo_all = row_lo(p, (it.R - 1) / p.g, it.off), hi_all = row_hi(p, 0, it.off, it.sk);
+    if constexpr (TREE) {
+      lo_all = 0;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) lo_all = max(lo_all, max(klo[mt][0], klo[mt][1]));
+      lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+      hi_all = it.off;
+    }
 
     float o[MT][D / 8][4];
     float m[MT][2], l[MT][2];
@@ -530,7 +543,12 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = key0 + x * 8 + fc + (e & 1);
-              if (key < klo[mt][e >> 1] || key >= khi[mt][e >> 1]) sc[mt][x][e] = -INFINITY;
+              bool out = key < klo[mt][e >> 1] || key >= khi[mt][e >> 1];
+              if constexpr (TREE) {
+                const unsigned int node = key - it.off;
+                out = out && !(node < 32u && kept[mt][e >> 1] >> node & 1u);
+              }
+              if (out) sc[mt][x][e] = -INFINITY;
             }
         }
         // running maximum (exp2 domain): it moves only when it grows by more than 8, so the
@@ -909,27 +927,119 @@ int check(const attn_fwd_paged_params_t& a) {
   return ATTN_OK;
 }
 
-template <int D, int MT, bool BF16>
-int launch(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& plan, int sms, int dev, cudaStream_t st) {
+template <int D, int MT, bool BF16, bool TREE>
+int launch_rows(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& plan, int sms, int dev, cudaStream_t st) {
   using C = Rows<D, MT>;
   static std::atomic<unsigned long long> attr_set{0};  // bit per device
   const unsigned long long bit = 1ull << dev;
   if (!(attr_set.load() & bit)) {
-    if (cudaFuncSetAttribute(rows_kernel<D, MT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(rows_kernel<D, MT, BF16, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
       return ATTN_ERR_CUDA;
     attr_set.fetch_or(bit);
   }
   const bool tiles = p.tile.max_units > 0;
   TileParams tp = {};
   int rc = tiles ? tile_prepare(p, a, tp) : ATTN_OK;
-  if (rc == ATTN_OK && !p.tile.no_plan) rc = launch_dependent(rows_kernel<D, MT, BF16>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
+  if (rc == ATTN_OK && !p.tile.no_plan) rc = launch_dependent(rows_kernel<D, MT, BF16, TREE>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
   if (rc == ATTN_OK && tiles) rc = tile_launch(tp, a, sms, dev, st);
   if (rc != ATTN_OK) return rc;
   const int joins = p.tile.no_plan ? sms * JOINS_OF_RUN : plan.rows_grid;
   return launch_dependent(join_kernel<D, BF16>, dim3(joins), 32 * JOIN_WARPS, 0, st, p);
 }
 
+template <int D, int MT, bool BF16>
+int launch(const RowsParams& p, const attn_fwd_paged_params_t& a, const Plan& plan, int sms, int dev, cudaStream_t st) {
+  return p.tree ? launch_rows<D, MT, BF16, true>(p, a, plan, sms, dev, st) : launch_rows<D, MT, BF16, false>(p, a, plan, sms, dev, st);
+}
+
 }  // namespace
+
+int paged_fwd_impl(const attn_fwd_paged_params_t& a, const attn_fwd_paged_tree_params_t* tree) {
+  int rc = check(a);
+  if (rc != ATTN_OK) return rc;
+  if (tree) {
+    if (!tree->tree_mask || misaligned(tree->tree_mask, 4) || misaligned(tree->positions, 4) || tree->mask_words < 1 || tree->mask_words > (1 << 20) ||
+        tree->mask_stride < tree->mask_words || !a.causal || (a.window_left >= 0 && !tree->positions))
+      return ATTN_ERR_INVALID;
+  }
+  int sms = 0, dev = 0;
+  if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
+  const Plan plan(a, sms);
+  if (a.workspace && a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
+  RowsParams p = {};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.k = static_cast<const uint16_t*>(a.k_cache);
+  p.v = static_cast<const uint16_t*>(a.v_cache);
+  p.o = static_cast<uint16_t*>(a.o);
+  p.lse = a.lse;
+  p.table = a.block_table;
+  p.cu_q = a.cu_seqlens_q;
+  p.lens_k = a.seqlens_k;
+  p.q_row = a.q_row_stride;
+  p.q_head = a.q_head_stride;
+  p.o_row = a.o_row_stride;
+  p.o_head = a.o_head_stride;
+  p.c_page = a.cache_page_stride;
+  p.c_head = a.cache_head_stride;
+  p.c_row = a.cache_row_stride;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.g = a.Hq / a.Hkv;
+  p.total_q = a.total_q;
+  p.max_q = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.width = a.table_width;
+  p.table_stride = a.table_stride;
+  p.wl = a.window_left;
+  p.er = a.causal ? 0 : a.window_right;
+  p.scale_log2 = a.scale * LOG2E;
+  if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
+  void* scratch = a.workspace;
+  std::unique_lock<std::mutex> hold;  // until the launches are enqueued
+  if (!scratch) {
+    // a captured call would share the stream's workspace with whatever runs beside its replays
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) return ATTN_ERR_INVALID;
+    if ((rc = host_workspace(dev, a.stream, plan.bytes, hold, &scratch)) != ATTN_OK) return rc;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(scratch);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+  p.split = reinterpret_cast<Split*>(ws + plan.off_split);
+  p.timeout_us = host_timeout_us();
+  p.rows_grid = plan.rows_grid;
+  p.tile.T = plan.T;
+  p.tile.max_units = plan.max_units;
+  p.tile.sms = sms;
+  p.tile.no_plan = plan.max_units > 0 && p.max_q <= plan.T && a.B <= NO_PLAN_B && (long long)a.total_q * p.g > (long long)ROWS_MAX * a.B;
+  if (plan.max_units > 0) {
+    p.tile.queue = reinterpret_cast<TileQueue*>(ws + plan.off_queue);
+    p.tile.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);
+    p.tile.joins = reinterpret_cast<TileJoin*>(ws + plan.off_joins);
+    p.tile.part_ml = reinterpret_cast<float2*>(ws + plan.off_tile_ml);
+    p.tile.part_o = reinterpret_cast<float*>(ws + plan.off_tile_o);
+  }
+  p.slot_rows = plan.slot_rows;
+  if (tree) {
+    p.tree = tree->tree_mask;
+    p.pos = tree->positions;
+    p.tree_words = tree->mask_words;
+    p.tree_stride = tree->mask_stride;
+  }
+  const bool bf16 = a.dtype == ATTN_BF16;
+  const auto go = [&](auto launch) { return launch(p, a, plan, sms, dev, st); };
+  if (plan.slot_rows == 16) {
+    if (a.d == 64) return go(bf16 ? launch<64, 1, true> : launch<64, 1, false>);
+    return go(bf16 ? launch<128, 1, true> : launch<128, 1, false>);
+  }
+  if (a.d == 64) return go(bf16 ? launch<64, 2, true> : launch<64, 2, false>);
+  return go(bf16 ? launch<128, 2, true> : launch<128, 2, false>);
+}
+
 }  // namespace attn
 
 extern "C" {
@@ -948,83 +1058,7 @@ int attn_paged_workspace(const attn_fwd_paged_params_t* params, unsigned long lo
 }
 
 int attn_fwd_paged(const attn_fwd_paged_params_t* params) {
-  return attn::entry([&]() -> int {
-    using namespace attn;
-    if (!params) return ATTN_ERR_INVALID;
-    const attn_fwd_paged_params_t& a = *params;
-    int rc = check(a);
-    if (rc != ATTN_OK) return rc;
-    int sms = 0, dev = 0;
-    if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
-    const Plan plan(a, sms);
-    if (a.workspace && a.workspace_bytes < plan.bytes) return ATTN_ERR_INVALID;
-    RowsParams p = {};
-    p.q = static_cast<const uint16_t*>(a.q);
-    p.k = static_cast<const uint16_t*>(a.k_cache);
-    p.v = static_cast<const uint16_t*>(a.v_cache);
-    p.o = static_cast<uint16_t*>(a.o);
-    p.lse = a.lse;
-    p.table = a.block_table;
-    p.cu_q = a.cu_seqlens_q;
-    p.lens_k = a.seqlens_k;
-    p.q_row = a.q_row_stride;
-    p.q_head = a.q_head_stride;
-    p.o_row = a.o_row_stride;
-    p.o_head = a.o_head_stride;
-    p.c_page = a.cache_page_stride;
-    p.c_head = a.cache_head_stride;
-    p.c_row = a.cache_row_stride;
-    p.B = a.B;
-    p.Hq = a.Hq;
-    p.Hkv = a.Hkv;
-    p.g = a.Hq / a.Hkv;
-    p.total_q = a.total_q;
-    p.max_q = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
-    p.num_pages = a.num_pages;
-    p.page_size = a.page_size;
-    p.width = a.table_width;
-    p.table_stride = a.table_stride;
-    p.wl = a.window_left;
-    p.er = a.causal ? 0 : a.window_right;
-    p.scale_log2 = a.scale * LOG2E;
-    if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
-    void* scratch = a.workspace;
-    std::unique_lock<std::mutex> hold;  // until the launches are enqueued
-    if (!scratch) {
-      // a captured call would share the stream's workspace with whatever runs beside its replays
-      cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-      if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return ATTN_ERR_CUDA;
-      if (capture != cudaStreamCaptureStatusNone) return ATTN_ERR_INVALID;
-      if ((rc = host_workspace(dev, a.stream, plan.bytes, hold, &scratch)) != ATTN_OK) return rc;
-    }
-    uint8_t* ws = static_cast<uint8_t*>(scratch);
-    p.part_o = reinterpret_cast<float*>(ws);
-    p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
-    p.split = reinterpret_cast<Split*>(ws + plan.off_split);
-    p.timeout_us = host_timeout_us();
-    p.rows_grid = plan.rows_grid;
-    p.tile.T = plan.T;
-    p.tile.max_units = plan.max_units;
-    p.tile.sms = sms;
-    p.tile.no_plan = plan.max_units > 0 && p.max_q <= plan.T && a.B <= NO_PLAN_B && (long long)a.total_q * p.g > (long long)ROWS_MAX * a.B;
-    if (plan.max_units > 0) {
-      p.tile.queue = reinterpret_cast<TileQueue*>(ws + plan.off_queue);
-      p.tile.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);
-      p.tile.joins = reinterpret_cast<TileJoin*>(ws + plan.off_joins);
-      p.tile.part_ml = reinterpret_cast<float2*>(ws + plan.off_tile_ml);
-      p.tile.part_o = reinterpret_cast<float*>(ws + plan.off_tile_o);
-    }
-    p.slot_rows = plan.slot_rows;
-    const bool bf16 = a.dtype == ATTN_BF16;
-    const auto go = [&](auto launch) { return launch(p, a, plan, sms, dev, st); };
-    if (plan.slot_rows == 16) {
-      if (a.d == 64) return go(bf16 ? launch<64, 1, true> : launch<64, 1, false>);
-      return go(bf16 ? launch<128, 1, true> : launch<128, 1, false>);
-    }
-    if (a.d == 64) return go(bf16 ? launch<64, 2, true> : launch<64, 2, false>);
-    return go(bf16 ? launch<128, 2, true> : launch<128, 2, false>);
-  });
+  return attn::entry([&]() -> int { return params ? attn::paged_fwd_impl(*params, nullptr) : ATTN_ERR_INVALID; });
 }
 
 }  // extern "C"

@@ -103,10 +103,11 @@ struct RunStart {
   int b, h, runs;
   long long in, line, pos, left;  // (pos: the run's first step, left: its steps)
 };
+template <bool TREE>
 __device__ __forceinline__ bool request_unit(const TileParams& p, int b, TileUnit& x) {
   int k0, k1;
   request_span(p, b, x.row0, x.sq, x.sk);
-  tile_keys(p, x.sq, x.sk, 0, 0, TILE_QT, k0, k1);
+  tile_keys<TREE>(p, x.sq, x.sk, 0, 0, TILE_QT, k0, k1);
   x.b = b;
   x.blk = 0;
   x.j0 = k0 / TILE_KEYS;
@@ -114,12 +115,13 @@ __device__ __forceinline__ bool request_unit(const TileParams& p, int b, TileUni
   return x.sq > 0;
 }
 // By a warp; false where there are fewer runs.
+template <bool TREE>
 __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane, RunStart& r) {
   const int per = (p.B + 31) / 32, b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B);
   TileUnit x;
   long long own = 0;
   for (int b = b0; b < b1; ++b)
-    if (request_unit(p, b, x)) own += x.w + UNIT_COST;
+    if (request_unit<TREE>(p, b, x)) own += x.w + UNIT_COST;
   own *= p.Hkv;
   long long incl = own;
 #pragma unroll
@@ -138,7 +140,7 @@ __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane
   if (mine) {
     long long at = incl - own;
     for (int b = b0; b < b1; ++b) {
-      if (!request_unit(p, b, x)) continue;
+      if (!request_unit<TREE>(p, b, x)) continue;
       const int steps = x.w + UNIT_COST;
       if (r.pos < at + (long long)steps * p.Hkv) {
         r.b = b;
@@ -159,14 +161,15 @@ __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane
 // ------------------------------------------------------------------ join list
 // One warp of each CTA lists the cut pairs for join_kernel while the others work (the plan, which all wait
 // for, was 2.5 - 4 us longer with it).  Each pair is found by the run that takes its second piece.
+template <bool TREE>
 __device__ __forceinline__ void run_join_list(const TileParams& p, int lane) {  // (without a plan)
   const int r = blockIdx.x;
   TileJoin* list = p.tile.joins + r * JOINS_OF_RUN;
   RunStart rs;
   TileJoin jn = {};
-  if (run_start(p, r, lane, rs)) {
+  if (run_start<TREE>(p, r, lane, rs)) {
     TileUnit un;
-    request_unit(p, rs.b, un);
+    request_unit<TREE>(p, rs.b, un);
     const long long at = rs.pos - rs.in;  // where the pair begins
     const int first = run_of(rs.line, rs.runs, at + UNIT_COST), last = run_of(rs.line, rs.runs, at + un.w + UNIT_COST - 1);
     if (r == first + 1 && r <= last)
@@ -204,7 +207,7 @@ __device__ __forceinline__ void tile_join_list(const TileParams& p, int lane) {
 }
 
 // ------------------------------------------------------------------ load warp
-template <int D, bool TURNS>
+template <int D, bool TURNS, bool TREE>
 __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t base, uint8_t* gbase, volatile int* abort_flag, int lane) {
   using L = TileLayout<D>;
   const uint32_t to = p.timeout_us;
@@ -245,13 +248,13 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
           h = 0;
           ++s;
           if (no_plan)
-            while (s < p.B && !request_unit(p, s, pt)) ++s;
+            while (s < p.B && !request_unit<TREE>(p, s, pt)) ++s;
         }
         if (!no_plan) pt = p.tile.units[s];
       } else {
         const unsigned int x = x_next;
         RunStart rs;
-        const bool more = no_plan ? !begun && run_start(p, blockIdx.x, lane, rs) : x < entries;
+        const bool more = no_plan ? !begun && run_start<TREE>(p, blockIdx.x, lane, rs) : x < entries;
         if (!more) {
           if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
           if (lane == 0) {
@@ -268,7 +271,7 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
           h = rs.h;
           in = rs.in;
           left = rs.left;
-          request_unit(p, s, pt);
+          request_unit<TREE>(p, s, pt);
           begun = true;
         } else {
           pt = u_next;
@@ -302,13 +305,13 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
     const int j0 = pt.j0 + from, j1 = j0 + tiles;
     const int row0 = pt.row0, sq = pt.sq, sk = pt.sk;
     int lo, hi;
-    tile_keys(p, sq, sk, pt.blk, 0, QT, lo, hi);
+    tile_keys<TREE>(p, sq, sk, pt.blk, 0, QT, lo, hi);
     int jlo[QT], jhi[QT];  // key tiles of each Q tile, [jlo, jhi)
     bool rows1 = false;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       int a, e;
-      const bool any = tile_keys(p, sq, sk, pt.blk, t, t + 1, a, e);
+      const bool any = tile_keys<TREE>(p, sq, sk, pt.blk, t, t + 1, a, e);
       if (t == 1) rows1 = any;
       jlo[t] = a / BN;
       jhi[t] = (e + BN - 1) / BN;
@@ -422,7 +425,27 @@ struct TileEnv {
 };
 
 // ------------------------------------------------------------------ softmax warpgroup t
-template <int D, bool BF16, bool TURNS>
+// Which of a key tile's columns a row keeps, 32 to a word: those of the range [lo, hi), and, where `mask` is not NULL,
+// those of new rows (the first at column `first`, n of them) whose bit it has.
+struct KeptBits {
+  uint32_t w[BN / 32];
+  __device__ __forceinline__ KeptBits(int lo, int hi, const uint32_t* mask, int words, int first, int n) {
+#pragma unroll
+    for (int x = 0; x < BN / 32; ++x) w[x] = low_bits(hi - 32 * x) & ~low_bits(lo - 32 * x);
+    if (mask == nullptr || first >= BN) return;
+    const int at = -first >> 5, sh = -first & 31;  // column 0 is bit sh of word `at` (below 0: before the first)
+    uint32_t m[BN / 32 + 1];
+#pragma unroll
+    for (int x = 0; x <= BN / 32; ++x) {
+      const int i = at + x;
+      m[x] = i >= 0 && i < words ? mask[i] & low_bits(n - 32 * i) : 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < BN / 32; ++x) w[x] |= __funnelshift_r(m[x], m[x + 1], sh);
+  }
+};
+
+template <int D, bool BF16, bool TURNS, bool TREE>
 __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t base, uint8_t* gbase, volatile int* abort_flag, uint32_t tmem,
                                                   int t, int quarter, int lane) {
   using L = TileLayout<D>;
@@ -455,10 +478,19 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
     }
     const auto first_token = [&](int e) { return (hdr[e].blk * QT + (TURNS ? 0 : t)) * p.tile.T; };
     int klo, khi;
+    const uint32_t* mask = nullptr;  // the row's, of the request's nodes, which begin at key mask_at
+    int mask_at = 0, nodes = 0;
     {
       const int sq = hdr[ie].sq, sk = hdr[ie].sk, i = min(first_token(ie) + token_of(min(r, p.tile.T * p.g - 1)), sq - 1);
       klo = row_lo(p, i, sk - sq);
       khi = row_hi(p, i, sk - sq, sk);
+      if (has_mask<TREE>(p, sq)) {
+        const int at = hdr[ie].row0 + i;
+        mask = p.tree + (long long)at * p.tree_stride;
+        mask_at = khi = sk - sq;
+        nodes = sq;
+        klo = masked_lo(p, at, sk - sq);
+      }
     }
     int row0 = 0, sq = 0, h = 0, slot_out = 0, tok0 = 0;  // the unit's place, read at its end
     float m = -INFINITY, l = 0.f;
@@ -496,7 +528,17 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       const auto make_mask = [&] {
         const int hi = khi - j * BN, lo = klo - j * BN;
         const bool edge = __any_sync(0xffffffffu, hi < BN || lo > 0);
-        return [=](uint32_t(&x)[64], int c0) {
+        if constexpr (TREE) {
+          KeptBits kept(0, BN, nullptr, 0, 0, 0);
+          if (edge) kept = KeptBits(lo, hi, mask, p.tree_words, mask_at - j * BN, nodes);
+          return [=](uint32_t(&x)[64], int c0) {
+            if (edge) {
+#pragma unroll
+              for (int cc = 0; cc < 64; ++cc)
+                if (!(kept.w[(c0 + cc) / 32] >> (cc % 32) & 1u)) x[cc] = __float_as_uint(-INFINITY);
+            }
+          };
+        } else return [=](uint32_t(&x)[64], int c0) {
           if (edge) {
 #pragma unroll
             for (int cc = 0; cc < 64; ++cc)
@@ -656,7 +698,7 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int D, bool BF16, bool TURNS>
+template <int D, bool BF16, bool TURNS, bool TREE>
 __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_constant__ TileParams p) {
   using L = TileLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -693,17 +735,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
   if (warp < 4) {
     setmaxnreg_dec<L::REGS_LOADMMA>();
     if (warp == 0) {
-      tile_load_role<D, TURNS>(p, base, gbase, abort_flag, lane);
+      tile_load_role<D, TURNS, TREE>(p, base, gbase, abort_flag, lane);
     } else if (warp == 1) {
       TileEnv<D, TURNS> env;
       mma_role<D, BF16, L>(env, p.timeout_us, base, gbase, abort_flag, tmem, lane);
     } else if (warp == 2) {
-      if (TURNS && p.tile.no_plan) run_join_list(p, lane);
+      if (TURNS && p.tile.no_plan) run_join_list<TREE>(p, lane);
       else tile_join_list(p, lane);
     }
   } else {
     setmaxnreg_inc<L::REGS_SOFTMAX>();
-    tile_softmax_role<D, BF16, TURNS>(p, base, gbase, abort_flag, tmem, (warp - 4) >> 2, warp & 3, lane);
+    tile_softmax_role<D, BF16, TURNS, TREE>(p, base, gbase, abort_flag, tmem, (warp - 4) >> 2, warp & 3, lane);
   }
 
   tc_fence_before();
@@ -715,10 +757,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ host side
-template <int D, bool BF16, bool TURNS>
+template <int D, bool BF16, bool TURNS, bool TREE>
 int launch_tiles(const TileParams& p, int sms, int dev, cudaStream_t st) {
   using L = TileLayout<D>;
-  auto kern = paged_tile_kernel<D, BF16, TURNS>;
+  auto kern = paged_tile_kernel<D, BF16, TURNS, TREE>;
   static std::atomic<unsigned long long> attr_set{0};  // bit per device
   const unsigned long long bit = 1ull << dev;
   if (!(attr_set.load() & bit)) {
@@ -759,7 +801,8 @@ int tile_prepare(const PagedParams& base, const attn_fwd_paged_params_t& a, Tile
   return ATTN_OK;
 }
 
-int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
+template <bool TREE>
+int launch_any(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
   const bool bf16 = a.dtype == ATTN_BF16;
   // Where no request has more rows than one Q tile, both Q tiles take the same rows and the key tiles by turns,
   // so that one's products run while the other's softmax does.  24 requests of 3 - 6 tokens x 8 heads
@@ -767,11 +810,15 @@ int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, 
   const bool turns = p.max_q <= p.tile.T;
   const auto go = [&](auto launch) { return launch(p, sms, dev, st); };
   if (a.d == 64) {
-    if (turns) return go(bf16 ? launch_tiles<64, true, true> : launch_tiles<64, false, true>);
-    return go(bf16 ? launch_tiles<64, true, false> : launch_tiles<64, false, false>);
+    if (turns) return go(bf16 ? launch_tiles<64, true, true, TREE> : launch_tiles<64, false, true, TREE>);
+    return go(bf16 ? launch_tiles<64, true, false, TREE> : launch_tiles<64, false, false, TREE>);
   }
-  if (turns) return go(bf16 ? launch_tiles<128, true, true> : launch_tiles<128, false, true>);
-  return go(bf16 ? launch_tiles<128, true, false> : launch_tiles<128, false, false>);
+  if (turns) return go(bf16 ? launch_tiles<128, true, true, TREE> : launch_tiles<128, false, true, TREE>);
+  return go(bf16 ? launch_tiles<128, true, false, TREE> : launch_tiles<128, false, false, TREE>);
+}
+
+int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
+  return p.tree ? launch_any<true>(p, a, sms, dev, st) : launch_any<false>(p, a, sms, dev, st);
 }
 
 }  // namespace attn

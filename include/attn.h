@@ -98,7 +98,7 @@ typedef enum {
     ATTN_ERR_CUDA = -3,        /* a CUDA runtime/driver call failed (launch, tensor map, memory) */
     ATTN_ERR_TIMEOUT = -4,     /* a kernel barrier wait ran out of time; outputs undefined */
     ATTN_ERR_DEVICE = -5,      /* no usable sm_103 device */
-    ATTN_ERR_PAGE = -6         /* a kernel met a page id, slot or page count out of range */
+    ATTN_ERR_PAGE = -6         /* a kernel met a page id, slot, page count or parent out of range */
 } attn_status_t;
 
 /*
@@ -349,6 +349,146 @@ int attn_fwd_paged(const attn_fwd_paged_params_t *params);
  * on the current device.  It goes by B, Hq, Hkv, d, total_q and max_seqlen_q alone and reads no pointer.
  */
 int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long long *bytes);
+
+/*
+ * ---------------------------------------------------------------- drafted trees, norms and rotation
+ *
+ * A step that checks several continuations of every request at once.  A request's new rows are the nodes of
+ * a tree: the last token that is known (node 0; or the last few, a chain) and drafted tokens below it, each with the
+ * number of its parent among the request's nodes, below its own.  A step then runs attn_paged_tables (nodes
+ * as new tokens), attn_paged_tree (positions, masks), per layer attn_rope (queries, keys and values from the
+ * projections into a buffer and into the cache) and attn_fwd_paged_tree, and, once the model's choice behind every node is
+ * known, attn_paged_accept and attn_paged_move.  Requests of more nodes than the masks have bits are chunks of a
+ * prompt: chains that need no mask, in the same calls.  What holds for the paged cache above (layout, index arrays,
+ * bad values, ATTN_ERR_PAGE, replays) holds here.
+ */
+
+/*
+ * attn_rope -- norms of queries and keys for each head and their rotation by position, in one pass over rows of
+ * q [Hq], k [Hkv] and v [Hkv] heads (element (h, t, x) at h*head + t*row + x of their own strides):
+ *     y = x * rsqrt(mean(x^2) + eps) * weight      (over the d elements of a head's row; y = x where the weight is NULL)
+ *     phi_i = sum over axes a of positions[a][t] * inv_freq[a][i],  0 <= i < rot_dim / 2
+ *     (y_a, y_b) -> (y_a cos phi_i - y_b sin phi_i, y_b cos phi_i + y_a sin phi_i)
+ * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved is not 0; elements from rot_dim on are not turned.
+ * One axis is the usual rotation; with several (time, height, width) each pair's frequency stands in its axis's row and
+ * the other rows hold 0 there.  All in 32 bits, rounded once; angles are exact to 2^-21 of a turn at any position (with frequencies
+ * of at most 1; positions may be negative).
+ * Where slots is NULL, rows go to q_out and k_out (each may be its input with the same strides; nothing else overlaps), and
+ * v and the caches are not looked at.  Otherwise q goes to q_out, k and, unturned, v go to slot slots[t] of the caches, and a row
+ * of a negative slot is left out, of q_out as well; so is one of a slot at or past num_pages*page_size, with ATTN_ERR_PAGE.
+ * Slots are distinct.  A contiguous [B][H][S][d] tensor whose entries share their positions counts as B*H heads of S rows.
+ * q_weight, k_weight: [d], of the rows' type, or float where weight_f32 is not 0.  positions: int32, axis a at
+ * positions + a*position_stride; inv_freq: float [axes][rot_dim/2].  With rot_dim = 0 both may be NULL.
+ * rot_dim is a multiple of 16, at most d; 1 <= axes <= 4; eps >= 0; rows <= 2^30; at most 65536 heads.
+ */
+typedef struct {
+    const void *q, *k, *v;
+    void *q_out, *k_out, *k_cache, *v_cache;
+    const void *q_weight, *k_weight;
+    const int *positions, *slots;
+    const float *inv_freq;
+    long long q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+    long long q_out_row_stride, q_out_head_stride, k_out_row_stride, k_out_head_stride;
+    long long cache_page_stride, cache_head_stride, cache_row_stride;
+    long long position_stride;
+    int rows, Hq, Hkv, d, rot_dim, axes, interleaved, weight_f32, num_pages, page_size;
+    float eps;
+    int dtype;
+    void *stream;
+} attn_rope_params_t;
+
+int attn_rope(const attn_rope_params_t *params);
+
+/*
+ * attn_paged_tree -- positions and masks of the nodes.  Request b's nodes are rows cu_seqlens_q[b] ..
+ * cu_seqlens_q[b+1]-1, its context the seqlens_k[b] tokens less these.  Node i's position is context + depth, and bit j of its
+ * mask (word j / 32 of tree_mask + t*mask_stride, least significant bit first) is 1 for itself and the nodes above it, with
+ * window_left >= 0 those at most window_left positions back.  parents[t]: number of the node above among the request's
+ * nodes, -1 for none; one that is not below the node's own number counts as none, with ATTN_ERR_PAGE.  Requests of
+ * more than 32*mask_words nodes are chunks: positions context + i, parents not read, masks not written.  Rows of no
+ * request are left as they are.  1 <= B <= 16384, 1 <= mask_words <= 32, rows <= 2^30.
+ */
+typedef struct {
+    const int *parents;                  /* [rows] */
+    const int *cu_seqlens_q, *seqlens_k; /* [B+1], [B] */
+    int *positions;                      /* [rows] */
+    uint32_t *tree_mask;                 /* [rows][mask_words] */
+    int B, rows, mask_words, mask_stride, window_left;
+    void *stream;
+} attn_paged_tree_params_t;
+
+int attn_paged_tree(const attn_paged_tree_params_t *params);
+
+/*
+ * attn_fwd_paged_tree -- attn_fwd_paged with a mask among each request's new rows.  Row t of a request of sq <= 32*mask_words query
+ * rows and sk keys keeps key j
+ *     of the context, j < sk - sq:  where window_left < 0 or j >= positions[t] - window_left,
+ *     of the new rows, j >= sk - sq:  where bit j - (sk - sq) of its mask is 1, whatever the window
+ * (positions below the context's length count as that; positions may be NULL without a window; bits at or past sq are of no
+ * account).  Any mask will do, not a tree's alone.  Requests of more rows are chunks, causal with the window, as in
+ * attn_fwd_paged.  call.causal is 1 and call.window_right has no effect; all else of `call` is as for attn_fwd_paged, its workspace
+ * too (attn_paged_workspace(&call)).  Cache rows of a request from the first context key that a window of its first position
+ * leaves on, up to its last key, hold finite values, whether a mask keeps them or not.
+ */
+typedef struct {
+    attn_fwd_paged_params_t call;
+    const uint32_t *tree_mask; /* [total_q][mask_words], row t at tree_mask + t*mask_stride */
+    const int *positions;      /* [total_q] or NULL */
+    int mask_words, mask_stride;
+} attn_fwd_paged_tree_params_t;
+
+int attn_fwd_paged_tree(const attn_fwd_paged_tree_params_t *params);
+
+/*
+ * attn_paged_accept -- which nodes of every request the model confirms.  The first confirmed[b] nodes (1 at least; NULL: 1 for
+ * every request) are known, a chain; a prompt's chunk has all of its rows confirmed.  From the last of them a walk goes to the
+ * first child (the lowest number above the node's own whose parent it is) whose token is the model's choice behind the node, targets[node],
+ * and on from there, max_path drafted nodes at most.  Writes, for every request,
+ *   accepted[b]:     tokens it keeps of this step, confirmed and drafted (0 without rows);
+ *   ctx_lens[b]:     its tokens in the cache from now on, seqlens_k - nodes + accepted (what attn_paged_tables takes next);
+ *   next_tokens[b]:  the model's choice behind the last node (-1 without rows): the next step's node 0;
+ *   path[b][j]:      the j-th drafted node on the walk, -1 behind the last;
+ *   src_slots[b][j], dst_slots[b][j]: where that node's row lies in the cache and where a chain would have it, both -1 where
+ *                    these are the same place, or (with ATTN_ERR_PAGE) where the table names no such page: attn_paged_move's lists.
+ * Pages from ceil(ctx_lens[b] / page_size) on, which hold no token any longer, go back: behind the *free_count ids of the free list, requests and
+ * pages in ascending order, *free_count_out (which may be free_count itself) is their number then.  Ids out of range or behind the table's end are
+ * left out, and so is what the list (max_free ids) has no room for, each with ATTN_ERR_PAGE.  The table keeps its entries, which
+ * attn_paged_tables overwrites.  With free_pages NULL (max_free = 0, free_count and free_count_out not looked at) no page goes back.
+ * No output overlaps an input but for that.  1 <= B <= 16384, 1 <= max_path <= 1024, rows <= 2^30; with rows = 0 (no request has
+ * any) tokens, targets and parents may be NULL.
+ */
+typedef struct {
+    const int *tokens, *targets, *parents; /* [rows] */
+    const int *confirmed;                  /* [B] or NULL */
+    const int *cu_seqlens_q, *seqlens_k;   /* [B+1], [B] */
+    const int *block_table;
+    int *free_pages;           /* [max_free] in / out, or NULL */
+    const int *free_count;     /* [1] */
+    int *free_count_out;       /* [1] */
+    int *accepted, *ctx_lens, *next_tokens;  /* [B] */
+    int *path, *src_slots, *dst_slots;       /* [B][max_path] */
+    int B, rows, max_path, table_width, table_stride, max_free, page_size, num_pages;
+    void *stream;
+} attn_paged_accept_params_t;
+
+int attn_paged_accept(const attn_paged_accept_params_t *params);
+
+/*
+ * attn_paged_move -- rows of the caches of `layers` layers (element offset cache_layer_stride from one to the next) go from slot
+ * src_slots[list][i] to slot dst_slots[list][i], K and V.  A pair with a negative slot is left out; one with a slot at or past
+ * num_pages*page_size too, with ATTN_ERR_PAGE.  Within a list no source is the destination of an earlier pair (it may be that of
+ * a later one: it is read before), and destinations are distinct; different lists share no slot that either writes.
+ * What attn_paged_accept writes is so, where no two requests share pages that they write.  layers, Hkv <= 65536, lists and length <= 2^20.
+ */
+typedef struct {
+    void *k_cache, *v_cache;
+    const int *src_slots, *dst_slots; /* [lists][length] */
+    long long cache_layer_stride, cache_page_stride, cache_head_stride, cache_row_stride;
+    int layers, lists, length, Hkv, d, num_pages, page_size, dtype;
+    void *stream;
+} attn_paged_move_params_t;
+
+int attn_paged_move(const attn_paged_move_params_t *params);
 
 /*
  * attn_check -- read (and clear) the status word of `stream` on the current
