@@ -8,9 +8,8 @@
 //     (y_a, y_b) -> (y_a cos phi_i - y_b sin phi_i, y_b cos phi_i + y_a sin phi_i)
 //
 // for pairs i < rot / 2, (a, b) = (i, i + rot / 2) or (2 i, 2 i + 1); elements from rot on are not turned.  All in 32 bits,
-// rounded once at the end.  An angle is a part of a turn: f / 2 pi is held in 64 bits of fixed point (f in 64 bits of
-// floating point before), whose product with an integer position wraps at whole turns by itself and so keeps its
-// accuracy at any position; its top 32 bits, as a float, go to sincospi.
+// rounded once at the end.  An angle is a part of a turn: f / 2 pi is held in 64 bits of fixed point, whose product with an integer position wraps at
+// whole turns by itself and so keeps its accuracy at any position; its top 32 bits, as a float, go to sincospi.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,12 +26,13 @@
 namespace attn {
 namespace {
 
-constexpr int ROPE_WARPS = 8, ROPE_THREADS = 32 * ROPE_WARPS, ROPE_TOKENS = 8, ROPE_AXES = 4;
+constexpr int ROPE_WARPS = 8, ROPE_THREADS = 32 * ROPE_WARPS, ROPE_CTAS = 2, ROPE_AXES = 4;
 
 struct RopeParams {
   attn_rope_params_t a;
   unsigned int* status;
   int q_items, k_items, v_items;  // items of a token
+  int parts;                      // parts of a token
 };
 
 template <bool BF16>
@@ -57,147 +57,210 @@ __device__ __forceinline__ float weight_at(const void* w, bool f32, int i) {
   return widen2<BF16>(x).x;
 }
 
-// f / 2 pi in parts of a turn of 2^-64 (whole turns left out).
+// f / 2 pi in parts of a turn of 2^-64 (whole turns left out), in whole numbers: 64-bit floating point is slow on this machine
+// (six such operations for every pair and axis took a CTA of 256 threads more than 2000 cycles).  f = m 2^e with 24 bits of m, times the
+// first 128 bits of 1 / 2 pi.
 __device__ __forceinline__ unsigned long long turn_of(float f) {
-  double t = (double)f * 0.15915494309189533577;
-  t -= rint(t);
-  return (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+  constexpr unsigned long long HI = 0x28BE60DB9391054Aull, LO = 0x7F09D5F47D4D3770ull;
+  const uint32_t x = __float_as_uint(f), exponent = x >> 23 & 255u;
+  const unsigned long long m = exponent ? (x & 0x7FFFFFu) | 0x800000u : x & 0x7FFFFFu;
+  const int shift = 64 + 150 - (int)max(exponent, 1u);  // the product's bits from here on count
+  const unsigned long long p0 = m * LO, mid = m * HI, p1 = __umul64hi(m, LO) + mid, p2 = __umul64hi(m, HI) + (p1 < mid);
+  unsigned long long t = 0;
+  if (shift >= 128) t = shift < 192 ? p2 >> (shift - 128) : 0;
+  else if (shift >= 64) t = shift == 64 ? p1 : p1 >> (shift - 64) | p2 << (128 - shift);
+  else if (shift > 0) t = p0 >> shift | p1 << (64 - shift);
+  return x >> 31 ? 0ull - t : t;
 }
 
-// A CTA takes TOKENS tokens.  First its threads work out, for every token and pair, the four products of weight and
-// cosine or sine that turn a row (for q and for k), which all heads share, in shared memory.  Then its warps take
-// items of VECS heads of a token: D / 16 lanes to a row, eight pairs to a lane, all of an item's loads in flight at
-// once; the values' items are plain copies.
-template <int D, bool BF16, bool ADJACENT, int TOKENS>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeParams p) {
+// The frequencies' parts of a turn and the weights are worked out once a CTA.  Then warps take (token, part) pairs, a part
+// being the whole token or, where there are few, some of its items: VECS heads of q, k or v.  A row is D / 16 lanes, eight pairs to a
+// lane.  The loads run an item ahead of the rest, on into the next token, whose positions and slot have been read a token ahead: a warp
+// always has loads in flight.  At a token's first item a warp works out the four products of weight and cosine or sine
+// that turn its pairs (two pairs to a lane) and leaves them in shared memory of its own, so no warp waits for another; a lane keeps its
+// pairs' products for all heads of q, then of k.  The values' items are plain copies.
+template <int D, bool BF16, bool ADJACENT>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __grid_constant__ RopeParams p) {
   const attn_rope_params_t& a = p.a;
   constexpr int LANES = D / 16, ROWS = 32 / LANES, UNROLL = 2, VECS = ROWS * UNROLL, PAIRS = D / 2;
-  __shared__ __align__(16) float coef[TOKENS][2][4][PAIRS];  // [q, k][w_a cos, w_b sin, w_b cos, w_a sin]
-  __shared__ long long dst_s[TOKENS];                        // where the token's row of the cache begins, -1: left out
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ unsigned long long turn[ROPE_AXES][PAIRS];
+  __shared__ float weight[4][PAIRS];                              // of q: first and second of the pair; of k
+  __shared__ __align__(16) float coef[ROPE_WARPS][2][4][PAIRS];   // [q, k][w_a cos, w_b sin, w_b cos, w_a sin], lanes' first fours ahead of their second ones
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = a.rot_dim / 2;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int t0 = blockIdx.x * TOKENS, tokens = min(TOKENS, a.rows - t0);
-
-  // ---- what the heads of a token share
-  if (tid < tokens) {
-    long long at = 0;
-    if (a.slots) {
-      const int slot = load_cg(a.slots + t0 + tid), page = slot / a.page_size;
-      at = -1;
-      if (slot >= 0 && page < a.num_pages)
-        at = (long long)page * a.cache_page_stride + (long long)(slot - page * a.page_size) * a.cache_row_stride;
-      else if (slot >= 0)
-        atomicOr(p.status, STATUS_PAGE);
-    }
-    dst_s[tid] = at;
-  }
-  {
-    const int pair = tid % PAIRS, half = a.rot_dim / 2;
-    const bool turns = pair < half;
-    // elements of the pair (those that are not turned: chunks of eight, paired off)
-    int ea, eb;
-    if (ADJACENT) ea = 2 * pair, eb = ea + 1;
-    else if (turns) ea = pair, eb = pair + half;
-    else ea = a.rot_dim + (pair - half) / 8 * 16 + pair % 8, eb = ea + 8;
-    float wa[2] = {1.f, 1.f}, wb[2] = {1.f, 1.f};
-    if (a.q_weight) {
-      wa[0] = weight_at<BF16>(a.q_weight, a.weight_f32, ea);
-      wb[0] = weight_at<BF16>(a.q_weight, a.weight_f32, eb);
-    }
-    if (a.k_weight) {
-      wa[1] = weight_at<BF16>(a.k_weight, a.weight_f32, ea);
-      wb[1] = weight_at<BF16>(a.k_weight, a.weight_f32, eb);
-    }
-    unsigned long long turn[ROPE_AXES] = {};
-#pragma unroll
-    for (int x = 0; x < ROPE_AXES; ++x)
-      if (turns && x < a.axes) turn[x] = turn_of(a.inv_freq[x * half + pair]);
-    for (int t = tid / PAIRS; t < tokens; t += ROPE_THREADS / PAIRS) {
-      float s = 0.f, c = 1.f;
-      if (turns) {
-        unsigned long long phi = 0;
-#pragma unroll
-        for (int x = 0; x < ROPE_AXES; ++x)
-          if (x < a.axes) phi += turn[x] * (unsigned long long)(long long)load_cg(a.positions + (long long)x * a.position_stride + t0 + t);
-        sincospif((float)(int)(phi >> 32) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        coef[t][k][0][pair] = wa[k] * c;
-        coef[t][k][1][pair] = wb[k] * s;
-        coef[t][k][2][pair] = wb[k] * c;
-        coef[t][k][3][pair] = wa[k] * s;
-      }
-    }
-  }
-  __syncthreads();
-
-  // ---- the rows
   const int sub = lane / LANES, l = lane % LANES;
   // the lane's two chunks of eight elements
-  const int half = a.rot_dim / 2;
   int ca, cb;
   if (ADJACENT || l * 8 >= half) ca = ADJACENT ? l * 16 : a.rot_dim + (l * 8 - half) * 2, cb = ca + 8;
   else ca = l * 8, cb = ca + half;
-  const int per = p.q_items + p.k_items + p.v_items;
-  for (int item = warp; item < tokens * per; item += ROPE_WARPS) {
-    const int t = item / per, i = item - t * per;
-    const long long at = dst_s[t];
-    if (at < 0) continue;
-    const int kind = i < p.q_items ? 0 : i < p.q_items + p.k_items ? 1 : 2;
-    const int h0 = (kind == 0 ? i : kind == 1 ? i - p.q_items : i - p.q_items - p.k_items) * VECS + sub;
-    const int heads = kind == 0 ? a.Hq : a.Hkv;
-    const long long row = t0 + t;
-    const uint16_t* src = kind == 0   ? static_cast<const uint16_t*>(a.q) + row * a.q_row_stride
-                          : kind == 1 ? static_cast<const uint16_t*>(a.k) + row * a.k_row_stride
-                                      : static_cast<const uint16_t*>(a.v) + row * a.v_row_stride;
-    const long long src_head = kind == 0 ? a.q_head_stride : kind == 1 ? a.k_head_stride : a.v_head_stride;
+  const int qk_items = p.q_items + p.k_items, items = qk_items + p.v_items;
+  float(&mine)[2][4][PAIRS] = coef[warp];
+  // (at most 2^30 tokens, in parts only while they are fewer than the machine's warps)
+  const unsigned int units = (unsigned int)a.rows * p.parts, step = gridDim.x * ROPE_WARPS;
+
+  // a token's positions (lane x: of axis x) and slot (lane ROPE_AXES)
+  const auto read_token = [&](unsigned int unit) {
+    int x = 0;
+    if (unit < units) {
+      const unsigned int t = p.parts == 1 ? unit : unit / p.parts;
+      if (lane < a.axes && half > 0) x = load_cg(a.positions + lane * a.position_stride + t);
+      else if (lane == ROPE_AXES && a.slots) x = load_cg(a.slots + t);
+    }
+    return x;
+  };
+  struct Item {
+    int t, i, token;
+    long long at;  // where the token's row of the cache begins
+  };
+  unsigned int unit = blockIdx.x * ROPE_WARPS + warp;
+  int token_next = read_token(unit);
+  Item next{0, 0, 0, 0};
+  int last = 0;
+  // the first item of the first pair from `unit` on that is not left out
+  const auto open = [&] {
+    for (; unit < units; unit += step) {
+      next.token = token_next;
+      token_next = read_token(unit + step);
+      next.t = unit;
+      next.i = 0;
+      last = items;
+      if (p.parts > 1) {
+        next.t = unit / p.parts;
+        const int part = unit - next.t * p.parts;
+        next.i = part * items / p.parts;
+        last = (part + 1) * items / p.parts;
+      }
+      if (a.slots) {
+        const int slot = __shfl_sync(0xffffffffu, next.token, ROPE_AXES), page = slot / a.page_size;
+        if (slot < 0) continue;
+        if (page >= a.num_pages) {
+          if (lane == 0) atomicOr(p.status, STATUS_PAGE);
+          continue;
+        }
+        next.at = (long long)page * a.cache_page_stride + (long long)(slot - page * a.page_size) * a.cache_row_stride;
+      }
+      return;
+    }
+  };
+  const auto kind_of = [&](int i) { return i < p.q_items ? 0 : i < qk_items ? 1 : 2; };
+  const auto head_of = [&](int i) { return (i < p.q_items ? i : i < qk_items ? i - p.q_items : i - qk_items) * VECS + sub; };
+  const auto fetch = [&](uint4(&raw)[UNROLL][2]) {
+    const int kind = kind_of(next.i), h0 = head_of(next.i), heads = kind == 0 ? a.Hq : a.Hkv;
+    const void* from = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    const long long row = kind == 0 ? a.q_row_stride : kind == 1 ? a.k_row_stride : a.v_row_stride;
+    const long long head = kind == 0 ? a.q_head_stride : kind == 1 ? a.k_head_stride : a.v_head_stride;
+    const uint16_t* src = static_cast<const uint16_t*>(from) + next.t * row + h0 * head + ca;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u, src += ROWS * head) {
+      raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (h0 + u * ROWS < heads) {
+        raw[u][0] = load_cg_x4(src);
+        raw[u][1] = load_cg_x4(src + (cb - ca));
+      }
+    }
+  };
+  const auto advance = [&] {
+    if (++next.i < last) return;
+    unit += step;
+    open();
+  };
+
+  float f[4][8];
+  int f_kind = -1, f_token = -1, coef_token = -1;  // whose products f and the shared memory hold
+  uint4 raw[UNROLL][2], ahead[UNROLL][2];
+  open();
+  bool more = unit < units;
+  if (more) fetch(ahead);
+  for (int x = tid; x < PAIRS * ROPE_AXES; x += ROPE_THREADS) {
+    const int pair = x % PAIRS, axis = x / PAIRS;
+    if (pair < half && axis < a.axes) turn[axis][pair] = turn_of(a.inv_freq[axis * half + pair]);
+    // elements of the pair (those that are not turned: chunks of eight, paired off)
+    int e;
+    if (ADJACENT) e = 2 * pair + (axis & 1);
+    else if (pair < half) e = pair + (axis & 1) * half;
+    else e = a.rot_dim + (pair - half) / 8 * 16 + pair % 8 + (axis & 1) * 8;
+    const void* w = axis < 2 ? a.q_weight : a.k_weight;
+    weight[axis][pair] = w ? weight_at<BF16>(w, a.weight_f32, e) : 1.f;
+  }
+  __syncthreads();
+
+  while (more) {
+    const Item it = next;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) raw[u][0] = ahead[u][0], raw[u][1] = ahead[u][1];
+    advance();
+    more = unit < units;
+    if (more) fetch(ahead);
+
+    const int kind = kind_of(it.i), h0 = head_of(it.i), heads = kind == 0 ? a.Hq : a.Hkv;
     uint16_t* dst;
     long long dst_head;
     if (kind == 0) {
-      dst = static_cast<uint16_t*>(a.q_out) + row * a.q_out_row_stride;
+      dst = static_cast<uint16_t*>(a.q_out) + it.t * a.q_out_row_stride;
       dst_head = a.q_out_head_stride;
     } else if (a.slots) {
-      dst = static_cast<uint16_t*>(kind == 1 ? a.k_cache : a.v_cache) + at;
+      dst = static_cast<uint16_t*>(kind == 1 ? a.k_cache : a.v_cache) + it.at;
       dst_head = a.cache_head_stride;
     } else {
-      dst = static_cast<uint16_t*>(a.k_out) + row * a.k_out_row_stride;
+      dst = static_cast<uint16_t*>(a.k_out) + it.t * a.k_out_row_stride;
       dst_head = a.k_out_head_stride;
     }
-    uint4 raw[UNROLL][2];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
-      const int h = h0 + u * ROWS;
-      if (h < heads) {
-        raw[u][0] = load_cg_x4(src + h * src_head + ca);
-        raw[u][1] = load_cg_x4(src + h * src_head + cb);
-      }
-    }
+    dst += h0 * dst_head + ca;
+    dst_head *= ROWS;
     if (kind == 2) {
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int h = h0 + u * ROWS;
-        if (h < heads) {
-          *reinterpret_cast<uint4*>(dst + h * dst_head + ca) = raw[u][0];
-          *reinterpret_cast<uint4*>(dst + h * dst_head + cb) = raw[u][1];
+      for (int u = 0; u < UNROLL; ++u, dst += dst_head)
+        if (h0 + u * ROWS < heads) {
+          *reinterpret_cast<uint4*>(dst) = raw[u][0];
+          *reinterpret_cast<uint4*>(dst + (cb - ca)) = raw[u][1];
         }
-      }
       continue;
     }
-    float f[4][8];
+    if (coef_token != it.t) {
+      coef_token = it.t;
+      __syncwarp();  // those of the token before have been read
+      unsigned long long position[ROPE_AXES];
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+      for (int axis = 0; axis < ROPE_AXES; ++axis) position[axis] = (unsigned long long)(long long)__shfl_sync(0xffffffffu, it.token, axis);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const float4 v = *reinterpret_cast<const float4*>(&coef[t][kind][x][l * 8 + y * 4]);
-        f[x][4 * y] = v.x, f[x][4 * y + 1] = v.y, f[x][4 * y + 2] = v.z, f[x][4 * y + 3] = v.w;
+      for (int x = 0; x < PAIRS / 32; ++x) {
+        const int pair = lane + 32 * x, place = (pair & 4) * (PAIRS / 8) + pair / 8 * 4 + (pair & 3);
+        float s = 0.f, c = 1.f;
+        if (pair < half) {
+          unsigned long long phi = 0;
+#pragma unroll
+          for (int axis = 0; axis < ROPE_AXES; ++axis)
+            if (axis < a.axes) phi += turn[axis][pair] * position[axis];
+          sincospif((float)(int)(phi >> 32) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float wa = weight[2 * k][pair], wb = weight[2 * k + 1][pair];
+          mine[k][0][place] = wa * c;
+          mine[k][1][place] = wb * s;
+          mine[k][2][place] = wb * c;
+          mine[k][3][place] = wa * s;
+        }
       }
+      __syncwarp();
+    }
+    if (f_kind != kind || f_token != it.t) {
+      f_kind = kind;
+      f_token = it.t;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float4 v = *reinterpret_cast<const float4*>(&mine[kind][x][y * (PAIRS / 2) + l * 4]);
+          f[x][4 * y] = v.x, f[x][4 * y + 1] = v.y, f[x][4 * y + 2] = v.z, f[x][4 * y + 3] = v.w;
+        }
+    }
     const bool norm = (kind ? a.k_weight : a.q_weight) != nullptr;
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < UNROLL; ++u, dst += dst_head) {
       const int h = h0 + u * ROWS;
+      if (h - sub >= heads) break;  // (the whole warp's)
       const uint32_t x0[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w}, x1[4] = {raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
       float va[8], vb[8];
 #pragma unroll
@@ -217,7 +280,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(va[e], va[e], fmaf(vb[e], vb[e], ss));
 #pragma unroll
-        for (int s = 1; s < LANES; s <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+        for (int y = 1; y < LANES; y <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, y);
         r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
       }
       float oa[8], ob[8];
@@ -238,8 +301,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
         }
       }
       if (h < heads) {
-        *reinterpret_cast<uint4*>(dst + h * dst_head + ca) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
-        *reinterpret_cast<uint4*>(dst + h * dst_head + cb) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
+        *reinterpret_cast<uint4*>(dst + (cb - ca)) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
       }
     }
   }
@@ -287,8 +350,12 @@ int launch(RopeParams& p, int sms, cudaStream_t st) {
   p.q_items = (p.a.Hq + VECS - 1) / VECS;
   p.k_items = (p.a.Hkv + VECS - 1) / VECS;
   p.v_items = p.a.slots ? p.k_items : 0;
-  if (p.a.rows <= 2 * sms) return launch_dependent(rope_kernel<D, BF16, ADJACENT, 1>, dim3(p.a.rows), ROPE_THREADS, 0, st, p);
-  return launch_dependent(rope_kernel<D, BF16, ADJACENT, ROPE_TOKENS>, dim3((p.a.rows + ROPE_TOKENS - 1) / ROPE_TOKENS), ROPE_THREADS, 0, st, p);
+  const int items = p.q_items + p.k_items + p.v_items, most = sms * ROPE_CTAS;
+  // few tokens: an item to a warp; as many warps as the machine holds: the whole token, so that its angles are worked out once
+  const long long warps = (long long)most * ROPE_WARPS;
+  p.parts = (int)(p.a.rows >= warps ? 1 : warps / p.a.rows < items ? warps / p.a.rows : items);
+  const long long units = (long long)p.a.rows * p.parts, ctas = (units + ROPE_WARPS - 1) / ROPE_WARPS;
+  return launch_dependent(rope_kernel<D, BF16, ADJACENT>, dim3((unsigned int)(ctas < most ? ctas : most)), ROPE_THREADS, 0, st, p);
 }
 
 }  // namespace
@@ -303,7 +370,7 @@ extern "C" int attn_rope(const attn_rope_params_t* params) {
     if (rc != ATTN_OK) return rc;
     int sms = 0, dev = 0;
     if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
-    RopeParams p{a, nullptr, 0, 0, 0};
+    RopeParams p{a, nullptr, 0, 0, 0, 0};
     if (a.slots && (rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
     const bool bf16 = a.dtype == ATTN_BF16;
