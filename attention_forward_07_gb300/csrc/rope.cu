@@ -32,7 +32,6 @@ struct RopeParams {
   attn_rope_params_t a;
   unsigned int* status;
   int q_items, k_items, v_items;  // items of a token
-  int parts;                      // parts of a token
 };
 
 template <bool BF16>
@@ -73,19 +72,19 @@ __device__ __forceinline__ unsigned long long turn_of(float f) {
   return x >> 31 ? 0ull - t : t;
 }
 
-// The frequencies' parts of a turn and the weights are worked out once a CTA.  Then warps take (token, part) pairs, a part
-// being the whole token or, where there are few, some of its items: VECS heads of q, k or v.  A row is D / 16 lanes, eight pairs to a
-// lane.  The loads run an item ahead of the rest, on into the next token, whose positions and slot have been read a token ahead: a warp
-// always has loads in flight.  At a token's first item a warp works out the four products of weight and cosine or sine
-// that turn its pairs (two pairs to a lane) and leaves them in shared memory of its own, so no warp waits for another; a lane keeps its
-// pairs' products for all heads of q, then of k.  The values' items are plain copies.
+// A token's items are VECS heads of q, k or v each; all tokens' items, laid end to end, are cut into equal runs, one to a warp
+// of as many CTAs as the machine holds.  A row is D / 16 lanes, eight pairs to a lane.  The loads run an item ahead of the rest, on into the
+// next token, whose positions and slot have been read a token ahead: a warp always has loads in flight.  At a token's first
+// item a warp works out the four products of weight and cosine or sine that turn its pairs (two pairs to a lane; the frequencies'
+// parts of a turn and the weights are the CTA's) and leaves them in shared memory of its own, so no warp waits for another; a lane keeps
+// its pairs' products for all heads of q, then of k.  The values' items are plain copies.
 template <int D, bool BF16, bool ADJACENT>
 __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __grid_constant__ RopeParams p) {
   const attn_rope_params_t& a = p.a;
   constexpr int LANES = D / 16, ROWS = 32 / LANES, UNROLL = 2, VECS = ROWS * UNROLL, PAIRS = D / 2;
   __shared__ unsigned long long turn[ROPE_AXES][PAIRS];
   __shared__ float weight[4][PAIRS];                              // of q: first and second of the pair; of k
-  __shared__ __align__(16) float coef[ROPE_WARPS][2][4][PAIRS];   // [q, k][w_a cos, w_b sin, w_b cos, w_a sin], lanes' first fours ahead of their second ones
+  __shared__ __align__(16) float coef[ROPE_WARPS][2][4][PAIRS];   // [q, k][w_a cos, -w_b sin, w_b cos, w_a sin], lanes' first fours ahead of their second ones
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = a.rot_dim / 2;
   grid_launch_dependents();
   grid_dependency_wait();
@@ -96,14 +95,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
   else ca = l * 8, cb = ca + half;
   const int qk_items = p.q_items + p.k_items, items = qk_items + p.v_items;
   float(&mine)[2][4][PAIRS] = coef[warp];
-  // (at most 2^30 tokens, in parts only while they are fewer than the machine's warps)
-  const unsigned int units = (unsigned int)a.rows * p.parts, step = gridDim.x * ROPE_WARPS;
-
   // a token's positions (lane x: of axis x) and slot (lane ROPE_AXES)
-  const auto read_token = [&](unsigned int unit) {
+  const auto read_token = [&](int t) {
     int x = 0;
-    if (unit < units) {
-      const unsigned int t = p.parts == 1 ? unit : unit / p.parts;
+    if (t < a.rows) {
       if (lane < a.axes && half > 0) x = load_cg(a.positions + lane * a.position_stride + t);
       else if (lane == ROPE_AXES && a.slots) x = load_cg(a.slots + t);
     }
@@ -113,24 +108,16 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
     int t, i, token;
     long long at;  // where the token's row of the cache begins
   };
-  unsigned int unit = blockIdx.x * ROPE_WARPS + warp;
-  int token_next = read_token(unit);
-  Item next{0, 0, 0, 0};
-  int last = 0;
-  // the first item of the first pair from `unit` on that is not left out
+  const long long all = (long long)a.rows * items, run = (long long)blockIdx.x * ROPE_WARPS + warp, runs = (long long)gridDim.x * ROPE_WARPS;
+  const long long begin = all * run / runs;
+  long long left = all * (run + 1) / runs - begin;  // the run's items, `next` the first of them
+  Item next{(int)(begin / items), (int)(begin % items), 0, 0};
+  int token_next = read_token(next.t);
+  // reads a token that the run comes to, and skips it if it is left out
   const auto open = [&] {
-    for (; unit < units; unit += step) {
+    for (; left > 0; left -= items - next.i, ++next.t, next.i = 0) {
       next.token = token_next;
-      token_next = read_token(unit + step);
-      next.t = unit;
-      next.i = 0;
-      last = items;
-      if (p.parts > 1) {
-        next.t = unit / p.parts;
-        const int part = unit - next.t * p.parts;
-        next.i = part * items / p.parts;
-        last = (part + 1) * items / p.parts;
-      }
+      token_next = read_token(next.t + 1);
       if (a.slots) {
         const int slot = __shfl_sync(0xffffffffu, next.token, ROPE_AXES), page = slot / a.page_size;
         if (slot < 0) continue;
@@ -161,16 +148,18 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
     }
   };
   const auto advance = [&] {
-    if (++next.i < last) return;
-    unit += step;
+    --left;
+    if (++next.i < items) return;
+    ++next.t;
+    next.i = 0;
     open();
   };
 
-  float f[4][8];
+  uint64_t f[4][4];
   int f_kind = -1, f_token = -1, coef_token = -1;  // whose products f and the shared memory hold
   uint4 raw[UNROLL][2], ahead[UNROLL][2];
   open();
-  bool more = unit < units;
+  bool more = left > 0;
   if (more) fetch(ahead);
   for (int x = tid; x < PAIRS * ROPE_AXES; x += ROPE_THREADS) {
     const int pair = x % PAIRS, axis = x / PAIRS;
@@ -190,7 +179,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) raw[u][0] = ahead[u][0], raw[u][1] = ahead[u][1];
     advance();
-    more = unit < units;
+    more = left > 0;
     if (more) fetch(ahead);
 
     const int kind = kind_of(it.i), h0 = head_of(it.i), heads = kind == 0 ? a.Hq : a.Hkv;
@@ -238,7 +227,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
         for (int k = 0; k < 2; ++k) {
           const float wa = weight[2 * k][pair], wb = weight[2 * k + 1][pair];
           mine[k][0][place] = wa * c;
-          mine[k][1][place] = wb * s;
+          mine[k][1][place] = -wb * s;
           mine[k][2][place] = wb * c;
           mine[k][3][place] = wa * s;
         }
@@ -252,8 +241,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
       for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float4 v = *reinterpret_cast<const float4*>(&mine[kind][x][y * (PAIRS / 2) + l * 4]);
-          f[x][4 * y] = v.x, f[x][4 * y + 1] = v.y, f[x][4 * y + 2] = v.z, f[x][4 * y + 3] = v.w;
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&mine[kind][x][y * (PAIRS / 2) + l * 4]);
+          f[x][2 * y] = v.x, f[x][2 * y + 1] = v.y;
         }
     }
     const bool norm = (kind ? a.k_weight : a.q_weight) != nullptr;
@@ -262,42 +251,45 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
       const int h = h0 + u * ROWS;
       if (h - sub >= heads) break;  // (the whole warp's)
       const uint32_t x0[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w}, x1[4] = {raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
-      float va[8], vb[8];
+      uint64_t va[4], vb[4];  // two of the lane's pairs each: their first elements, their second ones
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 lo = widen2<BF16>(x0[e]), hi = widen2<BF16>(x1[e]);
         if (ADJACENT) {  // (each word is a pair)
-          va[e] = lo.x, vb[e] = lo.y;
-          va[e + 4] = hi.x, vb[e + 4] = hi.y;
+          const float2 lo = widen2<BF16>(e < 2 ? x0[2 * e] : x1[2 * e - 4]), hi = widen2<BF16>(e < 2 ? x0[2 * e + 1] : x1[2 * e - 3]);
+          va[e] = f2_pack(lo.x, hi.x), vb[e] = f2_pack(lo.y, hi.y);
         } else {
-          va[2 * e] = lo.x, va[2 * e + 1] = lo.y;
-          vb[2 * e] = hi.x, vb[2 * e + 1] = hi.y;
+          const float2 lo = widen2<BF16>(x0[e]), hi = widen2<BF16>(x1[e]);
+          va[e] = f2_pack(lo.x, lo.y), vb[e] = f2_pack(hi.x, hi.y);
         }
       }
       float r = 1.f;
       if (norm) {
-        float ss = 0.f;
+        uint64_t s2 = fmul2(va[0], va[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(va[e], va[e], fmaf(vb[e], vb[e], ss));
+        for (int e = 0; e < 4; ++e) {
+          if (e > 0) s2 = ffma2(va[e], va[e], s2);
+          s2 = ffma2(vb[e], vb[e], s2);
+        }
+        float ss, other;
+        f2_unpack(s2, ss, other);
+        ss += other;
 #pragma unroll
         for (int y = 1; y < LANES; y <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, y);
         r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
       }
-      float oa[8], ob[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        oa[e] = r * fmaf(va[e], f[0][e], -(vb[e] * f[1][e]));
-        ob[e] = r * fmaf(vb[e], f[2][e], va[e] * f[3][e]);
-      }
+      const uint64_t rr = f2_pack(r, r);
       uint32_t y0[4], y1[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
+        float a0, a1, b0, b1;
+        f2_unpack(fmul2(rr, ffma2(va[e], f[0][e], fmul2(vb[e], f[1][e]))), a0, a1);
+        f2_unpack(fmul2(rr, ffma2(vb[e], f[2][e], fmul2(va[e], f[3][e]))), b0, b1);
         if (ADJACENT) {
-          y0[e] = narrow2<BF16>(oa[e], ob[e]);
-          y1[e] = narrow2<BF16>(oa[e + 4], ob[e + 4]);
+          (e < 2 ? y0[2 * e] : y1[2 * e - 4]) = narrow2<BF16>(a0, b0);
+          (e < 2 ? y0[2 * e + 1] : y1[2 * e - 3]) = narrow2<BF16>(a1, b1);
         } else {
-          y0[e] = narrow2<BF16>(oa[2 * e], oa[2 * e + 1]);
-          y1[e] = narrow2<BF16>(ob[2 * e], ob[2 * e + 1]);
+          y0[e] = narrow2<BF16>(a0, a1);
+          y1[e] = narrow2<BF16>(b0, b1);
         }
       }
       if (h < heads) {
@@ -351,10 +343,7 @@ int launch(RopeParams& p, int sms, cudaStream_t st) {
   p.k_items = (p.a.Hkv + VECS - 1) / VECS;
   p.v_items = p.a.slots ? p.k_items : 0;
   const int items = p.q_items + p.k_items + p.v_items, most = sms * ROPE_CTAS;
-  // few tokens: an item to a warp; as many warps as the machine holds: the whole token, so that its angles are worked out once
-  const long long warps = (long long)most * ROPE_WARPS;
-  p.parts = (int)(p.a.rows >= warps ? 1 : warps / p.a.rows < items ? warps / p.a.rows : items);
-  const long long units = (long long)p.a.rows * p.parts, ctas = (units + ROPE_WARPS - 1) / ROPE_WARPS;
+  const long long ctas = ((long long)p.a.rows * items + ROPE_WARPS - 1) / ROPE_WARPS;
   return launch_dependent(rope_kernel<D, BF16, ADJACENT>, dim3((unsigned int)(ctas < most ? ctas : most)), ROPE_THREADS, 0, st, p);
 }
 
@@ -370,7 +359,7 @@ extern "C" int attn_rope(const attn_rope_params_t* params) {
     if (rc != ATTN_OK) return rc;
     int sms = 0, dev = 0;
     if ((rc = host_device(sms, dev)) != ATTN_OK) return rc;
-    RopeParams p{a, nullptr, 0, 0, 0, 0};
+    RopeParams p{a, nullptr, 0, 0, 0};
     if (a.slots && (rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(a.stream);
     const bool bf16 = a.dtype == ATTN_BF16;
