@@ -28,6 +28,7 @@ namespace attn {
 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr long long MAX_STRIDE = 1ll << 38;  // elements: no memory holds two entries that far apart, and tensor maps end there
+constexpr int NO_PLAN_UNITS = 2048;  // (attn_fwd_paged_tree) units that they may have at most
 constexpr int NO_PLAN_B = 512;  // requests at most whose lengths every CTA looks at (16 to a lane)
 constexpr int ROWS_MAX = 16, ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile
@@ -57,7 +58,7 @@ struct TileJoin {  // up to JOIN_ROWS packed rows of a cut (unit, head) pair
   int in, pad;          // first row within the slot
 };
 constexpr int JOIN_ROWS = 16;
-constexpr int JOINS_OF_RUN = TILE_ROWS / JOIN_ROWS;  // without a plan
+constexpr int JOINS_OF_RUN = TILE_ROWS / JOIN_ROWS;  // without a plan (attn_fwd_paged_tree: as many as a unit may have rows)
 
 // Scratch of the tcgen05 path.
 struct TileWork {
@@ -69,7 +70,7 @@ struct TileWork {
   int T;             // tokens of a Q tile
   int max_units;     // 0: no request takes this path
   int sms;
-  int no_plan;       // every CTA finds its run by itself (NO_PLAN_B), and lists joins at places of its own
+  int no_plan;       // not 0: every CTA finds its run by itself (NO_PLAN_B), and lists joins at places of its own, this many in all
 };
 
 struct PagedParams {

@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
   grid_launch_dependents();
   grid_dependency_wait();
   const int halves = p.slot_rows / JOIN_ROWS, items = p.tile.no_plan ? 0 : p.rows_grid * halves;
-  const int total = items + (p.tile.no_plan ? p.tile.sms * JOINS_OF_RUN : p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
+  const int total = items + (p.tile.no_plan ? p.tile.no_plan : p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
     if (x >= items) {
       join_unit<D, BF16>(p, p.tile.joins[x - items]);
@@ -943,7 +943,7 @@ int launch_rows(const RowsParams& p, const attn_fwd_paged_params_t& a, const Pla
   if (rc == ATTN_OK && !p.tile.no_plan) rc = launch_dependent(rows_kernel<D, MT, BF16, TREE>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
   if (rc == ATTN_OK && tiles) rc = tile_launch(tp, a, sms, dev, st);
   if (rc != ATTN_OK) return rc;
-  const int joins = p.tile.no_plan ? sms * JOINS_OF_RUN : plan.rows_grid;
+  const int joins = p.tile.no_plan ? p.tile.no_plan : plan.rows_grid;
   return launch_dependent(join_kernel<D, BF16>, dim3(joins), 32 * JOIN_WARPS, 0, st, p);
 }
 
@@ -1015,7 +1015,13 @@ int paged_fwd_impl(const attn_fwd_paged_params_t& a, const attn_fwd_paged_tree_p
   p.tile.T = plan.T;
   p.tile.max_units = plan.max_units;
   p.tile.sms = sms;
-  p.tile.no_plan = plan.max_units > 0 && p.max_q <= plan.T && a.B <= NO_PLAN_B && (long long)a.total_q * p.g > (long long)ROWS_MAX * a.B;
+  // (attn_fwd_paged_tree: positions of the line that its kernel cuts, whatever the lengths and offsets)
+  const long long most_tiles = ((long long)a.table_width * a.page_size + TILE_KEYS - 1) / TILE_KEYS;
+  const int joins_of_unit = (int)(((long long)p.max_q * p.g < TILE_QT * TILE_ROWS ? p.max_q * p.g : TILE_QT * TILE_ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
+  const long long most_units = a.B * (((long long)p.max_q + TILE_QT * plan.T - 1) / (TILE_QT * plan.T)), most_line = most_units * (4 * most_tiles + 64) * a.Hkv;
+  if (plan.max_units > 0 && (tree ? plan.max_units <= NO_PLAN_UNITS && most_line < INT_MAX / 2 : p.max_q <= plan.T) && a.B <= NO_PLAN_B &&
+      (long long)a.total_q * p.g > (long long)ROWS_MAX * a.B)
+    p.tile.no_plan = sms * (tree ? joins_of_unit : JOINS_OF_RUN);
   if (plan.max_units > 0) {
     p.tile.queue = reinterpret_cast<TileQueue*>(ws + plan.off_queue);
     p.tile.units = reinterpret_cast<TileUnit*>(ws + plan.off_units);

@@ -103,11 +103,10 @@ struct RunStart {
   int b, h, runs;
   long long in, line, pos, left;  // (pos: the run's first step, left: its steps)
 };
-template <bool TREE>
 __device__ __forceinline__ bool request_unit(const TileParams& p, int b, TileUnit& x) {
   int k0, k1;
   request_span(p, b, x.row0, x.sq, x.sk);
-  tile_keys<TREE>(p, x.sq, x.sk, 0, 0, TILE_QT, k0, k1);
+  tile_keys<false>(p, x.sq, x.sk, 0, 0, TILE_QT, k0, k1);
   x.b = b;
   x.blk = 0;
   x.j0 = k0 / TILE_KEYS;
@@ -115,13 +114,12 @@ __device__ __forceinline__ bool request_unit(const TileParams& p, int b, TileUni
   return x.sq > 0;
 }
 // By a warp; false where there are fewer runs.
-template <bool TREE>
 __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane, RunStart& r) {
   const int per = (p.B + 31) / 32, b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B);
   TileUnit x;
   long long own = 0;
   for (int b = b0; b < b1; ++b)
-    if (request_unit<TREE>(p, b, x)) own += x.w + UNIT_COST;
+    if (request_unit(p, b, x)) own += x.w + UNIT_COST;
   own *= p.Hkv;
   long long incl = own;
 #pragma unroll
@@ -140,7 +138,7 @@ __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane
   if (mine) {
     long long at = incl - own;
     for (int b = b0; b < b1; ++b) {
-      if (!request_unit<TREE>(p, b, x)) continue;
+      if (!request_unit(p, b, x)) continue;
       const int steps = x.w + UNIT_COST;
       if (r.pos < at + (long long)steps * p.Hkv) {
         r.b = b;
@@ -158,24 +156,149 @@ __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane
   return true;
 }
 
+// ------------------------------------------------------------------ runs of attn_fwd_paged_tree without a plan
+// Requests have any number of units here.  A key tile takes BOTH_COST positions of the line where both Q tiles have rows; where one has, as
+// many at d = 128, whose keys come no faster (24 trees of 40 - 64 nodes x 8 heads: 113 us, with three quarters 119), three quarters at
+// d = 64 (30 trees beside two chunks: 89 us, with as many 94).  Where the pieces of every (unit, head) pair, at most `piece`
+// positions long, find a CTA each, all runs are one piece (a pair's length is rounded up to full pieces): no CTA then starts and ends
+// twice, and few keys are spread over all SMs (26 nodes against 2000 keys, 8 heads: 16.8 us, 21.2 with runs of eight tiles).  Otherwise
+// the line is cut into runs that differ by a position at most, with PAIR_COST positions for a pair's start and end.  The host sees
+// to it that the line's positions fit 31 bits.  All loops stay loops: with two copies of this code, unrolled, the kernel outgrew the
+// instruction cache and took a third longer.  (Taking key tiles by turns in units of one Q tile, beside others, was slower: 122 us for
+// 112, 106 for 94.)
+constexpr int BOTH_COST = 4, PAIR_COST = 10, MIN_TREE_RUN = BOTH_COST * MIN_RUN, MIN_PIECE = 2 * BOTH_COST;
+struct TreeRun {
+  int piece, cost;        // piece: 1 for equal runs; cost: of a pair's start and end
+  int runs, each, longer; // the first `longer` runs have each + 1 positions, the others `each`
+  int b, blk, h;
+  int in, left;  // positions of the pair that lie before the run; the run's that are left
+  __device__ __forceinline__ int length(const TileUnit& x) const { return (x.w * x.pad + cost + piece - 1) / piece * piece; }
+  __device__ __forceinline__ int begin(int i) const { return each * i + min(i, longer); }
+  __device__ __forceinline__ int run(int x) const {  // that holds position x
+    const int border = (each + 1) * longer;
+    return x < border ? x / (each + 1) : longer + (x - border) / each;
+  }
+};
+__device__ __forceinline__ int tree_units(const TileParams& p, int sq) { return (sq + TILE_QT * p.tile.T - 1) / (TILE_QT * p.tile.T); }
+template <int D>
+__device__ __forceinline__ void tree_unit(const TileParams& p, int b, int blk, TileUnit& x) {
+  int k0, k1;
+  request_span(p, b, x.row0, x.sq, x.sk);
+  tile_keys<true>(p, x.sq, x.sk, blk, 0, TILE_QT, k0, k1);
+  x.b = b;
+  x.blk = blk;
+  x.j0 = k0 / TILE_KEYS;
+  x.w = max((k1 + TILE_KEYS - 1) / TILE_KEYS - x.j0, 1);
+  x.pad = x.sq - blk * TILE_QT * p.tile.T > p.tile.T || D == 128 ? BOTH_COST : 3;  // positions of a tile
+}
+// By a warp; false where there are fewer runs.
+template <int D>
+__device__ __forceinline__ bool tree_run(const TileParams& p, int run, int lane, TreeRun& r) {
+  const int per = (p.B + 31) / 32, b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B), sms = p.tile.sms;
+  r.piece = 1;
+  r.cost = r.b = r.blk = r.h = r.in = r.left = 0;
+  int pos = INT_MAX, before = 0;
+  bool mine = false;
+  // passes over the lane's units: their tiles' positions, which say how the line is cut; the line as it is cut; the run's first pair
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    int own = 0, units = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1 && !mine; ++b) {
+      TileUnit x;
+      int n = 1, alike;  // units of the request; those as long as this one (under a mask: all but the last)
+#pragma unroll 1
+      for (int blk = 0; blk < n; blk += alike) {
+        tree_unit<D>(p, b, blk, x);
+        n = tree_units(p, x.sq);
+        if (n == 0) break;
+        alike = has_mask<true>(p, x.sq) && blk < n - 1 ? n - 1 - blk : 1;
+        const int steps = r.length(x), unit = steps * p.Hkv;
+        if (pass == 2 && pos < before + own + unit * alike) {
+          const int at = pos - before - own, skip = at / unit;
+          r.b = b;
+          r.blk = blk + skip;
+          r.h = (at - skip * unit) / steps;
+          r.in = at - skip * unit - r.h * steps;
+          mine = true;
+          break;
+        }
+        own += unit * alike;
+        units += p.Hkv * alike;
+      }
+    }
+    if (pass == 2) break;
+    int incl = own;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    const int line = __shfl_sync(0xffffffffu, incl, 31);
+    if (pass == 0) {
+      // pieces of this length find a CTA each (every pair has at most one that is not full)
+      units = __reduce_add_sync(0xffffffffu, units);
+      const int room = sms - units, piece = max((line + room - 1) / max(room, 1), MIN_PIECE);
+      if (room > 0 && piece <= line / sms + PAIR_COST) r.piece = piece;
+      else r.cost = PAIR_COST;
+      continue;
+    }
+    if (line == 0) return false;
+    r.runs = r.cost ? max(1, min(sms, line / MIN_TREE_RUN)) : line / r.piece;
+    r.each = line / r.runs;
+    r.longer = line - r.each * r.runs;
+    if (run >= r.runs) return false;
+    pos = r.begin(run);
+    r.left = r.begin(run + 1) - pos;
+    before = incl - own;
+    if (pos < before || pos >= incl) break;
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  r.b = __shfl_sync(0xffffffffu, r.b, from);
+  r.blk = __shfl_sync(0xffffffffu, r.blk, from);
+  r.h = __shfl_sync(0xffffffffu, r.h, from);
+  r.in = __shfl_sync(0xffffffffu, r.in, from);
+  return true;
+}
+
 // ------------------------------------------------------------------ join list
 // One warp of each CTA lists the cut pairs for join_kernel while the others work (the plan, which all wait
 // for, was 2.5 - 4 us longer with it).  Each pair is found by the run that takes its second piece.
-template <bool TREE>
 __device__ __forceinline__ void run_join_list(const TileParams& p, int lane) {  // (without a plan)
   const int r = blockIdx.x;
   TileJoin* list = p.tile.joins + r * JOINS_OF_RUN;
   RunStart rs;
   TileJoin jn = {};
-  if (run_start<TREE>(p, r, lane, rs)) {
+  if (run_start(p, r, lane, rs)) {
     TileUnit un;
-    request_unit<TREE>(p, rs.b, un);
+    request_unit(p, rs.b, un);
     const long long at = rs.pos - rs.in;  // where the pair begins
     const int first = run_of(rs.line, rs.runs, at + UNIT_COST), last = run_of(rs.line, rs.runs, at + un.w + UNIT_COST - 1);
     if (r == first + 1 && r <= last)
       jn = TileJoin{un.row0, lane * JOIN_ROWS, max(min(un.sq * p.g - lane * JOIN_ROWS, JOIN_ROWS), 0), rs.h, first, last - first + 1, lane * JOIN_ROWS, 0};
   }
   if (lane < JOINS_OF_RUN) list[lane] = jn;
+}
+// (attn_fwd_paged_tree without a plan: by the load warp, which knows its run, at its end.)  b < 0: no run.
+template <int D>
+__device__ __forceinline__ void tree_join_list(const TileParams& p, const TreeRun& r, int b, int blk, int h, int in, int lane) {
+  const int run = blockIdx.x;
+  TileJoin jn = {};
+  if (b >= 0) {
+    TileUnit un;
+    tree_unit<D>(p, b, blk, un);
+    const int at = r.begin(run) - in + r.cost;  // where the pair's tiles begin
+    const int first = r.run(at + un.pad - 1), last = r.run(at + un.w * un.pad - 1);
+    if (run == first + 1 && run <= last) {
+      const int t = lane / JOINS_OF_RUN, k = lane % JOINS_OF_RUN;
+      const int rows = min(p.tile.T, un.sq - (un.blk * TILE_QT + t) * p.tile.T) * p.g;
+      jn = TileJoin{un.row0, (un.blk * TILE_QT + t) * p.tile.T * p.g + k * JOIN_ROWS, max(min(rows - k * JOIN_ROWS, JOIN_ROWS), 0), h,
+                    first, last - first + 1, t * TILE_ROWS + k * JOIN_ROWS, 0};
+    }
+  }
+  static_assert(TILE_QT * JOINS_OF_RUN <= 32, "a lane to an entry");
+  const int entries = p.tile.no_plan / p.tile.sms;
+  if (lane < entries) p.tile.joins[run * entries + lane] = jn;
 }
 __device__ __forceinline__ void tile_join_list(const TileParams& p, int lane) {
   TileQueue* q = p.tile.queue;
@@ -218,7 +341,9 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
   uint32_t kpar = 1, vpar = 1, ie_par = 1;
   uint32_t kpend = 0, kpend_par = 0, vpend = 0, vpend_par = 0;
   bool inject = p.inject != 0;
-  const bool no_plan = TURNS && p.tile.no_plan;
+  const bool no_plan = (TURNS || TREE) && p.tile.no_plan;
+  TreeRun tr;  // (TREE, without a plan)
+  int first_b = -1, first_blk = 0, first_h = 0, first_in = 0;  // its first pair
   bool begun = false;  // (without a plan)
   const unsigned int whole = no_plan ? 0 : p.tile.queue->whole, entries = no_plan ? 0 : whole + p.tile.queue->runs;
 
@@ -242,19 +367,66 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
     int slot = -1, from = 0, tiles = 0;  // this piece: tiles from .. from + tiles of the unit
     while (tiles == 0) {
       long long in = 0;  // steps of the pair that lie before the run
+      if constexpr (TREE) {
+        if (no_plan) {
+          TileUnit un;
+          bool more = true;
+          if (!begun) {
+            more = tree_run<D>(p, blockIdx.x, lane, tr);
+            begun = true;
+            run = blockIdx.x;
+            if (more) first_b = tr.b, first_blk = tr.blk, first_h = tr.h, first_in = tr.in;
+          } else if (tr.left > 0) {
+            tr.in = 0;
+            if (++tr.h == p.Hkv) {
+              tr.h = 0;
+              int row0, sq, sk;
+              request_span(p, tr.b, row0, sq, sk);
+              if (++tr.blk >= tree_units(p, sq)) {
+                tr.blk = 0;
+                do request_span(p, ++tr.b, row0, sq, sk);
+                while (sq == 0);  // (the line does not end here)
+              }
+            }
+          } else {
+            more = false;
+          }
+          if (!more) {
+            if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
+            if (lane == 0) {
+              hdr[ie].j = -1;
+              hdr[ie].flags = FLAG_EXIT;
+              mbar_arrive(bars + 8u * (L::B_IFULL + ie));
+            }
+            __syncwarp();
+            tree_join_list<D>(p, tr, first_b, first_blk, first_h, first_in, lane);
+            return;
+          }
+          tree_unit<D>(p, tr.b, tr.blk, un);
+          // the tiles of the pair's positions [in, out): a tile goes with its last position
+          const int out = min(tr.in + tr.left, tr.length(un));
+          tr.left -= out - tr.in;
+          from = max(tr.in - tr.cost, 0) / un.pad;
+          tiles = min(max(out - tr.cost, 0) / un.pad, un.w) - from;
+          pt = un;
+          h = tr.h;
+          slot = tiles == pt.w ? -1 : from == 0 ? 2 * run + 1 : 2 * run;
+          continue;
+        }
+      }
       if (left > 0) {
         // the run's next unit
         if (++h == p.Hkv) {
           h = 0;
           ++s;
           if (no_plan)
-            while (s < p.B && !request_unit<TREE>(p, s, pt)) ++s;
+            while (s < p.B && !request_unit(p, s, pt)) ++s;
         }
         if (!no_plan) pt = p.tile.units[s];
       } else {
         const unsigned int x = x_next;
         RunStart rs;
-        const bool more = no_plan ? !begun && run_start<TREE>(p, blockIdx.x, lane, rs) : x < entries;
+        const bool more = no_plan ? !begun && run_start(p, blockIdx.x, lane, rs) : x < entries;
         if (!more) {
           if (!bwait_warp(bars + 8u * (L::B_IEMPTY + ie), ie_par, abort_flag, to)) goto drain;
           if (lane == 0) {
@@ -271,7 +443,7 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
           h = rs.h;
           in = rs.in;
           left = rs.left;
-          request_unit<TREE>(p, s, pt);
+          request_unit(p, s, pt);
           begun = true;
         } else {
           pt = u_next;
@@ -740,8 +912,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) paged_tile_kernel(const __grid_co
       TileEnv<D, TURNS> env;
       mma_role<D, BF16, L>(env, p.timeout_us, base, gbase, abort_flag, tmem, lane);
     } else if (warp == 2) {
-      if (TURNS && p.tile.no_plan) run_join_list<TREE>(p, lane);
-      else tile_join_list(p, lane);
+      if (TURNS && p.tile.no_plan) run_join_list(p, lane);
+      else if (!TREE || !p.tile.no_plan) tile_join_list(p, lane);
     }
   } else {
     setmaxnreg_inc<L::REGS_SOFTMAX>();

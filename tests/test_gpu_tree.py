@@ -214,7 +214,7 @@ def test_attention(case, kind):
 
 @pytest.mark.parametrize("d,Hq,Hkv,n,ctx", [(128, 8, 2, 40, 3000), (64, 4, 1, 8, 5000), (128, 4, 4, 4, 900)])
 def test_a_chain_is_what_the_causal_call_computes(d, Hq, Hkv, n, ctx):
-    """The same rows as a chain under a mask and under attn_fwd_paged's causal order: equal bits (the same paths with the same order)."""
+    """The same rows as a chain under a mask and in attn_fwd_paged's causal order: both within the bounds of one reference."""
     bt = Batch([n, n - 3, 1], [ctx + n, ctx // 2, n], Hq, Hkv, d, "bf16", 32, seed=n)
     mask = np.zeros((bt.q.shape[1], 64), np.int64)
     for b in range(3):
@@ -224,21 +224,27 @@ def test_a_chain_is_what_the_causal_call_computes(d, Hq, Hkv, n, ctx):
     q, k, v, o2, lse2 = bt.device()
     af.attn_fwd_paged(q, k, v, o2, bt.table.cuda(), bt.cu.cuda(), bt.lens.cuda(), bt.max_q, lse=lse2, causal=True, scale=d ** -0.5)
     af.attn_check()
-    assert torch.equal(lse, lse2) and torch.equal(o, o2)
+    for got in ((o, lse), (o2, lse2)):
+        tree_ref.check_attention(bt, got[0].cpu(), got[1].cpu(), mask, 2, np.zeros(len(mask)), -1, d ** -0.5)
 
 
-@pytest.mark.parametrize("B,n,top", [(40, 24, 2600), (600, 3, 300)])
-def test_attention_of_many_requests(B, n, top):
-    rng = np.random.default_rng(B)
-    nodes = rng.integers(0, n + 1, B).tolist()
-    keys = [m + int(rng.integers(0, top)) for m in nodes]
-    bt = Batch(nodes, keys, 4, 1, 64, "bf16", 16, seed=B)
+@pytest.mark.parametrize("B,n,top,Hq,Hkv,d,words", [(40, 24, 2600, 4, 1, 64, 1), (600, 3, 300, 4, 1, 64, 1), (1, 20, 9000, 8, 2, 128, 1), (3, 70, 7000, 8, 2, 64, 3),
+                                                   (25, 64, 1500, 8, 1, 128, 2), (70, 40, 900, 16, 2, 64, 2), (160, 20, 400, 7, 1, 128, 1)])
+def test_attention_of_many_requests(B, n, top, Hq, Hkv, d, words):
+    """Few requests whose keys are spread over all SMs, many whose units are cut into equal runs, chunks (B > 3: one) among them."""
+    rng = np.random.default_rng(B + d)
+    nodes = rng.integers(0 if B > 1 else n, n + 1, B).tolist()
+    if B > 3 and n > 10:
+        nodes[B // 2] = 32 * words + 100
+    keys = [m + int(rng.integers(top // 2 if B < 4 else 0, top)) for m in nodes]
+    bt = Batch(nodes, keys, Hq, Hkv, d, "bf16", 16, seed=B)
     parents = np.concatenate([tree_ref.random_parents(m, rng) for m in nodes])
-    pos, mask, _ = tree_ref.tree(parents, bt.cu.tolist(), keys, 1)
+    pos, mask, _ = tree_ref.tree(parents, bt.cu.tolist(), keys, words)
+    mask = np.maximum(mask, 0)
     for wl in (-1, 500):
-        o, lse = _run_attend(bt, 1, wl, 0.125, mask, pos)
+        o, lse = _run_attend(bt, words, wl, 0.125, mask, pos)
         af.attn_check()
-        tree_ref.check_attention(bt, o.cpu(), lse.cpu(), mask, 1, pos, wl, 0.125, what=str((B, wl)))
+        tree_ref.check_attention(bt, o.cpu(), lse.cpu(), mask, words, pos, wl, 0.125, what=str((B, wl)))
 
 
 def test_infinite_keys_in_masked_places():
