@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(TREE_THREADS) paged_tree_kernel(const __grid_c
 // longer are counted, every warp tells every CTA of the cluster its requests' counts, and behind the cluster's barrier
 // each CTA sums them up by itself and writes its requests' pages to the free list in the requests' order.
 // What bounds it is latency: offsets -> nodes -> walk -> table entries -> barrier -> sum -> list.
-constexpr int ACCEPT_THREADS = 1024, ACCEPT_WARPS = ACCEPT_THREADS / 32, ACCEPT_MAX_B = 16384, ACCEPT_CTAS = 8;
+constexpr int ACCEPT_THREADS = 1024, ACCEPT_WARPS = ACCEPT_THREADS / 32, ACCEPT_MAX_B = 16384;
 constexpr int ACCEPT_BLOCKS = 4, ACCEPT_HELD = 32 * ACCEPT_BLOCKS;
 
 struct AcceptParams {
@@ -115,21 +116,23 @@ __global__ void __launch_bounds__(ACCEPT_THREADS) paged_accept_kernel(const __gr
   int* after_s = counts + a.B;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nwarps = gridDim.x * ACCEPT_WARPS, gwarp = warp * gridDim.x + blockIdx.x;  // (neighbours in different CTAs)
-  // nobody writes to a CTA's shared memory before it runs
   cluster_arrive();
   grid_launch_dependents();
   grid_dependency_wait();
   const bool pages_back = a.free_pages != nullptr;
   const int count_in = pages_back ? load_cg(a.free_count) : 0, have = min(max(count_in, 0), a.max_free);
   bool bad = count_in != have;
-  cluster_wait();
 
-  const auto page_at = [&](int b, int idx) {  // -1: none
-    const int id = (unsigned)idx < (unsigned)a.table_width ? load_cg(a.block_table + (long long)b * a.table_stride + idx) : -1;
-    return id < a.num_pages ? id : -1;
+  const auto page_at = [&](int b, int idx) {  // (may be out of range)
+    return (unsigned)idx < (unsigned)a.table_width ? load_cg(a.block_table + (long long)b * a.table_stride + idx) : -1;
   };
+  // a request's tokens from now on, its entries whose pages go back and the first 32 of these pages: where a warp has no second
+  // request, it keeps them over the cluster's barrier
+  const bool alone = a.B <= nwarps;
+  int after = 0, back0 = 0, back1 = 0, id = -1;
   for (int b = gwarp; b < a.B; b += nwarps) {
     int row0, n;
+    id = -1;
     const int keys = max(load_cg(a.seqlens_k + b), 0);
     const int asked = a.confirmed ? load_cg(a.confirmed + b) : 1;
     rows_of(a.cu_seqlens_q, b, a.rows, row0, n);
@@ -180,42 +183,55 @@ __global__ void __launch_bounds__(ACCEPT_THREADS) paged_accept_kernel(const __gr
         next = choice(cur);
         ++taken;
       }
-      const int j = c0 + lane;
+      const int j = c0 + lane, from = ctx + mine, to = ctx + sure + j, i = from / a.page_size, o = to / a.page_size;
+      const bool moves = mine >= 0 && mine != sure + j;
+      int x = -1, y = -1;  // the pages (asked for before either is used)
+      if (moves && to >= 0) x = page_at(b, i), y = page_at(b, o);
+      if (c0 + 32 >= a.max_path) {
+        // the walk has ended: the first pages that may go back, too
+        after = max(ctx + sure + taken, 0);
+        back0 = ceil_div(after, a.page_size);
+        back1 = pages_back ? ceil_div(keys, a.page_size) : back0;
+        if (back0 + lane < back1) id = page_at(b, back0 + lane);
+      }
       if (j < a.max_path) {
         int src = -1, dst = -1;
-        if (mine >= 0 && mine != sure + j) {
-          const int from = ctx + mine, to = ctx + sure + j;
-          if (to >= 0) {
-            const int i = from / a.page_size, o = to / a.page_size, x = page_at(b, i), y = page_at(b, o);
-            if (x >= 0 && y >= 0) {
-              src = x * a.page_size + (from - i * a.page_size);
-              dst = y * a.page_size + (to - o * a.page_size);
-            }
-          }
-          bad |= src < 0;
+        x = x < a.num_pages ? x : -1;
+        y = y < a.num_pages ? y : -1;
+        if (x >= 0 && y >= 0) {
+          src = x * a.page_size + (from - i * a.page_size);
+          dst = y * a.page_size + (to - o * a.page_size);
         }
+        bad |= moves && src < 0;
         const long long at = (long long)b * a.max_path + j;
         a.path[at] = mine;
         a.src_slots[at] = src;
         a.dst_slots[at] = dst;
       }
     }
-    const int accepted = sure + taken, after = max(ctx + accepted, 0);
-    int back = 0;
-    if (pages_back)
-      for (int i0 = ceil_div(after, a.page_size), i1 = ceil_div(keys, a.page_size); i0 < i1; i0 += 32) {
-        const bool here = i0 + lane < i1, ok = here && page_at(b, i0 + lane) >= 0;
-        bad |= here && !ok;
-        back += __popc(__ballot_sync(0xffffffffu, ok));
-      }
     if (lane == 0) {
-      a.accepted[b] = accepted;
+      a.accepted[b] = sure + taken;
       a.ctx_lens[b] = after;
       a.next_tokens[b] = next;
       after_s[b] = after;
     }
+    id = id < a.num_pages ? id : -1;
+    const bool here = back0 + lane < back1;
+    bad |= here && id < 0;
+    int back = __popc(__ballot_sync(0xffffffffu, here && id >= 0));
+    for (int i0 = back0 + 32; i0 < back1; i0 += 32) {
+      const int later = i0 + lane < back1 ? page_at(b, i0 + lane) : -1;
+      const bool ok = later >= 0 && later < a.num_pages;
+      bad |= i0 + lane < back1 && !ok;
+      back += __popc(__ballot_sync(0xffffffffu, ok));
+    }
+    if (b == gwarp) {  // (nobody writes to a CTA's shared memory before it runs)
+      __syncwarp();
+      cluster_wait();
+    }
     if (lane < gridDim.x) store_remote(counts + b, lane, back);
   }
+  if (gwarp >= a.B) cluster_wait();
   __syncwarp();
   cluster_arrive();
   cluster_wait();
@@ -245,10 +261,14 @@ __global__ void __launch_bounds__(ACCEPT_THREADS) paged_accept_kernel(const __gr
     }
     __syncthreads();
     for (int b = gwarp; b < a.B; b += nwarps) {
-      const int keys = max(load_cg(a.seqlens_k + b), 0);
+      if (!alone) {
+        back0 = ceil_div(after_s[b], a.page_size);
+        back1 = ceil_div(max(load_cg(a.seqlens_k + b), 0), a.page_size);
+      }
       int at = have + counts[b];
-      for (int i0 = ceil_div(after_s[b], a.page_size), i1 = ceil_div(keys, a.page_size); i0 < i1; i0 += 32) {
-        const int id = i0 + lane < i1 ? page_at(b, i0 + lane) : -1;
+      for (int i0 = back0; i0 < back1; i0 += 32) {
+        if (!alone || i0 > back0) id = i0 + lane < back1 ? page_at(b, i0 + lane) : -1;
+        id = id < a.num_pages ? id : -1;
         const unsigned int yes = __ballot_sync(0xffffffffu, id >= 0);
         const int to = at + __popc(yes & ((1u << lane) - 1u));
         if (id >= 0) {
@@ -320,6 +340,34 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_move_kernel(const __grid_c
   }
 }
 
+// CTAs of a cluster of paged_accept_kernel at most: 16 where the device has that many SMs side by side for it, so that 512 requests have a
+// warp each.  Asked once per device.
+int widest_cluster(int dev, int& ctas) {
+  static std::atomic<int> known[64];
+  if ((ctas = known[dev].load()) != 0) return ATTN_OK;
+  const size_t smem = 2 * (size_t)ACCEPT_MAX_B * sizeof(int);
+  if (cudaFuncSetAttribute(paged_accept_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return ATTN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(ACCEPT_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  ctas = 8;
+  if (cudaFuncSetAttribute(paged_accept_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&clusters, paged_accept_kernel, &cfg) == cudaSuccess && clusters > 0)
+    ctas = 16;
+  else
+    cudaGetLastError();  // (the answer was no)
+  known[dev].store(ctas);
+  return ATTN_OK;
+}
+
 bool misaligned(const void* ptr, unsigned int to) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
 
 }  // namespace
@@ -373,11 +421,10 @@ int attn_paged_accept(const attn_paged_accept_params_t* params) {
     AcceptParams p{a, nullptr};
     if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
     const size_t smem = 2 * (size_t)a.B * sizeof(int);
-    if (smem > 40 * 1024 &&  // (48 KiB with what the kernel has by itself need no leave)
-        cudaFuncSetAttribute(paged_accept_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * ACCEPT_MAX_B * (int)sizeof(int)) != cudaSuccess)
-      return ATTN_ERR_CUDA;
+    int widest = 0;
+    if ((rc = widest_cluster(dev, widest)) != ATTN_OK) return rc;
     int ctas = 1;
-    while (ctas < ACCEPT_CTAS && ctas * ACCEPT_WARPS < a.B) ctas *= 2;
+    while (ctas < widest && ctas * ACCEPT_WARPS < a.B) ctas *= 2;
     return launch_dependent(paged_accept_kernel, dim3(ctas), ACCEPT_THREADS, smem, reinterpret_cast<cudaStream_t>(a.stream), p, ctas);
   });
 }
