@@ -551,58 +551,57 @@ def _one(t, n):
     return t.shape != (n,) or not t.is_contiguous()
 
 
-def _rope(q, k, v, q_out, k_out, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream):
-    torch = _torch or _with_torch()
-    dtype, index, i32 = q.dtype, q.get_device(), torch.int32
-    code = _dtype_code(q)
-    shape = q.shape
-    Hq, rows, d = shape
+def _refuse_rope(index, dtype, q, k, v, outs, slots, positions, inv_freq, weights):
+    """Raises for what attn_rope and attn_paged_rope cannot take (outs: (tensor, heads, name))."""
+    Hq, rows, d = q.shape
     Hkv = k.shape[0]
-    rot = axes = stride = 0
-    if inv_freq is not None:
-        axes, rot = (1, 2 * inv_freq.shape[0]) if inv_freq.dim() == 1 else (inv_freq.shape[0], 2 * inv_freq.shape[1])
-        wanted = (rows,) if positions is not None and positions.dim() == 1 and axes == 1 else (axes, rows)
-        if (positions is None or positions.dtype is not i32 or positions.get_device() != index or positions.shape != wanted or
-                (rows > 1 and positions.stride(-1) != 1)):
-            raise ValueError(f"positions must be int32 {wanted} on CUDA device {index}, each axis contiguous")
-        if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != index or not inv_freq.is_contiguous():
-            raise ValueError(f"inv_freq must be contiguous fp32 [pairs] or [axes, pairs] on CUDA device {index}")
-        stride = positions.stride(0) if axes > 1 else rows
-    weight = q_weight if q_weight is not None else k_weight
-    f32 = weight is not None and weight.dtype is torch.float32
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype is not (torch.float32 if f32 else dtype) or w.get_device() != index or _one(w, d)):
-            raise ValueError(f"{name} must be a contiguous vector of {d} entries of {dtype} or (both weights) fp32 on CUDA device {index}")
-    qs, ks, qo = q.stride(), k.stride(), q_out.stride()
     kv = (Hkv, rows, d)
-    if (index < 0 or q_out.dtype is not dtype or k.dtype is not dtype or q_out.get_device() != index or k.get_device() != index or
-            q_out.shape != shape or k.shape != kv or not qs[2] == ks[2] == qo[2] == 1):
-        _refuse(index, rows=((q, shape, dtype, "q"), (k, kv, dtype, "k"), (q_out, shape, dtype, "q_out")))
-    if slots is None:
-        vs = cs = (0, 0, 0)
-        num_pages = page_size = 0
-        ko = k_out.stride()
-        if k_out.dtype is not dtype or k_out.get_device() != index or k_out.shape != kv or ko[2] != 1:
-            _refuse(index, rows=((k_out, kv, dtype, "k_out"),))
-    else:
-        vs, cs, ko = v.stride(), k_cache.stride(), (0, 0, 0)
-        if (len(cs) != 4 or k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != index or
-                v_cache.get_device() != index or v_cache.shape != k_cache.shape or v_cache.stride() != cs or cs[3] != 1 or
-                k_cache.shape[1] != Hkv or k_cache.shape[3] != d):
-            _refuse(index, caches=(k_cache, v_cache, dtype, d))
-        num_pages, _, page_size, _ = k_cache.shape
-        if (v.dtype is not dtype or v.get_device() != index or v.shape != kv or vs[2] != 1 or slots.dtype is not i32 or
-                slots.get_device() != index or _one(slots, rows)):
-            _refuse(index, ((slots, rows, "slots"),), rows=((v, kv, dtype, "v"),))
-    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
-    if rows == 0:
-        return
-    at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    _launch(index, (_lib or library()).attn_rope,
-            _ROPE.pack(q.data_ptr(), k.data_ptr(), at(v), q_out.data_ptr(), at(k_out), at(k_cache), at(v_cache), at(q_weight), at(k_weight),
-                       at(positions) if axes else 0, at(slots), at(inv_freq), qs[1], qs[0], ks[1], ks[0], vs[1], vs[0], qo[1], qo[0], ko[1],
-                       ko[0], cs[0], cs[1], cs[2], stride, rows, Hq, Hkv, d, rot, axes, 1 if interleaved else 0, 1 if f32 else 0, num_pages,
-                       page_size, eps, code, handle))
+    if inv_freq is not None:
+        axes = 1 if inv_freq.dim() == 1 else inv_freq.shape[0]
+        wanted = (rows,) if axes == 1 and (positions is None or positions.dim() == 1) else (axes, rows)
+        _refuse(index, others=((positions is None or positions.dtype is not _torch.int32 or positions.get_device() != index or positions.shape != wanted or
+                                (rows > 1 and positions.stride(-1) != 1), f"positions must be int32 {wanted} on CUDA device {index}, each axis contiguous"),
+                               (inv_freq.dtype is not _torch.float32 or inv_freq.get_device() != index or not inv_freq.is_contiguous() or inv_freq.dim() > 2,
+                                f"inv_freq must be contiguous fp32 [pairs] or [axes, pairs] on CUDA device {index}")))
+    f32 = any(w is not None and w.dtype is _torch.float32 for w, _ in weights)
+    for w, name in weights:
+        if w is not None and (w.dtype is not (_torch.float32 if f32 else dtype) or w.get_device() != index or _one(w, d)):
+            raise ValueError(f"{name} must be a contiguous vector of {d} entries of {dtype} or (both weights) fp32 on CUDA device {index}")
+    _refuse(index, () if slots is None else ((slots, rows, "slots"),),
+            rows=((q, (Hq, rows, d), dtype, "q"), (k, kv, dtype, "k")) + (() if v is None else ((v, kv, dtype, "v"),)) +
+            tuple((t, (heads, rows, d), dtype, name) for t, heads, name in outs))
+
+
+def _rope_shared(q, k, positions, inv_freq, q_weight, k_weight, dtype, index, rows, d):
+    """What both calls check and pack alike: (wrong, pairs turned, axes, from an axis to the next, addresses, whether weights are fp32)."""
+    f32 = _torch.float32
+    wrong = k.dtype is not dtype or k.get_device() != index
+    rot = axes = step = at_pos = at_inv = at_q = at_k = 0
+    if inv_freq is not None:
+        shape = inv_freq.shape
+        axes, pairs = (1, shape[0]) if len(shape) == 1 else shape if len(shape) == 2 else (0, 0)
+        rot = 2 * pairs
+        if positions is None:
+            return True, 0, 0, 0, 0, 0, 0, 0, False
+        ps = positions.shape
+        wrong = (wrong or inv_freq.dtype is not f32 or inv_freq.get_device() != index or not inv_freq.is_contiguous() or axes == 0 or
+                 positions.dtype is not _torch.int32 or positions.get_device() != index or
+                 (ps != (axes, rows) if len(ps) != 1 else axes != 1 or ps[0] != rows) or (rows > 1 and positions.stride(-1) != 1))
+        step = positions.stride(0) if axes > 1 and not wrong else rows
+        at_pos, at_inv = positions.data_ptr(), inv_freq.data_ptr()
+    fp32 = False
+    if q_weight is not None:
+        fp32 = q_weight.dtype is f32
+        wrong = (wrong or (not fp32 and q_weight.dtype is not dtype) or q_weight.get_device() != index or q_weight.shape != (d,) or
+                 not q_weight.is_contiguous())
+        at_q = q_weight.data_ptr()
+    if k_weight is not None:
+        mine = k_weight.dtype
+        wrong = (wrong or (mine is not q_weight.dtype if q_weight is not None else mine is not f32 and mine is not dtype) or
+                 k_weight.get_device() != index or k_weight.shape != (d,) or not k_weight.is_contiguous())
+        fp32 = fp32 or mine is f32
+        at_k = k_weight.data_ptr()
+    return wrong, rot, axes, step, at_pos, at_inv, at_q, at_k, fp32
 
 
 def attn_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, stream=None):
@@ -611,37 +610,76 @@ def attn_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=N
     its input.  positions int32 [rows] with inv_freq fp32 [pairs], or [axes, rows] with [axes, pairs], whose columns hold a pair's
     frequency in its axis and 0 elsewhere; pairs are halves' or, interleaved, neighbours', and elements past 2 * pairs are not
     turned.  inv_freq None: norms alone.  A contiguous [B, H, S, d] of shared positions goes in as view(B * H, S, d).  See include/attn.h."""
-    _rope(q, k, None, q_out, k_out, None, None, None, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream)
+    _torch or _with_torch()
+    dtype, index, shape = q.dtype, q.get_device(), q.shape
+    code = _dtype_code(q)
+    Hq, rows, d = shape
+    kv = k.shape
+    Hkv = kv[0]
+    qs, ks, qo, ko = q.stride(), k.stride(), q_out.stride(), k_out.stride()
+    wrong, rot, axes, step, at_pos, at_inv, at_q, at_k, fp32 = _rope_shared(q, k, positions, inv_freq, q_weight, k_weight, dtype, index, rows, d)
+    if (wrong or index < 0 or kv != (Hkv, rows, d) or q_out.shape != shape or k_out.shape != kv or not qs[2] == ks[2] == qo[2] == ko[2] == 1 or
+            not q_out.dtype is k_out.dtype is dtype or not index == q_out.get_device() == k_out.get_device()):
+        _refuse_rope(index, dtype, q, k, None, ((q_out, Hq, "q_out"), (k_out, Hkv, "k_out")), None, positions, inv_freq,
+                     ((q_weight, "q_weight"), (k_weight, "k_weight")))
+    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
+    if rows == 0:
+        return
+    _launch(index, (_lib or library()).attn_rope,
+            _ROPE.pack(q.data_ptr(), k.data_ptr(), 0, q_out.data_ptr(), k_out.data_ptr(), 0, 0, at_q, at_k, at_pos, 0, at_inv, qs[1], qs[0], ks[1], ks[0], 0,
+                       0, qo[1], qo[0], ko[1], ko[0], 0, 0, 0, step, rows, Hq, Hkv, d, rot, axes, 1 if interleaved else 0, fp32, 0, 0, eps, code, handle))
 
 
 def attn_paged_rope(q, k, v, q_out, k_cache, v_cache, slots, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                     stream=None):
     """attn_rope whose keys go, with the values v [Hkv, rows, d], to their slots (int32 [rows]) of the caches [num_pages, Hkv, page_size, d];
     rows of negative slots are left out, of q_out too.  See include/attn.h."""
-    _rope(q, k, v, q_out, None, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream)
+    i32 = (_torch or _with_torch()).int32
+    dtype, index, shape = q.dtype, q.get_device(), q.shape
+    code = _dtype_code(q)
+    Hq, rows, d = shape
+    kv = k.shape
+    Hkv = kv[0]
+    cache, cs = k_cache.shape, k_cache.stride()
+    if (index < 0 or len(cs) != 4 or k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != index or
+            v_cache.get_device() != index or v_cache.shape != cache or v_cache.stride() != cs or cs[3] != 1 or cache[1] != Hkv or cache[3] != d):
+        _refuse(index, caches=(k_cache, v_cache, dtype, d))
+    qs, ks, vs, qo = q.stride(), k.stride(), v.stride(), q_out.stride()
+    wrong, rot, axes, step, at_pos, at_inv, at_q, at_k, fp32 = _rope_shared(q, k, positions, inv_freq, q_weight, k_weight, dtype, index, rows, d)
+    if (wrong or kv != (Hkv, rows, d) or q_out.shape != shape or v.shape != kv or not qs[2] == ks[2] == qo[2] == vs[2] == 1 or
+            not q_out.dtype is v.dtype is dtype or not index == q_out.get_device() == v.get_device() == slots.get_device() or slots.dtype is not i32 or
+            slots.shape != (rows,) or not slots.is_contiguous()):
+        _refuse_rope(index, dtype, q, k, v, ((q_out, Hq, "q_out"),), slots, positions, inv_freq, ((q_weight, "q_weight"), (k_weight, "k_weight")))
+    handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
+    if rows == 0:
+        return
+    _launch(index, (_lib or library()).attn_rope,
+            _ROPE.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), 0, k_cache.data_ptr(), v_cache.data_ptr(), at_q, at_k, at_pos,
+                       slots.data_ptr(), at_inv, qs[1], qs[0], ks[1], ks[0], vs[1], vs[0], qo[1], qo[0], 0, 0, cs[0], cs[1], cs[2], step, rows, Hq, Hkv, d,
+                       rot, axes, 1 if interleaved else 0, fp32, cache[0], cache[2], eps, code, handle))
 
 
 def attn_paged_tree(parents, cu_seqlens_q, seqlens_k, positions, tree_mask, window_left=-1, stream=None):
     """Positions (context + depth) and ancestor masks of drafted trees.  int32 device tensors: parents [rows] (number of the node above
     among the request's nodes, -1: none), cu_seqlens_q [B+1], seqlens_k [B] -> positions [rows], tree_mask [rows, words].  Requests of
     more than 32 * words nodes are chunks: chains without a mask.  See include/attn.h."""
-    torch = _torch or _with_torch()
-    i32, index = torch.int32, parents.get_device()
-    (rows,), (B,) = parents.shape, seqlens_k.shape
+    i32, index = (_torch or _with_torch()).int32, parents.get_device()
+    many, one, mask = parents.shape, seqlens_k.shape, tree_mask.shape
+    (rows,), (B,) = many, one
     if (index < 0 or not parents.dtype is cu_seqlens_q.dtype is seqlens_k.dtype is positions.dtype is tree_mask.dtype is i32 or
             not index == cu_seqlens_q.get_device() == seqlens_k.get_device() == positions.get_device() == tree_mask.get_device() or
-            _one(parents, rows) or _one(cu_seqlens_q, B + 1) or _one(seqlens_k, B) or _one(positions, rows) or tree_mask.dim() != 2 or
-            tree_mask.shape[0] != rows or (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1)):
+            not (parents.is_contiguous() and cu_seqlens_q.is_contiguous() and seqlens_k.is_contiguous() and positions.is_contiguous()) or
+            cu_seqlens_q.shape != (B + 1,) or positions.shape != many or len(mask) != 2 or mask[0] != rows or
+            (mask[1] > 1 and tree_mask.stride(1) != 1)):
         _refuse(index, ((parents, rows, "parents"), (cu_seqlens_q, B + 1, "cu_seqlens_q"), (seqlens_k, B, "seqlens_k"),
                         (positions, rows, "positions")),
                 others=((True, f"tree_mask must be int32 [{rows}, words] on CUDA device {index}, each row contiguous"),))
     handle = _raw_stream(index) if stream is None else _stream_on(index, stream)
     if rows == 0:
         return
-    words = tree_mask.shape[1]
     _launch(index, (_lib or library()).attn_paged_tree,
             _TREE.pack(parents.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), positions.data_ptr(), tree_mask.data_ptr(), B, rows,
-                       words, tree_mask.stride(0) if rows > 1 else words, window_left, handle))
+                       mask[1], tree_mask.stride(0) if rows > 1 else mask[1], window_left, handle))
 
 
 def attn_paged_accept(tokens, targets, parents, cu_seqlens_q, seqlens_k, block_table, free_pages, free_count, page_size, num_pages, accepted,
@@ -653,40 +691,41 @@ def attn_paged_accept(tokens, targets, parents, cu_seqlens_q, seqlens_k, block_t
     block_table [B, W], confirmed [B] (leading nodes that are known; None: 1 each) -> accepted, ctx_lens, next_tokens [B], path, src_slots,
     dst_slots [B, max path] (-1 behind the last; the slots are attn_paged_move's).  Pages without a token go back to free_pages [F] behind
     its free_count [1] ids, free_count_out [1] (default: free_count itself) counts them; free_pages None: they do not.  See include/attn.h."""
-    torch = _torch or _with_torch()
-    i32, index = torch.int32, tokens.get_device()
-    (rows,), (B,), lists = tokens.shape, seqlens_k.shape, path.shape
-    width = block_table.shape[-1]
+    i32, index = (_torch or _with_torch()).int32, tokens.get_device()
+    many, one, lists, width = tokens.shape, seqlens_k.shape, path.shape, block_table.shape[-1]
+    (rows,), (B,) = many, one
     if (index < 0 or not tokens.dtype is targets.dtype is parents.dtype is cu_seqlens_q.dtype is seqlens_k.dtype is block_table.dtype is
             accepted.dtype is ctx_lens.dtype is next_tokens.dtype is path.dtype is src_slots.dtype is dst_slots.dtype is i32 or
             not index == targets.get_device() == parents.get_device() == cu_seqlens_q.get_device() == seqlens_k.get_device() ==
             block_table.get_device() == accepted.get_device() == ctx_lens.get_device() == next_tokens.get_device() == path.get_device() ==
             src_slots.get_device() == dst_slots.get_device() or
-            _one(tokens, rows) or _one(targets, rows) or _one(parents, rows) or _one(cu_seqlens_q, B + 1) or _one(seqlens_k, B) or
-            _one(accepted, B) or _one(ctx_lens, B) or _one(next_tokens, B) or len(lists) != 2 or lists[0] != B or
-            not lists == src_slots.shape == dst_slots.shape or
-            not (path.is_contiguous() and src_slots.is_contiguous() and dst_slots.is_contiguous()) or
+            not many == targets.shape == parents.shape or not one == accepted.shape == ctx_lens.shape == next_tokens.shape or
+            cu_seqlens_q.shape != (B + 1,) or len(lists) != 2 or lists[0] != B or not lists == src_slots.shape == dst_slots.shape or
+            not (tokens.is_contiguous() and targets.is_contiguous() and parents.is_contiguous() and cu_seqlens_q.is_contiguous() and
+                 seqlens_k.is_contiguous() and accepted.is_contiguous() and ctx_lens.is_contiguous() and next_tokens.is_contiguous() and
+                 path.is_contiguous() and src_slots.is_contiguous() and dst_slots.is_contiguous()) or
             block_table.dim() != 2 or block_table.shape[0] != B or (block_table.stride(1) != 1 and width > 1)):
         _refuse(index, ((tokens, rows, "tokens"), (targets, rows, "targets"), (parents, rows, "parents"), (cu_seqlens_q, B + 1, "cu_seqlens_q"),
                         (seqlens_k, B, "seqlens_k"), (accepted, B, "accepted"), (ctx_lens, B, "ctx_lens"), (next_tokens, B, "next_tokens")),
                 (block_table, B), others=((True, f"path, src_slots and dst_slots must be contiguous int32 [{B}, max path] on CUDA device {index}"),))
-    free = 0
+    free = at_free = at_count = at_left = at_sure = 0
     if free_pages is not None:
         (free,) = free_pages.shape
+        left = free_count if free_count_out is None else free_count_out
         if free == 0:
             raise ValueError("free_pages must have room for one page at least (None: no page goes back)")
-        if free_count_out is None:
-            free_count_out = free_count
-        if (free_pages.dtype is not i32 or free_count.dtype is not i32 or free_count_out.dtype is not i32 or
-                not index == free_pages.get_device() == free_count.get_device() == free_count_out.get_device() or
-                _one(free_pages, free) or _one(free_count, 1) or _one(free_count_out, 1)):
-            _refuse(index, ((free_pages, free, "free_pages"), (free_count, 1, "free_count"), (free_count_out, 1, "free_count_out")))
-    if confirmed is not None and (confirmed.dtype is not i32 or confirmed.get_device() != index or _one(confirmed, B)):
-        _refuse(index, ((confirmed, B, "confirmed"),))
+        if (not free_pages.dtype is free_count.dtype is left.dtype is i32 or
+                not index == free_pages.get_device() == free_count.get_device() == left.get_device() or not free_pages.is_contiguous() or
+                free_count.shape != (1,) or left.shape != (1,)):
+            _refuse(index, ((free_pages, free, "free_pages"), (free_count, 1, "free_count"), (left, 1, "free_count_out")))
+        at_free, at_count, at_left = free_pages.data_ptr(), free_count.data_ptr(), left.data_ptr()
+    if confirmed is not None:
+        if confirmed.dtype is not i32 or confirmed.get_device() != index or confirmed.shape != one or not confirmed.is_contiguous():
+            _refuse(index, ((confirmed, B, "confirmed"),))
+        at_sure = confirmed.data_ptr()
     _launch(index, (_lib or library()).attn_paged_accept,
-            _ACCEPT.pack(tokens.data_ptr() if rows else 0, targets.data_ptr() if rows else 0, parents.data_ptr() if rows else 0, 0 if confirmed is None else confirmed.data_ptr(),
-                         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), free_pages.data_ptr() if free else 0,
-                         free_count.data_ptr() if free else 0, free_count_out.data_ptr() if free else 0, accepted.data_ptr(),
+            _ACCEPT.pack(tokens.data_ptr() if rows else 0, targets.data_ptr() if rows else 0, parents.data_ptr() if rows else 0, at_sure,
+                         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), at_free, at_count, at_left, accepted.data_ptr(),
                          ctx_lens.data_ptr(), next_tokens.data_ptr(), path.data_ptr(), src_slots.data_ptr(), dst_slots.data_ptr(), B, rows,
                          lists[1], width, block_table.stride(0) if B > 1 else width, free, page_size, num_pages,
                          _raw_stream(index) if stream is None else _stream_on(index, stream)))

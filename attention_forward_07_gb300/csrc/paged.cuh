@@ -28,7 +28,7 @@ namespace attn {
 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr long long MAX_STRIDE = 1ll << 38;  // elements: no memory holds two entries that far apart, and tensor maps end there
-constexpr int NO_PLAN_UNITS = 2048;  // (attn_fwd_paged_tree) units that they may have at most
+constexpr int NO_PLAN_UNITS = 2048, NO_PLAN_CHUNK = 32;  // (attn_fwd_paged_tree) units that they, and that one of them, may have at most
 constexpr int NO_PLAN_B = 512;  // requests at most whose lengths every CTA looks at (16 to a lane)
 constexpr int ROWS_MAX = 16, ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile

@@ -177,7 +177,8 @@ ATTEND = [
     ([256], [640], 1, 1, 64, "f16", 256, 8, 200, {}), ([40, 1, 64], [400, 64, 127], 32, 1, 128, "bf16", 16, 2, -1, {}),
     # chunks beside trees
     ([20, 300, 1, 33, 0, 32], [700, 500, 64, 33, 5, 90], 4, 2, 128, "bf16", 16, 1, -1, dict(spare_rows=5)),
-    ([10, 200, 3], [300, 260, 1500], 8, 1, 64, "f16", 32, 1, 90, {}), ([65, 64, 2, 400], [200, 70, 300, 410], 2, 2, 128, "f16", 48, 2, 130, {})]
+    ([10, 200, 3], [300, 260, 1500], 8, 1, 64, "f16", 32, 1, 90, {}), ([20, 1100, 3], [300, 1200, 50], 8, 1, 64, "bf16", 16, 1, -1, {}),
+    ([31, 1, 530], [70, 20, 600], 16, 1, 128, "f16", 64, 1, 300, {}), ([65, 64, 2, 400], [200, 70, 300, 410], 2, 2, 128, "f16", 48, 2, 130, {})]
 
 
 def _run_attend(bt, words, wl, scale, mask, pos, stride=0, max_q=None, dev=None, **kw):
