@@ -201,7 +201,7 @@ def attn_strerror(status: int) -> str:
 
 
 def _dtype_code(t) -> int:
-    import torch
+    torch = _torch or _with_torch()
     if t.dtype == torch.float16:
         return ATTN_F16
     if t.dtype == torch.bfloat16:
