@@ -719,18 +719,18 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
 // flight at a time.
 constexpr int JOIN_WARPS = JOIN_ROWS, JOIN_AHEAD = 4;
 
-template <int D, bool BF16>
+template <int D, bool BF16, int AHEAD>
 __device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& jn) {
   const int r = threadIdx.x % JOIN_ROWS, col = threadIdx.x / JOIN_ROWS * 4;
   static_assert(D / 4 <= 32 * JOIN_WARPS / JOIN_ROWS, "a thread to four columns of a row");
   if (r >= jn.rows || col >= D) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < jn.parts; k0 += JOIN_AHEAD) {
-    float2 ml[JOIN_AHEAD];
-    float4 v[JOIN_AHEAD];
+  for (int k0 = 0; k0 < jn.parts; k0 += AHEAD) {
+    float2 ml[AHEAD];
+    float4 v[AHEAD];
 #pragma unroll
-    for (int a = 0; a < JOIN_AHEAD; ++a) {
+    for (int a = 0; a < AHEAD; ++a) {
       const int k = k0 + a, slot = 2 * (jn.run + k) + (k == 0);
       ml[a] = make_float2(-INFINITY, 0.f);
       v[a] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -741,12 +741,12 @@ __device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& j
     }
     float mn = m;
 #pragma unroll
-    for (int a = 0; a < JOIN_AHEAD; ++a) mn = fmaxf(mn, ml[a].x);
+    for (int a = 0; a < AHEAD; ++a) mn = fmaxf(mn, ml[a].x);
     const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
     l *= f;
     acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-    for (int a = 0; a < JOIN_AHEAD; ++a) {
+    for (int a = 0; a < AHEAD; ++a) {
       const float fa = ml[a].x == -INFINITY ? 0.f : ex2_approx(ml[a].x - mn);
       l = fmaf(ml[a].y, fa, l);
       acc = make_float4(fmaf(v[a].x, fa, acc.x), fmaf(v[a].y, fa, acc.y), fmaf(v[a].z, fa, acc.z), fmaf(v[a].w, fa, acc.w));
@@ -758,6 +758,16 @@ __device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& j
   *reinterpret_cast<uint2*>(p.o + (long long)(jn.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
       make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
   if (col == 0 && p.lse) p.lse[(long long)hq * p.total_q + jn.row0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+}
+
+// Joins of attn_fwd_paged_tree without a plan, 16 rows to a CTA.  Many pairs (MANY) are cut once or twice: CTAs in flight count, parts of a row
+// do not (24 trees of 40 - 64 nodes against 8k keys: 107 us; with twice the parts ahead and half the CTAs 111).  Few pairs lie in many
+// pieces: the other way round (26 nodes against 2000 keys: 16.2 us, like the others 18.3).
+template <int D, bool BF16, bool MANY>
+__global__ void __launch_bounds__(32 * JOIN_WARPS, MANY ? 4 : 2) tree_join_kernel(const __grid_constant__ RowsParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  join_unit<D, BF16, MANY ? 2 : 4>(p, p.tile.joins[blockIdx.x]);
 }
 
 template <int D, bool BF16>
@@ -772,7 +782,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
   const int total = items + (p.tile.no_plan ? p.tile.no_plan : p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
     if (x >= items) {
-      join_unit<D, BF16>(p, p.tile.joins[x - items]);
+      join_unit<D, BF16, JOIN_AHEAD>(p, p.tile.joins[x - items]);
       continue;
     }
     const int c = x / halves, prow = x % halves * JOIN_ROWS;
@@ -943,6 +953,10 @@ int launch_rows(const RowsParams& p, const attn_fwd_paged_params_t& a, const Pla
   if (rc == ATTN_OK && !p.tile.no_plan) rc = launch_dependent(rows_kernel<D, MT, BF16, TREE>, dim3(plan.rows_grid + (tiles ? 1 : 0)), C::NTHREADS, C::SMEM, st, p);
   if (rc == ATTN_OK && tiles) rc = tile_launch(tp, a, sms, dev, st);
   if (rc != ATTN_OK) return rc;
+  if (TREE && p.tile.no_plan) {
+    const bool many = (long long)p.B * p.Hkv * ((p.max_q + TILE_QT * p.tile.T - 1) / (TILE_QT * p.tile.T)) > sms;
+    return launch_dependent(many ? tree_join_kernel<D, BF16, true> : tree_join_kernel<D, BF16, false>, dim3(p.tile.no_plan), 32 * JOIN_WARPS, 0, st, p);
+  }
   const int joins = p.tile.no_plan ? p.tile.no_plan : plan.rows_grid;
   return launch_dependent(join_kernel<D, BF16>, dim3(joins), 32 * JOIN_WARPS, 0, st, p);
 }
