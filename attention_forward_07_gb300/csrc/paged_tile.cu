@@ -617,6 +617,109 @@ struct KeptBits {
   }
 };
 
+__device__ __forceinline__ void tmem_load_wait(uint32_t taddr, uint32_t (&r)[64]) { tmem_ld32x32b_x64_wait(taddr, r); }
+__device__ __forceinline__ void tmem_load_wait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr) : "memory");
+}
+
+// Scores of the columns that a row does not keep become -inf where they are.
+__device__ __forceinline__ void exclude(uint32_t s_addr, const KeptBits& kept) {
+#pragma unroll 1
+  for (int h = 0; h < BN / 16; ++h) {
+    const uint32_t pair = h < 4 ? (h < 2 ? kept.w[0] : kept.w[1]) : h < 6 ? kept.w[2] : kept.w[3], w = pair >> (h & 1) * 16;
+    uint32_t r[16];
+    tmem_ld32x32b_x16_wait(s_addr + h * 16, r);
+#pragma unroll
+    for (int cc = 0; cc < 16; ++cc)
+      if (!(w >> cc & 1u)) r[cc] = __float_as_uint(-INFINITY);
+    tmem_st32x32b_x16(s_addr + h * 16, r);
+  }
+  tmem_wait_st();
+}
+
+// softmax_tile (roles.cuh) with its loops rolled: the scores are read twice, TREE_COLS columns at a time.
+constexpr int TREE_COLS = 64;
+template <int D, bool BF16, class L>
+__device__ __forceinline__ bool tree_softmax_tile(uint32_t s_addr, uint32_t o_addr, float c, uint32_t opv_bar, int np, int nact, volatile int* abort_flag,
+                                                  uint32_t to, float& m, float& l) {
+  const auto load = [&](int h, uint32_t(&r)[TREE_COLS]) {
+    tmem_load_wait(s_addr + h * TREE_COLS, r);
+  };
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < BN / TREE_COLS; ++h) {
+    uint32_t r[TREE_COLS];
+    load(h, r);
+    float a4[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      constexpr int N = TREE_COLS / 4;
+      a4[x] = fmaxf(__uint_as_float(r[N * x]), __uint_as_float(r[N * x + 1]));
+#pragma unroll
+      for (int e = 2; e < N; e += 2) a4[x] = fmax3(a4[x], __uint_as_float(r[N * x + e]), __uint_as_float(r[N * x + e + 1]));
+    }
+    mx = fmaxf(mx, fmax3(a4[0], a4[1], fmaxf(a4[2], a4[3])));
+  }
+  const float mx_s = mx * c;
+  const bool grow = mx_s > m + 8.f;  // also true on the first kept key (m = -inf)
+  const float m_new = grow ? mx_s : m;
+  const float alpha = grow ? ex2_approx(m - m_new) : 1.f;
+  const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+  if (nact > 0 && __any_sync(0xffffffffu, grow)) {
+    if constexpr (L::RING) {
+      if (!bwait_warp(opv_bar, (uint32_t)(np - 1) & 1u, abort_flag, to)) return false;
+      tc_fence_after();
+    }
+    const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16; ++ch) {
+      uint32_t ob[16];
+      tmem_ld32x32b_x16_wait(o_addr + ch * 16, ob);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        float lo, hi;
+        f2_unpack(fmul2(f2_pack(__uint_as_float(ob[2 * x]), __uint_as_float(ob[2 * x + 1])), a2), lo, hi);
+        ob[2 * x] = __float_as_uint(lo);
+        ob[2 * x + 1] = __float_as_uint(hi);
+      }
+      tmem_st32x32b_x16(o_addr + ch * 16, ob);
+    }
+  }
+  const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+  for (int h = 0; h < BN / TREE_COLS; ++h) {
+    uint32_t r[TREE_COLS];
+    load(h, r);
+#pragma unroll
+    for (int x = 0; x < TREE_COLS / 32; ++x) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int cc = 0; cc < 16; ++cc) {
+        float e0, e1;
+        f2_unpack(ffma2(f2_pack(__uint_as_float(r[32 * x + 2 * cc]), __uint_as_float(r[32 * x + 2 * cc + 1])), c2, nm2), e0, e1);
+        const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+        acc[cc & 3] = fadd2(acc[cc & 3], f2_pack(p0, p1));
+        pk[cc] = pack2<BF16>(p0, p1);
+      }
+      // (over columns that have been read)
+      tmem_st32x32b_x16(s_addr + (h * (TREE_COLS / 32) + x) * 16, pk);
+    }
+  }
+  tmem_wait_st();
+  float s0, s1, s2, s3, s4, s5, s6, s7;
+  f2_unpack(acc[0], s0, s1);
+  f2_unpack(acc[1], s2, s3);
+  f2_unpack(acc[2], s4, s5);
+  f2_unpack(acc[3], s6, s7);
+  l = l * alpha + (((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7)));
+  m = m_new;
+  return true;
+}
+
 template <int D, bool BF16, bool TURNS, bool TREE>
 __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t base, uint8_t* gbase, volatile int* abort_flag, uint32_t tmem,
                                                   int t, int quarter, int lane) {
@@ -697,28 +800,26 @@ __device__ __forceinline__ void tile_softmax_role(const TileParams& p, uint32_t 
       if (!bwait_warp(bars + 8u * (L::B_STILE + L::sp_bar(t, np)), spar, abort_flag, to)) return;
       if constexpr (!L::RING) s_par ^= 1u;
       tc_fence_after();
-      const auto make_mask = [&] {
-        const int hi = khi - j * BN, lo = klo - j * BN;
-        const bool edge = __any_sync(0xffffffffu, hi < BN || lo > 0);
-        if constexpr (TREE) {
-          KeptBits kept(0, BN, nullptr, 0, 0, 0);
-          if (edge) kept = KeptBits(lo, hi, mask, p.tree_words, mask_at - j * BN, nodes);
+      const int hi = khi - j * BN, lo = klo - j * BN;
+      const bool edge = __any_sync(0xffffffffu, hi < BN || lo > 0);
+      if constexpr (TREE) {
+        if (edge) {
+          const KeptBits kept(lo, hi, mask, p.tree_words, mask_at - j * BN, nodes);
+          exclude(s_addr, kept);
+        }
+        if (!tree_softmax_tile<D, BF16, L>(s_addr, o_addr, c, bars + 8u * (L::B_OPV + t), np, nact, abort_flag, to, m, l)) return;
+      } else {
+        const auto make_mask = [&] {
           return [=](uint32_t(&x)[64], int c0) {
             if (edge) {
 #pragma unroll
               for (int cc = 0; cc < 64; ++cc)
-                if (!(kept.w[(c0 + cc) / 32] >> (cc % 32) & 1u)) x[cc] = __float_as_uint(-INFINITY);
+                if (c0 + cc >= hi || c0 + cc < lo) x[cc] = __float_as_uint(-INFINITY);
             }
           };
-        } else return [=](uint32_t(&x)[64], int c0) {
-          if (edge) {
-#pragma unroll
-            for (int cc = 0; cc < 64; ++cc)
-              if (c0 + cc >= hi || c0 + cc < lo) x[cc] = __float_as_uint(-INFINITY);
-          }
         };
-      };
-      if (!softmax_tile<D, BF16, L>(s_addr, o_addr, c, make_mask, bars + 8u * (L::B_OPV + t), np, nact, abort_flag, to, m, l)) return;
+        if (!softmax_tile<D, BF16, L>(s_addr, o_addr, c, make_mask, bars + 8u * (L::B_OPV + t), np, nact, abort_flag, to, m, l)) return;
+      }
       tc_fence_before();
       mbar_arrive(bars + 8u * (L::B_PREADY + L::sp_bar(t, np)));
       ++nact;
@@ -973,24 +1074,23 @@ int tile_prepare(const PagedParams& base, const attn_fwd_paged_params_t& a, Tile
   return ATTN_OK;
 }
 
-template <bool TREE>
-int launch_any(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
+int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
   const bool bf16 = a.dtype == ATTN_BF16;
   // Where no request has more rows than one Q tile, both Q tiles take the same rows and the key tiles by turns,
   // so that one's products run while the other's softmax does.  24 requests of 3 - 6 tokens x 8 heads
   // against up to 6k keys, when their start took longer: 45 us by turns, 51 with the second Q tile idle.
   const bool turns = p.max_q <= p.tile.T;
   const auto go = [&](auto launch) { return launch(p, sms, dev, st); };
-  if (a.d == 64) {
-    if (turns) return go(bf16 ? launch_tiles<64, true, true, TREE> : launch_tiles<64, false, true, TREE>);
-    return go(bf16 ? launch_tiles<64, true, false, TREE> : launch_tiles<64, false, false, TREE>);
+  if (p.tree) {  // (not by turns: 24 trees of 5 - 16 nodes x 8 heads against 8k keys, d = 128 / 64: 59.5 / 42.7 us, by turns 60.8 / 45.5)
+    if (a.d == 64) return go(bf16 ? launch_tiles<64, true, false, true> : launch_tiles<64, false, false, true>);
+    return go(bf16 ? launch_tiles<128, true, false, true> : launch_tiles<128, false, false, true>);
   }
-  if (turns) return go(bf16 ? launch_tiles<128, true, true, TREE> : launch_tiles<128, false, true, TREE>);
-  return go(bf16 ? launch_tiles<128, true, false, TREE> : launch_tiles<128, false, false, TREE>);
-}
-
-int tile_launch(const TileParams& p, const attn_fwd_paged_params_t& a, int sms, int dev, cudaStream_t st) {
-  return p.tree ? launch_any<true>(p, a, sms, dev, st) : launch_any<false>(p, a, sms, dev, st);
+  if (a.d == 64) {
+    if (turns) return go(bf16 ? launch_tiles<64, true, true, false> : launch_tiles<64, false, true, false>);
+    return go(bf16 ? launch_tiles<64, true, false, false> : launch_tiles<64, false, false, false>);
+  }
+  if (turns) return go(bf16 ? launch_tiles<128, true, true, false> : launch_tiles<128, false, true, false>);
+  return go(bf16 ? launch_tiles<128, true, false, false> : launch_tiles<128, false, false, false>);
 }
 
 }  // namespace attn
