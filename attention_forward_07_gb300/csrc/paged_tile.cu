@@ -157,16 +157,17 @@ __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane
 }
 
 // ------------------------------------------------------------------ runs of attn_fwd_paged_tree without a plan
-// Requests have any number of units here.  A key tile takes BOTH_COST positions of the line where both Q tiles have rows; where one has, as
-// many at d = 128, whose keys come no faster (24 trees of 40 - 64 nodes x 8 heads: 113 us, with three quarters 119), three quarters at
-// d = 64 (30 trees beside two chunks: 89 us, with as many 94).  Where the pieces of every (unit, head) pair, at most `piece`
-// positions long, find a CTA each, all runs are one piece (a pair's length is rounded up to full pieces): no CTA then starts and ends
-// twice, and few keys are spread over all SMs (26 nodes against 2000 keys, 8 heads: 16.8 us, 21.2 with runs of eight tiles).  Otherwise
-// the line is cut into runs that differ by a position at most, with PAIR_COST positions for a pair's start and end.  The host sees
-// to it that the line's positions fit 31 bits.  All loops stay loops: with two copies of this code, unrolled, the kernel outgrew the
-// instruction cache and took a third longer.  (Taking key tiles by turns in units of one Q tile, beside others, was slower: 122 us for
-// 112, 106 for 94.)
-constexpr int BOTH_COST = 4, PAIR_COST = 10, MIN_TREE_RUN = BOTH_COST * MIN_RUN, MIN_PIECE = 2 * BOTH_COST;
+// Requests have any number of units here.  A key tile takes BOTH_COST positions of the line where both Q tiles have rows; where one has,
+// seven eighths of that at d = 128, whose keys come hardly faster, three quarters at d = 64 (with as many: 24 trees of 40 - 64 nodes x 8
+// heads at d = 128 103 us for 101, 30 trees beside two chunks at d = 64 80 for 76).  Where the pieces of every (unit, head) pair, at
+// most `piece` positions long, find a CTA each, all runs are one piece (a pair's length is rounded up to full pieces): no CTA
+// then starts and ends twice, and few keys are spread over all SMs (26 nodes against 2000 keys, 8 heads: 16.8 us, 21.2 with runs of eight
+// tiles).  Otherwise the line is cut into runs that differ by a position at most, with PAIR_COST positions for a pair's start and end
+// (12 - 28: within 2 %).  The host sees to it that the line's positions fit 31 bits.  All loops stay loops: with two copies of this
+// code, unrolled, the kernel outgrew the instruction cache and took a third longer.
+constexpr int BOTH_COST = 8, PAIR_COST = 16, MIN_TREE_RUN = BOTH_COST * MIN_RUN;
+template <int D>
+constexpr int ONE_COST = D == 128 ? 7 : 6;
 struct TreeRun {
   int piece, cost;        // piece: 1 for equal runs; cost: of a pair's start and end
   int runs, each, longer; // the first `longer` runs have each + 1 positions, the others `each`
@@ -189,7 +190,7 @@ __device__ __forceinline__ void tree_unit(const TileParams& p, int b, int blk, T
   x.blk = blk;
   x.j0 = k0 / TILE_KEYS;
   x.w = max((k1 + TILE_KEYS - 1) / TILE_KEYS - x.j0, 1);
-  x.pad = x.sq - blk * TILE_QT * p.tile.T > p.tile.T || D == 128 ? BOTH_COST : 3;  // positions of a tile
+  x.pad = x.sq - blk * TILE_QT * p.tile.T > p.tile.T ? BOTH_COST : ONE_COST<D>;  // positions of a tile
 }
 // By a warp; false where there are fewer runs.
 template <int D>
@@ -238,7 +239,7 @@ __device__ __forceinline__ bool tree_run(const TileParams& p, int run, int lane,
     if (pass == 0) {
       // pieces of this length find a CTA each (every pair has at most one that is not full)
       units = __reduce_add_sync(0xffffffffu, units);
-      const int room = sms - units, piece = max((line + room - 1) / max(room, 1), MIN_PIECE);
+      const int room = sms - units, piece = max((line + room - 1) / max(room, 1), 2 * ONE_COST<D>);
       if (room > 0 && piece <= line / sms + PAIR_COST) r.piece = piece;
       else r.cost = PAIR_COST;
       continue;
