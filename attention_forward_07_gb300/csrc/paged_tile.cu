@@ -400,8 +400,7 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
               mbar_arrive(bars + 8u * (L::B_IFULL + ie));
             }
             __syncwarp();
-            tree_join_list<D>(p, tr, first_b, first_blk, first_h, first_in, lane);
-            return;
+            goto finish;
           }
           tree_unit<D>(p, tr.b, tr.blk, un);
           // the tiles of the pair's positions [in, out): a tile goes with its last position
@@ -573,6 +572,11 @@ drain:
       if ((q_pend >> s) & 1u) wait_drain(bars + 8u * (L::B_QFULL + s), (q_pend_par >> s) & 1u);
   }
   __syncwarp();
+finish:
+  // (after an abort, too: the join's kernel reads the list whatever has happened)
+  if constexpr (TREE) {
+    if (no_plan) tree_join_list<D>(p, tr, first_b, first_blk, first_h, first_in, lane);
+  }
 }
 
 // What the MMA warp does beside its multiplications: it zeroes the rows of a V tile that no query row
