@@ -719,18 +719,18 @@ __global__ void __launch_bounds__(Rows<D, MT>::NTHREADS, Rows<D, MT>::CTAS_PER_S
 // flight at a time.
 constexpr int JOIN_WARPS = JOIN_ROWS, JOIN_AHEAD = 4;
 
-template <int D, bool BF16, int AHEAD>
+template <int D, bool BF16>
 __device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& jn) {
   const int r = threadIdx.x % JOIN_ROWS, col = threadIdx.x / JOIN_ROWS * 4;
   static_assert(D / 4 <= 32 * JOIN_WARPS / JOIN_ROWS, "a thread to four columns of a row");
   if (r >= jn.rows || col >= D) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < jn.parts; k0 += AHEAD) {
-    float2 ml[AHEAD];
-    float4 v[AHEAD];
+  for (int k0 = 0; k0 < jn.parts; k0 += JOIN_AHEAD) {
+    float2 ml[JOIN_AHEAD];
+    float4 v[JOIN_AHEAD];
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
+    for (int a = 0; a < JOIN_AHEAD; ++a) {
       const int k = k0 + a, slot = 2 * (jn.run + k) + (k == 0);
       ml[a] = make_float2(-INFINITY, 0.f);
       v[a] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -741,12 +741,12 @@ __device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& j
     }
     float mn = m;
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) mn = fmaxf(mn, ml[a].x);
+    for (int a = 0; a < JOIN_AHEAD; ++a) mn = fmaxf(mn, ml[a].x);
     const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
     l *= f;
     acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
+    for (int a = 0; a < JOIN_AHEAD; ++a) {
       const float fa = ml[a].x == -INFINITY ? 0.f : ex2_approx(ml[a].x - mn);
       l = fmaf(ml[a].y, fa, l);
       acc = make_float4(fmaf(v[a].x, fa, acc.x), fmaf(v[a].y, fa, acc.y), fmaf(v[a].z, fa, acc.z), fmaf(v[a].w, fa, acc.w));
@@ -760,14 +760,60 @@ __device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& j
   if (col == 0 && p.lse) p.lse[(long long)hq * p.total_q + jn.row0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
-// Joins of attn_fwd_paged_tree without a plan, 16 rows to a CTA.  Many pairs (MANY) are cut once or twice: CTAs in flight count, parts of a row
-// do not (24 trees of 40 - 64 nodes against 8k keys: 107 us; with twice the parts ahead and half the CTAs 111).  Few pairs lie in many
-// pieces: the other way round (26 nodes against 2000 keys: 16.2 us, like the others 18.3).
+// Joins of attn_fwd_paged_tree without a plan: 16 rows to a CTA, eight columns of a row to a thread (with four, what a row costs weighed more
+// than its columns).  Many pairs (MANY) are cut once or twice: CTAs in flight count, parts of a row do not.  Few pairs lie in many
+// pieces: the other way round.  With join_unit for both: 24 trees of 40 - 64 nodes against 8k keys 113 us, now 98; 26 nodes against 2000
+// keys 16.7, now 15.6.
 template <int D, bool BF16, bool MANY>
-__global__ void __launch_bounds__(32 * JOIN_WARPS, MANY ? 4 : 2) tree_join_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(JOIN_ROWS * D / 8, (MANY ? 6 : 2) * 128 / D) tree_join_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int AHEAD = MANY ? 2 : 4;
   grid_launch_dependents();
   grid_dependency_wait();
-  join_unit<D, BF16, MANY ? 2 : 4>(p, p.tile.joins[blockIdx.x]);
+  const TileJoin jn = p.tile.joins[blockIdx.x];
+  const int r = threadIdx.x % JOIN_ROWS, col = threadIdx.x / JOIN_ROWS * 8;
+  if (r >= jn.rows) return;
+  float m = -INFINITY, l = 0.f, acc[8] = {};
+  for (int k0 = 0; k0 < jn.parts; k0 += AHEAD) {
+    float2 ml[AHEAD];
+    float4 v[AHEAD][2];
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const int k = k0 + a, slot = 2 * (jn.run + k) + (k == 0);
+      ml[a] = make_float2(-INFINITY, 0.f);
+      v[a][0] = v[a][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < jn.parts) {
+        ml[a] = p.tile.part_ml[(long long)slot * (TILE_QT * TILE_ROWS) + jn.in + r];
+        v[a][0] = *reinterpret_cast<const float4*>(p.tile.part_o + part_at<D>(slot, jn.in + r, col));
+        v[a][1] = *reinterpret_cast<const float4*>(p.tile.part_o + part_at<D>(slot, jn.in + r, col + 4));
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) mn = fmaxf(mn, ml[a].x);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const float fa = ml[a].x == -INFINITY ? 0.f : ex2_approx(ml[a].x - mn);
+      l = fmaf(ml[a].y, fa, l);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        acc[4 * x] = fmaf(v[a][x].x, fa, acc[4 * x]);
+        acc[4 * x + 1] = fmaf(v[a][x].y, fa, acc[4 * x + 1]);
+        acc[4 * x + 2] = fmaf(v[a][x].z, fa, acc[4 * x + 2]);
+        acc[4 * x + 3] = fmaf(v[a][x].w, fa, acc[4 * x + 3]);
+      }
+    }
+    m = mn;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int rr = jn.row + r, i = rr / p.g, hq = jn.h * p.g + rr - i * p.g;
+  *reinterpret_cast<uint4*>(p.o + (long long)(jn.row0 + i) * p.o_row + (long long)hq * p.o_head + col) =
+      make_uint4(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv), pack2<BF16>(acc[4] * inv, acc[5] * inv),
+                 pack2<BF16>(acc[6] * inv, acc[7] * inv));
+  if (col == 0 && p.lse) p.lse[(long long)hq * p.total_q + jn.row0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
 template <int D, bool BF16>
@@ -782,7 +828,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
   const int total = items + (p.tile.no_plan ? p.tile.no_plan : p.tile.max_units > 0 ? p.tile.queue->njoins : 0);
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
     if (x >= items) {
-      join_unit<D, BF16, JOIN_AHEAD>(p, p.tile.joins[x - items]);
+      join_unit<D, BF16>(p, p.tile.joins[x - items]);
       continue;
     }
     const int c = x / halves, prow = x % halves * JOIN_ROWS;
@@ -955,7 +1001,7 @@ int launch_rows(const RowsParams& p, const attn_fwd_paged_params_t& a, const Pla
   if (rc != ATTN_OK) return rc;
   if (TREE && p.tile.no_plan) {
     const bool many = (long long)p.B * p.Hkv * ((p.max_q + TILE_QT * p.tile.T - 1) / (TILE_QT * p.tile.T)) > sms;
-    return launch_dependent(many ? tree_join_kernel<D, BF16, true> : tree_join_kernel<D, BF16, false>, dim3(p.tile.no_plan), 32 * JOIN_WARPS, 0, st, p);
+    return launch_dependent(many ? tree_join_kernel<D, BF16, true> : tree_join_kernel<D, BF16, false>, dim3(p.tile.no_plan), JOIN_ROWS * D / 8, 0, st, p);
   }
   const int joins = p.tile.no_plan ? p.tile.no_plan : plan.rows_grid;
   return launch_dependent(join_kernel<D, BF16>, dim3(joins), 32 * JOIN_WARPS, 0, st, p);
