@@ -29,7 +29,8 @@ __device__ __forceinline__ void rows_of(const int* cu, int b, int rows, int& row
 // mask(i) = bits of i and of the nodes above it, depth(i) = their number less one, position = context + depth.  One CTA
 // takes a request, its parents in shared memory, a thread a node: it walks up, and as the nodes above have
 // descending numbers, their bits gather in one word that is written once the walk has left it.  What bounds it is latency:
-// offsets -> parents -> a walk of the tree's depth (some 30 cycles a step).
+// offsets -> parents -> a walk of the tree's depth.  Measured: one tree of 26 nodes 1.7 us, 301 of up to 64 nodes with chunks of up to 2000
+// tokens among them 3.7.
 constexpr int TREE_THREADS = 256, TREE_WORDS = 32, TREE_NODES = 32 * TREE_WORDS;
 
 struct TreeParams {
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(TREE_THREADS) paged_tree_kernel(const __grid_c
 // registers, ACCEPT_HELD of them, so a step is a few ballots; further ones are read again at each step.  Pages that hold no token any
 // longer are counted, every warp tells every CTA of the cluster its requests' counts, and behind the cluster's barrier
 // each CTA sums them up by itself and writes its requests' pages to the free list in the requests' order.
-// What bounds it is latency: offsets -> nodes -> walk -> table entries -> barrier -> sum -> list.
+// What bounds it is latency: offsets -> nodes -> walk -> table entries -> barrier -> sum -> list.  Measured: 8 trees of 26 nodes 5.1 us, 301 of
+// up to 64 nodes 6.6 (with 8 CTAs, two requests to some warps, and the table read again behind the barrier 10.1).
 constexpr int ACCEPT_THREADS = 1024, ACCEPT_WARPS = ACCEPT_THREADS / 32, ACCEPT_MAX_B = 16384;
 constexpr int ACCEPT_BLOCKS = 4, ACCEPT_HELD = 32 * ACCEPT_BLOCKS;
 
@@ -287,7 +289,9 @@ __global__ void __launch_bounds__(ACCEPT_THREADS) paged_accept_kernel(const __gr
 // ------------------------------------------------------------------ moves
 // cache[l][dst] = cache[l][src] for the moves of every list and every layer l.  A CTA takes a list and a layer,
 // a thread 16-byte columns of K's and V's rows: it makes the list's moves in order, MOVE_AHEAD of them in flight, so
-// that a row which a later move overwrites has been read, without any other order between threads.
+// that a row which a later move overwrites has been read, without any other order between threads.  Bound by memory in rows of 256 bytes: 61
+// lists of up to 8 moves in 32 layers of 8 heads, d = 128 (66 MB) 12.9 us, 5.1 TB/s; two or four layers to a CTA 13.7 and 14.6, four moves ahead
+// 13.2, 128 threads 13.6.  8 lists in one layer: 2.3 us, a launch's time.
 constexpr int MOVE_THREADS = 256, MOVE_AHEAD = 8, MOVE_LIST = 64;
 
 struct MoveParams {
