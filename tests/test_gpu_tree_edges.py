@@ -73,6 +73,15 @@ def test_a_q_tile_that_never_comes_ends_the_launch(d, shape):
     call.check()
 
 
+@pytest.mark.parametrize("nodes,g,d", [([32, 30], 7, 128), ([2, 2, 1], 100, 64), ([80, 75], 3, 64), ([42], 6, 128), ([4, 3], 60, 128)])
+def test_groups_that_do_not_fill_a_q_tile(nodes, g, d):
+    """Cut units of two Q tiles of fewer than 128 rows each: all rows of the second one are joined."""
+    call = Call(nodes, [6000 + 500 * i + m for i, m in enumerate(nodes)], 2 * g, 2, d, words=3, seed=g)
+    call()
+    af.attn_check()
+    call.check()
+
+
 def test_a_workspace_that_is_too_small_is_refused():
     call = Call(*SHAPES[0], 128)
     n = af.attn_paged_workspace(2, 8, 1, 128, 31, 26)
