@@ -379,7 +379,7 @@ int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long lo
  * Slots are distinct.  A contiguous [B][H][S][d] tensor whose entries share their positions counts as B*H heads of S rows.
  * q_weight, k_weight: [d], of the rows' type, or float where weight_f32 is not 0.  positions: int32, axis a at
  * positions + a*position_stride; inv_freq: float [axes][rot_dim/2].  With rot_dim = 0 both may be NULL.
- * rot_dim is a multiple of 16, at most d; 1 <= axes <= 4; eps >= 0; rows <= 2^30; at most 65536 heads.
+ * rot_dim is a multiple of 16, at most d; 1 <= axes <= 4; frequencies are finite, of 2^60 at most; eps >= 0; rows <= 2^30; at most 65536 heads.
  */
 typedef struct {
     const void *q, *k, *v;
