@@ -146,6 +146,7 @@ struct TileParams : PagedParams {
   int box_rows;   // rows of one K/V box
   int z_page, z_head, z_extent;  // the maps' page-and-head coordinate: page * z_page + h * z_head, below z_extent
   unsigned int g_inverse;  // 65536 / g + 1: row / g = row * g_inverse >> 16 for rows below 128
+  unsigned int unit_inverse;  // 2^32 over a unit's tokens, rounded up
   int inject;
 };
 // Fills them in (ahead of any launch: a tensor map may fail), and launches the kernel.

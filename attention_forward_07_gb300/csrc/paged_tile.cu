@@ -177,14 +177,21 @@ struct TreeRun {
   int runs, each, longer; // the first `longer` runs have each + 1 positions, the others `each`
   int b, blk, h;
   int in, left;  // positions of the pair that lie before the run; the run's that are left
-  __device__ __forceinline__ int length(const TileUnit& x) const { return (x.w * x.pad + cost + piece - 1) / piece * piece; }
+  __device__ __forceinline__ int length(const TileUnit& x) const {
+    const int n = x.w * x.pad + cost;
+    return piece == 1 ? n : (n + piece - 1) / piece * piece;
+  }
   __device__ __forceinline__ int begin(int i) const { return each * i + min(i, longer); }
   __device__ __forceinline__ int run(int x) const {  // that holds position x
     const int border = (each + 1) * longer;
     return x < border ? x / (each + 1) : longer + (x - border) / each;
   }
 };
-__device__ __forceinline__ int tree_units(const TileParams& p, int sq) { return (sq + TILE_QT * p.tile.T - 1) / (TILE_QT * p.tile.T); }
+// (Without a plan a request has at most NO_PLAN_CHUNK units: the product below is exact up to 2^24.)
+__device__ __forceinline__ int tree_units(const TileParams& p, int sq) { return (int)__umulhi((unsigned int)(sq + TILE_QT * p.tile.T - 1), p.unit_inverse); }
+// Key tiles that x positions of a unit hold.
+template <int D>
+__device__ __forceinline__ int tiles_of(const TileUnit& u, int x) { return u.pad == BOTH_COST ? x / BOTH_COST : x / ONE_COST<D>; }
 template <int D>
 __device__ __forceinline__ void tree_unit(const TileParams& p, int b, int blk, TileUnit& x) {
   int k0, k1;
@@ -204,7 +211,8 @@ __device__ __forceinline__ bool tree_run(const TileParams& p, int run, int lane,
   r.cost = r.b = r.blk = r.h = r.in = r.left = 0;
   int pos = INT_MAX, before = 0;
   bool mine = false;
-  // passes over the lane's units: their tiles' positions, which say how the line is cut; the line as it is cut; the run's first pair
+  // Passes over the lane's units: their tiles' positions, which say how the line is cut; with pieces, the line as it is cut (without, it
+  // follows); the run's first pair.
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
     int own = 0, units = 0;
@@ -233,6 +241,18 @@ __device__ __forceinline__ bool tree_run(const TileParams& p, int run, int lane,
       }
     }
     if (pass == 2) break;
+    if (pass == 0) {
+      // pieces of this length find a CTA each (every pair has at most one that is not full)
+      const int tiles = __reduce_add_sync(0xffffffffu, own), room = sms - __reduce_add_sync(0xffffffffu, units);
+      const int piece = max((tiles + room - 1) / max(room, 1), 2 * ONE_COST<D>);
+      if (room > 0 && piece <= tiles / sms + PAIR_COST) {
+        r.piece = piece;
+        continue;
+      }
+      r.cost = PAIR_COST;
+      own += PAIR_COST * units;
+      pass = 1;
+    }
     int incl = own;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -240,14 +260,6 @@ __device__ __forceinline__ bool tree_run(const TileParams& p, int run, int lane,
       if (lane >= s) incl += y;
     }
     const int line = __shfl_sync(0xffffffffu, incl, 31);
-    if (pass == 0) {
-      // pieces of this length find a CTA each (every pair has at most one that is not full)
-      units = __reduce_add_sync(0xffffffffu, units);
-      const int room = sms - units, piece = max((line + room - 1) / max(room, 1), 2 * ONE_COST<D>);
-      if (room > 0 && piece <= line / sms + PAIR_COST) r.piece = piece;
-      else r.cost = PAIR_COST;
-      continue;
-    }
     if (line == 0) return false;
     r.runs = r.cost ? max(1, min(sms, line / MIN_TREE_RUN)) : line / r.piece;
     r.each = line / r.runs;
@@ -410,8 +422,8 @@ __device__ __forceinline__ void tile_load_role(const TileParams& p, uint32_t bas
           // the tiles of the pair's positions [in, out): a tile goes with its last position
           const int out = min(tr.in + tr.left, tr.length(un));
           tr.left -= out - tr.in;
-          from = max(tr.in - tr.cost, 0) / un.pad;
-          tiles = min(max(out - tr.cost, 0) / un.pad, un.w) - from;
+          from = tiles_of<D>(un, max(tr.in - tr.cost, 0));
+          tiles = min(tiles_of<D>(un, max(out - tr.cost, 0)), un.w) - from;
           pt = un;
           h = tr.h;
           slot = tiles == pt.w ? -1 : from == 0 ? 2 * run + 1 : 2 * run;
@@ -1069,6 +1081,7 @@ int tile_prepare(const PagedParams& base, const attn_fwd_paged_params_t& a, Tile
       (rc = host_map5(&p.tm_v, a.v_cache, bf16, kv)) != ATTN_OK)
     return rc;
   p.g_inverse = 65536u / p.g + 1;
+  p.unit_inverse = (unsigned int)(((1ull << 32) + TILE_QT * p.tile.T - 1) / (TILE_QT * p.tile.T));
   p.inject = host_take_inject();
   return ATTN_OK;
 }
