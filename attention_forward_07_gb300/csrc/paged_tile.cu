@@ -24,7 +24,7 @@
 //
 // attn_fwd_paged_tree (TREE): the new rows of a request of few rows see each other by masks, which only key tiles with new rows look at.
 // 24 trees of 40 - 64 nodes x 8 heads against 3 - 8k keys, d = 128: 98 us for 89 GFLOP (241 MB of keys and values); 27 trees of 5 - 17
-// nodes with a window beside two chunks, d = 64, 74 us; one tree of 26 nodes against 2000 keys 15.6 us, of which the keys take three.
+// nodes with a window beside two chunks, d = 64, 71 us; one tree of 26 nodes against 2000 keys 15.4 us, of which the keys take three.
 #include <cuda_runtime.h>
 
 #include <atomic>
