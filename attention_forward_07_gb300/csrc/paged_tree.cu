@@ -27,21 +27,25 @@ __device__ __forceinline__ void rows_of(const int* cu, int b, int rows, int& row
 
 // ------------------------------------------------------------------ masks and positions
 // mask(i) = bits of i and of the nodes above it, depth(i) = their number less one, position = context + depth.  One CTA
-// takes a request, its parents in shared memory, a thread a node: it walks up, and as the nodes above have
-// descending numbers, their bits gather in one word that is written once the walk has left it.  What bounds it is latency:
-// offsets -> parents -> a walk of the tree's depth.  Measured: one tree of 26 nodes 1.7 us, 301 of up to 64 nodes with chunks of up to 2000
-// tokens among them 3.7.
-constexpr int TREE_THREADS = 256, TREE_WORDS = 32, TREE_NODES = 32 * TREE_WORDS;
+// takes a request, its first warp the nodes, 32 at a time in order: within the 32 every node's mask joins that of the node
+// it has got to and goes on from there, twice as far each time (shuffles); the topmost one's parent lies in an earlier 32, whose masks and
+// depths are in shared memory.  So a chain takes no longer than a bush.  As the nodes above have descending numbers, those within a
+// window are a mask's highest bits.  What bounds it is latency: offsets -> parents -> shuffles.  Measured: one tree of 26 nodes
+// 1.3 us, 301 of up to 64 nodes with chunks of up to 2000 tokens among them 2.3, 46 chains of 256 nodes 11 (a thread walking up from every
+// node: 1.7, 3.7 and 28).
+constexpr int TREE_THREADS = 128, TREE_WORDS = 32, TREE_NODES = 32 * TREE_WORDS;
 
 struct TreeParams {
   attn_paged_tree_params_t a;
   unsigned int* status;
 };
+size_t tree_smem(int words) { return (size_t)32 * words * (words + 1) * sizeof(uint32_t); }  // masks, depths
 
 __global__ void __launch_bounds__(TREE_THREADS) paged_tree_kernel(const __grid_constant__ TreeParams p) {
   const attn_paged_tree_params_t& a = p.a;
-  __shared__ int up[TREE_NODES];
-  const int tid = threadIdx.x, b = blockIdx.x;
+  extern __shared__ uint32_t masks[];  // [nodes][mask_words]
+  int* depths = reinterpret_cast<int*>(masks + 32 * a.mask_words * a.mask_words);
+  const int lane = threadIdx.x, b = blockIdx.x;
   grid_launch_dependents();
   grid_dependency_wait();
   int row0, n;
@@ -49,38 +53,47 @@ __global__ void __launch_bounds__(TREE_THREADS) paged_tree_kernel(const __grid_c
   rows_of(a.cu_seqlens_q, b, a.rows, row0, n);
   const int ctx = max(keys - n, 0);
   if (n > 32 * a.mask_words) {  // a chunk: a chain without a mask
-    for (int i = tid; i < n; i += TREE_THREADS) a.positions[row0 + i] = ctx + i;
+    for (int i = threadIdx.x; i < n; i += TREE_THREADS) a.positions[row0 + i] = ctx + i;
     return;
   }
+  if (threadIdx.x >= 32) return;
   bool bad = false;
-  for (int i = tid; i < n; i += TREE_THREADS) {
-    int x = load_cg(a.parents + row0 + i);
-    if (x >= i || x < -1) {  // (only a node ahead of it can be above it, so that every walk ends)
-      x = -1;
+  int next = lane < n ? load_cg(a.parents + row0 + lane) : -1;
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane;
+    int up = next;
+    if (i + 32 < n) next = load_cg(a.parents + row0 + i + 32);
+    if (i >= n) up = -1;
+    if (up >= i || up < -1) {  // (only a node ahead of it can be above it)
+      up = -1;
       bad = true;
     }
-    up[i] = x;
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += TREE_THREADS) {
-    uint32_t* out = a.tree_mask + (long long)(row0 + i) * a.mask_stride;
-    int w = i >> 5, depth = 0;
-    for (int x = a.mask_words - 1; x > w; --x) out[x] = 0u;
-    uint32_t bits = 1u << (i & 31);
-    for (int x = up[i]; x >= 0; x = up[x]) {
-      ++depth;
-      if (a.window_left >= 0 && depth > a.window_left) continue;
-      while (w > x >> 5) {
-        out[w--] = bits;
-        bits = 0u;
+    uint32_t bits = 1u << lane;
+    int to = up - base;  // the lane that the node's mask ends ahead of; below 0: no more of these 32
+    while (__any_sync(0xffffffffu, to >= 0)) {
+      const uint32_t more = __shfl_sync(0xffffffffu, bits, max(to, 0));
+      const int further = __shfl_sync(0xffffffffu, to, max(to, 0));
+      if (to >= 0) {
+        bits |= more;
+        to = further;
       }
-      bits |= 1u << (x & 31);
     }
-    for (; w >= 0; --w) {
-      out[w] = bits;
-      bits = 0u;
+    const int above = __shfl_sync(0xffffffffu, up, __ffs(bits) - 1);  // the topmost one's parent, ahead of these 32 (or none)
+    if (i < n) {
+      const int depth = __popc(bits) - 1 + (above >= 0 ? depths[above] + 1 : 0);
+      uint32_t* out = a.tree_mask + (long long)(row0 + i) * a.mask_stride;
+      int left = a.window_left < 0 ? INT_MAX : min(a.window_left, INT_MAX - 1) + 1;  // nodes that the mask may hold
+      for (int w = a.mask_words - 1; w >= 0; --w) {
+        uint32_t x = w == base >> 5 ? bits : above >= 0 && w < base >> 5 ? masks[above * a.mask_words + w] : 0u;
+        for (int over = __popc(x) - left; over > 0; --over) x &= x - 1u;
+        left -= __popc(x);
+        masks[i * a.mask_words + w] = x;
+        out[w] = x;
+      }
+      depths[i] = depth;
+      a.positions[row0 + i] = (int)min((long long)ctx + depth, (long long)INT_MAX);
     }
-    a.positions[row0 + i] = (int)min((long long)ctx + depth, (long long)INT_MAX);
+    __syncwarp();
   }
   if (bad) atomicOr(p.status, STATUS_PAGE);
 }
@@ -394,7 +407,11 @@ int attn_paged_tree(const attn_paged_tree_params_t* params) {
     if (rc != ATTN_OK) return rc;
     TreeParams p{a, nullptr};
     if ((rc = host_status_word(dev, a.stream, &p.status)) != ATTN_OK) return rc;
-    return launch_dependent(paged_tree_kernel, dim3(a.B), TREE_THREADS, 0, reinterpret_cast<cudaStream_t>(a.stream), p);
+    const size_t smem = tree_smem(a.mask_words);
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(paged_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tree_smem(TREE_WORDS)) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    return launch_dependent(paged_tree_kernel, dim3(a.B), TREE_THREADS, smem, reinterpret_cast<cudaStream_t>(a.stream), p);
   });
 }
 
