@@ -1078,11 +1078,12 @@ int paged_fwd_impl(const attn_fwd_paged_params_t& a, const attn_fwd_paged_tree_p
   // Without a plan a lane of each CTA looks at all units of a chunk.  attn_fwd_paged_tree: most_line bounds the positions of the line that its
   // kernel cuts, whatever the lengths and offsets.
   const long long most_tiles = ((long long)a.table_width * a.page_size + TILE_KEYS - 1) / TILE_KEYS;
-  const long long most_units = ((long long)p.max_q + TILE_QT * plan.T - 1) / (TILE_QT * plan.T), most_line = a.B * most_units * (16 * most_tiles + 64) * a.Hkv;
+  const long long most_units = ((long long)p.max_q + TILE_QT * plan.T - 1) / (TILE_QT * plan.T);
+  const double most_line = (double)a.B * most_units * (16. * most_tiles + 64.) * a.Hkv;
   // (the second Q tile's entries begin behind those of a full one, whose rows a group need not fill)
   const auto joins_of = [&](int tokens) { return (tokens * p.g + JOIN_ROWS - 1) / JOIN_ROWS; };
   const int joins_of_unit = p.max_q <= plan.T ? joins_of(p.max_q) : JOINS_OF_RUN + joins_of(p.max_q < 2 * plan.T ? p.max_q - plan.T : plan.T);
-  if (plan.max_units > 0 && (tree ? most_units <= NO_PLAN_CHUNK && plan.max_units <= NO_PLAN_UNITS && most_line < INT_MAX / 2 : p.max_q <= plan.T) &&
+  if (plan.max_units > 0 && (tree ? most_units <= NO_PLAN_CHUNK && plan.max_units <= NO_PLAN_UNITS && most_line < (1 << 30) : p.max_q <= plan.T) &&
       a.B <= NO_PLAN_B && (long long)a.total_q * p.g > (long long)ROWS_MAX * a.B)
     p.tile.no_plan = sms * (tree ? joins_of_unit : JOINS_OF_RUN);
   if (plan.max_units > 0) {
