@@ -78,7 +78,7 @@ __device__ __forceinline__ unsigned long long turn_of(float f) {
 // parts of a turn and the weights are the CTA's) and leaves them in shared memory of its own, so no warp waits for another; a lane keeps
 // its pairs' products for all heads of q, then of k.  The values' items are plain copies.
 // Measured (d = 128): 16.9k rows of 32/8 heads into the cache 70.6 us, 5.9 TB/s (0.88 of measured copy bandwidth); 8190 rows of 16/2 heads,
-// three axes, to buffers 18.7 us, bound by its instructions (57 % of the issue slots: the angles and products of a token serve 18 rows
+// three axes, to buffers 18.8 us, bound by its instructions (57 % of the issue slots: the angles and products of a token serve 18 rows
 // only); 64 rows 3.7 us, a launch and a chain of loads.  16 warps an SM: 20 and 24, for which registers spill, take 74 and 90 us.
 template <int D, bool BF16, bool ADJACENT>
 __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __grid_constant__ RopeParams p) {
@@ -95,6 +95,9 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
   int ca, cb;
   if (ADJACENT || l * 8 >= half) ca = ADJACENT ? l * 16 : a.rot_dim + (l * 8 - half) * 2, cb = ca + 8;
   else ca = l * 8, cb = ca + half;
+  // Whether the lane's pairs are turned (eight of them, and half is a multiple of eight).  Those that are not are no pairs: an infinity or NaN in
+  // one of the two times a sine of 0 would reach the other.
+  const bool turned = l * 8 < half;
   const int qk_items = p.q_items + p.k_items, items = qk_items + p.v_items;
   float(&mine)[2][4][PAIRS] = coef[warp];
   // a token's positions (lane x: of axis x) and slot (lane ROPE_AXES)
@@ -280,12 +283,23 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __g
         r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
       }
       const uint64_t rr = f2_pack(r, r);
+      if (turned) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t x = va[e];
+          va[e] = ffma2(x, f[0][e], fmul2(vb[e], f[1][e]));
+          vb[e] = ffma2(vb[e], f[2][e], fmul2(x, f[3][e]));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) va[e] = fmul2(va[e], f[0][e]), vb[e] = fmul2(vb[e], f[2][e]);
+      }
       uint32_t y0[4], y1[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float a0, a1, b0, b1;
-        f2_unpack(fmul2(rr, ffma2(va[e], f[0][e], fmul2(vb[e], f[1][e]))), a0, a1);
-        f2_unpack(fmul2(rr, ffma2(vb[e], f[2][e], fmul2(va[e], f[3][e]))), b0, b1);
+        f2_unpack(fmul2(rr, va[e]), a0, a1);
+        f2_unpack(fmul2(rr, vb[e]), b0, b1);
         if (ADJACENT) {
           (e < 2 ? y0[2 * e] : y1[2 * e - 4]) = narrow2<BF16>(a0, b0);
           (e < 2 ? y0[2 * e + 1] : y1[2 * e - 3]) = narrow2<BF16>(a1, b1);

@@ -369,7 +369,8 @@ int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long lo
  *     y = x * rsqrt(mean(x^2) + eps) * weight      (over the d elements of a head's row; y = x where the weight is NULL)
  *     phi_i = sum over axes a of positions[a][t] * inv_freq[a][i],  0 <= i < rot_dim / 2
  *     (y_a, y_b) -> (y_a cos phi_i - y_b sin phi_i, y_b cos phi_i + y_a sin phi_i)
- * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved is not 0; elements from rot_dim on are not turned.
+ * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved is not 0; elements from rot_dim on are not turned (y = x
+ * to the bit without a weight, whatever stands beside them).
  * One axis is the usual rotation; with several (time, height, width) each pair's frequency stands in its axis's row and
  * the other rows hold 0 there.  All in 32 bits, rounded once; angles are exact to 2^-21 of a turn at any position (with frequencies
  * of at most 1; positions may be negative).
