@@ -607,8 +607,8 @@ def _rope_shared(q, k, positions, inv_freq, q_weight, k_weight, dtype, index, ro
 def attn_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, stream=None):
     """Norms of queries and keys for each head (where there are weights, [d] of q's type or fp32) and their rotation by position,
     in one pass: q, q_out [Hq, rows, d], k, k_out [Hkv, rows, d], any strides whose last dimension is contiguous; an output may be
-    its input.  positions int32 [rows] with inv_freq fp32 [pairs], or [axes, rows] with [axes, pairs], whose columns hold a pair's
-    frequency in its axis and 0 elsewhere; pairs are halves' or, interleaved, neighbours', and elements past 2 * pairs are not
+    its input.  positions int32 [rows] with inv_freq fp32 [pairs], or [axes, rows] (each axis contiguous, or one row expanded) with [axes, pairs],
+    whose columns hold a pair's frequency in its axis and 0 elsewhere; pairs are halves' or, interleaved, neighbours', and elements past 2 * pairs are not
     turned.  inv_freq None: norms alone.  A contiguous [B, H, S, d] of shared positions goes in as view(B * H, S, d).  See include/attn.h."""
     _torch or _with_torch()
     dtype, index, shape = q.dtype, q.get_device(), q.shape

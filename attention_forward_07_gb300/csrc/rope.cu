@@ -325,7 +325,7 @@ int check(const attn_rope_params_t& a) {
   if (a.dtype != ATTN_F16 && a.dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
   if (a.rows < 1 || a.rows > (1 << 30) || a.Hq < 1 || a.Hkv < 1 || a.Hq > (1 << 16) || a.Hkv > (1 << 16)) return ATTN_ERR_INVALID;
   if (a.rot_dim < 0 || a.rot_dim > a.d || a.rot_dim % 16 != 0) return ATTN_ERR_INVALID;
-  if (a.rot_dim > 0 && (!a.positions || !a.inv_freq || a.axes < 1 || a.axes > ROPE_AXES || (a.axes > 1 && a.position_stride < a.rows)))
+  if (a.rot_dim > 0 && (!a.positions || !a.inv_freq || a.axes < 1 || a.axes > ROPE_AXES || (a.axes > 1 && a.position_stride != 0 && a.position_stride < a.rows)))
     return ATTN_ERR_INVALID;
   if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return ATTN_ERR_INVALID;
   const void *k_to = a.slots ? a.k_cache : a.k_out, *v_to = a.slots ? a.v_cache : nullptr;

@@ -369,8 +369,8 @@ int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long lo
  *     y = x * rsqrt(mean(x^2) + eps) * weight      (over the d elements of a head's row; y = x where the weight is NULL)
  *     phi_i = sum over axes a of positions[a][t] * inv_freq[a][i],  0 <= i < rot_dim / 2
  *     (y_a, y_b) -> (y_a cos phi_i - y_b sin phi_i, y_b cos phi_i + y_a sin phi_i)
- * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved is not 0; elements from rot_dim on are not turned (y = x
- * to the bit without a weight, whatever stands beside them).
+ * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved is not 0; elements from rot_dim on are not turned (without
+ * a weight y = x, whatever stands beside them).
  * One axis is the usual rotation; with several (time, height, width) each pair's frequency stands in its axis's row and
  * the other rows hold 0 there.  All in 32 bits, rounded once; angles are exact to 2^-21 of a turn at any position (with frequencies
  * of at most 1; positions may be negative).
@@ -379,7 +379,7 @@ int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long lo
  * of a negative slot is left out, of q_out as well; so is one of a slot at or past num_pages*page_size, with ATTN_ERR_PAGE.
  * Slots are distinct.  A contiguous [B][H][S][d] tensor whose entries share their positions counts as B*H heads of S rows.
  * q_weight, k_weight: [d], of the rows' type, or float where weight_f32 is not 0.  positions: int32, axis a at
- * positions + a*position_stride; inv_freq: float [axes][rot_dim/2].  With rot_dim = 0 both may be NULL.
+ * positions + a*position_stride (at least rows, or 0: all axes share one row); inv_freq: float [axes][rot_dim/2].  With rot_dim = 0 both may be NULL.
  * rot_dim is a multiple of 16, at most d; 1 <= axes <= 4; frequencies are finite, of 2^60 at most; eps >= 0; rows <= 2^30; at most 65536 heads.
  */
 typedef struct {

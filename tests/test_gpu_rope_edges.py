@@ -1,4 +1,4 @@
-"""attn_rope where its arithmetic could go wrong: elements that are not turned beside infinities and NaN."""
+"""attn_rope where its arithmetic could go wrong: elements that are not turned beside infinities and NaN, axes that share their positions."""
 import math
 
 import pytest
@@ -83,3 +83,22 @@ def test_infinities_under_a_norm_are_what_the_formula_makes_of_them(d, rot, inte
     keep = torch.ones((3, 40), dtype=torch.bool)
     keep[tuple(zip(*odd))] = False
     assert ((got.double() - want).abs() <= tol)[keep].all()
+
+
+@pytest.mark.parametrize("axes", [2, 3])
+def test_axes_that_share_their_positions(axes):
+    """An expanded row of positions (its axes' stride is 0) is what a copy of it for every axis is."""
+    g = torch.Generator().manual_seed(axes)
+    x = torch.randn((6, 50, 128), generator=g).bfloat16().cuda()
+    pos = torch.randint(0, 1000, (1, 50), generator=g).int().cuda().expand(axes, 50)
+    inv = (1000.0 ** (-torch.arange(64) / 64.0))[None] * (torch.arange(64)[None] % axes == torch.arange(axes)[:, None])
+    assert pos.stride(0) == 0
+    outs = []
+    for p in (pos, pos.contiguous()):
+        q, k = torch.empty_like(x[:4]), torch.empty_like(x[4:])
+        af.attn_rope(x[:4], x[4:], q, k, p, inv.cuda())
+        outs.append((q, k))
+    af.attn_check()
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    want, tol = tree_ref.rope(x[:4].cpu(), None, pos.cpu(), inv, 1e-6, False, torch.bfloat16)
+    assert ((outs[0][0].cpu().double() - want).abs() <= tol).all()
