@@ -9,7 +9,8 @@
 //
 // for pairs i < rot / 2, (a, b) = (i, i + rot / 2) or (2 i, 2 i + 1); elements from rot on are not turned.  All in 32 bits,
 // rounded once at the end.  An angle is a part of a turn: f / 2 pi is held in 64 bits of fixed point, whose product with an integer position wraps at
-// whole turns by itself and so keeps its accuracy at any position; its top 32 bits, as a float, go to sincospi.
+// whole turns by itself and so keeps its accuracy at any position; its top 32 bits, as a float, go to sincospi.  An angle is off by A 2^-33 (f / 2 pi
+// cut at 2^-64 of a turn, times a position), 2^-32 (the cut to 32 bits) and 2^-26 (half a step of a float of at most half a turn) of a turn at most.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -372,8 +372,8 @@ int attn_paged_workspace(const attn_fwd_paged_params_t *params, unsigned long lo
  * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved is not 0; elements from rot_dim on are not turned (without
  * a weight y = x, whatever stands beside them).
  * One axis is the usual rotation; with several (time, height, width) each pair's frequency stands in its axis's row and
- * the other rows hold 0 there.  All in 32 bits, rounded once; angles are exact to 2^-21 of a turn at any position (with frequencies
- * of at most 1; positions may be negative).
+ * the other rows hold 0 there.  All in 32 bits, rounded once; angles are exact to 2^-25 of a turn at any position and
+ * frequency (positions may be negative).
  * Where slots is NULL, rows go to q_out and k_out (each may be its input with the same strides; nothing else overlaps), and
  * v and the caches are not looked at.  Otherwise q goes to q_out, k and, unturned, v go to slot slots[t] of the caches, and a row
  * of a negative slot is left out, of q_out as well; so is one of a slot at or past num_pages*page_size, with ATTN_ERR_PAGE.

@@ -1,4 +1,5 @@
-"""attn_rope where its arithmetic could go wrong: elements that are not turned beside infinities and NaN, axes that share their positions."""
+"""attn_rope where its arithmetic could go wrong: elements that are not turned beside infinities and NaN, axes that share their positions, positions
+at both ends of their type."""
 import math
 
 import pytest
@@ -102,3 +103,44 @@ def test_axes_that_share_their_positions(axes):
     assert all(torch.equal(a, b) for a, b in zip(*outs))
     want, tol = tree_ref.rope(x[:4].cpu(), None, pos.cpu(), inv, 1e-6, False, torch.bfloat16)
     assert ((outs[0][0].cpu().double() - want).abs() <= tol).all()
+
+
+def _turns(pos, inv):
+    """Angles sum_a pos[a, t] inv[a, i] as parts of a turn in [0, 1), in whole numbers of 2^-200 (inv's floats are exact; 2 pi from Machin's formula)."""
+    bits = 400
+    arctan = lambda n: sum((-1) ** i * (1 << bits) // ((2 * i + 1) * n ** (2 * i + 1)) for i in range(200))  # noqa: E731
+    two_pi = 2 * (16 * arctan(5) - 4 * arctan(239))
+    out = torch.empty((pos.shape[1], inv.shape[1]), dtype=torch.float64)
+    ratios = [[float(f).as_integer_ratio() for f in row] for row in inv]
+    for i in range(inv.shape[1]):
+        turns = [((n << (200 + bits)) // (den * two_pi)) for n, den in (row[i] for row in ratios)]
+        for t in range(pos.shape[1]):
+            out[t, i] = (sum(int(pos[a, t]) * turns[a] for a in range(len(turns))) % (1 << 200)) / (1 << 200)
+    return out
+
+
+@pytest.mark.parametrize("axes,d,interleaved,top", [(1, 128, False, 1.0), (1, 64, True, 1.0), (3, 128, False, 1.0), (4, 128, True, 1.0), (2, 64, True, 2.0 ** 60)])
+def test_angles_at_both_ends_of_the_positions(axes, d, interleaved, top):
+    """Angles keep 2^-25 of a turn at any position: a frequency's part of a turn is cut at 2^-64, so 2^-33 of a turn for each axis's position, the
+    sum at 2^-32 and then rounded to a float, half a step of which is 2^-26 of a turn.  The function: 2 ulp of a value of at most 1, 2^-23.  Ones and zeros are
+    turned, so the rounding to fp16, small next to 0, is all else: products by 0 and 1 and sums with 0 are exact."""
+    g = torch.Generator().manual_seed(axes * d)
+    half = d // 2
+    rows = 400
+    pos = torch.cat([torch.randint(2 ** 31 - 1000, 2 ** 31, (axes, rows // 2), generator=g), torch.randint(-2 ** 31, -2 ** 31 + 1000, (axes, rows // 2), generator=g)], 1)
+    pos[:, 0], pos[:, -1] = 2 ** 31 - 1, -2 ** 31
+    pos = torch.stack([p[torch.randperm(rows, generator=g)] for p in pos])
+    inv = (top * 10000.0 ** (-torch.arange(half) / half)).float()
+    inv = inv[None].repeat(axes, 1) * (0.5 + 0.5 * torch.rand((axes, half), generator=g))  # (every axis turns every pair)
+    first = torch.arange(0, d, 2) if interleaved else torch.arange(half)
+    second = first + (1 if interleaved else half)
+    x = torch.zeros((1, rows, d), dtype=torch.float16)
+    x[..., first] = 1.0
+    q, k = torch.empty((1, rows, d), dtype=torch.float16, device="cuda"), torch.empty((1, rows, d), dtype=torch.float16, device="cuda")
+    af.attn_rope(x.cuda(), x.cuda(), q, k, pos.int().cuda(), inv.cuda(), interleaved=interleaved)
+    af.attn_check()
+    phi = 2 * math.pi * _turns(pos, inv)
+    err = 2 * math.pi * (axes * 2.0 ** -33 + 2.0 ** -32 + 2.0 ** -26) + 2.0 ** -23
+    for got, want in ((q[0].cpu().double()[:, first], phi.cos()), (q[0].cpu().double()[:, second], phi.sin())):
+        assert ((got - want).abs() <= want.abs() * 2.0 ** -11 + 2.0 ** -25 + (1 + 2.0 ** -10) * err).all()
+    assert torch.equal(q, k)
