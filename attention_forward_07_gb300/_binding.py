@@ -690,7 +690,9 @@ def attn_paged_accept(tokens, targets, parents, cu_seqlens_q, seqlens_k, block_t
     int32 device tensors: tokens, targets (the model's choice behind each node), parents [rows], cu_seqlens_q [B+1], seqlens_k [B],
     block_table [B, W], confirmed [B] (leading nodes that are known; None: 1 each) -> accepted, ctx_lens, next_tokens [B], path, src_slots,
     dst_slots [B, max path] (-1 behind the last; the slots are attn_paged_move's).  Pages without a token go back to free_pages [F] behind
-    its free_count [1] ids, free_count_out [1] (default: free_count itself) counts them; free_pages None: they do not.  See include/attn.h."""
+    its free_count [1] ids, free_count_out [1] (default: free_count itself) counts them; free_pages None: they do not.  Such pages may hold rows
+    that are still to be moved: order every layer's attn_paged_move ahead of the next write to the caches behind an attn_paged_tables on this
+    free list (on one stream it is).  See include/attn.h."""
     i32, index = (_torch or _with_torch()).int32, tokens.get_device()
     many, one, lists, width = tokens.shape, seqlens_k.shape, path.shape, block_table.shape[-1]
     (rows,), (B,) = many, one
@@ -734,7 +736,8 @@ def attn_paged_accept(tokens, targets, parents, cu_seqlens_q, seqlens_k, block_t
 def attn_paged_move(k_cache, v_cache, src_slots, dst_slots, stream=None):
     """Rows of the caches ([num_pages, Hkv, page_size, d], or of all layers at once, [layers, num_pages, Hkv, page_size, d]) go from src_slots
     to dst_slots (int32 [lists, length]; pairs with a negative slot are left out).  Within a list no source is an earlier pair's
-    destination; lists share no slot that either writes.  See include/attn.h."""
+    destination; lists share no slot that either writes.  Lists of attn_paged_accept: to be moved before the caches are written with slots of a
+    later attn_paged_tables, which may hand out the sources' pages.  See include/attn.h."""
     torch = _torch or _with_torch()
     dtype, index, i32 = k_cache.dtype, k_cache.get_device(), torch.int32
     code = _dtype_code(k_cache)

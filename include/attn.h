@@ -455,6 +455,9 @@ int attn_fwd_paged_tree(const attn_fwd_paged_tree_params_t *params);
  * pages in ascending order, *free_count_out (which may be free_count itself) is their number then.  Ids out of range or behind the table's end are
  * left out, and so is what the list (max_free ids) has no room for, each with ATTN_ERR_PAGE.  The table keeps its entries, which
  * attn_paged_tables overwrites.  With free_pages NULL (max_free = 0, free_count and free_count_out not looked at) no page goes back.
+ * Pages that go back may still hold rows that src_slots names: every layer's attn_paged_move is ordered ahead of the first write to that
+ * layer's caches (attn_rope, attn_paged_append) behind an attn_paged_tables that takes from this free list.  On one stream the calls of a step in
+ * their order are; a move on another stream is waited for.
  * No output overlaps an input but for that.  1 <= B <= 16384, 1 <= max_path <= 1024, rows <= 2^30; with rows = 0 (no request has
  * any) tokens, targets and parents may be NULL.
  */
@@ -479,7 +482,8 @@ int attn_paged_accept(const attn_paged_accept_params_t *params);
  * src_slots[list][i] to slot dst_slots[list][i], K and V.  A pair with a negative slot is left out; one with a slot at or past
  * num_pages*page_size too, with ATTN_ERR_PAGE.  Within a list no source is the destination of an earlier pair (it may be that of
  * a later one: it is read before), and destinations are distinct; different lists share no slot that either writes.
- * What attn_paged_accept writes is so, where no two requests share pages that they write.  layers, Hkv <= 65536, lists and length <= 2^20.
+ * What attn_paged_accept writes is so, where no two requests share pages that they write, and until the caches are written with slots of a later
+ * attn_paged_tables (see there).  layers, Hkv <= 65536, lists and length <= 2^20.
  */
 typedef struct {
     void *k_cache, *v_cache;
