@@ -28,7 +28,13 @@ namespace attn {
 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr long long MAX_STRIDE = 1ll << 38;  // elements: no memory holds two entries that far apart, and tensor maps end there
-constexpr int NO_PLAN_UNITS = 2048, NO_PLAN_CHUNK = 32;  // (attn_fwd_paged_tree) units that they, and that one of them, may have at most
+// attn_fwd_paged_tree without a plan: units that its requests, and that one of them, may have at most (what the lanes of a CTA look at in turn).
+// 24 trees of 8 - 16 nodes x 4 heads on 4000 keys beside a chunk of 512 / 1900 / 2040 rows (8, 30 and 32 units): 85 / 109 / 113 us at d = 128,
+// with a plan 97 / 137 / 139; 73 / 100 / 104 at d = 64, with a plan 85 / 119 / 120.  Beside few rows the order can turn, as above: 60 single tokens on
+// 4000 keys and a chunk of 400 rows (32/8 heads) 181 and 182 us at d = 128, but 156 and 104 at d = 64; 30 chains of 4 on 2000 and one of 512: 61 and
+// 69, 53 and 47.  Trees alone (60 nodes x 8 heads on 1000 keys, d = 128): 100 units 113 us, with a plan 116; 200 units 211 and 201, 400 units 407 and 379,
+// 1000 units 1013 and 932, so from some 150 units on the plan would take 5 - 10 % less; 2000 units (100 nodes on 300 keys, d = 64) 489 and 474.
+constexpr int NO_PLAN_UNITS = 2048, NO_PLAN_CHUNK = 32;
 constexpr int NO_PLAN_B = 512;  // requests at most whose lengths every CTA looks at (16 to a lane)
 constexpr int ROWS_MAX = 16, ROWS_ONLY = 32;
 constexpr int TILE_QT = 2, TILE_ROWS = 128, TILE_KEYS = 128;  // Q tiles of a unit, rows of a Q tile, keys of a key tile

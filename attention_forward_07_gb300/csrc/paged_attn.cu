@@ -55,7 +55,8 @@ struct RowsParams : PagedParams {
 // (0.90 of measured copy bandwidth); 3 of 84 - 106 thousand: 95 us, 6.0 TB/s; one of 1001: 9.3 us, latency (of
 // launches, lengths -> table -> keys, and the join).  Ring depth, CTAs and keys to a stage were swept, with
 // weights in one part: 2 stages and 3 CTAs 112 us, 2 and 4 (128 registers, spills) 166, 8 KiB in half the
-// keys 126, this 110.
+// keys 126, this 110.  Masks of new rows (attn_fwd_paged_tree) cost nothing: 24 chains of 4 tokens on 4k keys, 8/8 and 32/8 heads, 68 and 70 us at
+// d = 128 (0.89, 0.86 of copy bandwidth), 38 and 39 at d = 64 (0.79, 0.78); in the causal order within 1 % of that.
 template <int D, int MT>
 struct Rows {
   static constexpr int WARPS = 4, NTHREADS = 32 * WARPS;
@@ -763,7 +764,8 @@ __device__ __forceinline__ void join_unit(const RowsParams& p, const TileJoin& j
 // Joins of attn_fwd_paged_tree without a plan: 16 rows to a CTA, eight columns of a row to a thread (with four, what a row costs weighed more
 // than its columns).  Many pairs (MANY) are cut once or twice: CTAs in flight count, parts of a row do not.  Few pairs lie in many
 // pieces: the other way round.  With join_unit for both: 24 trees of 40 - 64 nodes against 8k keys 113 us, now 98; 26 nodes against 2000
-// keys 16.7, now 15.6.
+// keys 16.7, now 15.6.  MANY and not in each other's place: 60 trees of 33 - 64 nodes x 8 heads on 0.5 - 3k keys, d = 128 / 64, 108 / 92.8 us -> 109 /
+// 93.1; three trees of 30 x 4 on 5000 keys 26.6 / 22.8 -> 27.6 / 23.6.
 template <int D, bool BF16, bool MANY>
 __global__ void __launch_bounds__(JOIN_ROWS * D / 8, (MANY ? 6 : 2) * 128 / D) tree_join_kernel(const __grid_constant__ RowsParams p) {
   constexpr int AHEAD = MANY ? 2 : 4;

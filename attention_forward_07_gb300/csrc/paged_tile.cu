@@ -163,11 +163,12 @@ __device__ __forceinline__ bool run_start(const TileParams& p, int run, int lane
 // ------------------------------------------------------------------ runs of attn_fwd_paged_tree without a plan
 // Requests have any number of units here.  A key tile takes BOTH_COST positions of the line where both Q tiles have rows; where one has,
 // seven eighths of that at d = 128, whose keys come hardly faster, three quarters at d = 64 (with as many: 24 trees of 40 - 64 nodes x 8
-// heads at d = 128 103 us for 101, 30 trees beside two chunks at d = 64 80 for 76).  Where the pieces of every (unit, head) pair, at
+// heads at d = 128 103 us for 101, 27 trees beside two chunks at d = 64 80 for 76; 60 trees of 33 - 64 nodes x 8 heads against 0.5 - 3k keys, d = 128 /
+// 64: 110 / 90 for 108 / 93, 24 of 8 - 16 x 4 against 4k beside a chunk of 1000 rows 96 / 80 for 92 / 80).  Where the pieces of every (unit, head) pair, at
 // most `piece` positions long, find a CTA each, all runs are one piece (a pair's length is rounded up to full pieces): no CTA
 // then starts and ends twice, and few keys are spread over all SMs (26 nodes against 2000 keys, 8 heads: 16.8 us, 21.2 with runs of eight
 // tiles).  Otherwise the line is cut into runs that differ by a position at most, with PAIR_COST positions for a pair's start and end
-// (12 - 28: within 2 %).  The host sees to it that the line's positions fit 31 bits.  All loops stay loops: with two copies of this
+// (12: within 1 % on eight other shapes, 28: up to 5 % slower).  The host sees to it that the line's positions fit 31 bits.  All loops stay loops: with two copies of this
 // code, unrolled, the kernel outgrew the instruction cache and took a third longer.
 constexpr int BOTH_COST = 8, PAIR_COST = 16, MIN_TREE_RUN = BOTH_COST * MIN_RUN;
 template <int D>
@@ -654,7 +655,7 @@ __device__ __forceinline__ void exclude(uint32_t s_addr, const KeptBits& kept) {
 }
 
 // softmax_tile (roles.cuh) with its loops rolled, 64 columns at a time: the scores are read twice, the code is half as long, and
-// the warps wait half as often for instructions, which they did 40 % of the time (30 trees beside two chunks at d = 64: 77 us,
+// the warps wait half as often for instructions, which they did 40 % of the time (27 trees beside two chunks at d = 64: 77 us,
 // unrolled 87, with 32 columns at a time 81; excluded scores set ahead of the loops 76).
 constexpr int TREE_COLS = 64;
 template <int D, bool BF16, class L>

@@ -302,9 +302,10 @@ __global__ void __launch_bounds__(ACCEPT_THREADS) paged_accept_kernel(const __gr
 // ------------------------------------------------------------------ moves
 // cache[l][dst] = cache[l][src] for the moves of every list and every layer l.  A CTA takes a list and a layer,
 // a thread 16-byte columns of K's and V's rows: it makes the list's moves in order, MOVE_AHEAD of them in flight, so
-// that a row which a later move overwrites has been read, without any other order between threads.  Bound by memory in rows of 256 bytes: 61
-// lists of up to 8 moves in 32 layers of 8 heads, d = 128 (66 MB) 12.9 us, 5.1 TB/s; two or four layers to a CTA 13.7 and 14.6, four moves ahead
-// 13.2, 128 threads 13.6.  8 lists in one layer: 2.3 us, a launch's time.
+// that a row which a later move overwrites has been read, without any other order between threads.  61 lists of up to 8 moves in
+// 32 layers of 8 heads, d = 128 (66 MB read and written) 12.9 us, 5.1 TB/s.  Half of what it reads and nearly all that it writes stays in L2 (DRAM at 33 % of
+// its peak), and what it waits for is the latency of slots and rows: 1952 CTAs of lists of uneven lengths, 760 at a time.  Two or four layers
+// to a CTA 13.7 and 14.6, four moves ahead 13.2, 128 threads 13.6.  8 lists in one layer: 2.3 us, a launch's time.
 constexpr int MOVE_THREADS = 256, MOVE_AHEAD = 8, MOVE_LIST = 64;
 
 struct MoveParams {

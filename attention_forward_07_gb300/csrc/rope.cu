@@ -78,9 +78,9 @@ __device__ __forceinline__ unsigned long long turn_of(float f) {
 // item a warp works out the four products of weight and cosine or sine that turn its pairs (two pairs to a lane; the frequencies'
 // parts of a turn and the weights are the CTA's) and leaves them in shared memory of its own, so no warp waits for another; a lane keeps
 // its pairs' products for all heads of q, then of k.  The values' items are plain copies.
-// Measured (d = 128): 16.9k rows of 32/8 heads into the cache 70.6 us, 5.9 TB/s (0.88 of measured copy bandwidth); 8190 rows of 16/2 heads,
-// three axes, to buffers 18.8 us, bound by its instructions (57 % of the issue slots: the angles and products of a token serve 18 rows
-// only); 64 rows 3.7 us, a launch and a chain of loads.  16 warps an SM: 20 and 24, for which registers spill, take 74 and 90 us.
+// Measured (d = 128): 16.9k rows of 32/8 heads into the cache 70.6 us, 5.9 TB/s (0.88 of measured copy bandwidth), neighbours' pairs 71.2; to buffers 58.3
+// and 58.7 (0.88; at d = 64 32.8, 0.79).  8190 rows of 16/2 heads to buffers, three axes 18.8 us, one axis 18.4, neighbours' pairs 18.9 and 18.5, bound by
+// its instructions (57 % of the issue slots: the angles and products of a token serve 18 rows only); 64 rows 3.8 us, a launch and a chain of loads.  16 warps an SM: 20 and 24, for which registers spill, take 74 and 90 us.
 template <int D, bool BF16, bool ADJACENT>
 __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_kernel(const __grid_constant__ RopeParams p) {
   const attn_rope_params_t& a = p.a;
